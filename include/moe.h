@@ -140,6 +140,54 @@ int moe_route(const uint16_t* x, const float* w_router, const float* bias, int T
  * (the same split is otherwise redone on every call).  Stream-ordered. */
 int moe_router_prepare(const float* w_router, int E, int H, uint16_t* w_terms, void* stream);
 
+/* Routing with softmax or sigmoid scores, expert groups and a scale.  The
+ * donor-reference page names the groups (group_scores, group_idx, score_mask)
+ * and gives no constants; moe_route is the case of one group.
+ *   s_e = 1 / (1 + exp(-z_e)), or exp(z_e - max z) / sum exp(z - max z)
+ *   c_e = s_e + bias_e, or the order of the z_e without a bias
+ *   group score: the sum of its two largest c (s without a bias), or its
+ *   largest c (z without a bias); groups are runs of E / groups experts
+ *   the topk_groups best groups are kept, and of their experts the k with the
+ *   largest c, in descending order (equal: lower id first, groups too)
+ *   w = s (unbiased); w /= sum w + 1e-20 if renorm; w *= scale
+ * The choice is that of 64-bit scores: fp32 scores decide where they can, and
+ * experts whose fp32 keys are within their rounding of one another are
+ * compared again in 64 bits.
+ * Unavailable experts: a logit of -inf or NaN, or a bias of -inf or NaN.  They
+ * rank below every other expert of the kept groups, count nothing in a
+ * group's score, and get weight 0 where they have to fill up the k (a row
+ * with no expert left lists k valid ids, all with weight 0). */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
+#define MOE_GROUP_TOP2 0
+#define MOE_GROUP_MAX 1
+
+typedef struct moe_route_config {
+  int32_t E;           /* experts, at most 2048, a multiple of groups */
+  int32_t k;           /* experts per token, at most 32 and topk_groups * (E / groups) */
+  int32_t score;       /* MOE_SCORE_* */
+  int32_t groups;      /* 1 .. 32 */
+  int32_t topk_groups; /* 1 .. groups */
+  int32_t group_score; /* MOE_GROUP_* */
+  int32_t renorm;
+  float scale; /* finite */
+} moe_route_config;
+
+/*   logits    fp32 or (logits_bf16 != 0) bf16, row t at logits + t * ld
+ *             elements, ld >= E; 16-byte aligned rows are read faster
+ *   bias      fp32 [E] or NULL
+ *   topk_idx  int32 [T, k] out;  topk_w fp32 [T, k] out */
+int moe_route_logits(const moe_route_config* cfg, const void* logits, int logits_bf16, int64_t ld,
+                     const float* bias, int T, int32_t* topk_idx, float* topk_w, void* stream);
+
+/* The same from x bf16 [T, H] (H % 64 == 0) and w_router fp32 [E, H]: logits
+ * as in moe_route, then moe_route_logits.  w_terms: from moe_router_prepare
+ * (used from T = 512 on) or NULL. */
+size_t moe_route_grouped_workspace_size(const moe_route_config* cfg, int T, int H);
+int moe_route_grouped(const moe_route_config* cfg, const uint16_t* x, const float* w_router,
+                      const uint16_t* w_terms, const float* bias, int T, int H, int32_t* topk_idx,
+                      float* topk_w, void* ws, size_t ws_bytes, void* stream);
+
 /* -------------------------------------------------------------- dispatch -- */
 
 size_t moe_dispatch_workspace_size(int T, int E, int k);
@@ -391,6 +439,41 @@ int moe_linear_bf16(const uint16_t* x, const uint16_t* w, int M, int N, int K, u
  * (donor-reference RMSNorm equations).  x, y bf16 [M, N]; gain bf16 [N]. */
 int moe_rmsnorm(const uint16_t* x, const uint16_t* gain, int M, int N, float eps, uint16_t* y,
                 void* stream);
+
+/* The norms on both sides of a block's output with its gate and residual, in
+ * one pass (donor-reference RMSNorm equations; the residual sums of its decoder
+ * layer).  Row by row, in fp32:
+ *   v  = y, or y / sqrt(mean(y^2) + eps) * post_gain   (post_gain not NULL)
+ *   v *= gate, or 1 / (1 + exp(-gate)) with gate_sigmoid (gate_mode)
+ *   r  = x + scale * v                                  (x NULL: scale * v)
+ *   x_out = r, rounded to the stream's type             (x_out not NULL)
+ *   h  = bf16( r / sqrt(mean(r^2) + eps) * pre_gain )   (h and pre_gain), of
+ *        the unrounded r
+ * y, gate, gains and h are bf16; x and x_out bf16 or (x_f32) fp32.  Every
+ * tensor of rows has its own row stride *_ld, in elements; gate is [T, N]
+ * (MOE_GATE_FULL), [N] (CHANNEL) or one value a row, gate_ld apart (TOKEN).
+ * x_out may be x itself, and h may be y, with the same stride; other overlaps
+ * are not supported.  Any N up to 32768 (else MOE_ERR_UNSUPPORTED); N % 8 == 0
+ * with 16-byte aligned rows is the fast path. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_FULL 1
+#define MOE_GATE_CHANNEL 2
+#define MOE_GATE_TOKEN 3
+
+typedef struct moe_block_norm_args {
+  const uint16_t* y;
+  const void* x;
+  const uint16_t* post_gain;
+  const uint16_t* gate;
+  const uint16_t* pre_gain;
+  void* x_out;
+  uint16_t* h;
+  int64_t y_ld, x_ld, gate_ld, x_out_ld, h_ld;
+  int32_t T, N, x_f32, gate_mode, gate_sigmoid;
+  float scale, eps;
+} moe_block_norm_args;
+
+int moe_block_norm(const moe_block_norm_args* args, void* stream);
 
 /* --------------------------------------------------------- shared expert -- */
 

@@ -7,13 +7,14 @@ no fallback).  ``int4_routed_expert_fp32_gb300.build`` compiles it.
 """
 import importlib
 
-_BINDING = ("MoeConfig", "MoeError", "MoeLayer", "MoeWeights", "check_error", "combine",
+_BINDING = ("MoeConfig", "MoeError", "MoeLayer", "MoeWeights", "block_norm", "check_error", "combine",
             "dispatch", "dispatch_noalloc", "expert_ffn", "int4_linear", "int4_linear_partials",
             "int4_linear_stall_selftest", "int4_linear_int16", "quantize_rows_int16",
             "last_cuda_error", "launch_count",
             "lib", "linear_bf16", "quantize_int4", "quantize_int8",
             "quantize_rows", "set_tc_pair", "shared_expert",
-            "rmsnorm", "route", "router_prepare", "status_string", "wait_selftest", "capi")
+            "rmsnorm", "route", "route_grouped", "route_logits",
+            "router_prepare", "status_string", "wait_selftest", "capi")
 
 
 def __getattr__(name):

@@ -9,6 +9,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 from typing import Dict, Optional
@@ -45,6 +46,19 @@ class MoeWeights(ctypes.Structure):
         "router_w", "router_bias", "gate_packed", "gate_scale", "up_packed", "up_scale",
         "down_packed", "down_scale", "lat_down", "lat_norm", "lat_up", "shared_gate", "shared_up",
         "shared_down", "router_w_terms")]
+
+
+class MoeRouteConfig(ctypes.Structure):
+    _fields_ = [("E", c_int32), ("k", c_int32), ("score", c_int32), ("groups", c_int32),
+                ("topk_groups", c_int32), ("group_score", c_int32), ("renorm", c_int32),
+                ("scale", c_float)]
+
+
+class MoeBlockNormArgs(ctypes.Structure):
+    _fields_ = ([(n, c_void_p) for n in ("y", "x", "post_gain", "gate", "pre_gain", "x_out", "h")]
+                + [(n, c_int64) for n in ("y_ld", "x_ld", "gate_ld", "x_out_ld", "h_ld")]
+                + [(n, c_int32) for n in ("T", "N", "x_f32", "gate_mode", "gate_sigmoid")]
+                + [("scale", c_float), ("eps", c_float)])
 
 
 # name -> (restype, argtypes); mirrors include/moe.h
@@ -122,6 +136,13 @@ SIGNATURES = {
                                              c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                              c_void_p, c_void_p, c_int, c_void_p, c_void_p,
                                              c_size_t, c_void_p]),
+    "moe_route_logits": (c_int, [POINTER(MoeRouteConfig), c_void_p, c_int, c_int64, c_void_p, c_int,
+                                 c_void_p, c_void_p, c_void_p]),
+    "moe_route_grouped_workspace_size": (c_size_t, [POINTER(MoeRouteConfig), c_int, c_int]),
+    "moe_route_grouped": (c_int, [POINTER(MoeRouteConfig), c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
+                                  c_void_p]),
+    "moe_block_norm": (c_int, [POINTER(MoeBlockNormArgs), c_void_p]),
 }
 
 
@@ -173,6 +194,12 @@ def _stream():
     return c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream of ``dev`` as an integer (a call of a few
+    microseconds notices the stream object that ``_stream`` makes)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
@@ -212,6 +239,30 @@ def _placed(**tensors: Optional[torch.Tensor]) -> torch.device:
     return dev
 
 
+def _rows(name: str, t: Optional[torch.Tensor], shape, dtype) -> torch.Tensor:
+    """Check a matrix of rows that may lie apart: as ``_arg``, but the row
+    stride can be any that keeps the rows from overlapping."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        want = tuple("*" if w is None else int(w) for w in shape)
+        raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name}: its rows must be dense and must not overlap")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a matrix that passed ``_rows``."""
+    rows, cols = t.shape
+    return max(t.stride(0), cols) if rows > 1 else cols
+
+
 EXPERT_NAMES = ("gate_packed", "gate_scale", "up_packed", "up_scale", "down_packed", "down_scale")
 
 
@@ -235,6 +286,68 @@ def route(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor, k: int, r
     ws = _ws(lib.moe_route_workspace_size(T, H, E), dev)
     _check("moe_route", lib.moe_route(_p(x), _p(w_router), _p(bias), T, H, E, k, int(renorm),
                                       _p(idx), _p(w), _p(ws), ws.numel(), _stream()))
+    return idx, w
+
+
+SCORES = {"sigmoid": 0, "softmax": 1}
+GROUP_SCORES = {"top2": 0, "max": 1}
+
+
+@functools.lru_cache(maxsize=256)
+def _route_config(E: int, k: int, score: str, groups: int, topk_groups: Optional[int],
+                  group_score: str, renorm: bool, scale: float):
+    if score not in SCORES:
+        raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
+    if group_score not in GROUP_SCORES:
+        raise ValueError(f"group_score: expected one of {sorted(GROUP_SCORES)}, got {group_score!r}")
+    return ctypes.pointer(MoeRouteConfig(E, k, SCORES[score], groups,
+                                         groups if topk_groups is None else topk_groups,
+                                         GROUP_SCORES[group_score], int(renorm), scale))
+
+
+def route_logits(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
+                 score: str = "sigmoid", groups: int = 1, topk_groups: Optional[int] = None,
+                 group_score: str = "top2", renorm: bool = True, scale: float = 1.0):
+    """topk_idx int32 [T, k], topk_w fp32 [T, k] from fp32 or bf16 logits
+    [T, E] (rows may lie apart): sigmoid or softmax scores, a ranking bias fp32
+    [E], the topk_groups best of ``groups`` groups by the sum of their two
+    best scores ("top2") or their best ("max"), renormalised and scaled
+    weights.  Logits of -inf or NaN take an expert out (moe_route_logits)."""
+    bf16 = logits.dtype == torch.bfloat16
+    T, E = _rows("logits", logits, (None, None), torch.bfloat16 if bf16 else torch.float32).shape
+    if bias is not None:
+        _arg("bias", bias, (E,), torch.float32)
+    cfg = _route_config(E, k, score, groups, topk_groups, group_score, renorm, scale)
+    dev = _placed(logits=logits, bias=bias)
+    idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
+    w = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)
+    _check("moe_route_logits", lib.moe_route_logits(
+        cfg, logits.data_ptr(), bf16, _ld(logits), None if bias is None else bias.data_ptr(), T,
+        idx.data_ptr(), w.data_ptr(), _raw_stream(dev)))
+    return idx, w
+
+
+def route_grouped(x: torch.Tensor, w_router: torch.Tensor, k: int,
+                  bias: Optional[torch.Tensor] = None, score: str = "sigmoid", groups: int = 1,
+                  topk_groups: Optional[int] = None, group_score: str = "top2",
+                  renorm: bool = True, scale: float = 1.0,
+                  w_terms: Optional[torch.Tensor] = None):
+    """``route_logits`` on the router's logits of bf16 x [T, H] against fp32
+    w_router [E, H] (w_terms: from ``router_prepare``)."""
+    T, H = _arg("x", x, (None, None), torch.bfloat16).shape
+    E = _arg("w_router", w_router, (None, H), torch.float32).shape[0]
+    if bias is not None:
+        _arg("bias", bias, (E,), torch.float32)
+    if w_terms is not None:
+        _arg("w_terms", w_terms, (3, E, H), torch.bfloat16)
+    cfg = _route_config(E, k, score, groups, topk_groups, group_score, renorm, scale)
+    dev = _placed(x=x, w_router=w_router, bias=bias, w_terms=w_terms)
+    idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
+    w = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)
+    ws = _ws(lib.moe_route_grouped_workspace_size(cfg, T, H), dev)
+    _check("moe_route_grouped", lib.moe_route_grouped(
+        cfg, _p(x), _p(w_router), _p(w_terms), _p(bias), T, H, _p(idx), _p(w), _p(ws), ws.numel(),
+        _stream()))
     return idx, w
 
 
@@ -508,6 +621,63 @@ def rmsnorm(x: torch.Tensor, gain: torch.Tensor, eps: float) -> torch.Tensor:
     y = torch.empty_like(x)
     _check("moe_rmsnorm", lib.moe_rmsnorm(_p(x), _p(gain), M, N, float(eps), _p(y), _stream()))
     return y
+
+
+def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None,
+               post_gain: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+               gate_sigmoid: bool = False, scale: float = 1.0,
+               pre_gain: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               x_out: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None):
+    """(x', h): the residual stream x' = x + scale * gate * norm(y) * post_gain
+    and the next block's input h = norm(x') * pre_gain (None without pre_gain),
+    in one pass (moe_block_norm).  y bf16 [T, N]; x bf16 or fp32 [T, N], or
+    None for no residual; gate bf16 [T, N], [N] or [T, 1].  x_out may be x
+    itself (in place); rows of every matrix may lie apart."""
+    bf16 = torch.bfloat16
+    T, N = _rows("y", y, (None, None), bf16).shape
+    a = MoeBlockNormArgs()
+    a.y, a.y_ld, a.T, a.N, a.scale, a.eps = y.data_ptr(), _ld(y), T, N, scale, eps
+    stream_type = bf16
+    if x is not None:
+        stream_type = torch.float32 if x.dtype == torch.float32 else bf16
+        _rows("x", x, (T, N), stream_type)
+        a.x, a.x_ld = x.data_ptr(), _ld(x)
+    elif x_out is not None and x_out.dtype == torch.float32:
+        stream_type = torch.float32
+    a.x_f32 = stream_type == torch.float32
+    if post_gain is not None:
+        a.post_gain = _arg("post_gain", post_gain, (N,), bf16).data_ptr()
+    if pre_gain is not None:
+        a.pre_gain = _arg("pre_gain", pre_gain, (N,), bf16).data_ptr()
+    elif h_out is not None:
+        raise ValueError("h_out needs pre_gain")
+    if gate is not None:
+        a.gate_sigmoid = gate_sigmoid
+        if gate.dim() == 1:
+            _arg("gate", gate, (N,), bf16)
+            a.gate_mode = 2
+        elif gate.dim() == 2 and gate.shape[1] == 1 and N != 1:
+            _rows("gate", gate, (T, 1), bf16)
+            a.gate_mode, a.gate_ld = 3, _ld(gate)
+        else:
+            _rows("gate", gate, (T, N), bf16)
+            a.gate_mode, a.gate_ld = 1, _ld(gate)
+        a.gate = gate.data_ptr()
+    if x_out is not None:
+        _rows("x_out", x_out, (T, N), stream_type)
+    if h_out is not None:
+        _rows("h_out", h_out, (T, N), bf16)
+    dev = _placed(y=y, x=x, post_gain=post_gain, gate=gate, pre_gain=pre_gain, x_out=x_out,
+                  h_out=h_out)
+    if x_out is None:
+        x_out = torch.empty(T, N, dtype=stream_type, device=dev)
+    if pre_gain is not None:
+        if h_out is None:
+            h_out = torch.empty(T, N, dtype=bf16, device=dev)
+        a.h, a.h_ld = h_out.data_ptr(), _ld(h_out)
+    a.x_out, a.x_out_ld = x_out.data_ptr(), _ld(x_out)
+    _check("moe_block_norm", lib.moe_block_norm(ctypes.byref(a), _raw_stream(dev)))
+    return x_out, h_out
 
 
 def check_error() -> int:

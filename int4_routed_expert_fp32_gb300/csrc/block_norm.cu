@@ -1,0 +1,334 @@
+// The norms on both sides of a block's output, its gate and its residual, in
+// one pass over the rows:
+//   v  = y                    or  y / sqrt(mean y^2 + eps) * post_gain
+//   v *= gate                 or  1 / (1 + exp(-gate))       (optional)
+//   r  = x + scale * v        (x optional)
+//   x_out = r rounded to x's type; h = r / sqrt(mean r^2 + eps) * pre_gain,
+// h from the unrounded r ("Kimi K2.5 donor reference" page, RMSNorm mean
+// square, normalisation and gain equations; the residual sums of its decoder
+// layer).  All arithmetic and both sums of squares in fp32, one rounding per
+// output.
+//
+// Bound: bytes.  Each element of y, x, gate, x_out and h crosses memory once:
+// a row is held in registers (8 columns to a vector, VPT vectors to a thread)
+// between the two reductions.  8 warps and more per row cost two block
+// barriers each; rows of up to 1024 columns take one warp and none.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace moe {
+
+namespace {
+
+enum Gate { kNoGate = 0, kGateFull = 1, kGateChannel = 2, kGateToken = 3 };
+
+struct NormArgs {
+  const uint16_t* y;
+  const void* x;
+  const uint16_t* post_gain;
+  const uint16_t* gate;
+  const uint16_t* pre_gain;
+  void* x_out;
+  uint16_t* h;
+  int64_t y_ld, x_ld, gate_ld, x_out_ld, h_ld;
+  int T, N, gate_mode, gate_sigmoid;
+  float scale, eps;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = static_cast<uint32_t>(f32_to_bf16_bits(f[2 * i])) |
+           (static_cast<uint32_t>(f32_to_bf16_bits(f[2 * i + 1])) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float gate_value(float g, int sigmoid) {
+  return sigmoid ? __fdividef(1.f, 1.f + __expf(-g)) : g;
+}
+
+// Sum over the threads of a row: a warp (WARPS == 1), or the whole CTA, whose
+// warps each add the partial sums in the same order.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if constexpr (WARP) return v;
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < warps ? red[lane] : 0.f);
+}
+
+__device__ __forceinline__ float inv_rms(float ss, int N, float eps) {
+  return 1.0f / sqrtf(ss / static_cast<float>(N) + eps);
+}
+
+// N % 8 == 0, every row 16-byte aligned.  WARP: a warp to a row, else a CTA.
+template <bool XF32, bool WARP, int VPT>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const NormArgs a) {
+  __shared__ float red[2][32];
+  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const int step = WARP ? 32 : blockDim.x;
+  const int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                         : blockIdx.x;
+  if (WARP && t >= a.T) return;
+  const int nv = a.N >> 3;
+  const uint4* yr = reinterpret_cast<const uint4*>(a.y + t * a.y_ld);
+  const bool full = a.gate_mode == kGateFull;
+  const uint4* gr = reinterpret_cast<const uint4*>(full ? a.gate + t * a.gate_ld : a.gate);
+  // every load of the row in flight before the first use
+  uint4 yv[VPT], xv[VPT * (XF32 ? 2 : 1)], gv[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * step;
+    if (v < nv) {
+      yv[i] = yr[v];
+      if (a.x) {
+        if constexpr (XF32) {
+          const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + t * a.x_ld);
+          xv[2 * i] = xr[2 * v];
+          xv[2 * i + 1] = xr[2 * v + 1];
+        } else {
+          xv[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + t * a.x_ld)[v];
+        }
+      }
+      if (full || a.gate_mode == kGateChannel) gv[i] = gr[v];
+    }
+  }
+  float s = a.scale;
+  if (a.gate_mode == kGateToken)
+    s *= gate_value(bf16_bits_to_f32(a.gate[t * a.gate_ld]), a.gate_sigmoid);
+  if (a.post_gain) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (tid + i * step < nv) {
+        float f[8];
+        unpack8(yv[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+      }
+    s *= inv_rms(row_sum<WARP>(ss, red[0]), a.N, a.eps);
+  }
+  float r[VPT][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * step;
+    if (v < nv) {
+      unpack8(yv[i], r[i]);
+      if (a.post_gain) {
+        float g[8];
+        unpack8(reinterpret_cast<const uint4*>(a.post_gain)[v], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] *= g[j];
+      }
+      if (full || a.gate_mode == kGateChannel) {
+        float g[8];
+        unpack8(gv[i], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] *= gate_value(g[j], a.gate_sigmoid);
+      }
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
+      if (a.x) {
+        if constexpr (XF32) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&xv[2 * i]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
+        } else {
+          unpack8(xv[i], x);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[i][j] = fmaf(r[i][j], s, x[j]);
+        ss = fmaf(r[i][j], r[i][j], ss);
+      }
+      if (a.x_out) {
+        if constexpr (XF32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.x_out) + t * a.x_out_ld) + 2 * v;
+          o[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
+          o[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+        } else {
+          reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x_out) + t * a.x_out_ld)[v] = pack8(r[i]);
+        }
+      }
+    }
+  }
+  if (!a.h) return;
+  const float inv = inv_rms(row_sum<WARP>(ss, red[1]), a.N, a.eps);
+  uint4* hr = reinterpret_cast<uint4*>(a.h + t * a.h_ld);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * step;
+    if (v < nv) {
+      float g[8];
+      unpack8(reinterpret_cast<const uint4*>(a.pre_gain)[v], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] *= r[i][j] * inv;
+      hr[v] = pack8(g);
+    }
+  }
+}
+
+// Any width, stride and alignment: a CTA to a row, column by column, the row
+// r in shared memory between its two uses.
+template <bool XF32>
+__global__ void __launch_bounds__(512) block_norm_any_kernel(const NormArgs a) {
+  extern __shared__ float rrow[];
+  __shared__ float red[2][32];
+  const int64_t t = blockIdx.x;
+  const uint16_t* yr = a.y + t * a.y_ld;
+  float s = a.scale;
+  if (a.gate_mode == kGateToken)
+    s *= gate_value(bf16_bits_to_f32(a.gate[t * a.gate_ld]), a.gate_sigmoid);
+  const uint16_t* gr = a.gate_mode == kGateFull ? a.gate + t * a.gate_ld
+                       : a.gate_mode == kGateChannel ? a.gate : nullptr;
+  if (a.post_gain) {
+    float ss = 0.f;
+    for (int c = threadIdx.x; c < a.N; c += blockDim.x) {
+      const float f = bf16_bits_to_f32(yr[c]);
+      ss = fmaf(f, f, ss);
+    }
+    s *= inv_rms(row_sum<false>(ss, red[0]), a.N, a.eps);
+  }
+  float ss = 0.f;
+  for (int c = threadIdx.x; c < a.N; c += blockDim.x) {
+    float f = bf16_bits_to_f32(yr[c]);
+    if (a.post_gain) f *= bf16_bits_to_f32(a.post_gain[c]);
+    if (gr) f *= gate_value(bf16_bits_to_f32(gr[c]), a.gate_sigmoid);
+    float x = 0.f;
+    if (a.x)
+      x = XF32 ? static_cast<const float*>(a.x)[t * a.x_ld + c]
+               : bf16_bits_to_f32(static_cast<const uint16_t*>(a.x)[t * a.x_ld + c]);
+    f = fmaf(f, s, x);
+    ss = fmaf(f, f, ss);
+    rrow[c] = f;  // read back by the same thread only
+    if (a.x_out) {
+      if (XF32)
+        static_cast<float*>(a.x_out)[t * a.x_out_ld + c] = f;
+      else
+        static_cast<uint16_t*>(a.x_out)[t * a.x_out_ld + c] = f32_to_bf16_bits(f);
+    }
+  }
+  if (!a.h) return;
+  const float inv = inv_rms(row_sum<false>(ss, red[1]), a.N, a.eps);
+  for (int c = threadIdx.x; c < a.N; c += blockDim.x)
+    a.h[t * a.h_ld + c] = f32_to_bf16_bits(rrow[c] * inv * bf16_bits_to_f32(a.pre_gain[c]));
+}
+
+constexpr int kMaxNormWidth = 32768;
+
+template <bool XF32>
+int launch_norm(const NormArgs& a, bool vec, cudaStream_t s) {
+  if (!vec) {
+    const size_t smem = static_cast<size_t>(a.N) * sizeof(float);
+    auto kern = block_norm_any_kernel<XF32>;
+    if (smem > 48 * 1024)
+      MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(smem)));
+    const int threads = std::min(512, (a.N + 31) / 32 * 32);
+    kern<<<a.T, threads, smem, s>>>(a);
+    MOE_LAUNCH_CHECK();
+    return MOE_OK;
+  }
+  const int nv = a.N / 8;
+  if (nv <= 128) {
+    const int warps = 8;
+    const unsigned grid = (a.T + warps - 1) / warps;
+    if (nv <= 32)
+      block_norm_kernel<XF32, true, 1><<<grid, 32 * warps, 0, s>>>(a);
+    else if (nv <= 64)
+      block_norm_kernel<XF32, true, 2><<<grid, 32 * warps, 0, s>>>(a);
+    else
+      block_norm_kernel<XF32, true, 4><<<grid, 32 * warps, 0, s>>>(a);
+  } else {
+    // few rows: as many threads as vectors (latency); many: fewer threads with
+    // more loads each
+    const int want = a.T <= 2 * num_sms() ? 1 : 2;
+    const int vpt = std::max(want, (nv + 1023) / 1024);
+    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+    if (vpt == 1)
+      block_norm_kernel<XF32, false, 1><<<a.T, threads, 0, s>>>(a);
+    else if (vpt == 2)
+      block_norm_kernel<XF32, false, 2><<<a.T, threads, 0, s>>>(a);
+    else
+      block_norm_kernel<XF32, false, 4><<<a.T, ((nv + 3) / 4 + 31) / 32 * 32, 0, s>>>(a);
+  }
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_block_norm(const moe_block_norm_args* p, void* stream) {
+  moe::Range range_("moe_block_norm");
+  if (!p) return MOE_ERR_INVALID;
+  if (p->T < 0 || p->N <= 0 || !(p->eps >= 0.f)) return MOE_ERR_INVALID;
+  if (!(p->scale == p->scale) || isinf(p->scale) || isinf(p->eps)) return MOE_ERR_INVALID;
+  if (p->gate_mode < MOE_GATE_NONE || p->gate_mode > MOE_GATE_TOKEN) return MOE_ERR_INVALID;
+  if (p->N > kMaxNormWidth) return MOE_ERR_UNSUPPORTED;
+  if (p->T == 0) return MOE_OK;
+  const bool gate = p->gate_mode != MOE_GATE_NONE;
+  if (!p->y || (!p->x_out && !p->h) || (gate && !p->gate)) return MOE_ERR_INVALID;
+  if ((p->h != nullptr) != (p->pre_gain != nullptr)) return MOE_ERR_INVALID;
+  const int64_t gate_cols = p->gate_mode == MOE_GATE_FULL ? p->N : 1;
+  const bool gate_rows = p->gate_mode == MOE_GATE_FULL || p->gate_mode == MOE_GATE_TOKEN;
+  if (p->y_ld < p->N || (p->x && p->x_ld < p->N) || (p->x_out && p->x_out_ld < p->N) ||
+      (p->h && p->h_ld < p->N) || (gate_rows && p->gate_ld < gate_cols))
+    return MOE_ERR_INVALID;
+  const size_t item = p->x_f32 ? 4 : 2;
+  if (!aligned(p->y, 2) || !aligned(p->x, item) || !aligned(p->x_out, item) || !aligned(p->h, 2) ||
+      !aligned(p->post_gain, 2) || !aligned(p->pre_gain, 2) || !aligned(p->gate, 2))
+    return MOE_ERR_INVALID;
+  NormArgs a{};
+  a.y = p->y;
+  a.x = p->x;
+  a.post_gain = p->post_gain;
+  a.gate = gate ? p->gate : nullptr;
+  a.pre_gain = p->pre_gain;
+  a.x_out = p->x_out;
+  a.h = p->h;
+  a.y_ld = p->y_ld;
+  a.x_ld = p->x_ld;
+  a.gate_ld = p->gate_ld;
+  a.x_out_ld = p->x_out_ld;
+  a.h_ld = p->h_ld;
+  a.T = p->T;
+  a.N = p->N;
+  a.gate_mode = p->gate_mode;
+  a.gate_sigmoid = p->gate_sigmoid;
+  a.scale = p->scale;
+  a.eps = p->eps;
+  // 16-byte vectors: widths and row strides of whole vectors, aligned bases
+  auto rows16 = [](const void* q, int64_t ld, size_t b) {
+    return !q || (aligned(q, 16) && ld * static_cast<int64_t>(b) % 16 == 0);
+  };
+  const bool vec = p->N % 8 == 0 && rows16(p->y, p->y_ld, 2) && rows16(p->x, p->x_ld, item) &&
+                   rows16(p->x_out, p->x_out_ld, item) && rows16(p->h, p->h_ld, 2) &&
+                   aligned(p->post_gain, 16) && aligned(p->pre_gain, 16) &&
+                   (p->gate_mode != MOE_GATE_FULL || rows16(p->gate, p->gate_ld, 2)) &&
+                   (p->gate_mode != MOE_GATE_CHANNEL || aligned(p->gate, 16));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return p->x_f32 ? launch_norm<true>(a, vec, s) : launch_norm<false>(a, vec, s);
+}

@@ -55,6 +55,19 @@ int launch_linear_tc_f32_splitk(const uint16_t* x, const uint16_t* w, int M, int
 int launch_linear_tc_f32_terms(const uint16_t* x, const uint16_t* w, int terms, int M, int N, int K,
                                int kc, float* y, cudaStream_t s);
 
+// The router's logits of bf16 x [T, H] against fp32 w_router [E, H], as
+// partial sums to be added in order: logit (t, e) is the sum over p < S of
+// part[t * st + p * sp + e].  Lives in ws (moe_route_workspace_size); w_terms
+// as in route_with_terms.  Validated arguments but for the alignment of the
+// tensors (MOE_ERR_INVALID).
+struct RouterLogits {
+  float* part;
+  int S;
+  size_t sp, st;
+};
+int launch_router_logits(const uint16_t* x, const float* w_router, const uint16_t* w_terms, int T,
+                         int H, int E, void* ws, RouterLogits* z, cudaStream_t s);
+
 // moe_route with, from 512 tokens, the three bf16 terms of the router weight
 // (bf16 [3, E, H] from moe_router_prepare) read from w_terms instead of
 // split into the workspace on every call (w_terms NULL: split them now).

@@ -1,0 +1,624 @@
+// Routing from logits: scores, balance bias, groups, top-k, weights.
+//
+//   s_e = 1 / (1 + exp(-z_e))              or  exp(z_e - max z) / sum exp(z - max z)
+//   c_e = s_e + b_e                        (no bias: the order of the z_e)
+//   group score = max c  or  sum of the two largest c of the group
+//   the topk_groups best groups stay; of their experts the k largest c, in
+//   descending order (equal: lower id first); w = s / (sum s + 1e-20) * scale.
+//
+// One warp to a token, its E logits in registers.  A group is a run of L
+// lanes and a lane a run of c consecutive experts of it, so that the two
+// largest of every group come from one segmented shuffle tree and the order
+// of the lanes is the order of the ids.
+//
+// Selection.  The k-th largest of the 32 lane maxima is a lower bound of the
+// k-th largest key: only experts at or above it can be selected.  They are
+// compacted (about k + 2 of 384 for logits of a router), one to a lane, and
+// ranked against one another with m shuffles, in place of k warp-wide argmax
+// rounds over all registers.
+//
+// Rounding.  A key c = s + b in fp32 carries an error of some 1e-7, and two
+// experts are as near as that in about one token of a hundred.  The decisions
+// are those of 64-bit scores all the same: candidates within the slack of the
+// bound are kept, and where two that matter lie within the error of one
+// another the keys of the (few) candidates are evaluated again in 64 bits.
+// Without a bias the order of the scores is the order of the logits and no
+// rounding decides anything.  Unavailable experts (z or c -inf or NaN) rank
+// below all others, with weight 0; experts outside the kept groups are never
+// chosen.
+//
+// Bound: at T = 8192, E = 384 the kernel reads 12.6 MB (1.9 us at the HBM
+// rate); it is bound by instructions, not by bytes.
+#include <float.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "combine.cuh"
+#include "common.cuh"
+#include "route_select.cuh"
+
+namespace moe {
+
+namespace {
+
+struct SelectArgs {
+  const void* z;
+  size_t ld, sp;
+  int S;
+  const float* bias;
+  int T, E, k, G, tg, gs;  // gs: experts to a group
+  int L, c;                // lanes to a group, experts to a lane
+  int best_only, renorm;   // group score: the best key only
+  int vec;                 // 4 logits a load
+  float scale;
+  int32_t* idx;
+  float* w;
+};
+
+constexpr int kListBytes = 10;           // shared memory per expert: a 64-bit key and a 16-bit id
+constexpr uint32_t kAbsent = 0;          // not a candidate: outside the kept groups
+constexpr uint32_t kUnavail = 0x007fffffu;  // order_key(-inf)
+
+// Unsigned order of floats (no NaN): a < b <=> order_key(a) < order_key(b),
+// but for -0 < +0, which the callers remove.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t o) {
+  return __uint_as_float(o ^ (static_cast<uint32_t>(~(static_cast<int32_t>(o) >> 31)) | 0x80000000u));
+}
+
+__device__ __forceinline__ float clean(float z) {  // NaN -> -inf, -0 -> +0
+  return z != z ? -INFINITY : z + 0.0f;
+}
+
+template <typename ZT>
+__device__ __forceinline__ float logit(const SelectArgs& a, const ZT* row, int e) {
+  if constexpr (sizeof(ZT) == 2) {
+    return clean(bf16_bits_to_f32(row[e]));
+  } else {
+    float z = row[e];
+    for (int p = 1; p < a.S; ++p) z += row[p * a.sp + e];
+    return clean(z);
+  }
+}
+
+__device__ __forceinline__ double warp_sum64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// 64-bit score of one logit; m and sum: the softmax maximum and denominator.
+template <bool SOFTMAX>
+__device__ __forceinline__ double score64(float z, float m, double sum) {
+  if (z == -INFINITY) return 0.0;
+  if constexpr (SOFTMAX) {
+    const double d = z == m ? 0.0 : static_cast<double>(z) - static_cast<double>(m);
+    return exp(d) / sum;
+  } else {
+    return 1.0 / (1.0 + exp(-static_cast<double>(z)));
+  }
+}
+
+__device__ __forceinline__ double key64(double s, float z, float b) {
+  const double c = s + static_cast<double>(b);
+  return (z == -INFINITY || c != c) ? static_cast<double>(-INFINITY) : c;
+}
+
+// exp(a - b), a <= b: of the rounded difference, corrected by what the
+// rounding lost (up to 2^-24 |a - b| of the value).  Equal infinities: 1.
+__device__ __forceinline__ float exp_diff(float a, float b) {
+  if (a == b) return 1.f;
+  const float d = a - b, back = d - a;
+  if (d == -INFINITY) return 0.f;
+  const float lost = (a - (d - back)) - (b + back);
+  const float e = expf(d);
+  return fmaf(e, lost, e);
+}
+
+// Softmax denominator in 64 bits (warp-wide, rare).
+template <typename ZT>
+__device__ __noinline__ double softmax_sum64(const SelectArgs& a, const ZT* row, float m) {
+  double sum = 0.0;
+  for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+    const float z = logit(a, row, e);
+    if (z == -INFINITY) continue;
+    sum += z == m ? 1.0 : exp(static_cast<double>(z) - static_cast<double>(m));
+  }
+  return warp_sum64(sum);
+}
+
+// The segment leader's two largest of its L lanes' (hi >= lo) pairs.
+template <typename F>
+__device__ __forceinline__ void top2_segment(F& hi, F& lo, int r, int L) {
+#pragma unroll 1
+  for (int o = 1; o < L; o <<= 1) {
+    const F oh = __shfl_down_sync(0xffffffffu, hi, o);
+    const F ol = __shfl_down_sync(0xffffffffu, lo, o);
+    if ((r & (2 * o - 1)) == 0 && r + o < L) {
+      lo = hi > oh ? (lo > oh ? lo : oh) : (hi > ol ? hi : ol);
+      hi = hi > oh ? hi : oh;
+    }
+  }
+}
+
+// Rank of group g among the G scores held by the segment leaders.
+template <typename F>
+__device__ __forceinline__ int group_rank(F score, int g, int G, int L) {
+  const F mine = __shfl_sync(0xffffffffu, score, min(g, G - 1) * L);
+  int rank = 0;
+  for (int j = 0; j < G; ++j) {
+    const F o = __shfl_sync(0xffffffffu, score, j * L);
+    rank += (o > mine || (o == mine && j < g)) ? 1 : 0;
+  }
+  return rank;
+}
+
+// Whether this lane's group is kept, from 64-bit scores (rare: the boundary
+// between kept and dropped groups lies within the fp32 error).
+template <typename ZT, bool SOFTMAX, bool BIAS>
+__device__ __noinline__ bool group_kept64(const SelectArgs& a, const ZT* row, float m, int g, int r,
+                                          int base, int cnt) {
+  const double none = -INFINITY;
+  double hi = none, lo = none;
+  double sum = 1.0;
+  if constexpr (SOFTMAX && BIAS) sum = softmax_sum64(a, row, m);
+  for (int i = 0; i < cnt; ++i) {
+    const float z = logit(a, row, base + i);
+    if (z == -INFINITY) continue;
+    double v = score64<SOFTMAX>(z, m, sum);
+    if constexpr (BIAS) v = key64(v, z, a.bias[base + i]);
+    if (v > hi) {
+      lo = hi;
+      hi = v;
+    } else if (v > lo) {
+      lo = v;
+    }
+  }
+  __syncwarp();
+  top2_segment(hi, lo, r, a.L);
+  double score = hi;
+  if (!a.best_only && hi > none && lo > none) score = hi + lo;
+  return group_rank(score, g, a.G, a.L) < a.tg;
+}
+
+}  // namespace
+
+// Error bounds of the fast keys.  Sigmoid: the relative error of ex2.approx
+// and of its rounded argument enters damped by s (1 - s) |z| <= 0.23, so s is
+// within 3e-7 of its value, and the sum with b within half a step of |c|.
+// Softmax: p |z - m| <= 0.37 likewise, but the denominator of up to 2048
+// terms adds a relative 1e-6.
+constexpr float kSlackSigmoid = 4e-7f, kSlackSoftmax = 2e-6f, kSlackStep = 1.3e-7f;
+// Relative error of a sum of two unbiased scores, |z - m| up to 90.
+constexpr float kSlackPair = 1.2e-5f;
+
+template <typename ZT, int NPL, bool SOFTMAX, bool BIAS>
+__global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint8_t rs_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
+  if (t >= a.T) return;
+  const ZT* row = static_cast<const ZT*>(a.z) + static_cast<size_t>(t) * a.ld;
+  double* ckey = reinterpret_cast<double*>(rs_smem) + static_cast<size_t>(warp) * a.E;
+  uint16_t* cid = reinterpret_cast<uint16_t*>(rs_smem + (blockDim.x >> 5) * a.E * sizeof(double)) +
+                  static_cast<size_t>(warp) * a.E;
+
+  const int g = lane / a.L, r = lane - g * a.L;
+  const int base = g * a.gs + r * a.c;
+  const int cnt = g < a.G ? max(0, min(a.c, a.gs - r * a.c)) : 0;
+
+  // NPL > 0: the lane's logits and keys are in registers; NPL == 0 (more
+  // experts to a lane than are worth unrolling): in shared memory
+  constexpr bool REG = NPL > 0;
+  float zreg[REG ? NPL : 1];
+  uint32_t oreg[REG ? NPL : 1];
+  float* zmem = reinterpret_cast<float*>(rs_smem + ((blockDim.x >> 5) * a.E * kListBytes + 3) / 4 * 4) +
+                static_cast<size_t>(warp) * 2 * a.E + base;
+  uint32_t* omem = reinterpret_cast<uint32_t*>(zmem + a.E);
+  auto Z = [&](int i) -> float& {
+    if constexpr (REG) return zreg[i]; else return zmem[i];
+  };
+  auto O = [&](int i) -> uint32_t& {
+    if constexpr (REG) return oreg[i]; else return omem[i];
+  };
+  const int NI = REG ? NPL : cnt;
+
+  // ---- logits
+  if (a.vec) {
+#pragma unroll
+    for (int i = 0; i < NI; i += 4) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (!REG || i < cnt) {
+        if constexpr (sizeof(ZT) == 2) {
+          const uint2 q = *reinterpret_cast<const uint2*>(row + base + i);
+          v = make_float4(bf16_bits_to_f32(q.x & 0xffffu), bf16_bits_to_f32(q.x >> 16),
+                          bf16_bits_to_f32(q.y & 0xffffu), bf16_bits_to_f32(q.y >> 16));
+        } else {
+          v = *reinterpret_cast<const float4*>(row + base + i);
+          for (int p = 1; p < a.S; ++p) {
+            const float4 q = *reinterpret_cast<const float4*>(row + p * a.sp + base + i);
+            v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+          }
+        }
+      }
+      Z(i) = clean(v.x); Z(i + 1) = clean(v.y); Z(i + 2) = clean(v.z); Z(i + 3) = clean(v.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) Z(i) = i < cnt ? logit(a, row, base + i) : -INFINITY;
+  }
+
+  // ---- softmax maximum and denominator
+  float m = 0.f, sum = 1.f;
+  if constexpr (SOFTMAX) {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) m = fmaxf(m, Z(i));
+    m = warp_max(m);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      sum += Z(i) == -INFINITY ? 0.f : (Z(i) == m ? 1.f : __expf(Z(i) - m));
+    sum = warp_sum(sum);
+    if (sum == 0.f) sum = 1.f;  // no expert available: every score is 0
+  }
+  auto fast_score = [&](float v) {
+    if constexpr (SOFTMAX)
+      return v == -INFINITY ? 0.f : (v == m ? 1.f : __expf(v - m)) * __fdividef(1.f, sum);
+    else
+      return __fdividef(1.f, 1.f + __expf(-v));
+  };
+
+  // ---- keys
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    if (i >= cnt) {
+      O(i) = kAbsent;
+      continue;
+    }
+    float c = Z(i);
+    if constexpr (BIAS) {
+      c = fast_score(Z(i)) + a.bias[base + i];
+      c = Z(i) == -INFINITY ? -INFINITY : clean(c);
+    }
+    O(i) = order_key(c);
+  }
+
+  // ---- groups
+  if (a.tg < a.G) {
+    uint32_t uh = kAbsent, ul = kAbsent;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      ul = max(ul, min(uh, O(i)));
+      uh = max(uh, O(i));
+    }
+    float hi = uh == kAbsent ? -INFINITY : key_value(uh);
+    float lo = ul == kAbsent ? -INFINITY : key_value(ul);
+    top2_segment(hi, lo, r, a.L);
+    float score = hi, slack = 0.f;
+    if (!a.best_only && hi > -INFINITY) {
+      if constexpr (BIAS) {
+        if (lo > -INFINITY) score = hi + lo;
+      } else {  // the order of the logits gave the two; their scores are summed
+        score = fast_score(hi) + (lo > -INFINITY ? fast_score(lo) : 0.f);
+        slack = 2.f * kSlackPair * score;
+      }
+    }
+    if constexpr (BIAS)
+      slack = 4.f * (SOFTMAX ? kSlackSoftmax : kSlackSigmoid) +
+              4.f * kSlackStep * (fabsf(hi) + (lo > -INFINITY ? fabsf(lo) : 0.f));
+    bool kept = group_rank(score, g, a.G, a.L) < a.tg;
+    // the lowest kept and the highest dropped score
+    const uint32_t os = order_key(score);
+    const bool lead = g < a.G && r == 0;
+    const uint32_t low = __reduce_min_sync(0xffffffffu, lead && kept ? os : 0xffffffffu);
+    const uint32_t high = __reduce_max_sync(0xffffffffu, lead && !kept ? os : 0u);
+    const float sl = key_value(__reduce_max_sync(0xffffffffu, order_key(lead && slack < INFINITY
+                                                                           ? slack : 0.f)));
+    // NaN (inf - inf) compares false: equal infinities are ties of their own
+    if (sl > 0.f && key_value(low) - key_value(high) <= sl)
+      kept = group_kept64<ZT, SOFTMAX, BIAS>(a, row, m, g, r, base, cnt);
+    if (!kept) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) O(i) = kAbsent;
+    }
+  }
+
+  // ---- candidates: at or above the k-th largest lane maximum
+  uint32_t mx = kAbsent;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) mx = max(mx, O(i));
+  uint32_t srt = mx;  // bitonic, descending over the lanes
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, srt, d);
+      const bool keep_max = ((lane & size) == 0) == ((lane & d) == 0);
+      srt = keep_max ? max(srt, other) : min(srt, other);
+    }
+  }
+  uint32_t thr = max(__shfl_sync(0xffffffffu, srt, a.k - 1), kUnavail);
+  constexpr float near = 2.f * (SOFTMAX ? kSlackSoftmax : kSlackSigmoid);
+  if constexpr (BIAS) {
+    const float tv = key_value(thr);
+    if (tv > -INFINITY && tv < INFINITY)
+      thr = order_key(clean(tv - (near + 2.f * kSlackStep * fabsf(tv))));
+  }
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) mine += O(i) >= thr ? 1 : 0;
+  int pos = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, pos, d);
+    if (lane >= d) pos += v;
+  }
+  const int n = __shfl_sync(0xffffffffu, pos, 31);
+  pos -= mine;
+  uint32_t* ckey32 = reinterpret_cast<uint32_t*>(ckey);
+  const bool fit = n <= 32;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    if (O(i) >= thr) {
+      if (fit) ckey32[pos] = O(i);
+      cid[pos] = static_cast<uint16_t>(base + i);
+      ++pos;
+    }
+  }
+  __syncwarp();
+
+  int my_id = -1, rank = 32;
+  if (fit) {
+    // one candidate to a lane, in id order; ranked against the others
+    uint32_t key = 0;
+    if (lane < n) {
+      key = ckey32[lane];
+      my_id = cid[lane];
+    }
+    const float kv = key_value(key);
+    bool close = false;
+    rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t other = __shfl_sync(0xffffffffu, key, j);
+      rank += (other > key || (other == key && j < lane)) ? 1 : 0;
+      if constexpr (BIAS) {
+        const float ov = key_value(other);
+        close |= j != lane && fabsf(ov - kv) <= near + kSlackStep * (fabsf(kv) + fabsf(ov));
+      }
+    }
+    if (lane >= n) rank = 32;
+    if constexpr (BIAS) {
+      if (__any_sync(0xffffffffu, close && rank < a.k)) {
+        double s64 = 1.0;
+        if constexpr (SOFTMAX) s64 = softmax_sum64(a, row, m);
+        double k64 = -INFINITY;
+        if (lane < n) {
+          const float zz = logit(a, row, my_id);
+          k64 = key64(score64<SOFTMAX>(zz, m, s64), zz, a.bias[my_id]);
+        }
+        __syncwarp();
+        rank = 0;
+        for (int j = 0; j < n; ++j) {
+          const double other = __shfl_sync(0xffffffffu, k64, j);
+          rank += (other > k64 || (other == k64 && j < lane)) ? 1 : 0;
+        }
+        if (lane >= n) rank = 32;
+      }
+    }
+  } else {
+    // many candidates (few lanes hold the kept groups, k near 32, or equal
+    // keys): 64-bit keys in shared memory, k rounds of the largest
+    double s64 = 1.0;
+    if constexpr (SOFTMAX && BIAS) s64 = softmax_sum64(a, row, m);
+    for (int j = lane; j < n; j += 32) {
+      const int e = cid[j];
+      const float zz = logit(a, row, e);
+      double v = zz;
+      if constexpr (BIAS) v = key64(score64<SOFTMAX>(zz, m, s64), zz, a.bias[e]);
+      ckey[j] = v;
+    }
+    __syncwarp();
+    for (int q = 0; q < a.k; ++q) {
+      double best = -INFINITY;
+      int at = n;  // position = id order
+      for (int j = lane; j < n; j += 32) {
+        if (cid[j] & 0x8000u) continue;
+        if (at == n || ckey[j] > best) {
+          best = ckey[j];
+          at = j;
+        }
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        const double ob = __shfl_xor_sync(0xffffffffu, best, d);
+        const int oa = __shfl_xor_sync(0xffffffffu, at, d);
+        if (oa < n && (at == n || ob > best || (ob == best && oa < at))) {
+          best = ob;
+          at = oa;
+        }
+      }
+      if (lane == q) {
+        my_id = cid[at];
+        rank = q;
+      }
+      __syncwarp();
+      if (lane == q) cid[at] |= 0x8000u;
+      __syncwarp();
+    }
+  }
+
+  // ---- weights of the selected, unbiased
+  float zz = -INFINITY;
+  if (rank < a.k) {
+    zz = logit(a, row, my_id);
+    if constexpr (BIAS) {  // a bias of -inf or NaN takes an expert out as well
+      const float b = a.bias[my_id];
+      if (b != b || b == -INFINITY) zz = -INFINITY;
+    }
+  }
+  // s = u exp(ref) / sum with u = exp(z' - ref), z' = z (softmax) or min(z, 0)
+  // over 1 + exp(-|z|) (sigmoid).  Renormalised, ref is the largest z' selected
+  // and exp(ref) cancels but for the stabiliser, so that scores below fp32's
+  // range keep their ratios.
+  const float zp = SOFTMAX ? zz : fminf(zz, 0.f);
+  const float top = SOFTMAX ? m : 0.f;  // s = exp(z' - top) / sum
+  const float ref = a.renorm ? fmaxf(warp_max(zp), -FLT_MAX) : top;
+  float w = zz == -INFINITY ? 0.f : exp_diff(zp, ref);
+  if constexpr (SOFTMAX) {
+    if (!a.renorm) w /= sum;
+  } else {
+    w /= 1.0f + expf(-fabsf(zz));
+  }
+  if (a.renorm) {
+    const float den = warp_sum(w);
+    const float far = top - ref;  // NaN (inf - inf): 0
+    if (far > 40.f) {  // the stabiliser weighs in: 64 bits (rare)
+      const double stab = 1e-20 * sum * exp(static_cast<double>(top) - static_cast<double>(ref));
+      w = static_cast<float>(w / (den + stab));
+    } else {
+      w = __fdiv_rn(w, den + 1e-20f * (far > 0.f ? sum * expf(far) : sum));
+    }
+  }
+  if (rank < a.k) {
+    const size_t at = static_cast<size_t>(t) * a.k + rank;
+    a.idx[at] = my_id;
+    a.w[at] = w * a.scale;
+  }
+}
+
+int check_route_config(const moe_route_config* cfg) {
+  if (!cfg) return MOE_ERR_INVALID;
+  const moe_route_config& c = *cfg;
+  if (c.E <= 0 || c.k <= 0 || c.groups <= 0 || c.topk_groups <= 0) return MOE_ERR_INVALID;
+  if (c.score != MOE_SCORE_SIGMOID && c.score != MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID;
+  if (c.group_score != MOE_GROUP_TOP2 && c.group_score != MOE_GROUP_MAX) return MOE_ERR_INVALID;
+  if (c.topk_groups > c.groups) return MOE_ERR_INVALID;
+  if (!(c.scale == c.scale) || isinf(c.scale)) return MOE_ERR_INVALID;
+  if (c.E > kMaxExperts || c.groups > 32 || c.E % c.groups != 0 || c.k > kMaxTopK)
+    return MOE_ERR_UNSUPPORTED;
+  if (c.k > c.topk_groups * (c.E / c.groups)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+namespace {
+
+template <typename ZT, int NPL>
+int launch_npl(const moe_route_config& cfg, const SelectArgs& a, int warps, size_t smem,
+               cudaStream_t s) {
+  const bool soft = cfg.score == MOE_SCORE_SOFTMAX, bias = a.bias != nullptr;
+  auto kern = soft ? (bias ? route_select_kernel<ZT, NPL, true, true>
+                           : route_select_kernel<ZT, NPL, true, false>)
+                   : (bias ? route_select_kernel<ZT, NPL, false, true>
+                           : route_select_kernel<ZT, NPL, false, false>);
+  if (smem > 48 * 1024)
+    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(smem)));
+  kern<<<(a.T + warps - 1) / warps, 32 * warps, smem, s>>>(a);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+template <typename ZT>
+int launch_type(const moe_route_config& cfg, const SelectArgs& a, int warps, size_t smem,
+                cudaStream_t s) {
+  if (a.c <= 4) return launch_npl<ZT, 4>(cfg, a, warps, smem, s);
+  if (a.c <= 8) return launch_npl<ZT, 8>(cfg, a, warps, smem, s);
+  if (a.c <= 12) return launch_npl<ZT, 12>(cfg, a, warps, smem, s);
+  if (a.c <= 16) return launch_npl<ZT, 16>(cfg, a, warps, smem, s);
+  return launch_npl<ZT, 0>(cfg, a, warps, smem, s);
+}
+
+}  // namespace
+
+int launch_route_select(const moe_route_config& cfg, const void* in, bool bf16, size_t ld, int S,
+                        size_t sp, const float* bias, int T, int32_t* topk_idx, float* topk_w,
+                        cudaStream_t s) {
+  SelectArgs a{};
+  a.z = in;
+  a.ld = ld;
+  a.sp = sp;
+  a.S = S;
+  a.bias = bias;
+  a.T = T;
+  a.E = cfg.E;
+  a.k = cfg.k;
+  a.G = cfg.groups;
+  a.tg = cfg.topk_groups;
+  // all groups kept: one group of everything
+  if (a.tg == a.G) a.G = a.tg = 1;
+  a.gs = a.E / a.G;
+  a.L = 32 / a.G;
+  a.c = (a.gs + a.L - 1) / a.L;
+  const size_t item = bf16 ? 2 : 4;
+  if (a.gs % 4 == 0 && ld % 4 == 0 && sp % 4 == 0 && aligned(in, 4 * item)) {
+    a.vec = 1;
+    a.c = (a.c + 3) / 4 * 4;
+  }
+  a.best_only = cfg.group_score == MOE_GROUP_MAX;
+  a.renorm = cfg.renorm;
+  a.scale = cfg.scale;
+  a.idx = topk_idx;
+  a.w = topk_w;
+  // eight tokens to a CTA once every SM has some; few tokens are spread over
+  // the SMs; a large E leaves room for fewer candidate lists
+  const int sms = num_sms();
+  int warps = T >= 16 * sms ? 8 : (T >= 4 * sms ? 2 : 1);
+  const size_t per = static_cast<size_t>(a.E) * (kListBytes + (a.c > 16 ? 8 : 0));
+  while (warps > 1 && warps * per > 40 * 1024) warps >>= 1;
+  // a candidate list rounded up so that what follows it is 4-byte aligned
+  const size_t smem = warps * per + 4;
+  return bf16 ? launch_type<uint16_t>(cfg, a, warps, smem, s)
+              : launch_type<float>(cfg, a, warps, smem, s);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_route_logits(const moe_route_config* cfg, const void* logits, int logits_bf16,
+                                int64_t ld, const float* bias, int T, int32_t* topk_idx,
+                                float* topk_w, void* stream) {
+  moe::Range range_("moe_route_logits");
+  const int rc = check_route_config(cfg);
+  if (rc) return rc;
+  if (T < 0 || ld < cfg->E) return MOE_ERR_INVALID;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_w) return MOE_ERR_INVALID;
+  if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+      !aligned(topk_w, 4))
+    return MOE_ERR_INVALID;
+  return launch_route_select(*cfg, logits, logits_bf16 != 0, static_cast<size_t>(ld), 1, 0, bias, T,
+                             topk_idx, topk_w, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t moe_route_grouped_workspace_size(const moe_route_config* cfg, int T, int H) {
+  if (!cfg) return 0;
+  return moe_route_workspace_size(T, H, cfg->E);
+}
+
+extern "C" int moe_route_grouped(const moe_route_config* cfg, const uint16_t* x,
+                                 const float* w_router, const uint16_t* w_terms, const float* bias,
+                                 int T, int H, int32_t* topk_idx, float* topk_w, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  moe::Range range_("moe_route_grouped");
+  int rc = check_route_config(cfg);
+  if (rc) return rc;
+  if (T < 0 || H <= 0) return MOE_ERR_INVALID;
+  if (H % 64 != 0) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !w_router || !topk_idx || !topk_w || !ws) return MOE_ERR_INVALID;
+  if (!aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(ws, 256))
+    return MOE_ERR_INVALID;
+  if (ws_bytes < moe_route_workspace_size(T, H, cfg->E)) return MOE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  RouterLogits z;
+  rc = launch_router_logits(x, w_router, w_terms, T, H, cfg->E, ws, &z, s);
+  if (rc) return rc;
+  return launch_route_select(*cfg, z.part, false, z.st, z.S, z.sp, bias, T, topk_idx, topk_w, s);
+}

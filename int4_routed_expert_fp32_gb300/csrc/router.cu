@@ -384,6 +384,48 @@ extern "C" size_t moe_route_workspace_size(int T, int H, int E) {
   return align_up((size_t)sp.splits * T * E * sizeof(float), 256);
 }
 
+int moe::launch_router_logits(const uint16_t* x, const float* w_router, const uint16_t* w_terms,
+                              int T, int H, int E, void* ws, RouterLogits* z, cudaStream_t s) {
+  if (w_terms && !aligned(w_terms, 16)) return MOE_ERR_INVALID;
+  if (T >= kRtTcMinTokens) {
+    // tensor cores: partial logits per K slice, the three weight terms
+    // accumulated together, [T, splits, E] fp32, summed in slice order
+    const uint16_t* Ws = w_terms;
+    z->part = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                       align_up((size_t)3 * E * H * sizeof(uint16_t), 256));
+    if (!aligned(x, 16)) return MOE_ERR_INVALID;
+    if (!Ws) {  // split the weight now (moe_router_prepare does it once ahead)
+      uint16_t* Wt = static_cast<uint16_t*>(ws);
+      const size_t n = (size_t)E * H;
+      router_split_kernel<<<std::min<size_t>((n + 255) / 256, 4096), 256, 0, s>>>(w_router, n, Wt);
+      MOE_LAUNCH_CHECK();
+      Ws = Wt;
+    }
+    z->S = router_tc_splits(H);
+    z->sp = E;
+    z->st = (size_t)z->S * E;
+    return launch_linear_tc_f32_terms(x, Ws, 3, T, E, H, kRtTcKSlice, z->part, s);
+  }
+  z->part = static_cast<float*>(ws);
+  z->sp = (size_t)T * E;
+  z->st = E;
+  if (T <= kRwMaxTokens) {
+    if (!aligned(x, 16) || !aligned(w_router, 16)) return MOE_ERR_INVALID;
+    z->S = (H + kRwK - 1) / kRwK;
+    MOE_TRY_CUDA(cudaFuncSetAttribute(router_logits_warp_kernel,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kRwSmem));
+    dim3 grid((E + kRwExperts - 1) / kRwExperts, z->S);
+    router_logits_warp_kernel<<<grid, 256, kRwSmem, s>>>(x, w_router, T, H, E, z->part);
+  } else {
+    const RouterSplit spl = router_split(T, H, E);
+    z->S = spl.splits;
+    dim3 grid((T + kRtTokens - 1) / kRtTokens, (E + kRtExperts - 1) / kRtExperts, spl.splits);
+    router_logits_kernel<<<grid, 256, 0, s>>>(x, w_router, T, H, E, spl.kslice, z->part);
+  }
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
 int moe::route_with_terms(const uint16_t* x, const float* w_router, const uint16_t* w_terms,
                           const float* bias, int T, int H, int E, int k, int renorm,
                           int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
@@ -393,51 +435,12 @@ int moe::route_with_terms(const uint16_t* x, const float* w_router, const uint16
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !bias || !topk_idx || !topk_w || !ws) return MOE_ERR_INVALID;
   if (ws_bytes < moe_route_workspace_size(T, H, E)) return MOE_ERR_WORKSPACE;
-  if (w_terms && !aligned(w_terms, 16)) return MOE_ERR_INVALID;
-  float* part;
-  int S;
-  size_t sp_stride, st_stride;
-  if (T >= kRtTcMinTokens) {
-    // tensor cores: partial logits per K slice, the three weight terms
-    // accumulated together, [T, splits, E] fp32, summed in slice order
-    const uint16_t* Ws = w_terms;
-    part = reinterpret_cast<float*>(static_cast<char*>(ws) +
-                                    align_up((size_t)3 * E * H * sizeof(uint16_t), 256));
-    if (!aligned(x, 16)) return MOE_ERR_INVALID;
-    if (!Ws) {  // split the weight now (moe_router_prepare does it once ahead)
-      uint16_t* Wt = static_cast<uint16_t*>(ws);
-      const size_t n = (size_t)E * H;
-      router_split_kernel<<<std::min<size_t>((n + 255) / 256, 4096), 256, 0, s>>>(w_router, n, Wt);
-      MOE_LAUNCH_CHECK();
-      Ws = Wt;
-    }
-    const int splits = router_tc_splits(H);
-    const int rc = launch_linear_tc_f32_terms(x, Ws, 3, T, E, H, kRtTcKSlice, part, s);
-    if (rc) return rc;
-    S = splits;
-    sp_stride = E;
-    st_stride = (size_t)S * E;
-  } else if (T <= kRwMaxTokens) {
-    if (!aligned(x, 16) || !aligned(w_router, 16)) return MOE_ERR_INVALID;
-    part = static_cast<float*>(ws);
-    S = (H + kRwK - 1) / kRwK;
-    MOE_TRY_CUDA(cudaFuncSetAttribute(router_logits_warp_kernel,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kRwSmem));
-    dim3 grid((E + kRwExperts - 1) / kRwExperts, S);
-    router_logits_warp_kernel<<<grid, 256, kRwSmem, s>>>(x, w_router, T, H, E, part);
-    MOE_LAUNCH_CHECK();
-    sp_stride = (size_t)T * E;
-    st_stride = E;
-  } else {
-    const RouterSplit spl = router_split(T, H, E);
-    part = static_cast<float*>(ws);
-    dim3 grid((T + kRtTokens - 1) / kRtTokens, (E + kRtExperts - 1) / kRtExperts, spl.splits);
-    router_logits_kernel<<<grid, 256, 0, s>>>(x, w_router, T, H, E, spl.kslice, part);
-    MOE_LAUNCH_CHECK();
-    S = spl.splits;
-    sp_stride = (size_t)T * E;
-    st_stride = E;
-  }
+  RouterLogits z;
+  const int rc = launch_router_logits(x, w_router, w_terms, T, H, E, ws, &z, s);
+  if (rc) return rc;
+  const float* part = z.part;
+  const int S = z.S;
+  const size_t sp_stride = z.sp, st_stride = z.st;
   if (E <= 512 && T >= kTopkWarpMinTokens) {
     const int grid = (T + kTopkWarpTokens - 1) / kTopkWarpTokens, thr = 32 * kTopkWarpTokens;
     if (E <= 128)

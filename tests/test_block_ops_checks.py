@@ -1,0 +1,161 @@
+"""Refusals of grouped routing, the block norm and the adapter projection: by
+the Python binding on host tensors, and by the C entry points before any launch
+(no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+CUDA_ONLY = "must live on a CUDA device"
+FAKE = 0x10000  # an aligned non-null address that no refused call reads
+
+
+@pytest.fixture(scope="module")
+def capi():
+    from int4_routed_expert_fp32_gb300.build import build
+    build()
+    from int4_routed_expert_fp32_gb300 import capi as c
+    return c
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def f32(*shape):
+    return torch.zeros(*shape, dtype=torch.float32)
+
+
+def raises(match, fn, *args, **kwargs):
+    with pytest.raises(ValueError, match=match):
+        fn(*args, **kwargs)
+
+
+def test_route_logits_binding(capi):
+    r = capi.route_logits
+    raises(CUDA_ONLY, r, f32(4, 16), 2)
+    raises(CUDA_ONLY, r, bf16(4, 16), 2, f32(16), groups=4, topk_groups=2)
+    raises(CUDA_ONLY, r, f32(4, 24)[:, 3:19], 2)          # rows that lie apart
+    raises("logits: expected torch.float32", r, f32(4, 16).double(), 2)
+    raises("logits: expected shape", r, f32(16), 2)
+    raises("logits: its rows", r, f32(16, 4).t(), 2)
+    raises("logits: its rows", r, f32(1, 16).expand(4, 16), 2)
+    raises("bias: expected shape", r, f32(4, 16), 2, f32(15))
+    raises("bias: expected torch.float32", r, f32(4, 16), 2, bf16(16))
+    raises("score: expected one of", r, f32(4, 16), 2, score="tanh")
+    raises("group_score: expected one of", r, f32(4, 16), 2, group_score="mean")
+
+
+def test_route_grouped_binding(capi):
+    r = capi.route_grouped
+    raises(CUDA_ONLY, r, bf16(4, 64), f32(16, 64), 2)
+    raises("w_router: expected shape", r, bf16(4, 64), f32(16, 32), 2)
+    raises("x: expected torch.bfloat16", r, f32(4, 64), f32(16, 64), 2)
+    raises("w_terms: expected shape", r, bf16(4, 64), f32(16, 64), 2, w_terms=bf16(2, 16, 64))
+
+
+def route_config(capi, **kw):
+    c = dict(E=16, k=2, score=0, groups=4, topk_groups=2, group_score=0, renorm=1, scale=1.0)
+    c.update(kw)
+    return capi.MoeRouteConfig(*c.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(E=0), "INVALID"), (dict(k=0), "INVALID"), (dict(score=2), "INVALID"),
+    (dict(score=-1), "INVALID"), (dict(groups=0), "INVALID"), (dict(topk_groups=0), "INVALID"),
+    (dict(topk_groups=5), "INVALID"), (dict(group_score=2), "INVALID"),
+    (dict(scale=float("nan")), "INVALID"), (dict(scale=float("inf")), "INVALID"),
+    (dict(groups=3), "UNSUPPORTED"), (dict(E=4096), "UNSUPPORTED"),
+    (dict(E=66, groups=33), "UNSUPPORTED"), (dict(k=9), "UNSUPPORTED"),
+    (dict(E=64, k=33, topk_groups=4), "UNSUPPORTED"),
+])
+def test_route_config_refusals(capi, kw, code):
+    L, want = capi.lib, getattr(capi, "MOE_ERR_" + code)
+    cfg = ctypes.byref(route_config(capi, **kw))
+    n = capi.launch_count()
+    assert L.moe_route_logits(cfg, FAKE, 0, 4096, None, 4, FAKE, FAKE, None) == want
+    assert L.moe_route_grouped(cfg, FAKE, FAKE, None, None, 4, 64, FAKE, FAKE, FAKE, 1 << 30,
+                               None) == want
+    assert capi.launch_count() == n
+
+
+def test_route_argument_refusals(capi):
+    L, cfg = capi.lib, ctypes.byref(route_config(capi))
+    bad, uns = capi.MOE_ERR_INVALID, capi.MOE_ERR_UNSUPPORTED
+    n = capi.launch_count()
+    assert L.moe_route_logits(None, FAKE, 0, 16, None, 4, FAKE, FAKE, None) == bad
+    assert L.moe_route_logits(cfg, None, 0, 16, None, 4, FAKE, FAKE, None) == bad
+    assert L.moe_route_logits(cfg, FAKE, 0, 15, None, 4, FAKE, FAKE, None) == bad
+    assert L.moe_route_logits(cfg, FAKE, 0, 16, None, -1, FAKE, FAKE, None) == bad
+    assert L.moe_route_logits(cfg, FAKE + 2, 0, 16, None, 4, FAKE, FAKE, None) == bad
+    assert L.moe_route_logits(cfg, FAKE, 0, 16, FAKE + 1, 4, FAKE, FAKE, None) == bad
+    assert L.moe_route_logits(cfg, FAKE, 0, 16, None, 4, None, FAKE, None) == bad
+    assert L.moe_route_logits(cfg, None, 0, 16, None, 0, None, None, None) == capi.MOE_OK
+    g = L.moe_route_grouped
+    assert g(cfg, FAKE, FAKE, None, None, 4, 100, FAKE, FAKE, FAKE, 1 << 30, None) == uns
+    assert g(cfg, None, FAKE, None, None, 4, 64, FAKE, FAKE, FAKE, 1 << 30, None) == bad
+    assert g(cfg, FAKE, FAKE, None, None, 4, 64, FAKE, FAKE, FAKE + 16, 1 << 30, None) == bad
+    assert g(cfg, FAKE, FAKE, None, None, 4, 64, FAKE, FAKE, FAKE, 16, None) == \
+        capi.MOE_ERR_WORKSPACE
+    assert L.moe_route_grouped_workspace_size(cfg, 4, 64) >= 4 * 16 * 4
+    assert L.moe_route_grouped_workspace_size(None, 4, 64) == 0
+    assert capi.launch_count() == n
+
+
+def test_block_norm_binding(capi):
+    f = capi.block_norm
+    raises(CUDA_ONLY, f, bf16(4, 64), bf16(4, 64), pre_gain=bf16(64))
+    raises(CUDA_ONLY, f, bf16(4, 64), f32(4, 64), post_gain=bf16(64), gate=bf16(4, 1))
+    raises(CUDA_ONLY, f, bf16(4, 70)[:, 3:67], None, gate=bf16(64))
+    raises("y: expected torch.bfloat16", f, f32(4, 64))
+    raises("y: its rows", f, bf16(64, 4).t())
+    raises("x: expected shape", f, bf16(4, 64), bf16(4, 65))
+    raises("x: expected torch.bfloat16", f, bf16(4, 64), bf16(4, 64).half())
+    raises("post_gain: expected shape", f, bf16(4, 64), post_gain=bf16(32))
+    raises("pre_gain: expected torch.bfloat16", f, bf16(4, 64), pre_gain=f32(64))
+    raises("gate: expected shape", f, bf16(4, 64), gate=bf16(3, 64))
+    raises("gate: expected shape", f, bf16(4, 64), gate=bf16(3, 1))
+    raises("gate: expected shape", f, bf16(4, 64), gate=bf16(32))
+    raises("gate: its rows", f, bf16(4, 64), gate=bf16(1, 1).expand(4, 1))
+    raises("x_out: expected torch.float32", f, bf16(4, 64), f32(4, 64), x_out=bf16(4, 64))
+    raises("h_out needs pre_gain", f, bf16(4, 64), h_out=bf16(4, 64))
+    raises("h_out: expected shape", f, bf16(4, 64), pre_gain=bf16(64), h_out=bf16(5, 64))
+
+
+def norm_args(capi, **kw):
+    a = capi.MoeBlockNormArgs()
+    d = dict(y=FAKE, x=FAKE, x_out=FAKE, h=FAKE, pre_gain=FAKE, y_ld=64, x_ld=64, x_out_ld=64,
+             h_ld=64, T=4, N=64, scale=1.0, eps=1e-6)
+    d.update(kw)
+    for name, v in d.items():
+        setattr(a, name, v)
+    return ctypes.byref(a)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), "INVALID"), (dict(N=0), "INVALID"), (dict(eps=-1.0), "INVALID"),
+    (dict(eps=float("nan")), "INVALID"), (dict(scale=float("inf")), "INVALID"),
+    (dict(scale=float("nan")), "INVALID"), (dict(gate_mode=4), "INVALID"),
+    (dict(gate_mode=-1), "INVALID"), (dict(gate_mode=1), "INVALID"), (dict(y=None), "INVALID"),
+    (dict(x_out=None, h=None, pre_gain=None), "INVALID"), (dict(pre_gain=None), "INVALID"),
+    (dict(h=None), "INVALID"), (dict(y_ld=63), "INVALID"), (dict(x_ld=0), "INVALID"),
+    (dict(x_out_ld=63), "INVALID"), (dict(h_ld=63), "INVALID"),
+    (dict(gate=FAKE, gate_mode=1, gate_ld=63), "INVALID"),
+    (dict(gate=FAKE, gate_mode=3, gate_ld=0), "INVALID"), (dict(y=FAKE + 1), "INVALID"),
+    (dict(x=FAKE + 2, x_f32=1), "INVALID"),
+    (dict(N=32769, y_ld=40000, x_ld=40000, x_out_ld=40000, h_ld=40000), "UNSUPPORTED"),
+])
+def test_block_norm_refusals(capi, kw, code):
+    n = capi.launch_count()
+    assert capi.lib.moe_block_norm(norm_args(capi, **kw), None) == \
+        getattr(capi, "MOE_ERR_" + code)
+    assert capi.lib.moe_block_norm(None, None) == capi.MOE_ERR_INVALID
+    assert capi.lib.moe_block_norm(norm_args(capi, T=0, y=None), None) == capi.MOE_OK
+    assert capi.launch_count() == n
+
+
+def test_struct_layouts_match_header(capi):
+    from tests.test_abi import _header_struct_fields
+    assert [n for n, _ in capi.MoeRouteConfig._fields_] == _header_struct_fields("moe_route_config")
+    assert ctypes.sizeof(capi.MoeRouteConfig) == 8 * 4
+    assert ctypes.sizeof(capi.MoeBlockNormArgs) == 12 * 8 + 7 * 4 + 4   # padded to 8 bytes
