@@ -475,6 +475,25 @@ typedef struct moe_block_norm_args {
 
 int moe_block_norm(const moe_block_norm_args* args, void* stream);
 
+/* A shared projection with the low-rank adapters of many requests (a latent
+ * projection or one of the shared expert's; no page has adapters):
+ *   y[t] = bf16( x[t] w^T + scale[a] (x[t] lora_a[a]^T) lora_b[a]^T ),
+ * a = ids[t], or x[t] w^T alone where ids[t] is -1; fp32 accumulation (the
+ * low-rank vector is kept to 16 bits of significand or more) and one rounding.
+ *   x       bf16 [T, K];  w bf16 [N, K];  y bf16 [T, N] out
+ *   lora_a  bf16 [adapters, R, K];  lora_b bf16 [adapters, N, R] (adapters of
+ *           lower rank: zeros in the rest of both)
+ *   ids     int32 [T], any order and repetition; a value outside
+ *           [-1, adapters) selects no adapter and records MOE_ERR_INVALID
+ *   scale   fp32 [adapters] or NULL (1)
+ * K % 32 == 0, N % 8 == 0, R % 8 == 0 and R <= 128, else MOE_ERR_UNSUPPORTED.
+ * All tensors 16-byte aligned (ids and scale 4), ws 256. */
+size_t moe_adapter_linear_workspace_size(int T, int K, int N, int R);
+int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* lora_a,
+                       const uint16_t* lora_b, const int32_t* ids, const float* scale, int T, int K,
+                       int N, int R, int adapters, uint16_t* y, void* ws, size_t ws_bytes,
+                       void* stream);
+
 /* --------------------------------------------------------- shared expert -- */
 
 /* Workspace bytes of moe_shared_expert. */

@@ -143,6 +143,10 @@ SIGNATURES = {
                                   c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
                                   c_void_p]),
     "moe_block_norm": (c_int, [POINTER(MoeBlockNormArgs), c_void_p]),
+    "moe_adapter_linear_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "moe_adapter_linear": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                   c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_size_t,
+                                   c_void_p]),
 }
 
 
@@ -678,6 +682,34 @@ def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None,
     a.x_out, a.x_out_ld = x_out.data_ptr(), _ld(x_out)
     _check("moe_block_norm", lib.moe_block_norm(ctypes.byref(a), _raw_stream(dev)))
     return x_out, h_out
+
+
+def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                   ids: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y bf16 [T, N] = x w^T + scale[a] (x lora_a[a]^T) lora_b[a]^T with a =
+    ids[t] for each row t (-1: no adapter): x bf16 [T, K], w bf16 [N, K],
+    lora_a bf16 [adapters, R, K], lora_b bf16 [adapters, N, R], ids int32 [T],
+    scale fp32 [adapters] or None (moe_adapter_linear)."""
+    bf16 = torch.bfloat16
+    T, K = _arg("x", x, (None, None), bf16).shape
+    N = _arg("w", w, (None, K), bf16).shape[0]
+    n, R, _ = _arg("lora_a", lora_a, (None, None, K), bf16).shape
+    _arg("lora_b", lora_b, (n, N, R), bf16)
+    _arg("ids", ids, (T,), torch.int32)
+    if scale is not None:
+        _arg("scale", scale, (n,), torch.float32)
+    if out is not None:
+        _arg("out", out, (T, N), bf16)
+    dev = _placed(x=x, w=w, lora_a=lora_a, lora_b=lora_b, ids=ids, scale=scale, out=out)
+    if out is None:
+        out = torch.empty(T, N, dtype=bf16, device=dev)
+    ws = _ws(lib.moe_adapter_linear_workspace_size(T, K, N, R), dev)
+    _check("moe_adapter_linear", lib.moe_adapter_linear(
+        x.data_ptr(), w.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), ids.data_ptr(),
+        None if scale is None else scale.data_ptr(), T, K, N, R, n, out.data_ptr(), ws.data_ptr(),
+        ws.numel(), _raw_stream(dev)))
+    return out
 
 
 def check_error() -> int:

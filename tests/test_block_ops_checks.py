@@ -159,3 +159,50 @@ def test_struct_layouts_match_header(capi):
     assert [n for n, _ in capi.MoeRouteConfig._fields_] == _header_struct_fields("moe_route_config")
     assert ctypes.sizeof(capi.MoeRouteConfig) == 8 * 4
     assert ctypes.sizeof(capi.MoeBlockNormArgs) == 12 * 8 + 7 * 4 + 4   # padded to 8 bytes
+
+
+def test_adapter_linear_binding(capi):
+    f = capi.adapter_linear
+    T, K, N, R, n = 4, 64, 24, 8, 3
+
+    def call(x=bf16(T, K), w=bf16(N, K), a=bf16(n, R, K), b=bf16(n, N, R),
+             ids=torch.zeros(T, dtype=torch.int32), **kw):
+        return f(x, w, a, b, ids, **kw)
+
+    raises(CUDA_ONLY, call)
+    raises(CUDA_ONLY, call, scale=f32(n), out=bf16(T, N))
+    raises("x: expected torch.bfloat16", call, x=f32(T, K))
+    raises("w: expected shape", call, w=bf16(N, K + 32))
+    raises("lora_a: expected shape", call, a=bf16(n, R, K + 32))
+    raises("lora_b: expected shape", call, b=bf16(n, R, N))
+    raises("lora_b: expected shape", call, b=bf16(n + 1, N, R))
+    raises("ids: expected torch.int32", call, ids=torch.zeros(T, dtype=torch.int64))
+    raises("ids: expected shape", call, ids=torch.zeros(T + 1, dtype=torch.int32))
+    raises("scale: expected shape", call, scale=f32(n + 1))
+    raises("out: expected shape", call, out=bf16(T, N + 8))
+    raises("x must be contiguous", call, x=bf16(K, T).t())
+
+
+def test_adapter_linear_refusals(capi):
+    L, n = capi.lib, capi.launch_count()
+    bad, uns = capi.MOE_ERR_INVALID, capi.MOE_ERR_UNSUPPORTED
+
+    def call(T=4, K=64, N=24, R=8, adapters=3, ws_bytes=1 << 30, **ptr):
+        p = dict(x=FAKE, w=FAKE, a=FAKE, b=FAKE, ids=FAKE, scale=None, y=FAKE, ws=FAKE)
+        p.update(ptr)
+        return L.moe_adapter_linear(p["x"], p["w"], p["a"], p["b"], p["ids"], p["scale"], T, K, N,
+                                    R, adapters, p["y"], p["ws"], ws_bytes, None)
+
+    for kw in (dict(T=-1), dict(K=0), dict(N=0), dict(R=0), dict(adapters=0), dict(x=None),
+               dict(w=None), dict(a=None), dict(b=None), dict(ids=None), dict(y=None),
+               dict(ws=None), dict(x=FAKE + 8), dict(w=FAKE + 2), dict(a=FAKE + 8),
+               dict(b=FAKE + 8), dict(ids=FAKE + 2), dict(scale=FAKE + 2), dict(y=FAKE + 8),
+               dict(ws=FAKE + 16)):
+        assert call(**kw) == bad, kw
+    for kw in (dict(K=48), dict(N=20), dict(R=12), dict(R=136)):
+        assert call(**kw) == uns, kw
+    assert call(ws_bytes=0) == capi.MOE_ERR_WORKSPACE
+    assert call(T=0, x=None) == capi.MOE_OK
+    assert L.moe_adapter_linear_workspace_size(4, 64, 24, 8) >= 4 * 8 * 4
+    assert L.moe_adapter_linear_workspace_size(0, 64, 24, 8) > 0
+    assert capi.launch_count() == n
