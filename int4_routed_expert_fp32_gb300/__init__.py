@@ -20,7 +20,9 @@ _BINDING = ("MoeConfig", "MoeError", "MoeLayer", "MoeWeights", "adapter_linear",
 def __getattr__(name):
     if name in _BINDING:
         capi = importlib.import_module(".capi", __name__)
-        return capi if name == "capi" else getattr(capi, name)
+        # kept: later uses of the name find it without coming here
+        globals()[name] = value = capi if name == "capi" else getattr(capi, name)
+        return value
     raise AttributeError(name)
 
 

@@ -198,10 +198,9 @@ def _stream():
     return c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _raw_stream(dev: torch.device) -> int:
-    """The current stream of ``dev`` as an integer (a call of a few
-    microseconds notices the stream object that ``_stream`` makes)."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+# The current stream of a device index, as an integer: a call of a few
+# microseconds notices the stream object that ``_stream`` makes.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -216,6 +215,8 @@ def _arg(name: str, t: Optional[torch.Tensor], shape=None, dtype=None) -> torch.
     metadata is checked here; ``_placed`` checks where the tensors live."""
     if t is None:
         raise ValueError(f"{name} is required")
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t  # the common case, without the generator below
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if shape is not None and (t.dim() != len(shape) or any(
@@ -246,6 +247,8 @@ def _placed(**tensors: Optional[torch.Tensor]) -> torch.device:
 def _rows(name: str, t: Optional[torch.Tensor], shape, dtype) -> torch.Tensor:
     """Check a matrix of rows that may lie apart: as ``_arg``, but the row
     stride can be any that keeps the rows from overlapping."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
@@ -265,6 +268,26 @@ def _ld(t: torch.Tensor) -> int:
     """Row stride of a matrix that passed ``_rows``."""
     rows, cols = t.shape
     return max(t.stride(0), cols) if rows > 1 else cols
+
+
+_DEVICES: Dict[int, torch.device] = {}
+
+
+def _device_of(tensors, names) -> torch.device:
+    """``_placed`` of positional tensors: the device they all share, which is
+    the current one; the error of ``_placed`` where that does not hold."""
+    index = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            index = -1
+    if index < 0:
+        dev = _placed(**dict(zip(names, tensors)))
+        assert dev is not None
+        return dev
+    dev = _DEVICES.get(index)
+    if dev is None:
+        dev = _DEVICES[index] = torch.device("cuda", index)
+    return dev
 
 
 EXPERT_NAMES = ("gate_packed", "gate_scale", "up_packed", "up_scale", "down_packed", "down_scale")
@@ -317,17 +340,25 @@ def route_logits(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
     [E], the topk_groups best of ``groups`` groups by the sum of their two
     best scores ("top2") or their best ("max"), renormalised and scaled
     weights.  Logits of -inf or NaN take an expert out (moe_route_logits)."""
-    bf16 = logits.dtype == torch.bfloat16
-    T, E = _rows("logits", logits, (None, None), torch.bfloat16 if bf16 else torch.float32).shape
+    bf16 = logits.dtype is torch.bfloat16
+    if logits.dim() == 2 and logits.is_contiguous() and (bf16 or logits.dtype is torch.float32):
+        T, E = logits.shape
+        ld = E
+    else:
+        T, E = _rows("logits", logits, (None, None),
+                     torch.bfloat16 if bf16 else torch.float32).shape
+        ld = _ld(logits)
     if bias is not None:
         _arg("bias", bias, (E,), torch.float32)
     cfg = _route_config(E, k, score, groups, topk_groups, group_score, renorm, scale)
-    dev = _placed(logits=logits, bias=bias)
-    idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
-    w = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)
-    _check("moe_route_logits", lib.moe_route_logits(
-        cfg, logits.data_ptr(), bf16, _ld(logits), None if bias is None else bias.data_ptr(), T,
-        idx.data_ptr(), w.data_ptr(), _raw_stream(dev)))
+    dev = _device_of((logits, bias), ("logits", "bias"))
+    idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    rc = lib.moe_route_logits(cfg, logits.data_ptr(), bf16, ld,
+                              None if bias is None else bias.data_ptr(), T, idx.data_ptr(),
+                              w.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check("moe_route_logits", rc)
     return idx, w
 
 
@@ -638,25 +669,23 @@ def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None,
     None for no residual; gate bf16 [T, N], [N] or [T, 1].  x_out may be x
     itself (in place); rows of every matrix may lie apart."""
     bf16 = torch.bfloat16
-    T, N = _rows("y", y, (None, None), bf16).shape
+    T, N = _rows("y", y, (None, None) if y.dim() != 2 else y.shape, bf16).shape
+    rows = (T, N)
     a = MoeBlockNormArgs()
     a.y, a.y_ld, a.T, a.N, a.scale, a.eps = y.data_ptr(), _ld(y), T, N, scale, eps
     stream_type = bf16
     if x is not None:
-        stream_type = torch.float32 if x.dtype == torch.float32 else bf16
-        _rows("x", x, (T, N), stream_type)
+        if x.dtype is torch.float32:
+            stream_type = torch.float32
+        _rows("x", x, rows, stream_type)
         a.x, a.x_ld = x.data_ptr(), _ld(x)
-    elif x_out is not None and x_out.dtype == torch.float32:
+    elif x_out is not None and x_out.dtype is torch.float32:
         stream_type = torch.float32
-    a.x_f32 = stream_type == torch.float32
+    if stream_type is torch.float32:
+        a.x_f32 = 1
     if post_gain is not None:
         a.post_gain = _arg("post_gain", post_gain, (N,), bf16).data_ptr()
-    if pre_gain is not None:
-        a.pre_gain = _arg("pre_gain", pre_gain, (N,), bf16).data_ptr()
-    elif h_out is not None:
-        raise ValueError("h_out needs pre_gain")
     if gate is not None:
-        a.gate_sigmoid = gate_sigmoid
         if gate.dim() == 1:
             _arg("gate", gate, (N,), bf16)
             a.gate_mode = 2
@@ -664,23 +693,35 @@ def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None,
             _rows("gate", gate, (T, 1), bf16)
             a.gate_mode, a.gate_ld = 3, _ld(gate)
         else:
-            _rows("gate", gate, (T, N), bf16)
+            _rows("gate", gate, rows, bf16)
             a.gate_mode, a.gate_ld = 1, _ld(gate)
-        a.gate = gate.data_ptr()
+        a.gate, a.gate_sigmoid = gate.data_ptr(), gate_sigmoid
+    if pre_gain is not None:
+        a.pre_gain = _arg("pre_gain", pre_gain, (N,), bf16).data_ptr()
+    elif h_out is not None:
+        raise ValueError("h_out needs pre_gain")
     if x_out is not None:
-        _rows("x_out", x_out, (T, N), stream_type)
+        _rows("x_out", x_out, rows, stream_type)
     if h_out is not None:
-        _rows("h_out", h_out, (T, N), bf16)
-    dev = _placed(y=y, x=x, post_gain=post_gain, gate=gate, pre_gain=pre_gain, x_out=x_out,
-                  h_out=h_out)
+        _rows("h_out", h_out, rows, bf16)
+    dev = _device_of((y, x, post_gain, gate, pre_gain, x_out, h_out),
+                     ("y", "x", "post_gain", "gate", "pre_gain", "x_out", "h_out"))
     if x_out is None:
-        x_out = torch.empty(T, N, dtype=stream_type, device=dev)
+        x_out = torch.empty(rows, dtype=stream_type, device=dev)
+        a.x_out_ld = N
+    else:
+        a.x_out_ld = _ld(x_out)
+    a.x_out = x_out.data_ptr()
     if pre_gain is not None:
         if h_out is None:
-            h_out = torch.empty(T, N, dtype=bf16, device=dev)
-        a.h, a.h_ld = h_out.data_ptr(), _ld(h_out)
-    a.x_out, a.x_out_ld = x_out.data_ptr(), _ld(x_out)
-    _check("moe_block_norm", lib.moe_block_norm(ctypes.byref(a), _raw_stream(dev)))
+            h_out = torch.empty(rows, dtype=bf16, device=dev)
+            a.h_ld = N
+        else:
+            a.h_ld = _ld(h_out)
+        a.h = h_out.data_ptr()
+    rc = lib.moe_block_norm(ctypes.byref(a), _raw_stream(dev.index))
+    if rc:
+        _check("moe_block_norm", rc)
     return x_out, h_out
 
 
@@ -692,23 +733,28 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_
     lora_a bf16 [adapters, R, K], lora_b bf16 [adapters, N, R], ids int32 [T],
     scale fp32 [adapters] or None (moe_adapter_linear)."""
     bf16 = torch.bfloat16
-    T, K = _arg("x", x, (None, None), bf16).shape
-    N = _arg("w", w, (None, K), bf16).shape[0]
-    n, R, _ = _arg("lora_a", lora_a, (None, None, K), bf16).shape
+    T, K = _arg("x", x, x.shape if x.dim() == 2 else (None, None), bf16).shape
+    N = _arg("w", w, (w.shape[0] if w.dim() == 2 else None, K), bf16).shape[0]
+    n, R = lora_a.shape[:2] if lora_a.dim() == 3 else (None, None)
+    n, R, _ = _arg("lora_a", lora_a, (n, R, K), bf16).shape
     _arg("lora_b", lora_b, (n, N, R), bf16)
     _arg("ids", ids, (T,), torch.int32)
     if scale is not None:
         _arg("scale", scale, (n,), torch.float32)
     if out is not None:
         _arg("out", out, (T, N), bf16)
-    dev = _placed(x=x, w=w, lora_a=lora_a, lora_b=lora_b, ids=ids, scale=scale, out=out)
+    dev = _device_of((x, w, lora_a, lora_b, ids, scale, out),
+                     ("x", "w", "lora_a", "lora_b", "ids", "scale", "out"))
     if out is None:
-        out = torch.empty(T, N, dtype=bf16, device=dev)
-    ws = _ws(lib.moe_adapter_linear_workspace_size(T, K, N, R), dev)
-    _check("moe_adapter_linear", lib.moe_adapter_linear(
+        out = torch.empty((T, N), dtype=bf16, device=dev)
+    need = lib.moe_adapter_linear_workspace_size(T, K, N, R)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = lib.moe_adapter_linear(
         x.data_ptr(), w.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), ids.data_ptr(),
         None if scale is None else scale.data_ptr(), T, K, N, R, n, out.data_ptr(), ws.data_ptr(),
-        ws.numel(), _raw_stream(dev)))
+        need, _raw_stream(dev.index))
+    if rc:
+        _check("moe_adapter_linear", rc)
     return out
 
 

@@ -78,6 +78,8 @@ SHAPES = [  # T, K, N, R, adapters
     (129, 256, 128, 8, 200), (200, 992, 328, 48, 12), (256, 512, 256, 16, 16),
     (257, 512, 264, 32, 6), (600, 736, 520, 16, 5), (1000, 256, 1032, 64, 3),
     (1500, 320, 768, 72, 4), (2049, 128, 512, 16, 40), (300, 7168, 256, 16, 4),
+    # many output tiles to a CTA pair, with one to a few K steps each
+    (4100, 64, 5000, 16, 30), (4100, 32, 4104, 48, 3), (3000, 512, 4600, 128, 9),
 ]
 
 
@@ -191,3 +193,30 @@ def test_adapter_offsets_pass_32_bits(moe):
         want[t] += x[t].double() @ a[n - 1].double().T @ b[n - 1].double().T
     rms = want.square().mean(dim=1, keepdim=True).sqrt()
     assert torch.all((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-3 * rms)
+
+
+@pytest.mark.parametrize("R", [16, 40, 128])
+@pytest.mark.parametrize("T", [40, 300, 1500])
+def test_an_adapter_that_is_not_finite_reaches_its_own_tokens_only(moe, T, R):
+    """Infinities and NaN in lora_b (some columns) and lora_a of one adapter:
+    tokens of the others keep their bits, its own have the formula's values."""
+    K, N, n = 256, 520, 5
+    x, w, a, b, ids, scale = inputs(T, K, N, R, n, "mixed", 17)
+    clean = moe.adapter_linear(x, w, a, b, ids, scale)
+    assert moe.check_error() == 0
+    b[2, 7, R - 1] = float("nan")
+    b[2, 300, 0] = float("inf")
+    b[2, 519, 3] = -float("inf")
+    got = moe.adapter_linear(x, w, a, b, ids, scale)
+    assert moe.check_error() == 0
+    own = ids == 2
+    assert torch.equal(got[~own], clean[~own])
+    cols = torch.tensor([c not in (7, 300, 519) for c in range(N)], device=DEV)
+    assert torch.equal(got[own][:, cols], clean[own][:, cols])
+    want = ref(x, w, a, b, ids, scale)[own][:, [7, 300, 519]]
+    bad = got[own][:, [7, 300, 519]].double()
+    assert torch.isnan(bad[:, 0]).all()
+    assert torch.equal(bad[:, 1:], want[:, 1:])      # +inf or -inf, by p's sign
+    a[2] = float("nan")
+    got = moe.adapter_linear(x, w, a, b, ids, scale)
+    assert torch.equal(got[~own], clean[~own]) and torch.isnan(got[own]).all()
