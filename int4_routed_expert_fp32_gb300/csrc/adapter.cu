@@ -12,6 +12,11 @@
 // dependent: it streams W while the shrink still runs and waits for p only
 // when it needs it.
 //
+// A few tokens of low rank take one launch: there the shrink is a small part of
+// the projection kernel's own K ranges, done by warps that are idle meanwhile.
+// Each kernel lets the next call's first kernel start early, and waits for its
+// predecessor before it reads anything.
+//
 //  - adapter_split_kernel, few tokens: bound by reading W.  128 rows of W are
 //    the MMA's M side and up to 256 tokens its N side; the K range is split
 //    over the CTAs of a cluster, which add their accumulators through
@@ -39,6 +44,11 @@ constexpr int kSpThreads = 256;  // warp 0: TMA, 1: MMA + TMEM, 2-5: TMEM -> sme
 constexpr int kSpWBytes = 128 * 64 * 2;
 constexpr int kSpMaxCluster = 8;
 
+// Up to here the split kernel does the shrink itself: every output tile reads the
+// adapters' A again (T R of them in place of 128 rows of W a tile).
+constexpr int kFusedLow = 64;  // T R
+constexpr int kLowWarps = 6;   // warps 2-7
+
 struct SplitShape {
   int tb;      // tokens to a block (the MMA's N), a multiple of 16
   int stages;
@@ -49,8 +59,10 @@ struct SplitShape {
 
 }  // namespace
 
+// FUSED: the low-rank vectors too (T R <= kFusedLow, one block of tokens).
 // Cluster (x = rank, y, z): rows 128 y of W, tokens tb z; rank j takes the
 // K steps [j n / cluster, (j + 1) n / cluster) of n = ceil(K / 64).
+template <bool FUSED>
 __global__ void __launch_bounds__(kSpThreads, 1)
     adapter_split_kernel(const __grid_constant__ CUtensorMap mw,
                          const __grid_constant__ CUtensorMap mx, const AdapterArgs a, int tb,
@@ -61,6 +73,9 @@ __global__ void __launch_bounds__(kSpThreads, 1)
   __shared__ __align__(8) uint64_t full[8], empty[8], done;
   __shared__ uint32_t tmem_slot;
   __shared__ int cta_abort;
+  __shared__ float lowp[kLowWarps + 1][kFusedLow];  // FUSED: the warps' sums, and the CTA's
+  __shared__ __align__(16) float lowv[kFusedLow];   // FUSED: scaled, of all ranks
+  __shared__ int16_t low_rows[8];
   const Waiter wt{&cta_abort, status, wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stage_bytes = kSpWBytes + tb * 128;
@@ -73,6 +88,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     cta_abort = 0;
     fence_mbarrier_init();
   }
+  if (FUSED && threadIdx.x < 8) low_rows[threadIdx.x] = 0;
   if (warp == 1) {
     tmem_alloc(&tmem_slot, cols);
     tmem_relinquish();
@@ -81,6 +97,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = tmem_slot;
+  if (FUSED) grid_wait();
+  grid_launch_dependents();
   const int ranks = gridDim.x, rank = blockIdx.x;
   const int n0 = blockIdx.y * 128, t0 = blockIdx.z * tb;
   const int tokens = min(tb, a.T - t0);
@@ -119,6 +137,35 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     }
     umma_commit_warp(&done);
     mbar_drain(&done, 0, status);
+  } else {
+    // B of this rank's tokens on its way to L2 while W streams
+    const int rows = min(128, a.N - n0);
+    for (int j = warp - 2; j * ranks + rank < tokens; j += kLowWarps) {
+      const int id = checked_id(a.ids[t0 + j * ranks + rank], a.adapters);
+      if (id < 0) continue;
+      const uint16_t* b = a.b + (static_cast<size_t>(id) * a.N + n0) * a.R;
+      for (int e = lane * 64; e < rows * a.R; e += 32 * 64)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(b + e));
+    }
+    if (FUSED) {
+      // this rank's columns, dealt to the warps in whole 32-column steps
+      const int k0 = s0 * 2, k1 = min(s1 * 2, a.K / 32);
+      const int w = warp - 2;
+      const int a0 = (k0 + (k1 - k0) * w / kLowWarps) * 32;
+      const int a1 = (k0 + (k1 - k0) * (w + 1) / kLowWarps) * 32;
+      for (int t = 0; t < tokens; ++t) {
+        const int id = checked_id(a.ids[t], a.adapters);
+        if (id != a.ids[t] && a.ids[t] != -1) record_status(status, MOE_ERR_INVALID);
+        if (id < 0) continue;
+        const uint16_t* A = a.a + static_cast<size_t>(id) * a.R * a.K;
+        const uint16_t* x = a.x + static_cast<size_t>(t) * a.K;
+        float* out = &lowp[w][t * a.R];
+        if (a.R <= 16)
+          shrink_item<1, 1>(x, A, a.K, a.R, low_rows, 1, a0, a1, out);
+        else
+          shrink_item<4, 1>(x, A, a.K, a.R, low_rows, 1, a0, a1, out);
+      }
+    }
   }
   // every copy has landed and every MMA is done: the ring becomes the fp32
   // tile [tokens][128 columns of y]
@@ -136,53 +183,84 @@ __global__ void __launch_bounds__(kSpThreads, 1)
       for (int i = 0; i < 16; ++i) red[(c0 + i) * 128 + 32 * q + lane] = __uint_as_float(r[i]);
     }
   }
+  if (FUSED && threadIdx.x < tokens * a.R) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLowWarps; ++w) v += lowp[w][threadIdx.x];
+    lowp[kLowWarps][threadIdx.x] = v;
+  }
   tc_fence_before();
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, cols);
   }
-  grid_wait();  // the low-rank vectors are complete
+  if (FUSED) {
+    if (threadIdx.x < tokens * a.R) {
+      const int id = checked_id(a.ids[threadIdx.x / a.R], a.adapters);
+      float v = 0.f;
+      if (id >= 0) {
+        for (int r = 0; r < ranks; ++r)
+          v += ld_cluster_f1(mapa_shared(&lowp[kLowWarps][threadIdx.x], r));
+        if (a.scale) v *= a.scale[id];
+      }
+      lowv[threadIdx.x] = v;
+    }
+    __syncthreads();
+  } else {
+    grid_wait();  // the low-rank vectors are complete
+  }
   // token by token: rank r takes tokens r, r + ranks, ... in turn with its
   // warps; a lane sums four columns over the cluster, in the order of the ranks
   const int n = n0 + 4 * lane;
-  for (int i = warp * ranks + rank; i < tokens; i += ranks * (kSpThreads / 32)) {
-    const int t = t0 + i;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < ranks; ++r) {
-      const float4 o = ld_cluster_f4(mapa_shared(red + i * 128 + 4 * lane, r));
-      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-    }
-    const int id = checked_id(a.ids[t], a.adapters);
-    if (id >= 0) {  // the same for the whole warp
-      const float* l = a.low + static_cast<size_t>(t) * a.R;  // the same for every lane
-      if (n < a.N) {  // N % 8 == 0: all four columns or none
-        const uint16_t* b = a.b + (static_cast<size_t>(id) * a.N + n) * a.R;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < a.R; j += 8) {
-          const float4 l0 = *reinterpret_cast<const float4*>(l + j);
-          const float4 l1 = *reinterpret_cast<const float4*>(l + j + 4);
+  const bool on = n < a.N;  // N % 8 == 0: all four columns or none
+  constexpr int kStep = kSpThreads / 32;
+  int id = -1, next = -1;
+  if (warp * ranks + rank < tokens) next = checked_id(a.ids[t0 + warp * ranks + rank], a.adapters);
+  for (int i = warp * ranks + rank; i < tokens; i += ranks * kStep) {
+    id = next;
+    if (i + ranks * kStep < tokens) next = checked_id(a.ids[t0 + i + ranks * kStep], a.adapters);
+    float4 o[kSpMaxCluster];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 w = ldg16(b + static_cast<size_t>(c) * a.R + j);
-            s[c] = fmaf(__uint_as_float(w.x << 16), l0.x, s[c]);
-            s[c] = fmaf(__uint_as_float(w.x & 0xffff0000u), l0.y, s[c]);
-            s[c] = fmaf(__uint_as_float(w.y << 16), l0.z, s[c]);
-            s[c] = fmaf(__uint_as_float(w.y & 0xffff0000u), l0.w, s[c]);
-            s[c] = fmaf(__uint_as_float(w.z << 16), l1.x, s[c]);
-            s[c] = fmaf(__uint_as_float(w.z & 0xffff0000u), l1.y, s[c]);
-            s[c] = fmaf(__uint_as_float(w.w << 16), l1.z, s[c]);
-            s[c] = fmaf(__uint_as_float(w.w & 0xffff0000u), l1.w, s[c]);
-          }
+    for (int r = 0; r < kSpMaxCluster; ++r)
+      if (r < ranks) o[r] = ld_cluster_f4(mapa_shared(red + i * 128 + 4 * lane, r));
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (id >= 0 && on) {
+      const uint16_t* b = a.b + (static_cast<size_t>(id) * a.N + n) * a.R;
+      const float* l = FUSED ? lowv + i * a.R : a.low + static_cast<size_t>(t0 + i) * a.R;
+#pragma unroll 2
+      for (int j = 0; j < a.R; j += 8) {
+        const float4 l0 = *reinterpret_cast<const float4*>(l + j);
+        const float4 l1 = *reinterpret_cast<const float4*>(l + j + 4);
+        uint4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = ldg16(b + c * a.R + j);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[c] = fmaf(__uint_as_float(w[c].x << 16), l0.x, s[c]);
+          s[c] = fmaf(__uint_as_float(w[c].x & 0xffff0000u), l0.y, s[c]);
+          s[c] = fmaf(__uint_as_float(w[c].y << 16), l0.z, s[c]);
+          s[c] = fmaf(__uint_as_float(w[c].y & 0xffff0000u), l0.w, s[c]);
+          s[c] = fmaf(__uint_as_float(w[c].z << 16), l1.x, s[c]);
+          s[c] = fmaf(__uint_as_float(w[c].z & 0xffff0000u), l1.y, s[c]);
+          s[c] = fmaf(__uint_as_float(w[c].w << 16), l1.z, s[c]);
+          s[c] = fmaf(__uint_as_float(w[c].w & 0xffff0000u), l1.w, s[c]);
         }
-        v.x += s[0]; v.y += s[1]; v.z += s[2]; v.w += s[3];
       }
     }
-    if (n < a.N) {
-      uint2 o;
-      o.x = f32_to_bf16_bits(v.x) | (static_cast<uint32_t>(f32_to_bf16_bits(v.y)) << 16);
-      o.y = f32_to_bf16_bits(v.z) | (static_cast<uint32_t>(f32_to_bf16_bits(v.w)) << 16);
-      *reinterpret_cast<uint2*>(a.y + static_cast<size_t>(t) * a.N + n) = o;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kSpMaxCluster; ++r)
+      if (r < ranks) {
+        v.x += o[r].x; v.y += o[r].y; v.z += o[r].z; v.w += o[r].w;
+      }
+    if (on) {
+      uint2 q;
+      q.x = f32_to_bf16_bits(v.x + s[0]) |
+            (static_cast<uint32_t>(f32_to_bf16_bits(v.y + s[1])) << 16);
+      q.y = f32_to_bf16_bits(v.z + s[2]) |
+            (static_cast<uint32_t>(f32_to_bf16_bits(v.w + s[3])) << 16);
+      *reinterpret_cast<uint2*>(a.y + static_cast<size_t>(t0 + i) * a.N + n) = q;
     }
   }
   cluster_sync_all();  // no CTA leaves while another reads its tile
@@ -196,9 +274,8 @@ SplitShape split_shape(int T, int K, int N) {
   s.tb = ((T + blocks - 1) / blocks + 15) / 16 * 16;
   const int tiles = (N + 127) / 128 * blocks;
   const int steps = (K + 63) / 64;
-  // about one CTA to an SM; two fit with up to 64 tokens
-  int c = std::max(1, std::min(kSpMaxCluster, (num_sms() + tiles / 2) / tiles));
-  s.cluster = std::min(c, steps);
+  // at most one CTA to an SM: a second one on some would take twice the time
+  s.cluster = std::min(std::max(1, std::min(kSpMaxCluster, num_sms() / tiles)), steps);
   const int stage = kSpWBytes + s.tb * 128;
   const int budget = s.tb <= 64 ? 104 * 1024 : 204 * 1024;
   s.stages = std::min(8, budget / stage);
@@ -209,11 +286,13 @@ SplitShape split_shape(int T, int K, int N) {
   return s;
 }
 
+template <bool FUSED>
 int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
   const SplitShape sh = split_shape(a.T, a.K, a.N);
   CUtensorMap mw, mx;
   if (!adapter_map_rows(&mw, a.w, a.N, a.K, 128) || !adapter_map_rows(&mx, a.x, a.T, a.K, sh.tb)) return MOE_ERR_CUDA;
-  MOE_TRY_CUDA(cudaFuncSetAttribute(adapter_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto kern = adapter_split_kernel<FUSED>;
+  MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(sh.smem)));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(sh.cluster, (a.N + 127) / 128, (a.T + sh.tb - 1) / sh.tb);
@@ -221,16 +300,9 @@ int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
   cfg.dynamicSmemBytes = sh.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = sh.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, adapter_split_kernel, mw, mx, a, sh.tb, sh.stages, sh.cols,
-                                  status, static_cast<long long>(kDefaultWaitNs)));
+  set_adapter_attrs(&cfg, attr, sh.cluster);
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, mw, mx, a, sh.tb, sh.stages, sh.cols, status,
+                                  static_cast<long long>(kDefaultWaitNs)));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -278,7 +350,8 @@ extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const ui
   a.low = static_cast<float*>(ws);
   a.y = y;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T * R <= kFusedLow && T <= 8) return launch_split<true>(a, status, st);
   const int rc = launch_adapter_shrink(a, status, st);
   if (rc) return rc;
-  return T > kSplitTokens ? launch_adapter_tile(a, status, st) : launch_split(a, status, st);
+  return T > kSplitTokens ? launch_adapter_tile(a, status, st) : launch_split<false>(a, status, st);
 }

@@ -41,6 +41,19 @@ inline bool adapter_map_rows(CUtensorMap* m, const uint16_t* base, int rows, int
                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Launch attributes: clusters of `ranks` CTAs, programmatic dependent of the
+// kernel before it in the stream.
+inline void set_adapter_attrs(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ranks) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = ranks > 0 ? 2 : 1;
+}
+
 // Programmatic dependent launch: the dependents may start now; wait until the
 // kernel this one depends on has finished and its writes are visible.
 __device__ __forceinline__ void grid_launch_dependents() {
@@ -60,6 +73,12 @@ __device__ __forceinline__ uint4 ldg16(const uint16_t* p) {
   return __ldg(reinterpret_cast<const uint4*>(p));
 }
 
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -67,6 +86,79 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// By one warp, over the columns [k0, k1): out[p][j] = x[row p] A[j]^T for j < R
+// and the rows p < c <= 8 NT (the low bytes of rows).  The rows of A are the M side of m16n8k16 MMAs and the tokens the
+// N side.  A lane's 16-byte loads (columns 8 (lane % 4) .. + 7 of a 32-column
+// step) feed two MMAs, of which each takes the same columns of both operands,
+// in an order of its own that the sum does not see.
+template <int MT, int NT>
+__device__ __forceinline__ void shrink_item(const uint16_t* x, const uint16_t* A, int K,
+                                            int R, const int16_t* rows, int c, int k0, int k1,
+                                            float* out) {
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+  const uint16_t* ap = A + static_cast<size_t>(g) * K + 8 * q;
+  const uint16_t* xp[NT];
+  bool xon[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    xon[n] = 8 * n + g < c;
+    xp[n] = x + static_cast<size_t>(xon[n] ? rows[8 * n + g] & 0xff : 0) * K + 8 * q;
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  constexpr int kUnroll = MT * NT <= 2 ? 4 : 2;
+#pragma unroll kUnroll
+  for (int k = k0; k < k1; k += 32) {
+    uint4 av[MT][2], xv[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xv[n] = xon[n] ? ldg16(xp[n] + k) : zero;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 16 * m + 8 * h;  // R % 8 == 0: all eight rows or none
+        av[m][h] = r < R ? ldg16(ap + static_cast<size_t>(r) * K + k) : zero;
+      }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_bf16(acc[m][n], av[m][0].x, av[m][1].x, av[m][0].y, av[m][1].y, xv[n].x, xv[n].y);
+        mma_bf16(acc[m][n], av[m][0].z, av[m][1].z, av[m][0].w, av[m][1].w, xv[n].z, xv[n].w);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int p = 8 * n + 2 * q + e;
+      if (p < c) {
+        float* o = out + p * R + g;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (16 * m + 8 * h < R) o[16 * m + 8 * h] = acc[m][n][2 * h + e];
+      }
+    }
 }
 
 }  // namespace moe

@@ -39,15 +39,6 @@ struct ShrinkArgs {
   int* status;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-      " {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // The rows of a tile, sorted by adapter, and the work in them: item j is up to
 // `cut` rows row[at[j]] .. of one adapter id[j] (the low byte of row is the row).
 struct __align__(16) Items {
@@ -114,70 +105,6 @@ __device__ void make_items(Items& u, int cut, const int32_t* ids, int t0, int ro
   __syncthreads();
 }
 
-// One item over the columns [k0, k1), by one warp: out[p][j] = x[row p] A[j]^T
-// for j < R and the item's rows p < c <= 8 NT.  The rows of A are the M side of m16n8k16 MMAs and the tokens the
-// N side.  A lane's 16-byte loads (columns 8 (lane % 4) .. + 7 of a 32-column
-// step) feed two MMAs, of which each takes the same columns of both operands,
-// in an order of its own that the sum does not see.
-template <int MT, int NT>
-__device__ __forceinline__ void shrink_item(const ShrinkArgs& s, const uint16_t* A,
-                                            const int16_t* rows, int c, int t0, int k0, int k1,
-                                            float* out) {
-  const int lane = threadIdx.x & 31;
-  const int g = lane >> 2, q = lane & 3;
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-  const uint16_t* ap = A + static_cast<size_t>(g) * s.K + 8 * q;
-  const uint16_t* xp[NT];
-  bool xon[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    xon[n] = 8 * n + g < c;
-    xp[n] = s.x + static_cast<size_t>(t0 + (xon[n] ? rows[8 * n + g] & 0xff : 0)) * s.K + 8 * q;
-  }
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  constexpr int kUnroll = MT * NT <= 2 ? 4 : 2;
-#pragma unroll kUnroll
-  for (int k = k0; k < k1; k += 32) {
-    uint4 av[MT][2], xv[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xv[n] = xon[n] ? ldg16(xp[n] + k) : zero;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * m + 8 * h;  // R % 8 == 0: all eight rows or none
-        av[m][h] = r < s.R ? ldg16(ap + static_cast<size_t>(r) * s.K + k) : zero;
-      }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma_bf16(acc[m][n], av[m][0].x, av[m][1].x, av[m][0].y, av[m][1].y, xv[n].x, xv[n].y);
-        mma_bf16(acc[m][n], av[m][0].z, av[m][1].z, av[m][0].w, av[m][1].w, xv[n].z, xv[n].w);
-      }
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int p = 8 * n + 2 * q + e;
-      if (p < c) {
-        float* o = out + p * s.R + g;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (16 * m + 8 * h < s.R) o[16 * m + 8 * h] = acc[m][n][2 * h + e];
-      }
-    }
-}
-
 }  // namespace
 
 // Cluster (rank = x) of CTAs over tile y: each takes a slice of K and the
@@ -185,7 +112,8 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& s, const uint16_t*
 // of the rank.
 template <int MT>
 __global__ void __launch_bounds__(32 * kShWarps) adapter_shrink_warp_kernel(const ShrinkArgs s) {
-  grid_launch_dependents();
+  grid_wait();
+  grid_launch_dependents();  // whose own reads of x and w are then safe
   extern __shared__ __align__(16) float sh_low[];  // [warp][kItemRows][R]
   __shared__ Items u;
   const int t0 = blockIdx.y * kAdTile;
@@ -202,13 +130,14 @@ __global__ void __launch_bounds__(32 * kShWarps) adapter_shrink_warp_kernel(cons
   if (warp / sub < items) {
     const int j = z + warp / sub * groups, part = warp % sub;
     const uint16_t* A = s.a + static_cast<size_t>(u.id[j]) * s.R * s.K;
+    const uint16_t* x = s.x + static_cast<size_t>(t0) * s.K;
     const int c = u.count[j];
     const int a0 = (k0 + (k1 - k0) * part / sub) * 32, a1 = (k0 + (k1 - k0) * (part + 1) / sub) * 32;
     float* out = sh_low + warp * kItemRows * s.R;
     if (c <= 8)
-      shrink_item<MT, 1>(s, A, u.row + u.at[j], c, t0, a0, a1, out);
+      shrink_item<MT, 1>(x, A, s.K, s.R, u.row + u.at[j], c, a0, a1, out);
     else
-      shrink_item<MT, 2>(s, A, u.row + u.at[j], c, t0, a0, a1, out);
+      shrink_item<MT, 2>(x, A, s.K, s.R, u.row + u.at[j], c, a0, a1, out);
   }
   cluster_sync_all();
   // the ranks take the items' rows in turn: 4 values to a thread
@@ -257,7 +186,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
     adapter_shrink_tile_kernel(const __grid_constant__ CUtensorMap mx,
                                const __grid_constant__ CUtensorMap ma, const ShrinkArgs s,
                                long long wait_ns) {
-  grid_launch_dependents();
+  grid_wait();
+  grid_launch_dependents();  // whose own reads of x and w are then safe
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -413,15 +343,6 @@ __global__ void __launch_bounds__(kStThreads, 1)
 
 namespace {
 
-void set_cluster(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ranks) {
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = ranks;
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cfg->attrs = attr;
-  cfg->numAttrs = 1;
-}
-
 template <int MT>
 int launch_warp(const ShrinkArgs& s, cudaStream_t st) {
   const int tiles = (s.T + kAdTile - 1) / kAdTile, rows = std::min(s.T, kAdTile);
@@ -434,12 +355,12 @@ int launch_warp(const ShrinkArgs& s, cudaStream_t st) {
   if (smem > 48 * 1024)
     MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(ranks, tiles, groups);
   cfg.blockDim = dim3(32 * kShWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  set_cluster(&cfg, attr, ranks);
+  set_adapter_attrs(&cfg, attr, ranks);
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, s));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
@@ -462,12 +383,12 @@ int launch_tile(const ShrinkArgs& s, cudaStream_t st) {
   MOE_TRY_CUDA(cudaFuncSetAttribute(adapter_shrink_tile_kernel,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem));
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(ranks, tiles);
   cfg.blockDim = dim3(kStThreads);
   cfg.dynamicSmemBytes = kStSmem;
   cfg.stream = st;
-  set_cluster(&cfg, attr, ranks);
+  set_adapter_attrs(&cfg, attr, ranks);
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, adapter_shrink_tile_kernel, mx, ma, s,
                                   static_cast<long long>(kDefaultWaitNs)));
   MOE_LAUNCH_CHECK();

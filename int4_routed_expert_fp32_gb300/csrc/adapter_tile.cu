@@ -138,6 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
                         const __grid_constant__ CUtensorMap mw,
                         const __grid_constant__ CUtensorMap mb, const AdapterArgs a, int* status,
                         long long wait_ns) {
+  grid_launch_dependents();
   using S = TileShape<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -537,11 +538,8 @@ int launch_tile(const AdapterArgs& a, int* status, cudaStream_t st) {
   cfg.blockDim = dim3(kTlThreads);
   cfg.dynamicSmemBytes = TileShape<BN>::kSmem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  set_adapter_attrs(&cfg, attr, 0);  // the cluster is the kernel's own
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, mx, mw, mb, a, status,
                                   static_cast<long long>(kDefaultWaitNs)));
   MOE_LAUNCH_CHECK();

@@ -138,7 +138,7 @@ def test_same_bits_again_on_another_stream_and_from_a_graph(moe, T):
     torch.cuda.synchronize()
     n0 = moe.launch_count()
     assert torch.equal(moe.adapter_linear(*args), want)
-    assert moe.launch_count() - n0 == 2
+    assert moe.launch_count() - n0 == (1 if T * args[2].shape[1] <= 64 else 2)
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         got = [moe.adapter_linear(*args) for _ in range(3)]
