@@ -18,11 +18,12 @@
 // predecessor before it reads anything.
 //
 //  - adapter_split_kernel, few tokens: bound by reading W.  128 rows of W are
-//    the MMA's M side and up to 256 tokens its N side; the K range is split
+//    the MMA's M side and up to 128 tokens its N side; the K range is split
 //    over the CTAs of a cluster, which add their accumulators through
 //    distributed shared memory in the order of their ranks, so that 100 and
 //    more SMs stream W whatever N is.  The low-rank term is a dot product of
-//    length R per output, with each token's own rows of B.
+//    length R per output with each token's own rows of B, on mma.sync: 16 rows
+//    of B are the M side, and p as hi + lo, both bf16, two of the N columns.
 //  - adapter_tile_kernel (adapter_tile.cu), many tokens: bound by the tensor
 //    cores; the low-rank term is R more columns of K for each adapter that
 //    occurs in an output tile's rows.
@@ -40,7 +41,8 @@ namespace {
 
 constexpr int kMaxRank = 128;
 
-constexpr int kSpThreads = 256;  // warp 0: TMA, 1: MMA + TMEM, 2-5: TMEM -> smem; all: the sums
+constexpr int kSpThreads = 256;  // warp 0: TMA, 1: MMA + TMEM, 4-7: TMEM -> smem; all: the sums
+constexpr int kSpTokens = 128;   // tokens to a block, at most
 constexpr int kSpWBytes = 128 * 64 * 2;
 constexpr int kSpMaxCluster = 8;
 
@@ -49,61 +51,146 @@ constexpr int kSpMaxCluster = 8;
 constexpr int kFusedLow = 64;  // T R
 constexpr int kLowWarps = 6;   // warps 2-7
 
+constexpr int kBBytes = 64 * 1024;  // of B that a CTA fetches while W streams, at most
+
 struct SplitShape {
   int tb;      // tokens to a block (the MMA's N), a multiple of 16
   int stages;
   int cluster;  // CTAs that share an output tile, each with its K range
   uint32_t cols;  // TMEM columns
+  int wave;       // tokens whose B is in one of two buffers
+  int buf0, buf1;  // their offsets in shared memory
   size_t smem;
 };
 
+// By one warp: out[r] = p b[r]^T for the rows r < rows of b [rows][R] in shared
+// memory (0 up to 128), p given as hi[R] and lo[R].  A lane's 16-byte loads of b
+// (columns 8 (lane % 4) .. + 7 of 32) feed two MMAs, as in shrink_item.
+__device__ __forceinline__ void expand_token(const uint16_t* b, int rows, int R,
+                                             const uint16_t* hi, float* out) {
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int m0 = 0; m0 < 8; m0 += 4) {
+    float acc[4][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+    for (int k = 8 * q; k - 8 * q < R; k += 32) {
+      const bool in = k < R;
+      // N column 0: hi, 1: lo
+      const uint4 p = in && g < 2 ? *reinterpret_cast<const uint4*>(hi + g * R + k) : zero;
+      uint4 w[4][2];
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * (m0 + m) + 8 * h;
+          w[m][h] = in && r < rows ? *reinterpret_cast<const uint4*>(b + (r + g) * R + k) : zero;
+        }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        mma_bf16(acc[m], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, p.x, p.y);
+        mma_bf16(acc[m], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, p.z, p.w);
+      }
+    }
+    if (q == 0) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * (m0 + m) + 8 * h + g;
+          float v = acc[m][2 * h] + acc[m][2 * h + 1];
+          if (!(fabsf(v) < INFINITY) && r < rows) {
+            // an infinity times hi and times lo can have two signs: one product
+            v = 0.f;
+            for (int j = 0; j < R; ++j)
+              v = fmaf(bf16_bits_to_f32(hi[j]) + bf16_bits_to_f32(hi[R + j]),
+                       bf16_bits_to_f32(b[r * R + j]), v);
+          }
+          out[r] = v;
+        }
+    }
+  }
+  __syncwarp();
+}
+
 }  // namespace
 
-// FUSED: the low-rank vectors too (T R <= kFusedLow, one block of tokens).
+// FUSED: the low-rank vectors too (T R <= kFusedLow, one block of tokens).  B of
+// the tokens is fetched into shared memory while W streams: a read of global
+// memory at the end costs 1 us and more a token, measured.
 // Cluster (x = rank, y, z): rows 128 y of W, tokens tb z; rank j takes the
 // K steps [j n / cluster, (j + 1) n / cluster) of n = ceil(K / 64).
 template <bool FUSED>
-__global__ void __launch_bounds__(kSpThreads, 1)
+__global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
     adapter_split_kernel(const __grid_constant__ CUtensorMap mw,
-                         const __grid_constant__ CUtensorMap mx, const AdapterArgs a, int tb,
-                         int stages, uint32_t cols, int* status, long long wait_ns) {
+                         const __grid_constant__ CUtensorMap mx, const AdapterArgs a,
+                         const SplitShape sh, int* status, long long wait_ns) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t full[8], empty[8], done;
+  __shared__ __align__(8) uint64_t full[8], empty[8], done, bfull[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int cta_abort;
+  __shared__ int32_t ids[kSpTokens];  // of this rank's tokens
   __shared__ float lowp[kLowWarps + 1][kFusedLow];  // FUSED: the warps' sums, and the CTA's
-  __shared__ __align__(16) float lowv[kFusedLow];   // FUSED: scaled, of all ranks
+  __shared__ __align__(16) uint16_t lowv[2 * kFusedLow];  // FUSED: as lows below
+  __shared__ __align__(16) float lowout[kSpThreads / 32][128];  // a token's low-rank term
   __shared__ int16_t low_rows[8];
   const Waiter wt{&cta_abort, status, wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tb = sh.tb, stages = sh.stages;
   const int stage_bytes = kSpWBytes + tb * 128;
+  const int ranks = gridDim.x, rank = blockIdx.x;
+  const int n0 = blockIdx.y * 128, t0 = blockIdx.z * tb;
+  const int tokens = min(tb, a.T - t0);
+  const int mine = (tokens - rank + ranks - 1) / ranks;  // tokens rank, rank + ranks, ...
+  const int rows = min(128, a.N - n0);                   // N % 8 == 0
+  if (FUSED) grid_wait();
+  grid_launch_dependents();
+  for (int j = threadIdx.x; j < mine; j += kSpThreads)
+    ids[j] = checked_id(a.ids[t0 + j * ranks + rank], a.adapters);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&done, 1);
+    mbar_init(&bfull[0], 1);
+    mbar_init(&bfull[1], 1);
     cta_abort = 0;
     fence_mbarrier_init();
   }
   if (FUSED && threadIdx.x < 8) low_rows[threadIdx.x] = 0;
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, cols);
+    tmem_alloc(&tmem_slot, sh.cols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = tmem_slot;
-  if (FUSED) grid_wait();
-  grid_launch_dependents();
-  const int ranks = gridDim.x, rank = blockIdx.x;
-  const int n0 = blockIdx.y * 128, t0 = blockIdx.z * tb;
-  const int tokens = min(tb, a.T - t0);
   const int steps = (a.K + 63) / 64;
   const int s0 = steps * rank / ranks, s1 = steps * (rank + 1) / ranks;
+  // B of the tokens of wave w (one thread): bulk copies of whole [rows][R] blocks
+  const int waves = (mine + sh.wave - 1) / sh.wave;
+  const uint32_t block = static_cast<uint32_t>(rows) * a.R * 2;
+  auto fetch_wave = [&](int w) {
+    if (w >= waves) return;
+    uint64_t* bar = &bfull[w & 1];
+    uint8_t* buf = smem + (w & 1 ? sh.buf1 : sh.buf0);
+    const int j0 = w * sh.wave, j1 = min(mine, j0 + sh.wave);
+    uint32_t bytes = 0;
+    for (int j = j0; j < j1; ++j) bytes += ids[j] >= 0 ? block : 0u;
+    mbar_arrive_expect_tx(bar, bytes);
+    for (int j = j0; j < j1; ++j)
+      if (ids[j] >= 0)
+        bulk_g2s(buf + (j - j0) * 256 * a.R, a.b + (static_cast<size_t>(ids[j]) * a.N + n0) * a.R,
+                 block, bar);
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -138,15 +225,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     umma_commit_warp(&done);
     mbar_drain(&done, 0, status);
   } else {
-    // B of this rank's tokens on its way to L2 while W streams
-    const int rows = min(128, a.N - n0);
-    for (int j = warp - 2; j * ranks + rank < tokens; j += kLowWarps) {
-      const int id = checked_id(a.ids[t0 + j * ranks + rank], a.adapters);
-      if (id < 0) continue;
-      const uint16_t* b = a.b + (static_cast<size_t>(id) * a.N + n0) * a.R;
-      for (int e = lane * 64; e < rows * a.R; e += 32 * 64)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(b + e));
-    }
+    if (warp == 2 && lane == 0) fetch_wave(0);
+    __syncwarp();
     if (FUSED) {
       // this rank's columns, dealt to the warps in whole 32-column steps
       const int k0 = s0 * 2, k1 = min(s1 * 2, a.K / 32);
@@ -172,8 +252,11 @@ __global__ void __launch_bounds__(kSpThreads, 1)
   __syncthreads();
   mbar_drain(&done, 0, status);  // complete: each reader observes it for itself
   tc_fence_after();
+  if (threadIdx.x == 64) fetch_wave(1);  // its buffer may be part of the ring
   float* red = reinterpret_cast<float*>(smem);
-  if (warp >= 2 && warp < 6) {
+  // this rank's low-rank vectors as bf16 hi and lo parts: [token][2][R]
+  uint16_t* lows = FUSED ? lowv : reinterpret_cast<uint16_t*>(red + tb * 128);
+  if (warp >= 4) {
     const int q = warp & 3;
     for (int c0 = 0; c0 < tb; c0 += 16) {
       uint32_t r[16];
@@ -193,7 +276,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, cols);
+    tmem_dealloc(tbase, sh.cols);
   }
   if (FUSED) {
     if (threadIdx.x < tokens * a.R) {
@@ -204,63 +287,75 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           v += ld_cluster_f1(mapa_shared(&lowp[kLowWarps][threadIdx.x], r));
         if (a.scale) v *= a.scale[id];
       }
-      lowv[threadIdx.x] = v;
+      uint32_t hi, lo;
+      split_bf16(v, hi, lo);
+      uint16_t* l = lowv + threadIdx.x / a.R * 2 * a.R + threadIdx.x % a.R;
+      l[0] = static_cast<uint16_t>(hi);
+      l[a.R] = static_cast<uint16_t>(lo);
     }
     __syncthreads();
   } else {
-    grid_wait();  // the low-rank vectors are complete
+    // the low-rank vectors are complete: those of this rank's tokens to shared
+    // memory, in one round trip (read where they are used, each token would
+    // wait for its own)
+    grid_wait();
+    const int quads = a.R / 4;
+    for (int i = threadIdx.x; i < (tokens - rank + ranks - 1) / ranks * quads; i += kSpThreads) {
+      const int j = i / quads, e = i % quads * 4;
+      const float4 v = *reinterpret_cast<const float4*>(
+          a.low + static_cast<size_t>(t0 + j * ranks + rank) * a.R + e);
+      uint32_t h[4], l[4];
+      split_bf16(v.x, h[0], l[0]);
+      split_bf16(v.y, h[1], l[1]);
+      split_bf16(v.z, h[2], l[2]);
+      split_bf16(v.w, h[3], l[3]);
+      uint16_t* o = lows + j * 2 * a.R + e;
+      *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+      *reinterpret_cast<uint2*>(o + a.R) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+    }
+    __syncthreads();
   }
   // token by token: rank r takes tokens r, r + ranks, ... in turn with its
   // warps; a lane sums four columns over the cluster, in the order of the ranks
   const int n = n0 + 4 * lane;
   const bool on = n < a.N;  // N % 8 == 0: all four columns or none
-  constexpr int kStep = kSpThreads / 32;
-  int id = -1, next = -1;
-  if (warp * ranks + rank < tokens) next = checked_id(a.ids[t0 + warp * ranks + rank], a.adapters);
-  for (int i = warp * ranks + rank; i < tokens; i += ranks * kStep) {
-    id = next;
-    if (i + ranks * kStep < tokens) next = checked_id(a.ids[t0 + i + ranks * kStep], a.adapters);
-    float4 o[kSpMaxCluster];
+  for (int w = 0; w < waves; ++w) {
+    const int j0 = w * sh.wave, j1 = min(mine, j0 + sh.wave);
+    const uint8_t* buf = smem + (w & 1 ? sh.buf1 : sh.buf0);
+    // (not a wait that gives up with the CTA: the copies are in flight)
+    mbar_drain(&bfull[w & 1], (w >> 1) & 1u, status);
+    for (int j = j0 + warp; j < j1; j += kSpThreads / 32) {
+      const int i = j * ranks + rank, id = ids[j];
+      float4 o[kSpMaxCluster];
 #pragma unroll
-    for (int r = 0; r < kSpMaxCluster; ++r)
-      if (r < ranks) o[r] = ld_cluster_f4(mapa_shared(red + i * 128 + 4 * lane, r));
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (id >= 0 && on) {
-      const uint16_t* b = a.b + (static_cast<size_t>(id) * a.N + n) * a.R;
-      const float* l = FUSED ? lowv + i * a.R : a.low + static_cast<size_t>(t0 + i) * a.R;
-#pragma unroll 2
-      for (int j = 0; j < a.R; j += 8) {
-        const float4 l0 = *reinterpret_cast<const float4*>(l + j);
-        const float4 l1 = *reinterpret_cast<const float4*>(l + j + 4);
-        uint4 w[4];
+      for (int r = 0; r < kSpMaxCluster; ++r)
+        if (r < ranks) o[r] = ld_cluster_f4(mapa_shared(red + i * 128 + 4 * lane, r));
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (id >= 0) {
+        expand_token(reinterpret_cast<const uint16_t*>(buf + (j - j0) * 256 * a.R), rows, a.R,
+                     lows + (FUSED ? i : j) * 2 * a.R, lowout[warp]);
+        s = *reinterpret_cast<const float4*>(&lowout[warp][4 * lane]);
+        __syncwarp();  // read before the next token's are written
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = ldg16(b + c * a.R + j);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[c] = fmaf(__uint_as_float(w[c].x << 16), l0.x, s[c]);
-          s[c] = fmaf(__uint_as_float(w[c].x & 0xffff0000u), l0.y, s[c]);
-          s[c] = fmaf(__uint_as_float(w[c].y << 16), l0.z, s[c]);
-          s[c] = fmaf(__uint_as_float(w[c].y & 0xffff0000u), l0.w, s[c]);
-          s[c] = fmaf(__uint_as_float(w[c].z << 16), l1.x, s[c]);
-          s[c] = fmaf(__uint_as_float(w[c].z & 0xffff0000u), l1.y, s[c]);
-          s[c] = fmaf(__uint_as_float(w[c].w << 16), l1.z, s[c]);
-          s[c] = fmaf(__uint_as_float(w[c].w & 0xffff0000u), l1.w, s[c]);
+      for (int r = 0; r < kSpMaxCluster; ++r)
+        if (r < ranks) {
+          v.x += o[r].x; v.y += o[r].y; v.z += o[r].z; v.w += o[r].w;
         }
+      if (on) {
+        uint2 q;
+        q.x = f32_to_bf16_bits(v.x + s.x) |
+              (static_cast<uint32_t>(f32_to_bf16_bits(v.y + s.y)) << 16);
+        q.y = f32_to_bf16_bits(v.z + s.z) |
+              (static_cast<uint32_t>(f32_to_bf16_bits(v.w + s.w)) << 16);
+        *reinterpret_cast<uint2*>(a.y + static_cast<size_t>(t0 + i) * a.N + n) = q;
       }
     }
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < kSpMaxCluster; ++r)
-      if (r < ranks) {
-        v.x += o[r].x; v.y += o[r].y; v.z += o[r].z; v.w += o[r].w;
-      }
-    if (on) {
-      uint2 q;
-      q.x = f32_to_bf16_bits(v.x + s[0]) |
-            (static_cast<uint32_t>(f32_to_bf16_bits(v.y + s[1])) << 16);
-      q.y = f32_to_bf16_bits(v.z + s[2]) |
-            (static_cast<uint32_t>(f32_to_bf16_bits(v.w + s[3])) << 16);
-      *reinterpret_cast<uint2*>(a.y + static_cast<size_t>(t0 + i) * a.N + n) = q;
+    if (w + 2 < waves) {  // the wave's buffer takes the one after next
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
+      if (threadIdx.x == 64) fetch_wave(w + 2);
     }
   }
   cluster_sync_all();  // no CTA leaves while another reads its tile
@@ -268,27 +363,45 @@ __global__ void __launch_bounds__(kSpThreads, 1)
 
 namespace {
 
-SplitShape split_shape(int T, int K, int N) {
+SplitShape split_shape(int T, int K, int N, int R) {
   SplitShape s;
-  const int blocks = (T + 255) / 256;
+  const int blocks = (T + kSpTokens - 1) / kSpTokens;
   s.tb = ((T + blocks - 1) / blocks + 15) / 16 * 16;
   const int tiles = (N + 127) / 128 * blocks;
   const int steps = (K + 63) / 64;
   // at most one CTA to an SM: a second one on some would take twice the time
   s.cluster = std::min(std::max(1, std::min(kSpMaxCluster, num_sms() / tiles)), steps);
   const int stage = kSpWBytes + s.tb * 128;
-  const int budget = s.tb <= 64 ? 104 * 1024 : 204 * 1024;
+  // up to 64 tokens ~92 KiB in flight an SM; more: with room for two CTAs of the
+  // shrink, which an SM still holds when this kernel starts
+  const int budget = s.tb <= 64 ? 104 * 1024 : 132 * 1024;
   s.stages = std::min(8, budget / stage);
   s.cols = 32;
   while (s.cols < static_cast<uint32_t>(s.tb)) s.cols *= 2;
-  s.smem = std::max<size_t>(static_cast<size_t>(s.stages) * stage, static_cast<size_t>(s.tb) * 512) +
-           1024;
+  // the ring, and in its place the fp32 tile and the rank's low-rank vectors
+  const int most = (s.tb + s.cluster - 1) / s.cluster;  // tokens of a rank
+  const int tail = s.tb * 512 + most * R * 4;
+  const int ring = std::max(s.stages * stage, (tail + 1023) / 1024 * 1024);
+  // B: a buffer of its own; the second in what the tail leaves of the ring, if
+  // it takes a token, else in the first one's upper half
+  const int token = 256 * R;
+  const int bytes = std::min(kBBytes, most * token);
+  const int fit = bytes / token, rest = (ring - tail) / token;
+  s.buf0 = ring;
+  if (fit >= most || rest >= 1) {
+    s.wave = fit >= most ? most : std::min(fit, rest);
+    s.buf1 = tail;
+  } else {
+    s.wave = fit / 2;  // kBBytes takes two tokens of the largest rank
+    s.buf1 = ring + s.wave * token;
+  }
+  s.smem = static_cast<size_t>(ring) + bytes + 1024;
   return s;
 }
 
 template <bool FUSED>
 int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
-  const SplitShape sh = split_shape(a.T, a.K, a.N);
+  const SplitShape sh = split_shape(a.T, a.K, a.N, a.R);
   CUtensorMap mw, mx;
   if (!adapter_map_rows(&mw, a.w, a.N, a.K, 128) || !adapter_map_rows(&mx, a.x, a.T, a.K, sh.tb)) return MOE_ERR_CUDA;
   auto kern = adapter_split_kernel<FUSED>;
@@ -301,7 +414,7 @@ int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   set_adapter_attrs(&cfg, attr, sh.cluster);
-  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, mw, mx, a, sh.tb, sh.stages, sh.cols, status,
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, mw, mx, a, sh, status,
                                   static_cast<long long>(kDefaultWaitNs)));
   MOE_LAUNCH_CHECK();
   return MOE_OK;

@@ -21,7 +21,7 @@ struct AdapterArgs {
   uint16_t* y;  // [T, N]
 };
 
-constexpr int kSplitTokens = 256;  // up to here adapter_split_kernel, one block of tokens
+constexpr int kSplitTokens = 256;  // up to here adapter_split_kernel
 
 // low from x, a and scale (adapter_shrink.cu).  Triggers its dependents at once.
 int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st);
@@ -88,6 +88,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// hi and lo of v = hi + lo + remainder, both bf16 bits.
+__device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) {
+  hi = f32_to_bf16_bits(v);
+  const float h = bf16_bits_to_f32(hi);
+  lo = fabsf(h) < INFINITY ? f32_to_bf16_bits(v - h) : 0u;
+}
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -124,7 +131,7 @@ __device__ __forceinline__ void shrink_item(const uint16_t* x, const uint16_t* A
     xp[n] = x + static_cast<size_t>(xon[n] ? rows[8 * n + g] & 0xff : 0) * K + 8 * q;
   }
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  constexpr int kUnroll = MT * NT <= 2 ? 4 : 2;
+  constexpr int kUnroll = MT == 1 ? 8 : MT == 2 ? 4 : 2;  // ~100 registers of loads
 #pragma unroll kUnroll
   for (int k = k0; k < k1; k += 32) {
     uint4 av[MT][2], xv[NT];

@@ -68,7 +68,7 @@ __device__ void make_items(Items& u, int cut, const int32_t* ids, int t0, int ro
   if (i < kAdTile) {
     const int id = u.ids[i];
     int before = 0, lower = 0;  // sorted by id, rows of one id in their order
-    for (int j = 0; j < kAdTile; j += 4) {
+    for (int j = 0; j < rows; j += 4) {  // rows after the last have no adapter
       const int4 o = *reinterpret_cast<const int4*>(&u.ids[j]);
       const int v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
@@ -347,9 +347,10 @@ template <int MT>
 int launch_warp(const ShrinkArgs& s, cudaStream_t st) {
   const int tiles = (s.T + kAdTile - 1) / kAdTile, rows = std::min(s.T, kAdTile);
   const int ranks = std::max(1, std::min(kShMaxCluster, s.K / 64));
-  // groups of items: enough CTAs for two to an SM, at most eight items each
+  // groups of items: about one CTA to an SM, which leaves room for the kernel
+  // that streams W beside it; at most eight items each
   const int groups = std::min(rows, std::max((rows + kShWarps - 1) / kShWarps,
-                                             2 * num_sms() / (ranks * tiles)));
+                                             num_sms() / (ranks * tiles)));
   auto kern = adapter_shrink_warp_kernel<MT>;
   const int smem = kShWarps * kItemRows * s.R * 4;
   if (smem > 48 * 1024)

@@ -122,13 +122,6 @@ static_assert(sizeof(TileList) % 16 == 0, "ids is read in 16-byte vectors");
 // the epilogue look at the rows for itself.
 constexpr int kBadRing = 8;
 
-// hi and lo of v = hi + lo + remainder, both bf16 bits.
-__device__ __forceinline__ void split_bf16(float v, uint32_t& hi, uint32_t& lo) {
-  hi = f32_to_bf16_bits(v);
-  const float h = bf16_bits_to_f32(hi);
-  lo = fabsf(h) < INFINITY ? f32_to_bf16_bits(v - h) : 0u;
-}
-
 }  // namespace
 
 // WIDE: R > 32, a hi and a lo stage for every 64 columns of the rank.
