@@ -49,8 +49,10 @@ struct SelectArgs {
   const float* bias;
   int T, E, k, G, tg, gs;  // gs: experts to a group
   int L, c;                // lanes to a group, experts to a lane
+  int inv_L;               // ceil(2^16 / L): lane / L by a product, exact for lane < 32
   int best_only, renorm;   // group score: the best key only
-  int vec;                 // 4 logits a load
+  int vec, vec_bias;       // 4 logits, and biases, a load
+  int full;                // every lane has c experts, and registers for no more
   float scale;
   int32_t* idx;
   float* w;
@@ -72,7 +74,7 @@ __device__ __forceinline__ float key_value(uint32_t o) {
 }
 
 __device__ __forceinline__ float clean(float z) {  // NaN -> -inf, -0 -> +0
-  return z != z ? -INFINITY : z + 0.0f;
+  return fmaxf(z, -INFINITY) + 0.0f;
 }
 
 template <typename ZT>
@@ -158,11 +160,45 @@ __device__ __forceinline__ int group_rank(F score, int g, int G, int L) {
   return rank;
 }
 
-// Whether this lane's group is kept, from 64-bit scores (rare: the boundary
-// between kept and dropped groups lies within the fp32 error).
+// Whether this lane's group g is kept, from 64-bit scores of the n <= 32 listed
+// experts, which hold the two best of every group (rare: the boundary between
+// kept and dropped groups lies within the fp32 error).
 template <typename ZT, bool SOFTMAX, bool BIAS>
-__device__ __noinline__ bool group_kept64(const SelectArgs& a, const ZT* row, float m, int g, int r,
-                                          int base, int cnt) {
+__device__ __noinline__ bool group_kept64(const SelectArgs& a, const ZT* row, float m, int g,
+                                          const uint16_t* cid, int n) {
+  const int lane = threadIdx.x & 31;
+  const double none = -INFINITY;
+  double sum = 1.0;
+  if constexpr (SOFTMAX && BIAS) sum = softmax_sum64(a, row, m);
+  double key = none;
+  int of = -1;
+  if (lane < n) {
+    const int e = cid[lane];
+    const float z = logit(a, row, e);
+    of = e / a.gs;
+    key = score64<SOFTMAX>(z, m, sum);
+    if constexpr (BIAS) key = key64(key, z, a.bias[e]);
+    if (z == -INFINITY) key = none;
+  }
+  __syncwarp();
+  double hi = none, lo = none;
+  for (int j = 0; j < n; ++j) {
+    const double v = __shfl_sync(0xffffffffu, key, j);
+    if (__shfl_sync(0xffffffffu, of, j) != g) continue;
+    lo = v > hi ? hi : (v > lo ? v : lo);
+    hi = v > hi ? v : hi;
+  }
+  __syncwarp();
+  double score = hi;
+  if (!a.best_only && hi > none && lo > none) score = hi + lo;
+  return group_rank(score, g, a.G, a.L) < a.tg;
+}
+
+// The same from all experts (more than 32 listed: many keys within the error
+// of one another).
+template <typename ZT, bool SOFTMAX, bool BIAS>
+__device__ __noinline__ bool group_kept64_all(const SelectArgs& a, const ZT* row, float m, int g,
+                                              int r, int base, int cnt) {
   const double none = -INFINITY;
   double hi = none, lo = none;
   double sum = 1.0;
@@ -186,6 +222,101 @@ __device__ __noinline__ bool group_kept64(const SelectArgs& a, const ZT* row, fl
   return group_rank(score, g, a.G, a.L) < a.tg;
 }
 
+// Ranks of the n <= 32 candidates (one to a lane, in id order) by their 64-bit
+// keys (rare: two that matter lie within the fp32 error of one another).
+template <typename ZT, bool SOFTMAX>
+__device__ __noinline__ int rank64(const SelectArgs& a, const ZT* row, float m, int id, int n) {
+  const int lane = threadIdx.x & 31;
+  double sum = 1.0;
+  if constexpr (SOFTMAX) sum = softmax_sum64(a, row, m);
+  double key = -INFINITY;
+  if (lane < n) {
+    const float z = logit(a, row, id);
+    key = key64(score64<SOFTMAX>(z, m, sum), z, a.bias[id]);
+  }
+  __syncwarp();
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double other = __shfl_sync(0xffffffffu, key, j);
+    rank += (other > key || (other == key && j < lane)) ? 1 : 0;
+  }
+  return lane < n ? rank : 32;
+}
+
+// The k best of n > 32 candidates (few lanes hold the kept groups, k near 32, or
+// equal keys): 64-bit keys in shared memory, k rounds of the largest.  Lane q
+// returns the id of rank q (-1: q >= k).
+template <typename ZT, bool SOFTMAX, bool BIAS>
+__device__ __noinline__ int select_many(const SelectArgs& a, const ZT* row, float m, double* ckey,
+                                        uint16_t* cid, int n) {
+  const int lane = threadIdx.x & 31;
+  double sum = 1.0;
+  if constexpr (SOFTMAX && BIAS) sum = softmax_sum64(a, row, m);
+  for (int j = lane; j < n; j += 32) {
+    const int e = cid[j];
+    const float z = logit(a, row, e);
+    double v = z;
+    if constexpr (BIAS) v = key64(score64<SOFTMAX>(z, m, sum), z, a.bias[e]);
+    ckey[j] = v;
+  }
+  __syncwarp();
+  int id = -1;
+  for (int q = 0; q < a.k; ++q) {
+    double best = -INFINITY;
+    int at = n;  // position = id order
+    for (int j = lane; j < n; j += 32) {
+      if (cid[j] & 0x8000u) continue;
+      if (at == n || ckey[j] > best) {
+        best = ckey[j];
+        at = j;
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const double ob = __shfl_xor_sync(0xffffffffu, best, d);
+      const int oa = __shfl_xor_sync(0xffffffffu, at, d);
+      if (oa < n && (at == n || ob > best || (ob == best && oa < at))) {
+        best = ob;
+        at = oa;
+      }
+    }
+    if (lane == q) id = cid[at];
+    __syncwarp();
+    if (lane == q) cid[at] |= 0x8000u;
+    __syncwarp();
+  }
+  return id;
+}
+
+// The weight (before the scale) of the lane's selected logit zz (-inf: none)
+// where scores below fp32's range are among them:
+// s = u exp(ref) / sum with u = exp(z' - ref), z' = z (softmax) or min(z, 0)
+// over 1 + exp(-|z|) (sigmoid).  Renormalised, ref is the largest z' selected
+// and exp(ref) cancels but for the stabiliser, so that their ratios are kept.
+template <bool SOFTMAX>
+__device__ __noinline__ float weight_far(const SelectArgs& a, float zz, float m, float sum) {
+  const float zp = SOFTMAX ? zz : fminf(zz, 0.f);
+  const float top = SOFTMAX ? m : 0.f;  // s = exp(z' - top) / sum
+  const float ref = a.renorm ? fmaxf(warp_max(zp), -FLT_MAX) : top;
+  float w = zz == -INFINITY ? 0.f : exp_diff(zp, ref);
+  if constexpr (SOFTMAX) {
+    if (!a.renorm) w /= sum;
+  } else {
+    w /= 1.0f + expf(-fabsf(zz));
+  }
+  if (a.renorm) {
+    const float den = warp_sum(w);
+    const float far = top - ref;
+    if (far > 40.f) {  // the stabiliser weighs in
+      const double stab = 1e-20 * sum * exp(static_cast<double>(top) - static_cast<double>(ref));
+      w = static_cast<float>(w / (den + stab));
+    } else {
+      w = __fdiv_rn(w, den + 1e-20f * (far > 0.f ? sum * expf(far) : sum));
+    }
+  }
+  return w;
+}
+
 }  // namespace
 
 // Error bounds of the fast keys.  Sigmoid: the relative error of ex2.approx
@@ -198,7 +329,7 @@ constexpr float kSlackSigmoid = 4e-7f, kSlackSoftmax = 2e-6f, kSlackStep = 1.3e-
 constexpr float kSlackPair = 1.2e-5f;
 
 template <typename ZT, int NPL, bool SOFTMAX, bool BIAS>
-__global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t rs_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
@@ -208,7 +339,7 @@ __global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
   uint16_t* cid = reinterpret_cast<uint16_t*>(rs_smem + (blockDim.x >> 5) * a.E * sizeof(double)) +
                   static_cast<size_t>(warp) * a.E;
 
-  const int g = lane / a.L, r = lane - g * a.L;
+  const int g = (lane * a.inv_L) >> 16, r = lane - g * a.L;  // lane / L
   const int base = g * a.gs + r * a.c;
   const int cnt = g < a.G ? max(0, min(a.c, a.gs - r * a.c)) : 0;
 
@@ -275,18 +406,33 @@ __global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
   };
 
   // ---- keys
+  if constexpr (BIAS) {
+    auto key = [&](int i, float b) {
+      const float c = fast_score(Z(i)) + b;
+      O(i) = order_key(Z(i) == -INFINITY ? -INFINITY : clean(c));
+    };
+    if (a.vec_bias) {
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    if (i >= cnt) {
-      O(i) = kAbsent;
-      continue;
+      for (int i = 0; i < NI; i += 4) {
+        float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!REG || i < cnt) b = *reinterpret_cast<const float4*>(a.bias + base + i);
+        key(i, b.x);
+        key(i + 1, b.y);
+        key(i + 2, b.z);
+        key(i + 3, b.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) key(i, i < cnt ? a.bias[base + i] : 0.f);
     }
-    float c = Z(i);
-    if constexpr (BIAS) {
-      c = fast_score(Z(i)) + a.bias[base + i];
-      c = Z(i) == -INFINITY ? -INFINITY : clean(c);
-    }
-    O(i) = order_key(c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) O(i) = order_key(Z(i));
+  }
+  if (!a.full) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (i >= cnt) O(i) = kAbsent;
   }
 
   // ---- groups
@@ -312,17 +458,57 @@ __global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
     if constexpr (BIAS)
       slack = 4.f * (SOFTMAX ? kSlackSoftmax : kSlackSigmoid) +
               4.f * kSlackStep * (fabsf(hi) + (lo > -INFINITY ? fabsf(lo) : 0.f));
-    bool kept = group_rank(score, g, a.G, a.L) < a.tg;
-    // the lowest kept and the highest dropped score
-    const uint32_t os = order_key(score);
+    // the best topk_groups groups: the highest score left, lowest group first
     const bool lead = g < a.G && r == 0;
-    const uint32_t low = __reduce_min_sync(0xffffffffu, lead && kept ? os : 0xffffffffu);
-    const uint32_t high = __reduce_max_sync(0xffffffffu, lead && !kept ? os : 0u);
-    const float sl = key_value(__reduce_max_sync(0xffffffffu, order_key(lead && slack < INFINITY
-                                                                           ? slack : 0.f)));
+    uint32_t left = lead ? order_key(score + 0.0f) : 0u, low = 0;
+    bool kept = false;
+    for (int j = 0; j < a.tg; ++j) {
+      low = __reduce_max_sync(0xffffffffu, left);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, left == low)) - 1) {
+        kept = true;
+        left = 0;
+      }
+    }
+    const uint32_t high = __reduce_max_sync(0xffffffffu, left);  // of the dropped ones
+    kept = __shfl_sync(0xffffffffu, kept, min(g, a.G - 1) * a.L);
+    float sl = 0.f;
+    if constexpr (BIAS) {  // largest slack of any group
+      sl = key_value(__reduce_max_sync(0xffffffffu, order_key(lead && slack < INFINITY ? slack : 0.f)));
+    } else {
+      if (!a.best_only)
+        sl = key_value(__reduce_max_sync(0xffffffffu, order_key(lead ? slack : 0.f)));
+    }
     // NaN (inf - inf) compares false: equal infinities are ties of their own
-    if (sl > 0.f && key_value(low) - key_value(high) <= sl)
-      kept = group_kept64<ZT, SOFTMAX, BIAS>(a, row, m, g, r, base, cnt);
+    if (sl > 0.f && key_value(low) - key_value(high) <= sl) {
+      // the experts that can be among their group's two best
+      float bound = __shfl_sync(0xffffffffu, lo, min(g, a.G - 1) * a.L);
+      if constexpr (BIAS) {
+        if (bound > -INFINITY && bound < INFINITY)
+          bound -= 2.f * (SOFTMAX ? kSlackSoftmax : kSlackSigmoid) + 2.f * kSlackStep * fabsf(bound);
+      }
+      const uint32_t low_key = max(order_key(clean(bound)), kUnavail + 1);
+      int take = 0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) take += O(i) >= low_key ? 1 : 0;
+      int at = take;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += v;
+      }
+      const int listed = __shfl_sync(0xffffffffu, at, 31);
+      if (listed <= 32) {
+        at -= take;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (O(i) >= low_key) cid[at++] = static_cast<uint16_t>(base + i);
+        __syncwarp();
+        kept = group_kept64<ZT, SOFTMAX, BIAS>(a, row, m, g, cid, listed);
+        __syncwarp();
+      } else {
+        kept = group_kept64_all<ZT, SOFTMAX, BIAS>(a, row, m, g, r, base, cnt);
+      }
+    }
     if (!kept) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) O(i) = kAbsent;
@@ -333,17 +519,29 @@ __global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
   uint32_t mx = kAbsent;
 #pragma unroll
   for (int i = 0; i < NI; ++i) mx = max(mx, O(i));
-  uint32_t srt = mx;  // bitonic, descending over the lanes
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int d = size >> 1; d > 0; d >>= 1) {
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, srt, d);
-      const bool keep_max = ((lane & size) == 0) == ((lane & d) == 0);
-      srt = keep_max ? max(srt, other) : min(srt, other);
+  uint32_t thr = 0;
+  if (a.k <= 12) {
+    // the k-th largest distinct maximum (equal ones leave together): a bound
+    // as good, and k reductions cost less than a sort
+    uint32_t left = mx;
+    for (int j = 0; j < a.k; ++j) {
+      thr = __reduce_max_sync(0xffffffffu, left);
+      if (left == thr) left = 0;
     }
+  } else {
+    uint32_t srt = mx;  // bitonic, descending over the lanes
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+      for (int d = size >> 1; d > 0; d >>= 1) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, srt, d);
+        const bool keep_max = ((lane & size) == 0) == ((lane & d) == 0);
+        srt = keep_max ? max(srt, other) : min(srt, other);
+      }
+    }
+    thr = __shfl_sync(0xffffffffu, srt, a.k - 1);
   }
-  uint32_t thr = max(__shfl_sync(0xffffffffu, srt, a.k - 1), kUnavail);
+  thr = max(thr, kUnavail);
   constexpr float near = 2.f * (SOFTMAX ? kSlackSoftmax : kSlackSigmoid);
   if constexpr (BIAS) {
     const float tv = key_value(thr);
@@ -381,76 +579,30 @@ __global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
       key = ckey32[lane];
       my_id = cid[lane];
     }
-    const float kv = key_value(key);
-    bool close = false;
     rank = 0;
     for (int j = 0; j < n; ++j) {
       const uint32_t other = __shfl_sync(0xffffffffu, key, j);
-      rank += (other > key || (other == key && j < lane)) ? 1 : 0;
-      if constexpr (BIAS) {
-        const float ov = key_value(other);
-        close |= j != lane && fabsf(ov - kv) <= near + kSlackStep * (fabsf(kv) + fabsf(ov));
-      }
+      rank += other > key || (other == key && j < lane) ? 1 : 0;
     }
     if (lane >= n) rank = 32;
+    bool close = false;
     if constexpr (BIAS) {
-      if (__any_sync(0xffffffffu, close && rank < a.k)) {
-        double s64 = 1.0;
-        if constexpr (SOFTMAX) s64 = softmax_sum64(a, row, m);
-        double k64 = -INFINITY;
-        if (lane < n) {
-          const float zz = logit(a, row, my_id);
-          k64 = key64(score64<SOFTMAX>(zz, m, s64), zz, a.bias[my_id]);
-        }
-        __syncwarp();
-        rank = 0;
-        for (int j = 0; j < n; ++j) {
-          const double other = __shfl_sync(0xffffffffu, k64, j);
-          rank += (other > k64 || (other == k64 && j < lane)) ? 1 : 0;
-        }
-        if (lane >= n) rank = 32;
+      // the keys in descending order; neighbours within their error are not
+      // decided yet (equal infinities give NaN: their order is that of the ids)
+      if (lane < n) ckey32[rank] = key;
+      __syncwarp();
+      if (lane < n && lane > 0) {
+        const float hi = key_value(ckey32[lane - 1]), lo = key_value(ckey32[lane]);
+        close = hi - lo <= near + kSlackStep * (fabsf(hi) + fabsf(lo)) && lane <= a.k;
       }
+    }
+    if constexpr (BIAS) {
+      if (__any_sync(0xffffffffu, close))
+        rank = rank64<ZT, SOFTMAX>(a, row, m, my_id, n);
     }
   } else {
-    // many candidates (few lanes hold the kept groups, k near 32, or equal
-    // keys): 64-bit keys in shared memory, k rounds of the largest
-    double s64 = 1.0;
-    if constexpr (SOFTMAX && BIAS) s64 = softmax_sum64(a, row, m);
-    for (int j = lane; j < n; j += 32) {
-      const int e = cid[j];
-      const float zz = logit(a, row, e);
-      double v = zz;
-      if constexpr (BIAS) v = key64(score64<SOFTMAX>(zz, m, s64), zz, a.bias[e]);
-      ckey[j] = v;
-    }
-    __syncwarp();
-    for (int q = 0; q < a.k; ++q) {
-      double best = -INFINITY;
-      int at = n;  // position = id order
-      for (int j = lane; j < n; j += 32) {
-        if (cid[j] & 0x8000u) continue;
-        if (at == n || ckey[j] > best) {
-          best = ckey[j];
-          at = j;
-        }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        const double ob = __shfl_xor_sync(0xffffffffu, best, d);
-        const int oa = __shfl_xor_sync(0xffffffffu, at, d);
-        if (oa < n && (at == n || ob > best || (ob == best && oa < at))) {
-          best = ob;
-          at = oa;
-        }
-      }
-      if (lane == q) {
-        my_id = cid[at];
-        rank = q;
-      }
-      __syncwarp();
-      if (lane == q) cid[at] |= 0x8000u;
-      __syncwarp();
-    }
+    my_id = select_many<ZT, SOFTMAX, BIAS>(a, row, m, ckey, cid, n);
+    if (my_id >= 0) rank = lane;
   }
 
   // ---- weights of the selected, unbiased
@@ -462,28 +614,17 @@ __global__ void __launch_bounds__(256) route_select_kernel(const SelectArgs a) {
       if (b != b || b == -INFINITY) zz = -INFINITY;
     }
   }
-  // s = u exp(ref) / sum with u = exp(z' - ref), z' = z (softmax) or min(z, 0)
-  // over 1 + exp(-|z|) (sigmoid).  Renormalised, ref is the largest z' selected
-  // and exp(ref) cancels but for the stabiliser, so that scores below fp32's
-  // range keep their ratios.
-  const float zp = SOFTMAX ? zz : fminf(zz, 0.f);
-  const float top = SOFTMAX ? m : 0.f;  // s = exp(z' - top) / sum
-  const float ref = a.renorm ? fmaxf(warp_max(zp), -FLT_MAX) : top;
-  float w = zz == -INFINITY ? 0.f : exp_diff(zp, ref);
-  if constexpr (SOFTMAX) {
-    if (!a.renorm) w /= sum;
+  // scores far below 1 take their own way: they may be below fp32's range
+  float w;
+  if (__any_sync(0xffffffffu, zz > -INFINITY && (SOFTMAX ? m - zz > 80.f : zz < -80.f))) {
+    w = weight_far<SOFTMAX>(a, zz, m, sum);
   } else {
-    w /= 1.0f + expf(-fabsf(zz));
-  }
-  if (a.renorm) {
-    const float den = warp_sum(w);
-    const float far = top - ref;  // NaN (inf - inf): 0
-    if (far > 40.f) {  // the stabiliser weighs in: 64 bits (rare)
-      const double stab = 1e-20 * sum * exp(static_cast<double>(top) - static_cast<double>(ref));
-      w = static_cast<float>(w / (den + stab));
-    } else {
-      w = __fdiv_rn(w, den + 1e-20f * (far > 0.f ? sum * expf(far) : sum));
-    }
+    if constexpr (SOFTMAX)
+      w = zz == -INFINITY ? 0.f : exp_diff(zz, m);
+    else
+      w = zz == -INFINITY ? 0.f : __fdividef(1.0f, 1.0f + expf(-zz));
+    const float den = a.renorm ? warp_sum(w) + 1e-20f * sum : sum;
+    w = __fdividef(w, den);
   }
   if (rank < a.k) {
     const size_t at = static_cast<size_t>(t) * a.k + rank;
@@ -554,12 +695,15 @@ int launch_route_select(const moe_route_config& cfg, const void* in, bool bf16, 
   if (a.tg == a.G) a.G = a.tg = 1;
   a.gs = a.E / a.G;
   a.L = 32 / a.G;
+  a.inv_L = (65536 + a.L - 1) / a.L;
   a.c = (a.gs + a.L - 1) / a.L;
   const size_t item = bf16 ? 2 : 4;
   if (a.gs % 4 == 0 && ld % 4 == 0 && sp % 4 == 0 && aligned(in, 4 * item)) {
     a.vec = 1;
     a.c = (a.c + 3) / 4 * 4;
   }
+  a.vec_bias = a.vec && aligned(bias, 16);
+  a.full = a.G * a.L == 32 && a.L * a.c == a.gs && (a.c > 16 || a.c % 4 == 0);
   a.best_only = cfg.group_score == MOE_GROUP_MAX;
   a.renorm = cfg.renorm;
   a.scale = cfg.scale;
