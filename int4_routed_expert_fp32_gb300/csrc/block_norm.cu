@@ -77,9 +77,11 @@ __device__ __forceinline__ float inv_rms(float ss, int N, float eps) {
   return 1.0f / sqrtf(ss / static_cast<float>(N) + eps);
 }
 
-// N % 8 == 0, every row 16-byte aligned.  WARP: a warp to a row, else a CTA.
-template <bool XF32, bool WARP, int VPT>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const NormArgs a) {
+// N % 8 == 0, every row 16-byte aligned.  WARP: a warp to a row, else a CTA.  Four
+// CTAs of 256 threads to an SM: at 64 registers 8192 x 7168 with a gate runs in
+// 92 us (6.4 TB/s), at 73 (three) in 102, at 48 (five, spilling) in 116.
+template <bool XF32, bool WARP, int VPT, int THREADS = 256>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
   const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int step = WARP ? 32 : blockDim.x;
@@ -259,17 +261,25 @@ int launch_norm(const NormArgs& a, bool vec, cudaStream_t s) {
     else
       block_norm_kernel<XF32, true, 4><<<grid, 32 * warps, 0, s>>>(a);
   } else {
-    // few rows: as many threads as vectors (latency); many: fewer threads with
-    // more loads each
-    const int want = a.T <= 2 * num_sms() ? 1 : 2;
-    const int vpt = std::max(want, (nv + 1023) / 1024);
+    // Few rows: as many threads as vectors (latency).  Many: about 224 threads
+    // with more loads each in flight, which leaves more rows to an SM (8192 x
+    // 7168 with a gate: 4 vectors 91 us, 2 114, 1 117; 2049 x 3584 in fp32: 4
+    // vectors 20.5 us, 2 16.1).
+    const int want = a.T <= 2 * num_sms() ? 1 : nv >= 768 ? 4 : nv >= 384 ? 2 : 1;
+    const int vpt = std::max(want, nv > 2048 ? 4 : nv > 1024 ? 2 : 1);
     const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
-    if (vpt == 1)
+    if (vpt == 1 && threads <= 256)
       block_norm_kernel<XF32, false, 1><<<a.T, threads, 0, s>>>(a);
-    else if (vpt == 2)
+    else if (vpt == 1)
+      block_norm_kernel<XF32, false, 1, 1024><<<a.T, threads, 0, s>>>(a);
+    else if (vpt == 2 && threads <= 256)
       block_norm_kernel<XF32, false, 2><<<a.T, threads, 0, s>>>(a);
+    else if (vpt == 2)
+      block_norm_kernel<XF32, false, 2, 1024><<<a.T, threads, 0, s>>>(a);
+    else if (threads <= 256)
+      block_norm_kernel<XF32, false, 4><<<a.T, threads, 0, s>>>(a);
     else
-      block_norm_kernel<XF32, false, 4><<<a.T, ((nv + 3) / 4 + 31) / 32 * 32, 0, s>>>(a);
+      block_norm_kernel<XF32, false, 4, 1024><<<a.T, threads, 0, s>>>(a);
   }
   MOE_LAUNCH_CHECK();
   return MOE_OK;
