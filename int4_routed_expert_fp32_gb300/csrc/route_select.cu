@@ -134,6 +134,24 @@ __device__ __noinline__ double softmax_sum64(const SelectArgs& a, const ZT* row,
   return warp_sum64(sum);
 }
 
+// The same from fp32 exponentials, within a relative 5e-7 (2 steps each, and 2^-24
+// |z - m| e^-|z - m| of the rounded differences).
+template <typename ZT>
+__device__ __noinline__ double softmax_sum_near(const SelectArgs& a, const ZT* row, float m) {
+  double sum = 0.0;
+  for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+    const float z = logit(a, row, e);
+    if (z > -INFINITY) sum += z == m ? 1.f : expf(z - m);
+  }
+  return warp_sum64(sum);
+}
+
+// How far a difference of two biased softmax scores p + b can be off when both
+// p share a denominator within 5e-7: an error of the difference of the p only.
+__device__ __forceinline__ double shared_error(double p, double q) {
+  return 2e-6 * fabs(p - q) + 1e-14;
+}
+
 // The segment leader's two largest of its L lanes' (hi >= lo) pairs.
 template <typename F>
 __device__ __forceinline__ void top2_segment(F& hi, F& lo, int r, int L) {
@@ -168,30 +186,58 @@ __device__ __noinline__ bool group_kept64(const SelectArgs& a, const ZT* row, fl
                                           const uint16_t* cid, int n) {
   const int lane = threadIdx.x & 31;
   const double none = -INFINITY;
-  double sum = 1.0;
-  if constexpr (SOFTMAX && BIAS) sum = softmax_sum64(a, row, m);
-  double key = none;
+  float z = -INFINITY, b = 0.f;
+  double e = 0.0;
   int of = -1;
   if (lane < n) {
-    const int e = cid[lane];
-    const float z = logit(a, row, e);
-    of = e / a.gs;
-    key = score64<SOFTMAX>(z, m, sum);
-    if constexpr (BIAS) key = key64(key, z, a.bias[e]);
-    if (z == -INFINITY) key = none;
+    z = logit(a, row, cid[lane]);
+    if constexpr (BIAS) b = a.bias[cid[lane]];
+    of = cid[lane] / a.gs;
+    e = score64<SOFTMAX>(z, m, 1.0);
   }
   __syncwarp();
-  double hi = none, lo = none;
-  for (int j = 0; j < n; ++j) {
-    const double v = __shfl_sync(0xffffffffu, key, j);
-    if (__shfl_sync(0xffffffffu, of, j) != g) continue;
-    lo = v > hi ? hi : (v > lo ? v : lo);
-    hi = v > hi ? v : hi;
+  bool kept = false;
+  for (int exact = SOFTMAX && BIAS ? 0 : 1; exact < 2; ++exact) {
+    double sum = 1.0;
+    if constexpr (SOFTMAX && BIAS)
+      sum = exact ? softmax_sum64(a, row, m) : softmax_sum_near(a, row, m);
+    const double p = e / sum;
+    double key = z == -INFINITY ? none : p;
+    if constexpr (BIAS) key = key64(p, z, b);
+    if (lane >= n) key = none;
+    double hi = none, lo = none, ph = 0.0, pl = 0.0;
+    for (int j = 0; j < n; ++j) {
+      const double v = __shfl_sync(0xffffffffu, key, j), pv = __shfl_sync(0xffffffffu, p, j);
+      if (__shfl_sync(0xffffffffu, of, j) != g) continue;
+      if (v > hi) {
+        lo = hi;
+        pl = ph;
+        hi = v;
+        ph = pv;
+      } else if (v > lo) {
+        lo = v;
+        pl = pv;
+      }
+    }
+    __syncwarp();
+    double score = hi, part = ph;
+    if (!a.best_only && hi > none && lo > none) {
+      score = hi + lo;
+      part = ph + pl;
+    }
+    kept = group_rank(score, g, a.G, a.L) < a.tg;
+    if (exact) break;
+    // decided, unless a kept and a dropped group are within what the sum leaves open
+    bool open = false;
+    for (int j = 0; j < a.G; ++j) {
+      const double o = __shfl_sync(0xffffffffu, score, j * a.L);
+      const double q = __shfl_sync(0xffffffffu, part, j * a.L);
+      const bool other = __shfl_sync(0xffffffffu, kept, j * a.L);
+      open |= g < a.G && other != kept && fabs(o - score) <= shared_error(q, part);
+    }
+    if (!__any_sync(0xffffffffu, open)) break;
   }
-  __syncwarp();
-  double score = hi;
-  if (!a.best_only && hi > none && lo > none) score = hi + lo;
-  return group_rank(score, g, a.G, a.L) < a.tg;
+  return kept;
 }
 
 // The same from all experts (more than 32 listed: many keys within the error
@@ -225,20 +271,39 @@ __device__ __noinline__ bool group_kept64_all(const SelectArgs& a, const ZT* row
 // Ranks of the n <= 32 candidates (one to a lane, in id order) by their 64-bit
 // keys (rare: two that matter lie within the fp32 error of one another).
 template <typename ZT, bool SOFTMAX>
-__device__ __noinline__ int rank64(const SelectArgs& a, const ZT* row, float m, int id, int n) {
+__device__ __noinline__ int rank64(const SelectArgs& a, const ZT* row, float m, int id, int n,
+                                   double* ckey) {
   const int lane = threadIdx.x & 31;
-  double sum = 1.0;
-  if constexpr (SOFTMAX) sum = softmax_sum64(a, row, m);
-  double key = -INFINITY;
+  float z = -INFINITY, b = 0.f;
+  double e = 0.0;  // sigmoid score, or softmax numerator
   if (lane < n) {
-    const float z = logit(a, row, id);
-    key = key64(score64<SOFTMAX>(z, m, sum), z, a.bias[id]);
+    z = logit(a, row, id);
+    b = a.bias[id];
+    e = score64<SOFTMAX>(z, m, 1.0);
   }
   __syncwarp();
   int rank = 0;
-  for (int j = 0; j < n; ++j) {
-    const double other = __shfl_sync(0xffffffffu, key, j);
-    rank += (other > key || (other == key && j < lane)) ? 1 : 0;
+  for (int exact = SOFTMAX ? 0 : 1; exact < 2; ++exact) {
+    double sum = 1.0;
+    if constexpr (SOFTMAX) sum = exact ? softmax_sum64(a, row, m) : softmax_sum_near(a, row, m);
+    const double key = lane < n ? key64(e / sum, z, b) : -INFINITY;
+    rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const double other = __shfl_sync(0xffffffffu, key, j);
+      rank += (other > key || (other == key && j < lane)) ? 1 : 0;
+    }
+    if (exact) break;
+    // decided, unless neighbours in the order are within what the sum leaves open
+    __syncwarp();
+    if (lane < n) ckey[rank] = key;
+    __syncwarp();
+    const double gap = lane < n && rank > 0 ? ckey[rank - 1] - key : INFINITY;
+    __syncwarp();
+    if (lane < n) ckey[rank] = e / sum;
+    __syncwarp();
+    const bool open = lane < n && rank > 0 && rank <= a.k &&
+                      gap <= shared_error(ckey[rank - 1], e / sum);
+    if (!__any_sync(0xffffffffu, open)) break;
   }
   return lane < n ? rank : 32;
 }
@@ -543,21 +608,45 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
   }
   thr = max(thr, kUnavail);
   constexpr float near = 2.f * (SOFTMAX ? kSlackSoftmax : kSlackSigmoid);
-  if constexpr (BIAS) {
-    const float tv = key_value(thr);
-    if (tv > -INFINITY && tv < INFINITY)
-      thr = order_key(clean(tv - (near + 2.f * kSlackStep * fabsf(tv))));
-  }
-  int mine = 0;
+  auto with_slack = [&](uint32_t k) {
+    if constexpr (BIAS) {
+      const float v = key_value(k);
+      if (v > -INFINITY && v < INFINITY)
+        return order_key(clean(v - (near + 2.f * kSlackStep * fabsf(v))));
+    }
+    return k;
+  };
+  auto at_or_above = [&](uint32_t k) {
+    int c = 0;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) mine += O(i) >= thr ? 1 : 0;
+    for (int i = 0; i < NI; ++i) c += O(i) >= k ? 1 : 0;
+    return c;
+  };
+  int mine = at_or_above(with_slack(thr));
+  int n = __reduce_add_sync(0xffffffffu, mine);
+  if (n > 32) {
+    // the bound is weak where few lanes hold the kept groups or k is near 32:
+    // halve the range of keys until k to 32 experts are left
+    uint32_t above = __reduce_max_sync(0xffffffffu, mx);  // fewer than k lie above it
+    while (thr < above) {
+      const uint32_t mid = thr + (above - thr + 1) / 2;
+      if (__reduce_add_sync(0xffffffffu, at_or_above(mid)) < a.k) {
+        above = mid - 1;
+        continue;
+      }
+      thr = mid;
+      mine = at_or_above(with_slack(thr));
+      n = __reduce_add_sync(0xffffffffu, mine);
+      if (n <= 32) break;
+    }
+  }
+  thr = with_slack(thr);
   int pos = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, pos, d);
     if (lane >= d) pos += v;
   }
-  const int n = __shfl_sync(0xffffffffu, pos, 31);
   pos -= mine;
   uint32_t* ckey32 = reinterpret_cast<uint32_t*>(ckey);
   const bool fit = n <= 32;
@@ -598,7 +687,7 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
     }
     if constexpr (BIAS) {
       if (__any_sync(0xffffffffu, close))
-        rank = rank64<ZT, SOFTMAX>(a, row, m, my_id, n);
+        rank = rank64<ZT, SOFTMAX>(a, row, m, my_id, n, ckey);
     }
   } else {
     my_id = select_many<ZT, SOFTMAX, BIAS>(a, row, m, ckey, cid, n);

@@ -358,3 +358,42 @@ def test_ops_follow_the_current_stream_and_capture(moe):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert moe.check_error() == 0
+
+
+@pytest.mark.parametrize("stream", [BF16, torch.float32])
+@pytest.mark.parametrize("gate", ["none", "full", "channel", "token"])
+@pytest.mark.parametrize("T,N", [(700, 65), (900, 129), (333, 2049), (1300, 4099), (400, 7001),
+                                 (310, 9003), (23, 16383), (640, 71), (5, 12345)])
+def test_block_norm_odd_widths_over_many_rows(moe, T, N, gate, stream):
+    """Dense rows whose 16-byte boundaries move from row to row, several rows to
+    a CTA: x_out and h, x_out alone, and the pre-norm alone."""
+    y, x, post, pre, gv = norm_inputs(T, N, stream, gate, T + N)
+    for use_post, use_pre, sigmoid in [(True, True, True), (False, True, False),
+                                       (True, False, False), (False, False, True)]:
+        p, q = post if use_post else None, pre if use_pre else None
+        gx, gh = moe.block_norm(y, x, post_gain=p, gate=gv, gate_sigmoid=sigmoid, scale=1.3,
+                                pre_gain=q, eps=1e-6)
+        r, h, size, hsize = norm_ref(y, x, p, gv, sigmoid, 1.3, q, 1e-6)
+        check_norm(gx, r, size, stream, 4e-6)
+        if q is not None:
+            check_norm(gh, h, hsize, BF16, 8e-6)
+    x2, y2 = x.clone(), y.clone()
+    want = moe.block_norm(y, x, post_gain=post, gate=gv, pre_gain=pre)
+    moe.block_norm(y2, x2, post_gain=post, gate=gv, pre_gain=pre, x_out=x2, h_out=y2)
+    assert torch.equal(x2, want[0]) and torch.equal(y2, want[1])
+    assert moe.check_error() == 0
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("E,k,groups,kept", [(512, 16, 8, 2), (500, 32, 4, 2), (384, 8, 8, 1),
+                                             (300, 30, 1, 1), (2048, 32, 16, 2)])
+def test_route_few_lanes_hold_the_kept_groups(moe, E, k, groups, kept, biased, score):
+    """k near the lanes that hold the kept groups, or near 32; equal logits."""
+    z = logits(60, E, E + k)
+    z[40:50] = z[40:50].round(decimals=1)
+    z[50:] = 0.5
+    z[55:, ::7] = 1.5
+    for group_score in ("top2", "max"):
+        check_route(moe, z, k, ranking_bias(E, 3) if biased else None, score=score,
+                    groups=groups, topk_groups=kept, group_score=group_score)
