@@ -30,6 +30,8 @@
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
+#include <vector>
 
 #include "adapter.cuh"
 #include "common.cuh"
@@ -96,22 +98,31 @@ __device__ __forceinline__ void expand_token(const uint16_t* b, int rows, int R,
         mma_bf16(acc[m], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, p.z, p.w);
       }
     }
+    float v[4][2];
+    bool odd = false;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v[m][h] = acc[m][2 * h] + acc[m][2 * h + 1];
+        odd |= !(fabsf(v[m][h]) < INFINITY);
+      }
     if (q == 0) {
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = 16 * (m0 + m) + 8 * h + g;
-          float v = acc[m][2 * h] + acc[m][2 * h + 1];
-          if (!(fabsf(v) < INFINITY) && r < rows) {
-            // an infinity times hi and times lo can have two signs: one product
-            v = 0.f;
-            for (int j = 0; j < R; ++j)
-              v = fmaf(bf16_bits_to_f32(hi[j]) + bf16_bits_to_f32(hi[R + j]),
-                       bf16_bits_to_f32(b[r * R + j]), v);
-          }
-          out[r] = v;
-        }
+        for (int h = 0; h < 2; ++h) out[16 * (m0 + m) + 8 * h + g] = v[m][h];
+    }
+    if (__any_sync(0xffffffffu, odd && q == 0)) {
+      __syncwarp();  // the rows above are written
+      // an infinity times hi and times lo can have two signs: one product
+      for (int r = 16 * m0 + lane; r < min(16 * m0 + 64, rows); r += 32) {
+        float u = 0.f;
+        for (int j = 0; j < R; ++j)
+          u = fmaf(bf16_bits_to_f32(hi[j]) + bf16_bits_to_f32(hi[R + j]),
+                   bf16_bits_to_f32(b[r * R + j]), u);
+        if (!(fabsf(u) < INFINITY)) out[r] = u;
+      }
     }
   }
   __syncwarp();
@@ -142,6 +153,10 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
   __shared__ int16_t low_rows[8];
   const Waiter wt{&cta_abort, status, wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tensor_map(&mw);
+    prefetch_tensor_map(&mx);
+  }
   const int tb = sh.tb, stages = sh.stages;
   const int stage_bytes = kSpWBytes + tb * 128;
   const int ranks = gridDim.x, rank = blockIdx.x;
@@ -194,8 +209,6 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
 
   if (warp == 0) {
     if (lane == 0) {
-      prefetch_tensor_map(&mw);
-      prefetch_tensor_map(&mx);
       uint32_t it = 0;
       for (int k = s0; k < s1; ++k, ++it) {
         const int s = it % stages;
@@ -361,16 +374,59 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
   cluster_sync_all();  // no CTA leaves while another reads its tile
 }
 
+// Asked of the runtime once for each kernel, cluster size and amount of shared
+// memory; what a device holds does not change.
+int adapter_cluster(const void* kernel, int threads, int smem, int clusters, int most) {
+  struct Known {
+    const void* kernel;
+    int device, threads, smem, size, held;
+  };
+  static std::mutex mu;
+  static std::vector<Known> known;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return 1;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int size = most; size > 1; --size) {
+    int held = -1;
+    for (const Known& k : known)
+      if (k.kernel == kernel && k.device == device && k.threads == threads && k.smem == smem &&
+          k.size == size)
+        held = k.held;
+    if (held < 0) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(size);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = size;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      held = 0;
+      if (cudaOccupancyMaxActiveClusters(&held, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        held = 0;
+      }
+      known.push_back(Known{kernel, device, threads, smem, size, held});
+    }
+    if (held >= clusters) return size;
+  }
+  return 1;
+}
+
 namespace {
 
-SplitShape split_shape(int T, int K, int N, int R) {
+int split_tiles(int T, int N) {
+  return (N + 127) / 128 * ((T + kSpTokens - 1) / kSpTokens);
+}
+
+SplitShape split_shape(int T, int R, int cluster) {
   SplitShape s;
   const int blocks = (T + kSpTokens - 1) / kSpTokens;
   s.tb = ((T + blocks - 1) / blocks + 15) / 16 * 16;
-  const int tiles = (N + 127) / 128 * blocks;
-  const int steps = (K + 63) / 64;
-  // at most one CTA to an SM: a second one on some would take twice the time
-  s.cluster = std::min(std::max(1, std::min(kSpMaxCluster, num_sms() / tiles)), steps);
+  s.cluster = cluster;
   const int stage = kSpWBytes + s.tb * 128;
   // up to 64 tokens ~92 KiB in flight an SM; more: with room for two CTAs of the
   // shrink, which an SM still holds when this kernel starts
@@ -401,12 +457,22 @@ SplitShape split_shape(int T, int K, int N, int R) {
 
 template <bool FUSED>
 int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
-  const SplitShape sh = split_shape(a.T, a.K, a.N, a.R);
-  CUtensorMap mw, mx;
-  if (!adapter_map_rows(&mw, a.w, a.N, a.K, 128) || !adapter_map_rows(&mx, a.x, a.T, a.K, sh.tb)) return MOE_ERR_CUDA;
   auto kern = adapter_split_kernel<FUSED>;
-  MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(sh.smem)));
+  // at most one CTA to an SM (a second one on some would take twice the time),
+  // and as many clusters as the device holds at once
+  const int tiles = split_tiles(a.T, a.N);
+  const int most = std::min({kSpMaxCluster, std::max(1, num_sms() / tiles), (a.K + 63) / 64});
+  SplitShape sh = split_shape(a.T, a.R, most);
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern), static_cast<int>(sh.smem)));
+  const int held = adapter_cluster(reinterpret_cast<const void*>(kern), kSpThreads,
+                                   static_cast<int>(sh.smem), tiles, most);
+  if (held < most) {  // fewer ranks, more tokens to each
+    sh = split_shape(a.T, a.R, held);
+    MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern), static_cast<int>(sh.smem)));
+  }
+  CUtensorMap mw, mx;
+  if (!adapter_map_rows(&mw, a.w, a.N, a.K, 128) || !adapter_map_rows(&mx, a.x, a.T, a.K, sh.tb))
+    return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(sh.cluster, (a.N + 127) / 128, (a.T + sh.tb - 1) / sh.tb);
   cfg.blockDim = dim3(kSpThreads);

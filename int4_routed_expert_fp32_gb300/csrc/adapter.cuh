@@ -41,6 +41,20 @@ inline bool adapter_map_rows(CUtensorMap* m, const uint16_t* base, int rows, int
                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Dynamic shared memory of a kernel, and all of an SM's L1 as shared memory while it
+// runs: the split in force is the first kernel's, and a CTA of the next one that
+// wants more of it waits until the SM is empty.
+inline cudaError_t adapter_smem(const void* kernel, int bytes) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                              cudaSharedmemCarveoutMaxShared);
+}
+
+// The largest cluster (at most `most` CTAs) of which the device holds `clusters` at
+// a time, or 1: one cluster too many would wait for a whole other one to finish.
+int adapter_cluster(const void* kernel, int threads, int smem, int clusters, int most);
+
 // Launch attributes: clusters of `ranks` CTAs, programmatic dependent of the
 // kernel before it in the stream.
 inline void set_adapter_attrs(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ranks) {
@@ -62,6 +76,13 @@ __device__ __forceinline__ void grid_launch_dependents() {
 
 __device__ __forceinline__ void grid_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A tile of a tensor map on its way to L2.
+__device__ __forceinline__ void prefetch_tile_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0),
+               "r"(c1)
+               : "memory");
 }
 
 // An id outside [0, adapters) selects none.

@@ -1,19 +1,15 @@
 // The low-rank vectors of the adapter projection: low[t] = scale x[t] A^T, A the
 // [R, K] of token t's adapter (see adapter.cu).
 //
-// The tokens of a tile of 128 are sorted by adapter in shared memory.  The K
-// range of a tile is split over the CTAs of a cluster, whose fp32 sums meet in
-// distributed shared memory and are added in the order of the ranks.
-//
-//  - adapter_shrink_warp_kernel, few tokens: bound by reading the A of each
-//    adapter in use, and in practice by latency.  A warp takes up to 16 tokens
-//    of one adapter; where a CTA has fewer such items than warps, several
-//    warps share an item's columns, so that a single token's 2 R K bytes are
-//    still spread over 64 warps.
-//  - adapter_shrink_tile_kernel, many tokens: bound by reading x.  tcgen05 over
-//    the whole tile: tokens are the M side, the rows of A of the adapters that
-//    occur in the tile (as many as fit 256 columns at a time) the N side, both
-//    through a TMA ring; each token then keeps its own adapter's columns.
+// The tokens of a tile of 128 are sorted by adapter in shared memory.  tcgen05
+// over the whole tile: tokens are the M side, the rows of A of the adapters that
+// occur in the tile (as many as fit `cols` columns at a time) the N side, both
+// through a TMA ring; each token then keeps its own adapter's columns.  The MMAs
+// of rows that do not use an adapter are wasted, and cost nothing that matters:
+// the kernel is bound by reading x and the A in use.  The K range of a tile is
+// split over the CTAs of a cluster, whose fp32 sums meet in distributed shared
+// memory and are added in the order of the ranks; with few tokens, which can
+// have an adapter each, the adapters are dealt to further clusters.
 #include <algorithm>
 
 #include "adapter.cuh"
@@ -25,9 +21,7 @@ namespace moe {
 namespace {
 
 constexpr int kAdTile = 128;
-constexpr int kShWarps = 8;
 constexpr int kShMaxCluster = 8;
-constexpr int kItemRows = 16;
 
 struct ShrinkArgs {
   const uint16_t* x;
@@ -35,7 +29,9 @@ struct ShrinkArgs {
   const int32_t* ids;
   const float* scale;
   int T, K, R, adapters;
-  float* low;  // [T, R]
+  int per, stages;  // adapters to a pass, slots of the ring
+  int xrows;        // rows of x in a slot: a multiple of 8, those there are
+  float* low;       // [T, R]
   int* status;
 };
 
@@ -105,71 +101,9 @@ __device__ void make_items(Items& u, int cut, const int32_t* ids, int t0, int ro
   __syncthreads();
 }
 
-}  // namespace
-
-// Cluster (rank = x) of CTAs over tile y: each takes a slice of K and the
-// tile's items z, z + gridDim.z, ..., at most eight of them.  MT: 16-row tiles
-// of the rank.
-template <int MT>
-__global__ void __launch_bounds__(32 * kShWarps) adapter_shrink_warp_kernel(const ShrinkArgs s) {
-  grid_wait();
-  grid_launch_dependents();  // whose own reads of x and w are then safe
-  extern __shared__ __align__(16) float sh_low[];  // [warp][kItemRows][R]
-  __shared__ Items u;
-  const int t0 = blockIdx.y * kAdTile;
-  const int rank = blockIdx.x, ranks = gridDim.x, groups = gridDim.z, z = blockIdx.z;
-  make_items(u, kItemRows, s.ids, t0, min(kAdTile, s.T - t0), s.adapters, s.status,
-             rank == 0 && z == 0);
-  const int items = min((u.n - z + groups - 1) / groups, kShWarps);
-  if (u.n <= z) return;  // the whole cluster: it has the same z
-  // warps to an item: 8, 4, 2 or 1
-  const int sub = items == 1 ? 8 : items == 2 ? 4 : items <= 4 ? 2 : 1;
-  const int warp = threadIdx.x >> 5;
-  const int steps = s.K / 32;  // K % 32 == 0
-  const int k0 = steps * rank / ranks, k1 = steps * (rank + 1) / ranks;
-  if (warp / sub < items) {
-    const int j = z + warp / sub * groups, part = warp % sub;
-    const uint16_t* A = s.a + static_cast<size_t>(u.id[j]) * s.R * s.K;
-    const uint16_t* x = s.x + static_cast<size_t>(t0) * s.K;
-    const int c = u.count[j];
-    const int a0 = (k0 + (k1 - k0) * part / sub) * 32, a1 = (k0 + (k1 - k0) * (part + 1) / sub) * 32;
-    float* out = sh_low + warp * kItemRows * s.R;
-    if (c <= 8)
-      shrink_item<MT, 1>(x, A, s.K, s.R, u.row + u.at[j], c, a0, a1, out);
-    else
-      shrink_item<MT, 2>(x, A, s.K, s.R, u.row + u.at[j], c, a0, a1, out);
-  }
-  cluster_sync_all();
-  // the ranks take the items' rows in turn: 4 values to a thread
-  const int quads = s.R / 4, per_item = kItemRows * quads;
-  for (int i = rank * 32 * kShWarps + threadIdx.x; i < items * per_item;
-       i += ranks * 32 * kShWarps) {
-    const int l = i / per_item, p = i % per_item / quads, e = i % quads * 4;
-    const int j = z + l * groups;
-    if (p >= u.count[j]) continue;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < ranks; ++r) {
-      const uint32_t at = mapa_shared(sh_low + (l * sub * kItemRows + p) * s.R + e, r);
-      for (int q = 0; q < sub; ++q) {
-        const float4 o = ld_cluster_f4(at + q * kItemRows * s.R * 4);
-        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-      }
-    }
-    const float sc = s.scale ? s.scale[u.id[j]] : 1.f;
-    const int t = t0 + (u.row[u.at[j] + p] & 0xff);
-    *reinterpret_cast<float4*>(s.low + static_cast<size_t>(t) * s.R + e) =
-        make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
-  }
-  cluster_sync_all();  // no CTA leaves while another reads its sums
-}
-
-namespace {
-
 constexpr int kStThreads = 192;  // warp 0: TMA, 1: MMA + TMEM, 2-5: epilogue
-constexpr int kStXBytes = kAdTile * 64 * 2;
 constexpr int kStMaxCols = 256;
 constexpr int kStMaxStages = 8;
-constexpr int kStSmem = 200 * 1024;
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
@@ -181,13 +115,26 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 
 }  // namespace
 
-// Cluster (rank = x) of CTAs over tile y; ma: [adapters R][K], boxes of R rows.
+// Cluster (rank = x) of CTAs over tile y and passes z, z + gridDim.z, ...; ma:
+// [adapters][R][K], boxes of R rows of one adapter.
 __global__ void __launch_bounds__(kStThreads, 1)
     adapter_shrink_tile_kernel(const __grid_constant__ CUtensorMap mx,
                                const __grid_constant__ CUtensorMap ma, const ShrinkArgs s,
                                long long wait_ns) {
+  if (threadIdx.x == 0) {
+    prefetch_tensor_map(&mx);
+    prefetch_tensor_map(&ma);
+  }
   grid_wait();
   grid_launch_dependents();  // whose own reads of x and w are then safe
+  const int rank = blockIdx.x, ranks = gridDim.x;
+  const int t0 = blockIdx.y * kAdTile;
+  const int steps = (s.K + 63) / 64;
+  const int s0 = steps * rank / ranks, s1 = steps * (rank + 1) / ranks;
+  // x on its way to L2 while the rows are sorted
+  if (threadIdx.x >= kStThreads - 32)
+    for (int k = s0 + threadIdx.x - (kStThreads - 32); k < s1; k += 32)
+      prefetch_tile_2d(&mx, k * 64, t0);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -198,8 +145,6 @@ __global__ void __launch_bounds__(kStThreads, 1)
   __shared__ int16_t of_row[kAdTile];  // the row's adapter among the tile's (-1: none)
   const Waiter wt{&cta_abort, s.status, wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x, ranks = gridDim.x;
-  const int t0 = blockIdx.y * kAdTile;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStMaxStages; ++i) {
       mbar_init(&full[i], 1);
@@ -218,7 +163,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
   }
   tc_fence_before();
   // the barriers in here cover the initialisation too
-  make_items(u, kAdTile, s.ids, t0, min(kAdTile, s.T - t0), s.adapters, s.status, rank == 0);
+  make_items(u, kAdTile, s.ids, t0, min(kAdTile, s.T - t0), s.adapters, s.status,
+             rank == 0 && blockIdx.z == 0);
   tc_fence_after();
   const uint32_t tbase = tmem_slot;
   const int n = u.n;
@@ -226,27 +172,24 @@ __global__ void __launch_bounds__(kStThreads, 1)
     for (int p = lane; p < u.count[j]; p += 32) of_row[u.row[u.at[j] + p] & 0xff] = j;
   __syncthreads();
 
-  // the ring goes by the columns that a pass needs
-  float* sums = reinterpret_cast<float*>(smem);  // [kAdTile][R]
-  uint8_t* ring = smem + kAdTile * s.R * 4;  // R % 8 == 0: whole KiB
-  const int per = kStMaxCols / s.R;  // adapters to a pass
+  const int per = s.per, stages = s.stages;
   const int passes = (n + per - 1) / per;
-  const int most = (min(n, per) * s.R + 15) / 16 * 16;
-  const int stage_bytes = kStXBytes + (most * 128 + 1023) / 1024 * 1024;
-  const int stages = min(kStMaxStages,
-                         static_cast<int>(smem_raw + kStSmem - ring) / stage_bytes);
-  const int steps = (s.K + 63) / 64;
-  const int s0 = steps * rank / ranks, s1 = steps * (rank + 1) / ranks;
+  // a slot: A, then x.  The MMA's M side is 128 rows all the same: with fewer rows
+  // of x it goes on into what follows (the sums, after the last slot), whose
+  // products are no token's
+  const int abytes = (per * s.R + 15) / 16 * 2048;
+  const int xbytes = s.xrows * 128;
+  const int stage_bytes = abytes + xbytes;
+  uint8_t* ring = smem;
+  float* sums = reinterpret_cast<float*>(ring + stages * stage_bytes);  // [xrows][R]
 
   if (warp == 0) {
     if (lane == 0) {
-      prefetch_tensor_map(&mx);
-      prefetch_tensor_map(&ma);
       uint32_t it = 0;
       bool ok = true;
-      for (int pass = 0; pass < passes && ok; ++pass) {
+      for (int pass = blockIdx.z; pass < passes && ok; pass += gridDim.z) {
         const int d0 = pass * per, d1 = min(n, d0 + per);
-        const uint32_t bytes = kStXBytes + (d1 - d0) * s.R * 128;
+        const uint32_t bytes = xbytes + (d1 - d0) * s.R * 128;
         for (int k = s0; k < s1; ++k, ++it) {
           const int i = it % stages;
           if (!mbar_wait(&empty[i], ((it / stages) & 1u) ^ 1u, wt)) {
@@ -255,9 +198,9 @@ __global__ void __launch_bounds__(kStThreads, 1)
           }
           uint8_t* st = ring + i * stage_bytes;
           mbar_arrive_expect_tx(&full[i], bytes);
-          tma_g2s_2d(st, &mx, &full[i], k * 64, t0);
+          tma_g2s_2d(st + abytes, &mx, &full[i], k * 64, t0);
           for (int d = d0; d < d1; ++d)
-            tma_g2s_3d(st + kStXBytes + (d - d0) * s.R * 128, &ma, &full[i], k * 64, 0, u.id[d]);
+            tma_g2s_3d(st + (d - d0) * s.R * 128, &ma, &full[i], k * 64, 0, u.id[d]);
         }
       }
       drain_ring(full, it, stages, s.status);
@@ -265,10 +208,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
   } else if (warp == 1) {
     uint32_t it = 0;
     bool ok = true;
-    for (int pass = 0; pass < passes && ok; ++pass) {
+    for (int pass = blockIdx.z, turn = 0; pass < passes && ok; pass += gridDim.z, ++turn) {
       const int cols = (min(n - pass * per, per) * s.R + 15) / 16 * 16;
       const uint32_t idesc = idesc_bf16(kAdTile, cols);
-      if (!__all_sync(0xffffffffu, mbar_wait(&accempty, (pass & 1u) ^ 1u, wt))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&accempty, (turn & 1u) ^ 1u, wt))) break;
       tc_fence_after();
       for (int k = s0; k < s1; ++k, ++it) {
         const int i = it % stages;
@@ -277,8 +220,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint64_t da = smem_desc_sw128(ring + i * stage_bytes);
-        const uint64_t db = smem_desc_sw128(ring + i * stage_bytes + kStXBytes);
+        const uint64_t da = smem_desc_sw128(ring + i * stage_bytes + abytes);
+        const uint64_t db = smem_desc_sw128(ring + i * stage_bytes);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_f16_warp(tbase, da + 2 * kk, db + 2 * kk, idesc, (k != s0) | (kk != 0));
@@ -292,8 +235,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
     const int q = warp & 3;
     const int row = 32 * q + lane;
     const int mine = of_row[row];
-    for (int pass = 0; pass < passes; ++pass) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&accfull, pass & 1u, wt))) break;
+    for (int pass = blockIdx.z, turn = 0; pass < passes; pass += gridDim.z, ++turn) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&accfull, turn & 1u, wt))) break;
       tc_fence_after();
       const int d0 = pass * per, d1 = min(n, d0 + per);
       for (int d = d0; d < d1; ++d) {
@@ -328,7 +271,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   for (int i = rank * kStThreads + threadIdx.x; i < kAdTile * quads; i += ranks * kStThreads) {
     const int row = i / quads, e = i % quads * 4;
     const int d = of_row[row];
-    if (d < 0) continue;
+    if (d < 0 || d / per % gridDim.z != blockIdx.z) continue;  // none, or another cluster's
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < ranks; ++r) {
       const float4 o = ld_cluster_f4(mapa_shared(sums + row * s.R + e, r));
@@ -342,59 +285,6 @@ __global__ void __launch_bounds__(kStThreads, 1)
 }
 
 namespace {
-
-template <int MT>
-int launch_warp(const ShrinkArgs& s, cudaStream_t st) {
-  const int tiles = (s.T + kAdTile - 1) / kAdTile, rows = std::min(s.T, kAdTile);
-  const int ranks = std::max(1, std::min(kShMaxCluster, s.K / 64));
-  // groups of items: about one CTA to an SM, which leaves room for the kernel
-  // that streams W beside it; at most eight items each
-  const int groups = std::min(rows, std::max((rows + kShWarps - 1) / kShWarps,
-                                             num_sms() / (ranks * tiles)));
-  auto kern = adapter_shrink_warp_kernel<MT>;
-  const int smem = kShWarps * kItemRows * s.R * 4;
-  if (smem > 48 * 1024)
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(ranks, tiles, groups);
-  cfg.blockDim = dim3(32 * kShWarps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  set_adapter_attrs(&cfg, attr, ranks);
-  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, s));
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
-}
-
-int launch_tile(const ShrinkArgs& s, cudaStream_t st) {
-  const int tiles = (s.T + kAdTile - 1) / kAdTile;
-  const int ranks =
-      std::max(1, std::min({kShMaxCluster, num_sms() / tiles, (s.K + 63) / 64}));
-  CUtensorMap mx, ma;
-  const uint64_t dims[3] = {static_cast<uint64_t>(s.K), static_cast<uint64_t>(s.R),
-                            static_cast<uint64_t>(s.adapters)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(s.K) * 2,
-                               static_cast<uint64_t>(s.K) * s.R * 2};
-  const uint32_t box[3] = {64, static_cast<uint32_t>(s.R), 1};
-  if (!adapter_map_rows(&mx, s.x, s.T, s.K, kAdTile) ||
-      !encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, s.a, dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
-    return MOE_ERR_CUDA;
-  MOE_TRY_CUDA(cudaFuncSetAttribute(adapter_shrink_tile_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem));
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(ranks, tiles);
-  cfg.blockDim = dim3(kStThreads);
-  cfg.dynamicSmemBytes = kStSmem;
-  cfg.stream = st;
-  set_adapter_attrs(&cfg, attr, ranks);
-  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, adapter_shrink_tile_kernel, mx, ma, s,
-                                  static_cast<long long>(kDefaultWaitNs)));
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
-}
 
 }  // namespace
 
@@ -410,11 +300,60 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
   s.adapters = a.adapters;
   s.low = a.low;
   s.status = status;
-  if (a.T > kSplitTokens) return launch_tile(s, st);
-  if (a.R <= 16) return launch_warp<1>(s, st);
-  if (a.R <= 32) return launch_warp<2>(s, st);
-  if (a.R <= 64) return launch_warp<4>(s, st);
-  return launch_warp<8>(s, st);
+  const int tiles = (s.T + kAdTile - 1) / kAdTile, rows = std::min(s.T, kAdTile);
+  const int steps = (s.K + 63) / 64;
+  // Many tokens: one cluster to a tile, all the columns a pass can have.  Few:
+  // adapters dealt to clusters, some 128 CTAs in all if every token has its own.
+  int groups = 1;
+  s.per = kStMaxCols / s.R;
+  if (s.T <= kSplitTokens) {
+    const int want = std::min(rows, 16 / tiles);
+    s.per = std::min(s.per, (rows + want - 1) / want);
+    groups = std::min(want, (rows + s.per - 1) / s.per);
+  }
+  // Little enough for the projection kernel to start beside it, where that leaves
+  // two slots, if need be with half the adapters to a pass; else its CTAs come when
+  // these have gone (32 tokens of rank 32: 17 us against 27; with fewer adapters
+  // still, x is read too often: 64 tokens of rank 64, 63 us against 41).
+  s.xrows = (rows + 7) / 8 * 8;
+  const int fixed = std::max(s.xrows * s.R * 4, (kAdTile - s.xrows) * 128) + 1024;
+  auto slot = [&](int per) { return (per * s.R + 15) / 16 * 2048 + s.xrows * 128; };
+  auto slots = [&](int per, int bytes) { return (bytes - fixed) / slot(per); };
+  constexpr int kBeside = 50 * 1024, kAlone = 198 * 1024;
+  const int beside = slots(s.per, kBeside) >= 2 ? s.per : (s.per + 1) / 2;
+  if (s.T <= 64 && slots(beside, kBeside) >= 2) {
+    s.per = beside;
+    s.stages = slots(s.per, kBeside);
+  } else {
+    s.stages = std::max(2, slots(s.per, kAlone));
+  }
+  s.stages = std::min(kStMaxStages, s.stages);
+  const int smem = s.stages * slot(s.per) + fixed;
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(adapter_shrink_tile_kernel), smem));
+  const int ranks =
+      adapter_cluster(reinterpret_cast<const void*>(adapter_shrink_tile_kernel), kStThreads, smem,
+                      tiles * groups, std::min(kShMaxCluster, steps));
+  CUtensorMap mx, ma;
+  const uint64_t dims[3] = {static_cast<uint64_t>(s.K), static_cast<uint64_t>(s.R),
+                            static_cast<uint64_t>(s.adapters)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(s.K) * 2,
+                               static_cast<uint64_t>(s.K) * s.R * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(s.R), 1};
+  if (!adapter_map_rows(&mx, s.x, s.T, s.K, s.xrows) ||
+      !encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, s.a, dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+    return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(ranks, tiles, groups);
+  cfg.blockDim = dim3(kStThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  set_adapter_attrs(&cfg, attr, ranks);
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, adapter_shrink_tile_kernel, mx, ma, s,
+                                  static_cast<long long>(kDefaultWaitNs)));
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
 }
 
 }  // namespace moe
