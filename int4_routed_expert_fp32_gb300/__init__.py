@@ -18,6 +18,9 @@ _BINDING = ("MoeConfig", "MoeError", "MoeLayer", "MoeWeights", "adapter_linear",
 
 
 def __getattr__(name):
+    if name == "MoeBlock":
+        globals()[name] = value = importlib.import_module(".block", __name__).MoeBlock
+        return value
     if name in _BINDING:
         capi = importlib.import_module(".capi", __name__)
         # kept: later uses of the name find it without coming here
@@ -27,4 +30,4 @@ def __getattr__(name):
 
 
 def __dir__():
-    return sorted(list(globals()) + list(_BINDING))
+    return sorted({*globals(), *_BINDING, "MoeBlock"})

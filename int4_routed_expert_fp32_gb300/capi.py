@@ -748,11 +748,11 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=dev)
     need = lib.moe_adapter_linear_workspace_size(T, K, N, R)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     rc = lib.moe_adapter_linear(
         x.data_ptr(), w.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), ids.data_ptr(),
-        None if scale is None else scale.data_ptr(), T, K, N, R, n, out.data_ptr(), ws.data_ptr(),
-        need, _raw_stream(dev.index))
+        None if scale is None else scale.data_ptr(), T, K, N, R, n, out.data_ptr(),
+        None if ws is None else ws.data_ptr(), need, _raw_stream(dev.index))
     if rc:
         _check("moe_adapter_linear", rc)
     return out

@@ -55,6 +55,8 @@ constexpr int kLowWarps = 6;   // warps 2-7
 
 constexpr int kBBytes = 64 * 1024;  // of B that a CTA fetches while W streams, at most
 
+bool fused(int T, int R) { return T <= 8 && T * R <= kFusedLow; }
+
 struct SplitShape {
   int tb;      // tokens to a block (the MMA's N), a multiple of 16
   int stages;
@@ -495,7 +497,7 @@ using namespace moe;
 extern "C" size_t moe_adapter_linear_workspace_size(int T, int K, int N, int R) {
   (void)K;
   (void)N;
-  if (T <= 0 || R <= 0) return 256;
+  if (T <= 0 || R <= 0 || fused(T, R)) return 0;
   return align_up(static_cast<size_t>(T) * R * sizeof(float), 256);
 }
 
@@ -507,11 +509,12 @@ extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const ui
   if (T < 0 || K <= 0 || N <= 0 || R <= 0 || adapters <= 0) return MOE_ERR_INVALID;
   if (K % 32 != 0 || N % 8 != 0 || R % 8 != 0 || R > kMaxRank) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
-  if (!x || !w || !lora_a || !lora_b || !ids || !y || !ws) return MOE_ERR_INVALID;
+  const size_t need = moe_adapter_linear_workspace_size(T, K, N, R);
+  if (!x || !w || !lora_a || !lora_b || !ids || !y || (need && !ws)) return MOE_ERR_INVALID;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) ||
       !aligned(ids, 4) || !aligned(scale, 4) || !aligned(y, 16) || !aligned(ws, 256))
     return MOE_ERR_INVALID;
-  if (ws_bytes < moe_adapter_linear_workspace_size(T, K, N, R)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   int* status = status_word();
   if (!status) return MOE_ERR_CUDA;
   AdapterArgs a{};
@@ -529,7 +532,7 @@ extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const ui
   a.low = static_cast<float*>(ws);
   a.y = y;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (T * R <= kFusedLow && T <= 8) return launch_split<true>(a, status, st);
+  if (fused(T, R)) return launch_split<true>(a, status, st);
   const int rc = launch_adapter_shrink(a, status, st);
   if (rc) return rc;
   return T > kSplitTokens ? launch_adapter_tile(a, status, st) : launch_split<false>(a, status, st);

@@ -187,7 +187,7 @@ def test_adapter_linear_refusals(capi):
     L, n = capi.lib, capi.launch_count()
     bad, uns = capi.MOE_ERR_INVALID, capi.MOE_ERR_UNSUPPORTED
 
-    def call(T=4, K=64, N=24, R=8, adapters=3, ws_bytes=1 << 30, **ptr):
+    def call(T=9, K=64, N=24, R=8, adapters=3, ws_bytes=1 << 30, **ptr):
         p = dict(x=FAKE, w=FAKE, a=FAKE, b=FAKE, ids=FAKE, scale=None, y=FAKE, ws=FAKE)
         p.update(ptr)
         return L.moe_adapter_linear(p["x"], p["w"], p["a"], p["b"], p["ids"], p["scale"], T, K, N,
@@ -203,6 +203,19 @@ def test_adapter_linear_refusals(capi):
         assert call(**kw) == uns, kw
     assert call(ws_bytes=0) == capi.MOE_ERR_WORKSPACE
     assert call(T=0, x=None) == capi.MOE_OK
-    assert L.moe_adapter_linear_workspace_size(4, 64, 24, 8) >= 4 * 8 * 4
-    assert L.moe_adapter_linear_workspace_size(0, 64, 24, 8) > 0
+    assert L.moe_adapter_linear_workspace_size(9, 64, 24, 8) >= 9 * 8 * 4
+    assert L.moe_adapter_linear_workspace_size(1, 64, 24, 16) == 0   # one launch, no scratch
+    assert L.moe_adapter_linear_workspace_size(0, 64, 24, 8) == 0
     assert capi.launch_count() == n
+
+
+def test_moe_block_checks_its_weights(capi, monkeypatch):
+    from int4_routed_expert_fp32_gb300.block import MoeBlock
+    monkeypatch.setattr(capi, "router_prepare", lambda w: None)
+    w = {n: None for n in capi.EXPERT_NAMES}
+    w["router_w"] = f32(16, 64)
+    MoeBlock(w, 2)
+    raises("lat_down and lat_up", MoeBlock, {**w, "lat_down": bf16(32, 64)}, 2)
+    raises("no projection for the adapters", MoeBlock, w, 2, adapters={"lat_up": ()})
+    latent = {**w, "lat_down": bf16(32, 64), "lat_up": bf16(64, 32)}
+    raises("no projection for the adapters", MoeBlock, latent, 2, adapters={"router": ()})

@@ -1,0 +1,128 @@
+"""The mixture-of-experts block: routing in groups, adapters beside the latent
+projections, experts, norm, gate and residual, run together.
+
+Reference: 64-bit arithmetic on the same weights, with the block's own routing
+(which has tests of its own).  Tolerance on the change of the residual stream:
+six roundings to bf16 lie on its way (down-projection, expert output, combine,
+latent norm, up-projection, and the stream's own where it is bf16), each of
+relative size 2^-8 / sqrt(3) at most: 5.6e-3 together, 8e-3 with the products
+between them.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import workloads as wl
+from oracle import inputs as oi
+from tests._helpers import device_weights, rel_l2
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from int4_routed_expert_fp32_gb300.build import build
+    build()
+    import int4_routed_expert_fp32_gb300 as m
+    torch.cuda.set_device(DEV)
+    assert m.check_error() == 0
+    yield m
+    assert m.check_error() == 0
+
+
+def rms(v, gain, eps):
+    return v / torch.sqrt((v * v).mean(dim=1, keepdim=True) + eps) * gain.double().cpu()
+
+
+def project(x, w, adapters, ids):
+    y = x @ w.double().cpu().T
+    if adapters is not None and ids is not None:
+        a, b, scale = (None if t is None else t.double().cpu() for t in adapters)
+        for t, i in enumerate(ids.tolist()):
+            if i >= 0:
+                s = 1.0 if scale is None else scale[i]
+                y[t] += s * (x[t] @ a[i].T @ b[i].T)
+    return y
+
+
+@pytest.mark.parametrize("T,latent,stream", [(1, True, BF16), (37, True, torch.float32),
+                                             (300, True, BF16), (700, True, torch.float32),
+                                             (20, False, BF16)])
+def test_block(moe, T, latent, stream):
+    w = wl.workload("tiny", name="block", T=T, H=512, L=256 if latent else 0, E=16, k=4, I=128,
+                    seed=9, norm_gain_std=0.1)
+    weights = device_weights(w, DEV)
+    g = torch.Generator().manual_seed(T)
+
+    def randn(*shape, std=1.0, dtype=BF16):
+        return (std * torch.randn(*shape, generator=g)).to(dtype).to(DEV)
+
+    H, L, n = w.H, 256, 3
+    adapters, ids = None, None
+    if latent:
+        adapters = {"lat_down": (randn(n, 16, H, std=0.03), randn(n, L, 16, std=0.1),
+                                 randn(n, std=1.0, dtype=torch.float32)),
+                    "lat_up": (randn(n, 8, L, std=0.05), randn(n, H, 8, std=0.1), None)}
+        ids = torch.randint(-1, n, (T,), generator=g).to(torch.int32).to(DEV)
+    gains = [(1.0 + randn(H, std=0.1, dtype=torch.float32)).to(BF16) for _ in range(3)]
+    gate = randn(H)
+    x = randn(T, H, std=2.0, dtype=stream)
+    block = moe.MoeBlock(weights, w.k, score="sigmoid", groups=4, topk_groups=2, route_scale=1.5,
+                         adapters=adapters, post_gain=gains[1], next_gain=gains[2], gate=gate,
+                         gate_sigmoid=True, residual_scale=0.5, eps=1e-6)
+    h = moe.rmsnorm(x.to(BF16), gains[0], 1e-6)
+    x2, h2 = block.forward(x, h, ids)
+    assert moe.check_error() == 0
+    assert x2.dtype == stream and h2.dtype == BF16
+
+    idx, wt = (t.cpu().numpy() for t in block.route(h))
+    assert all(len({int(e) // 4 for e in row}) <= 2 for row in idx)
+    h64 = h.double().cpu()
+    u = project(h64, weights["lat_down"], adapters["lat_down"], ids) if latent else h64
+    y = np.zeros(tuple(u.shape))
+    for e in sorted({int(e) for e in idx.ravel()}):
+        t, j = np.nonzero(idx == e)
+        y[t] += wt[t, j].astype(np.float64)[:, None] * \
+            O.expert_ffn(u.numpy()[t], oi.expert_arrays(w, e), 16)
+    y = torch.from_numpy(y)
+    if latent:
+        y = project(rms(y, weights["lat_norm"], 1e-6), weights["lat_up"], adapters["lat_up"], ids)
+    change = 0.5 * torch.sigmoid(gate.double().cpu()) * rms(y, gains[1], 1e-6)
+    x64 = x.double().cpu()
+    got = x2.double().cpu() - x64
+    # a bf16 stream rounds the sum, not the change: its rounding is taken out
+    slack = (2.0 ** -8 * (x64 + change).abs()).norm() if stream == BF16 else 0.0
+    err = (got - change).norm()
+    assert err <= 8e-3 * change.norm() + slack, (float(err), float(change.norm()))
+    assert rel_l2(h2.double().cpu(), rms(x64 + change, gains[2], 1e-6)) <= 8e-3
+    # in place, and the same bits again
+    x3 = x.clone()
+    same, h3 = block.forward(x3, h, ids, x_out=x3)
+    assert same is x3 and torch.equal(x3, x2) and torch.equal(h3, h2)
+
+
+def test_block_tokens_alone_are_the_batch(moe):
+    """Single-token calls (the decode kernels) agree with the batch's rows."""
+    T = 40
+    w = wl.workload("tiny", name="block", T=T, H=512, L=256, E=16, k=4, I=128, seed=9)
+    weights = device_weights(w, DEV)
+    g = torch.Generator().manual_seed(1)
+    a = (0.03 * torch.randn(2, 16, 512, generator=g)).to(BF16).to(DEV)
+    b = (0.1 * torch.randn(2, 256, 16, generator=g)).to(BF16).to(DEV)
+    gain = torch.ones(512, dtype=BF16, device=DEV)
+    block = moe.MoeBlock(weights, w.k, groups=4, topk_groups=2,
+                         adapters={"lat_down": (a, b, None)}, next_gain=gain)
+    x = torch.randn(T, 512, generator=g).to(DEV)
+    h = moe.rmsnorm(x.to(BF16), gain, 1e-6)
+    ids = (torch.arange(T) % 3 - 1).to(torch.int32).to(DEV)
+    x2, _ = block.forward(x, h, ids)
+    idx, _ = block.route(h)
+    for t in range(0, T, 7):
+        one, _ = block.forward(x[t:t + 1], h[t:t + 1], ids[t:t + 1])
+        if torch.equal(block.route(h[t:t + 1])[0], idx[t:t + 1]):
+            d1, d2 = one[0] - x[t], x2[t] - x[t]
+            assert float((d1 - d2).norm()) <= 8e-3 * float(d2.norm())
+    assert moe.check_error() == 0
