@@ -27,6 +27,7 @@
 //  - adapter_tile_kernel (adapter_tile.cu), many tokens: bound by the tensor
 //    cores; the low-rank term is R more columns of K for each adapter that
 //    occurs in an output tile's rows.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -43,7 +44,6 @@ namespace {
 
 constexpr int kMaxRank = 128;
 
-constexpr int kSpThreads = 256;  // warp 0: TMA, 1: MMA + TMEM, 4-7: TMEM -> smem; all: the sums
 constexpr int kSpTokens = 128;   // tokens to a block, at most
 constexpr int kSpWBytes = 128 * 64 * 2;
 constexpr int kSpMaxCluster = 8;
@@ -51,7 +51,6 @@ constexpr int kSpMaxCluster = 8;
 // Up to here the split kernel does the shrink itself: every output tile reads the
 // adapters' A again (T R of them in place of 128 rows of W a tile).
 constexpr int kFusedLow = 64;  // T R
-constexpr int kLowWarps = 6;   // warps 2-7
 
 constexpr int kBBytes = 64 * 1024;  // of B that a CTA fetches while W streams, at most
 
@@ -132,23 +131,34 @@ __device__ __forceinline__ void expand_token(const uint16_t* b, int rows, int R,
 
 }  // namespace
 
+// Warp 0: TMA, 1: MMA + TMEM, 4 and up: TMEM -> shared memory; all: the sums.  Up
+// to 64 tokens 8 warps, beside which an SM holds a CTA of the shrink; 16 for more.
 // FUSED: the low-rank vectors too (T R <= kFusedLow, one block of tokens).  B of
 // the tokens is fetched into shared memory while W streams: a read of global
 // memory at the end costs 1 us and more a token, measured.
 // Cluster (x = rank, y, z): rows 128 y of W, tokens tb z; rank j takes the
 // K steps [j n / cluster, (j + 1) n / cluster) of n = ceil(K / 64).
-template <bool FUSED>
-__global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
+template <bool FUSED, int THREADS>
+__global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
     adapter_split_kernel(const __grid_constant__ CUtensorMap mw,
                          const __grid_constant__ CUtensorMap mx, const AdapterArgs a,
                          const SplitShape sh, int* status, long long wait_ns) {
+  constexpr int kSpThreads = THREADS;
+  constexpr int kLowWarps = THREADS / 32 - 2;  // warps 2 and up
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full[8], empty[8], done, bfull[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int cta_abort;
-  __shared__ int32_t ids[kSpTokens];  // of this rank's tokens
+  // The block's tokens in the order of their adapters; each rank takes a stretch of
+  // it, so that tokens that share an adapter share the copy of its B: slot j holds
+  // adapter slot_id[j], and local token j (order[p0 + j]) uses slot slot_of[j]
+  // (slot_first[s]: the first that uses slot s).
+  __shared__ __align__(16) int32_t ids[kSpTokens];
+  __shared__ int16_t order[kSpTokens], slot_of[kSpTokens], slot_first[kSpTokens];
+  __shared__ int32_t slot_id[kSpTokens];
+  __shared__ int slots;
   __shared__ float lowp[kLowWarps + 1][kFusedLow];  // FUSED: the warps' sums, and the CTA's
   __shared__ __align__(16) uint16_t lowv[2 * kFusedLow];  // FUSED: as lows below
   __shared__ __align__(16) float lowout[kSpThreads / 32][128];  // a token's low-rank term
@@ -164,12 +174,14 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
   const int ranks = gridDim.x, rank = blockIdx.x;
   const int n0 = blockIdx.y * 128, t0 = blockIdx.z * tb;
   const int tokens = min(tb, a.T - t0);
-  const int mine = (tokens - rank + ranks - 1) / ranks;  // tokens rank, rank + ranks, ...
-  const int rows = min(128, a.N - n0);                   // N % 8 == 0
+  const int p0 = tokens * rank / ranks;
+  const int mine = tokens * (rank + 1) / ranks - p0;  // tokens of this rank
+  const int rows = min(128, a.N - n0);                // N % 8 == 0
   if (FUSED) grid_wait();
   grid_launch_dependents();
-  for (int j = threadIdx.x; j < mine; j += kSpThreads)
-    ids[j] = checked_id(a.ids[t0 + j * ranks + rank], a.adapters);
+  if (threadIdx.x < kSpTokens)
+    ids[threadIdx.x] =
+        threadIdx.x < tokens ? checked_id(a.ids[t0 + threadIdx.x], a.adapters) : INT_MAX;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -192,21 +204,17 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
   const uint32_t tbase = tmem_slot;
   const int steps = (a.K + 63) / 64;
   const int s0 = steps * rank / ranks, s1 = steps * (rank + 1) / ranks;
-  // B of the tokens of wave w (one thread): bulk copies of whole [rows][R] blocks
-  const int waves = (mine + sh.wave - 1) / sh.wave;
+  // B of the slots of wave w (one thread): bulk copies of whole [rows][R] blocks
   const uint32_t block = static_cast<uint32_t>(rows) * a.R * 2;
   auto fetch_wave = [&](int w) {
-    if (w >= waves) return;
+    const int j0 = w * sh.wave, j1 = min(slots, j0 + sh.wave);
+    if (j0 >= j1) return;
     uint64_t* bar = &bfull[w & 1];
     uint8_t* buf = smem + (w & 1 ? sh.buf1 : sh.buf0);
-    const int j0 = w * sh.wave, j1 = min(mine, j0 + sh.wave);
-    uint32_t bytes = 0;
-    for (int j = j0; j < j1; ++j) bytes += ids[j] >= 0 ? block : 0u;
-    mbar_arrive_expect_tx(bar, bytes);
+    mbar_arrive_expect_tx(bar, (j1 - j0) * block);
     for (int j = j0; j < j1; ++j)
-      if (ids[j] >= 0)
-        bulk_g2s(buf + (j - j0) * 256 * a.R, a.b + (static_cast<size_t>(ids[j]) * a.N + n0) * a.R,
-                 block, bar);
+      bulk_g2s(buf + (j - j0) * 256 * a.R,
+               a.b + (static_cast<size_t>(slot_id[j]) * a.N + n0) * a.R, block, bar);
   };
 
   if (warp == 0) {
@@ -240,8 +248,40 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
     umma_commit_warp(&done);
     mbar_drain(&done, 0, status);
   } else {
-    if (warp == 2 && lane == 0) fetch_wave(0);
-    __syncwarp();
+    // sort the tokens: one counts the others before it
+    const int i = threadIdx.x - 64;
+    if (i < tokens) {
+      const int id = ids[i];
+      int p = 0;
+      for (int j = 0; j < tokens; j += 4) {  // beyond the last: INT_MAX
+        const int4 o = *reinterpret_cast<const int4*>(&ids[j]);
+        const int v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p += v[q] < id || (v[q] == id && j + q < i) ? 1 : 0;
+      }
+      order[p] = static_cast<int16_t>(i);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS - 64) : "memory");
+    if (warp == 2) {
+      int n = 0;
+      for (int j0 = 0; j0 < mine; j0 += 32) {
+        const int j = j0 + lane;
+        const int id = j < mine ? ids[order[p0 + j]] : -1;
+        const bool lead = id >= 0 && (j == 0 || ids[order[p0 + j - 1]] != id);
+        const uint32_t m = __ballot_sync(0xffffffffu, lead);
+        const int at = n + __popc(m & (0xffffffffu >> (31 - lane))) - 1;
+        if (lead) {
+          slot_id[at] = id;
+          slot_first[at] = static_cast<int16_t>(j);
+        }
+        if (j < mine) slot_of[j] = static_cast<int16_t>(id >= 0 ? at : -1);
+        n += __popc(m);
+      }
+      if (lane == 0) slots = n;
+      __syncwarp();
+      if (lane == 0) fetch_wave(0);
+      __syncwarp();
+    }
     if (FUSED) {
       // this rank's columns, dealt to the warps in whole 32-column steps
       const int k0 = s0 * 2, k1 = min(s1 * 2, a.K / 32);
@@ -272,8 +312,8 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
   // this rank's low-rank vectors as bf16 hi and lo parts: [token][2][R]
   uint16_t* lows = FUSED ? lowv : reinterpret_cast<uint16_t*>(red + tb * 128);
   if (warp >= 4) {
-    const int q = warp & 3;
-    for (int c0 = 0; c0 < tb; c0 += 16) {
+    const int q = warp & 3;  // lane quarter; 16 tokens in turn
+    for (int c0 = 16 * ((warp >> 2) - 1); c0 < tb; c0 += 4 * (kSpThreads / 32 - 4)) {
       uint32_t r[16];
       tmem_ld16(tbase + (static_cast<uint32_t>(32 * q) << 16) + c0, r);
       tmem_ld_wait();
@@ -315,10 +355,11 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
     // wait for its own)
     grid_wait();
     const int quads = a.R / 4;
-    for (int i = threadIdx.x; i < (tokens - rank + ranks - 1) / ranks * quads; i += kSpThreads) {
+    for (int i = threadIdx.x; i < mine * quads; i += kSpThreads) {
       const int j = i / quads, e = i % quads * 4;
+      if (slot_of[j] < 0) continue;
       const float4 v = *reinterpret_cast<const float4*>(
-          a.low + static_cast<size_t>(t0 + j * ranks + rank) * a.R + e);
+          a.low + static_cast<size_t>(t0 + order[p0 + j]) * a.R + e);
       uint32_t h[4], l[4];
       split_bf16(v.x, h[0], l[0]);
       split_bf16(v.y, h[1], l[1]);
@@ -330,24 +371,28 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
     }
     __syncthreads();
   }
-  // token by token: rank r takes tokens r, r + ranks, ... in turn with its
-  // warps; a lane sums four columns over the cluster, in the order of the ranks
+  // token by token, each by a warp: a lane sums four columns over the cluster, in
+  // the order of the ranks.  Wave w: the tokens of its slots (the first also those
+  // without an adapter)
   const int n = n0 + 4 * lane;
   const bool on = n < a.N;  // N % 8 == 0: all four columns or none
+  const int waves = max(1, (slots + sh.wave - 1) / sh.wave);
+  int j0 = 0;
   for (int w = 0; w < waves; ++w) {
-    const int j0 = w * sh.wave, j1 = min(mine, j0 + sh.wave);
+    const int j1 = (w + 1) * sh.wave < slots ? slot_first[(w + 1) * sh.wave] : mine;
     const uint8_t* buf = smem + (w & 1 ? sh.buf1 : sh.buf0);
     // (not a wait that gives up with the CTA: the copies are in flight)
-    mbar_drain(&bfull[w & 1], (w >> 1) & 1u, status);
+    if (slots > 0) mbar_drain(&bfull[w & 1], (w >> 1) & 1u, status);
     for (int j = j0 + warp; j < j1; j += kSpThreads / 32) {
-      const int i = j * ranks + rank, id = ids[j];
+      const int i = order[p0 + j], slot = slot_of[j];
       float4 o[kSpMaxCluster];
 #pragma unroll
       for (int r = 0; r < kSpMaxCluster; ++r)
         if (r < ranks) o[r] = ld_cluster_f4(mapa_shared(red + i * 128 + 4 * lane, r));
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (id >= 0) {
-        expand_token(reinterpret_cast<const uint16_t*>(buf + (j - j0) * 256 * a.R), rows, a.R,
+      if (slot >= 0) {
+        expand_token(reinterpret_cast<const uint16_t*>(buf + (slot - w * sh.wave) * 256 * a.R),
+                     rows, a.R,
                      lows + (FUSED ? i : j) * 2 * a.R, lowout[warp]);
         s = *reinterpret_cast<const float4*>(&lowout[warp][4 * lane]);
         __syncwarp();  // read before the next token's are written
@@ -367,6 +412,7 @@ __global__ void __launch_bounds__(kSpThreads, FUSED ? 1 : 2)
         *reinterpret_cast<uint2*>(a.y + static_cast<size_t>(t0 + i) * a.N + n) = q;
       }
     }
+    j0 = j1;
     if (w + 2 < waves) {  // the wave's buffer takes the one after next
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
@@ -457,16 +503,16 @@ SplitShape split_shape(int T, int R, int cluster) {
   return s;
 }
 
-template <bool FUSED>
+template <bool FUSED, int THREADS>
 int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
-  auto kern = adapter_split_kernel<FUSED>;
+  auto kern = adapter_split_kernel<FUSED, THREADS>;
   // at most one CTA to an SM (a second one on some would take twice the time),
   // and as many clusters as the device holds at once
   const int tiles = split_tiles(a.T, a.N);
   const int most = std::min({kSpMaxCluster, std::max(1, num_sms() / tiles), (a.K + 63) / 64});
   SplitShape sh = split_shape(a.T, a.R, most);
   MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern), static_cast<int>(sh.smem)));
-  const int held = adapter_cluster(reinterpret_cast<const void*>(kern), kSpThreads,
+  const int held = adapter_cluster(reinterpret_cast<const void*>(kern), THREADS,
                                    static_cast<int>(sh.smem), tiles, most);
   if (held < most) {  // fewer ranks, more tokens to each
     sh = split_shape(a.T, a.R, held);
@@ -477,7 +523,7 @@ int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
     return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(sh.cluster, (a.N + 127) / 128, (a.T + sh.tb - 1) / sh.tb);
-  cfg.blockDim = dim3(kSpThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = sh.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -532,8 +578,9 @@ extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const ui
   a.low = static_cast<float*>(ws);
   a.y = y;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (fused(T, R)) return launch_split<true>(a, status, st);
+  if (fused(T, R)) return launch_split<true, 256>(a, status, st);
   const int rc = launch_adapter_shrink(a, status, st);
   if (rc) return rc;
-  return T > kSplitTokens ? launch_adapter_tile(a, status, st) : launch_split<false>(a, status, st);
+  if (T > kSplitTokens) return launch_adapter_tile(a, status, st);
+  return T <= 64 ? launch_split<false, 256>(a, status, st) : launch_split<false, 512>(a, status, st);
 }

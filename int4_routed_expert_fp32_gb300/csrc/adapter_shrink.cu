@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(kStThreads, 1)
     for (int p = lane; p < u.count[j]; p += 32) of_row[u.row[u.at[j] + p] & 0xff] = j;
   __syncthreads();
 
-  const int per = s.per, stages = s.stages;
+  // the tile's adapters in even shares
+  const int per = max(1, min(s.per, (n + static_cast<int>(gridDim.z) - 1) / static_cast<int>(gridDim.z)));
+  const int stages = s.stages;
   const int passes = (n + per - 1) / per;
   // a slot: A, then x.  The MMA's M side is 128 rows all the same: with fewer rows
   // of x it goes on into what follows (the sums, after the last slot), whose
@@ -303,11 +305,11 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
   const int tiles = (s.T + kAdTile - 1) / kAdTile, rows = std::min(s.T, kAdTile);
   const int steps = (s.K + 63) / 64;
   // Many tokens: one cluster to a tile, all the columns a pass can have.  Few:
-  // adapters dealt to clusters, some 128 CTAs in all if every token has its own.
+  // adapters dealt to clusters, some 150 CTAs in all if every token has its own.
   int groups = 1;
   s.per = kStMaxCols / s.R;
   if (s.T <= kSplitTokens) {
-    const int want = std::min(rows, 16 / tiles);
+    const int want = std::min(rows, std::max(1, num_sms() / (kShMaxCluster * tiles)));
     s.per = std::min(s.per, (rows + want - 1) / want);
     groups = std::min(want, (rows + s.per - 1) / s.per);
   }
