@@ -52,7 +52,6 @@ constexpr int kSpMaxCluster = 8;
 // adapters' A again (T R of them in place of 128 rows of W a tile).
 constexpr int kFusedLow = 64;  // T R
 
-constexpr int kBBytes = 64 * 1024;  // of B that a CTA fetches while W streams, at most
 
 bool fused(int T, int R) { return T <= 8 && T * R <= kFusedLow; }
 
@@ -131,8 +130,8 @@ __device__ __forceinline__ void expand_token(const uint16_t* b, int rows, int R,
 
 }  // namespace
 
-// Warp 0: TMA, 1: MMA + TMEM, 4 and up: TMEM -> shared memory; all: the sums.  Up
-// to 64 tokens 8 warps, beside which an SM holds a CTA of the shrink; 16 for more.
+// Warp 0: TMA, 1: MMA + TMEM, 4 and up: TMEM -> shared memory; all: the sums.  8
+// warps where an SM is to hold a CTA of the shrink beside them, 16 elsewhere.
 // FUSED: the low-rank vectors too (T R <= kFusedLow, one block of tokens).  B of
 // the tokens is fetched into shared memory while W streams: a read of global
 // memory at the end costs 1 us and more a token, measured.
@@ -472,14 +471,13 @@ int split_tiles(int T, int N) {
 
 SplitShape split_shape(int T, int R, int cluster) {
   SplitShape s;
+  const bool beside = adapter_beside(T, R);
   const int blocks = (T + kSpTokens - 1) / kSpTokens;
   s.tb = ((T + blocks - 1) / blocks + 15) / 16 * 16;
   s.cluster = cluster;
   const int stage = kSpWBytes + s.tb * 128;
-  // up to 64 tokens ~92 KiB in flight an SM; more: with room for two CTAs of the
-  // shrink, which an SM still holds when this kernel starts
-  const int budget = s.tb <= 64 ? 104 * 1024 : 132 * 1024;
-  s.stages = std::min(8, budget / stage);
+  // ~92 KiB in flight an SM, and of B what leaves room for a CTA of the shrink
+  s.stages = std::min(8, (beside ? 104 : 132) * 1024 / stage);
   s.cols = 32;
   while (s.cols < static_cast<uint32_t>(s.tb)) s.cols *= 2;
   // the ring, and in its place the fp32 tile and the rank's low-rank vectors
@@ -489,14 +487,14 @@ SplitShape split_shape(int T, int R, int cluster) {
   // B: a buffer of its own; the second in what the tail leaves of the ring, if
   // it takes a token, else in the first one's upper half
   const int token = 256 * R;
-  const int bytes = std::min(kBBytes, most * token);
+  const int bytes = std::min(std::max(beside && T > 64 ? 32 * 1024 : 64 * 1024, 2 * token), most * token);
   const int fit = bytes / token, rest = (ring - tail) / token;
   s.buf0 = ring;
   if (fit >= most || rest >= 1) {
     s.wave = fit >= most ? most : std::min(fit, rest);
     s.buf1 = tail;
   } else {
-    s.wave = fit / 2;  // kBBytes takes two tokens of the largest rank
+    s.wave = fit / 2;  // at least two tokens fit
     s.buf1 = ring + s.wave * token;
   }
   s.smem = static_cast<size_t>(ring) + bytes + 1024;
@@ -582,5 +580,6 @@ extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const ui
   const int rc = launch_adapter_shrink(a, status, st);
   if (rc) return rc;
   if (T > kSplitTokens) return launch_adapter_tile(a, status, st);
-  return T <= 64 ? launch_split<false, 256>(a, status, st) : launch_split<false, 512>(a, status, st);
+  return adapter_beside(T, R) ? launch_split<false, 256>(a, status, st)
+                              : launch_split<false, 512>(a, status, st);
 }

@@ -23,6 +23,13 @@ struct AdapterArgs {
 
 constexpr int kSplitTokens = 256;  // up to here adapter_split_kernel
 
+// Whether the two kernels of a call with few tokens are laid out to share the SMs
+// (T <= kSplitTokens).  Low-rank work that is small beside W: 128 tokens of rank
+// 32 with an adapter each take 30 us so and 34 one after the other, 256 of rank 16
+// 38 and 50; 256 of rank 32 43 and 38, 128 of rank 64 58 and 45 (K 7168, N 2048 or
+// 3584), because little shared memory means few adapters to a pass over x.
+inline bool adapter_beside(int T, int R) { return T <= 64 || T * R <= 4096; }
+
 // low from x, a and scale (adapter_shrink.cu).  Triggers its dependents at once.
 int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st);
 

@@ -321,11 +321,12 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
   const int fixed = std::max(s.xrows * s.R * 4, (kAdTile - s.xrows) * 128) + 1024;
   auto slot = [&](int per) { return (per * s.R + 15) / 16 * 2048 + s.xrows * 128; };
   auto slots = [&](int per, int bytes) { return (bytes - fixed) / slot(per); };
-  constexpr int kBeside = 50 * 1024, kAlone = 198 * 1024;
-  const int beside = slots(s.per, kBeside) >= 2 ? s.per : (s.per + 1) / 2;
-  if (s.T <= 64 && slots(beside, kBeside) >= 2) {
+  const int room = s.T <= 64 ? 50 * 1024 : 84 * 1024;
+  constexpr int kAlone = 198 * 1024;
+  const int beside = slots(s.per, room) >= 2 ? s.per : (s.per + 1) / 2;
+  if (s.T <= kSplitTokens && adapter_beside(s.T, s.R) && slots(beside, room) >= 2) {
     s.per = beside;
-    s.stages = slots(s.per, kBeside);
+    s.stages = slots(s.per, room);
   } else {
     s.stages = std::max(2, slots(s.per, kAlone));
   }
