@@ -98,9 +98,10 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Whether a word of two bf16 holds an infinity or NaN.
+// Bits 15 and 31 tell whether the low or high bf16 of a word is an infinity or NaN:
+// an exponent of all ones carries into them (the others stay below).
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  return __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u);
+  return (w & 0x7f807f80u) + 0x00800080u;
 }
 
 // A tile's adapters, double buffered by tile parity: written by warps 6-9, read
@@ -138,7 +139,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full[kTlStages];   // rank 0: both CTAs' copies and A warps
   __shared__ __align__(8) uint64_t sfree[kTlStages];  // the stage's MMAs are done
-  __shared__ __align__(8) uint64_t bland[kTlStages];  // this CTA's half of a low-rank B
+  __shared__ __align__(8) uint64_t sgo[kTlStages];    // a low-rank stage's slot is free
+  __shared__ __align__(8) uint64_t bland[kTlStages];  // and its B (this CTA's half) there
   __shared__ __align__(8) uint64_t accfull[2], accempty[2], listfull[2], listempty[2], mma_done;
   __shared__ uint32_t tmem_slot;
   __shared__ int cta_abort;
@@ -152,6 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
     for (int s = 0; s < kTlStages; ++s) {
       mbar_init(&full[s], 9);  // rank 0's producer, and four A warps of each CTA
       mbar_init(&sfree[s], 1);
+      mbar_init(&sgo[s], 1);
       mbar_init(&bland[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -220,6 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
             break;
           }
           const int blk = e / (l.n * parts), d = e / parts % l.n;
+          mbar_arrive(&sgo[s]);
           mbar_arrive_expect_tx(&bland[s], S::kBBytes);
           tma_g2s_3d(smem + s * S::kStageBytes + kTlABytes, &mb, &bland[s], 64 * blk, n0,
                      l.adapter[d]);
@@ -357,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
     // --------------------------- the tile's adapters and the low-rank A operand
     const int i = threadIdx.x - 32 * kFillWarp0;  // row of this CTA
     const uint32_t leader_full = mapa_shared(full, 0);
-    uint32_t it = 0, uc = 0, bpar = 0;  // bpar: parity of bland[s], bit s
+    uint32_t it = 0, uc = 0, gpar = 0, bpar = 0;  // parities of sgo[s] and bland[s], bit s
     bool ok = true;
     grid_wait();  // the low-rank vectors are complete
     for (int t = pair; t < tiles; t += pairs, ++uc) {
@@ -420,6 +424,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
       const int n = l.n;
       const int row = m0 + static_cast<int>(rank) * 128 + i;
       it += ksteps;
+      // Looks over the B of slot s and hands the stage to the MMA warp.
+      auto finish = [&](int s, int d) {
+        const bool got = mbar_wait(&bland[s], (bpar >> s) & 1u, wt);
+        bpar ^= 1u << s;
+        if (!__all_sync(0xffffffffu, got)) return false;
+        uint8_t* B = smem + s * S::kStageBytes + kTlABytes;
+        if (i < S::kBRows) {
+          uint32_t odd = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(B + i * 128 + ((c ^ (i & 7)) << 4));
+            odd |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
+          }
+          if (odd & 0x80008000u) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(B + i * 128 + (c << 4)) = make_uint4(0, 0, 0, 0);
+            for (uint32_t to = 0; to < 2; ++to)
+              asm volatile("st.relaxed.cluster.shared::cluster.u16 [%0], %1;" ::"r"(
+                               mapa_shared(&bad[uc % kBadRing][d], to)),
+                           "h"(static_cast<uint16_t>(uc + 1))
+                           : "memory");
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          }
+        }
+        fence_async_smem();  // this row of A and of B, for the MMAs
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(leader_full + 8u * s);
+        return true;
+      };
+      int last = -1, last_d = 0;  // the stage whose A is written and B not yet seen
       for (int blk = 0; blk < blocks && ok; ++blk) {
         // this row's vector: hi and lo of columns 64 blk .. (or all, R <= 32)
         constexpr int kWords = WIDE ? 32 : 16;
@@ -441,58 +476,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
           hi[j + 1] = h0 | (h1 << 16);
           lo[j + 1] = l0 | (l1 << 16);
         }
-        for (int d = 0; d < n && ok; ++d) {
-          for (int part = 0; part < parts; ++part, ++it) {
-            const int s = it % kTlStages;
-            const bool got = mbar_wait(&bland[s], (bpar >> s) & 1u, wt);
-            bpar ^= 1u << s;
-            if (!__all_sync(0xffffffffu, got)) {
-              ok = false;
-              break;
-            }
-            uint8_t* A = smem + s * S::kStageBytes;
-            uint8_t* B = A + kTlABytes;
-            // 16-byte chunk c of row i sits at chunk c ^ (i & 7)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (d == my_d) {
-                if constexpr (WIDE) {
-                  v = part == 0 ? make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3])
-                                : make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-                } else {
-                  const int e = 4 * (c & 3);
-                  v = c < 4 ? make_uint4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3])
-                            : make_uint4(lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
-                }
-              }
-              *reinterpret_cast<uint4*>(A + i * 128 + ((c ^ (i & 7)) << 4)) = v;
-            }
-            if (i < S::kBRows) {
-              uint32_t odd = 0;
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4*>(B + i * 128 + ((c ^ (i & 7)) << 4));
-                odd |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
-              }
-              if (odd) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(B + i * 128 + (c << 4)) = make_uint4(0, 0, 0, 0);
-                for (uint32_t to = 0; to < 2; ++to)
-                  asm volatile("st.relaxed.cluster.shared::cluster.u16 [%0], %1;" ::"r"(
-                                   mapa_shared(&bad[uc % kBadRing][d], to)),
-                               "h"(static_cast<uint16_t>(uc + 1))
-                               : "memory");
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-              }
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(leader_full + 8u * s);
+        for (int e = 0; e < n * parts && ok; ++e, ++it) {
+          const int d = e / parts, part = e % parts;
+          const int s = it % kTlStages;
+          const bool got = mbar_wait(&sgo[s], (gpar >> s) & 1u, wt);
+          gpar ^= 1u << s;
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
           }
+          uint8_t* A = smem + s * S::kStageBytes;
+          // 16-byte chunk c of row i sits at chunk c ^ (i & 7)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (d == my_d) {
+              if constexpr (WIDE) {
+                v = part == 0 ? make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3])
+                              : make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+              } else {
+                const int q = 4 * (c & 3);
+                v = c < 4 ? make_uint4(hi[q], hi[q + 1], hi[q + 2], hi[q + 3])
+                          : make_uint4(lo[q], lo[q + 1], lo[q + 2], lo[q + 3]);
+              }
+            }
+            *reinterpret_cast<uint4*>(A + i * 128 + ((c ^ (i & 7)) << 4)) = v;
+          }
+          // the stage before, whose B has had this long to arrive
+          if (last >= 0) ok = finish(last, last_d);
+          last = s;
+          last_d = d;
         }
       }
+      if (ok && last >= 0) ok = finish(last, last_d);
     }
   }
   // every MMA is done before rank 0 arrives, every copy landed and every
