@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
         if (lo > -INFINITY) score = hi + lo;
       } else {  // the order of the logits gave the two; their scores are summed
         score = fast_score(hi) + (lo > -INFINITY ? fast_score(lo) : 0.f);
-        slack = 2.f * kSlackPair * score;
+        slack = 2.f * kSlackPair * score + 1e-37f;  // and what is below fp32's range
       }
     }
     if constexpr (BIAS)

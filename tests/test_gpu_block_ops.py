@@ -397,3 +397,13 @@ def test_route_few_lanes_hold_the_kept_groups(moe, E, k, groups, kept, biased, s
     for group_score in ("top2", "max"):
         check_route(moe, z, k, ranking_bias(E, 3) if biased else None, score=score,
                     groups=groups, topk_groups=kept, group_score=group_score)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("E,k,groups,kept", [(64, 4, 8, 3), (384, 8, 8, 4), (700, 6, 7, 2)])
+def test_route_groups_of_scores_below_fp32(moe, E, k, groups, kept, dtype):
+    """Sigmoid scores that all are below the smallest normal fp32 value: the
+    groups' order is still that of their 64-bit sums."""
+    for top in (-80.0, -89.0, -105.0, -200.0):
+        z = top - logits(12, E, E + k).abs().to(dtype) * 4
+        check_route(moe, z.to(dtype).contiguous(), k, groups=groups, topk_groups=kept)
