@@ -73,6 +73,19 @@ __device__ __forceinline__ float key_value(uint32_t o) {
   return __uint_as_float(o ^ (static_cast<uint32_t>(~(static_cast<int32_t>(o) >> 31)) | 0x80000000u));
 }
 
+// e^x and 1 / y of the fast keys, whose values below fp32's normal range are 0.
+__device__ __forceinline__ float fast_exp(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.44269504f));
+  return e;
+}
+
+__device__ __forceinline__ float fast_rcp(float y) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+
 __device__ __forceinline__ float clean(float z) {  // NaN -> -inf, -0 -> +0
   return fmaxf(z, -INFINITY) + 0.0f;
 }
@@ -120,6 +133,48 @@ __device__ __forceinline__ float exp_diff(float a, float b) {
   const float lost = (a - (d - back)) - (b + back);
   const float e = expf(d);
   return fmaf(e, lost, e);
+}
+
+// a + b = hi + lo, hi rounded to nearest.
+__device__ __forceinline__ float two_sum(float a, float b, float& lo) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  lo = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  return s;
+}
+
+// The key 1 / (1 + e^-z) + b as hi + lo within 1e-9: e^-|z| = 2^n e^r with the
+// linear and quadratic terms of e^r as pairs and those above (at most 0.008) in
+// fp32.  hi is the rounded sum, so that (hi, lo) compare in this order.
+__device__ __forceinline__ float fine_key(float z, float b, float& low) {
+  const float x = fmaxf(-fabsf(z), -80.f);
+  const float n = rintf(x * 1.44269504f);
+  // ln 2 = 11357 / 2^14 + c: the first product and difference are exact
+  float r0, e0, t0, d0;
+  const float r = two_sum(fmaf(-n, 0.69317626953125f, x), n * 2.90889713e-05f, r0);
+  const float q = r * r, q0 = fmaf(r, r, -q);
+  float tail = fmaf(r, 1.f / 40320.f, 1.f / 5040.f);
+  tail = fmaf(r, tail, 1.f / 720.f);
+  tail = fmaf(r, tail, 1.f / 120.f);
+  tail = fmaf(r, tail, 1.f / 24.f);
+  tail = r * q * fmaf(r, tail, 1.f / 6.f);
+  const float t = two_sum(two_sum(1.f, r, e0), 0.5f * q, t0);
+  t0 = (e0 + t0) + fmaf(r0, 1.f + r, 0.5f * q0) + tail;
+  const float scale = exp2f(n);
+  const float e = scale * two_sum(t, t0, e0);
+  e0 *= scale;
+  // 1 / (1 + e), or e / (1 + e) for z < 0
+  const float d = two_sum(1.f, e, d0);
+  d0 += e0;
+  const float inv = fast_rcp(d);
+  const float num = z < 0.f ? e : 1.f, num0 = z < 0.f ? e0 : 0.f;
+  const float s = num * inv;
+  const float s0 = inv * (fmaf(-s, d, num) + fmaf(-s, d0, num0));
+  const float c = two_sum(s, b, low);
+  if (!(fabsf(c) < INFINITY)) {
+    low = 0.f;
+    return c;
+  }
+  return two_sum(c, low + s0, low);
 }
 
 // Softmax denominator in 64 bits (warp-wide, rare).
@@ -390,12 +445,16 @@ __device__ __noinline__ float weight_far(const SelectArgs& a, float zz, float m,
 // Softmax: p |z - m| <= 0.37 likewise, but the denominator of up to 2048
 // terms adds a relative 1e-6.
 constexpr float kSlackSigmoid = 4e-7f, kSlackSoftmax = 2e-6f, kSlackStep = 1.3e-7f;
+// What two keys of fine_key leave open (and what 64 bits do, for large biases).
+constexpr float kFineNear = 4e-9f;
 // Relative error of a sum of two unbiased scores, |z - m| up to 90.
-constexpr float kSlackPair = 1.2e-5f;
+constexpr float kSlackPair = 1.4e-5f;
 
 template <typename ZT, int NPL, bool SOFTMAX, bool BIAS>
-__global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(const __grid_constant__ SelectArgs a) {
   extern __shared__ __align__(16) uint8_t rs_smem[];
+  __shared__ __align__(16) uint32_t ranked[8][32];
+  __shared__ float fine[BIAS && !SOFTMAX ? 8 : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= a.T) return;
@@ -459,23 +518,29 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      sum += Z(i) == -INFINITY ? 0.f : (Z(i) == m ? 1.f : __expf(Z(i) - m));
+      sum += Z(i) == -INFINITY ? 0.f : (Z(i) == m ? 1.f : fast_exp(Z(i) - m));
     sum = warp_sum(sum);
     if (sum == 0.f) sum = 1.f;  // no expert available: every score is 0
   }
+  const float inv_sum = SOFTMAX ? 1.f / sum : 1.f;
   auto fast_score = [&](float v) {
     if constexpr (SOFTMAX)
-      return v == -INFINITY ? 0.f : (v == m ? 1.f : __expf(v - m)) * __fdividef(1.f, sum);
+      return v == -INFINITY ? 0.f : (v == m ? 1.f : fast_exp(v - m)) * inv_sum;
     else
-      return __fdividef(1.f, 1.f + __expf(-v));
+      return fast_rcp(1.f + fast_exp(-v));
+  };
+  // of an expert's logit and bias (a sum of a score and a bias is never -0)
+  auto fast_key = [&](float z, float b) {
+    if constexpr (BIAS) {
+      const float c = fmaxf(fast_score(z) + b, -INFINITY);
+      return order_key(z == -INFINITY ? -INFINITY : c);
+    }
+    return order_key(z);
   };
 
   // ---- keys
   if constexpr (BIAS) {
-    auto key = [&](int i, float b) {
-      const float c = fast_score(Z(i)) + b;
-      O(i) = order_key(Z(i) == -INFINITY ? -INFINITY : clean(c));
-    };
+    auto key = [&](int i, float b) { O(i) = fast_key(Z(i), b); };
     if (a.vec_bias) {
 #pragma unroll
       for (int i = 0; i < NI; i += 4) {
@@ -492,7 +557,7 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) O(i) = order_key(Z(i));
+    for (int i = 0; i < NI; ++i) O(i) = fast_key(Z(i), 0.f);
   }
   if (!a.full) {
 #pragma unroll
@@ -501,6 +566,7 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
   }
 
   // ---- groups
+  uint32_t mx = kAbsent;
   if (a.tg < a.G) {
     uint32_t uh = kAbsent, ul = kAbsent;
 #pragma unroll
@@ -578,12 +644,13 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
 #pragma unroll
       for (int i = 0; i < NI; ++i) O(i) = kAbsent;
     }
+    mx = kept ? uh : kAbsent;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) mx = max(mx, O(i));
   }
 
   // ---- candidates: at or above the k-th largest lane maximum
-  uint32_t mx = kAbsent;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) mx = max(mx, O(i));
   uint32_t thr = 0;
   if (a.k <= 12) {
     // the k-th largest distinct maximum (equal ones leave together): a bound
@@ -616,73 +683,112 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
     }
     return k;
   };
-  auto at_or_above = [&](uint32_t k) {
-    int c = 0;
+  auto at_or_above = [&](uint32_t k) {  // in registers: one bit each
+    uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) c += O(i) >= k ? 1 : 0;
+    for (int i = 0; i < NI; ++i)
+      if (O(i) >= k) c += REG ? 1u << i : 1u;
     return c;
   };
-  int mine = at_or_above(with_slack(thr));
-  int n = __reduce_add_sync(0xffffffffu, mine);
+  auto count = [](uint32_t c) { return REG ? __popc(c) : static_cast<int>(c); };
+  uint32_t mine = at_or_above(with_slack(thr));
+  int n = __reduce_add_sync(0xffffffffu, count(mine));
   if (n > 32) {
     // the bound is weak where few lanes hold the kept groups or k is near 32:
     // halve the range of keys until k to 32 experts are left
     uint32_t above = __reduce_max_sync(0xffffffffu, mx);  // fewer than k lie above it
     while (thr < above) {
       const uint32_t mid = thr + (above - thr + 1) / 2;
-      if (__reduce_add_sync(0xffffffffu, at_or_above(mid)) < a.k) {
+      if (__reduce_add_sync(0xffffffffu, count(at_or_above(mid))) < a.k) {
         above = mid - 1;
         continue;
       }
       thr = mid;
       mine = at_or_above(with_slack(thr));
-      n = __reduce_add_sync(0xffffffffu, mine);
+      n = __reduce_add_sync(0xffffffffu, count(mine));
       if (n <= 32) break;
     }
   }
-  thr = with_slack(thr);
-  int pos = mine;
+  int pos = count(mine);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, pos, d);
     if (lane >= d) pos += v;
   }
-  pos -= mine;
-  uint32_t* ckey32 = reinterpret_cast<uint32_t*>(ckey);
-  const bool fit = n <= 32;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    if (O(i) >= thr) {
-      if (fit) ckey32[pos] = O(i);
-      cid[pos] = static_cast<uint16_t>(base + i);
-      ++pos;
-    }
+  pos -= count(mine);
+  if constexpr (REG) {
+    for (; mine; mine &= mine - 1) cid[pos++] = static_cast<uint16_t>(base + __ffs(mine) - 1);
+  } else {
+    thr = with_slack(thr);
+    for (int i = 0; i < NI; ++i)
+      if (O(i) >= thr) cid[pos++] = static_cast<uint16_t>(base + i);
   }
   __syncwarp();
 
   int my_id = -1, rank = 32;
-  if (fit) {
+  float my_z = -INFINITY, my_b = 0.f;
+  if (n <= 32) {
     // one candidate to a lane, in id order; ranked against the others
     uint32_t key = 0;
     if (lane < n) {
-      key = ckey32[lane];
       my_id = cid[lane];
+      my_z = logit(a, row, my_id);
+      if constexpr (BIAS) my_b = a.bias[my_id];
+      key = fast_key(my_z, my_b);
     }
+    uint32_t* keys = ranked[warp];
+    keys[lane] = key;
+    __syncwarp();
     rank = 0;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t other = __shfl_sync(0xffffffffu, key, j);
-      rank += other > key || (other == key && j < lane) ? 1 : 0;
+    for (int j = 0; j < n; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&keys[j]);  // 0 after the last
+      const uint32_t other[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        rank += other[q] > key || (other[q] == key && j + q < lane) ? 1 : 0;
     }
     if (lane >= n) rank = 32;
     bool close = false;
     if constexpr (BIAS) {
       // the keys in descending order; neighbours within their error are not
       // decided yet (equal infinities give NaN: their order is that of the ids)
-      if (lane < n) ckey32[rank] = key;
+      __syncwarp();
+      if (lane < n) keys[rank] = key;
       __syncwarp();
       if (lane < n && lane > 0) {
-        const float hi = key_value(ckey32[lane - 1]), lo = key_value(ckey32[lane]);
+        const float hi = key_value(keys[lane - 1]), lo = key_value(keys[lane]);
         close = hi - lo <= near + kSlackStep * (fabsf(hi) + fabsf(lo)) && lane <= a.k;
+      }
+    }
+    if constexpr (BIAS && !SOFTMAX) {
+      if (__any_sync(0xffffffffu, close)) {  // in some tokens of a thousand
+        __syncwarp();
+        float low = 0.f;
+        const float c = lane < n ? fine_key(my_z, my_b, low) : 0.f;
+        key = lane < n ? order_key(my_z == -INFINITY ? -INFINITY : clean(c)) : 0;
+        float* lows = fine[warp];
+        keys[lane] = key;
+        lows[lane] = low;
+        __syncwarp();
+        rank = 0;
+        for (int j = 0; j < n; ++j) {
+          const uint32_t other = keys[j];
+          const float ol = lows[j];
+          rank += other > key || (other == key && (ol > low || (ol == low && j < lane))) ? 1 : 0;
+        }
+        __syncwarp();
+        if (lane < n) {
+          keys[rank] = key;
+          lows[rank] = low;
+        } else {
+          rank = 32;
+        }
+        __syncwarp();
+        close = false;
+        if (lane < n && lane > 0)
+          close = (key_value(keys[lane - 1]) - key_value(keys[lane])) +
+                      (lows[lane - 1] - lows[lane]) <=
+                      kFineNear + 1e-14f * fabsf(key_value(keys[lane])) && lane <= a.k;
       }
     }
     if constexpr (BIAS) {
@@ -691,17 +797,19 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
     }
   } else {
     my_id = select_many<ZT, SOFTMAX, BIAS>(a, row, m, ckey, cid, n);
-    if (my_id >= 0) rank = lane;
+    if (my_id >= 0) {
+      rank = lane;
+      my_z = logit(a, row, my_id);
+      if constexpr (BIAS) my_b = a.bias[my_id];
+    }
   }
 
   // ---- weights of the selected, unbiased
   float zz = -INFINITY;
   if (rank < a.k) {
-    zz = logit(a, row, my_id);
-    if constexpr (BIAS) {  // a bias of -inf or NaN takes an expert out as well
-      const float b = a.bias[my_id];
-      if (b != b || b == -INFINITY) zz = -INFINITY;
-    }
+    zz = my_z;
+    if constexpr (BIAS)  // a bias of -inf or NaN takes an expert out as well
+      if (my_b != my_b || my_b == -INFINITY) zz = -INFINITY;
   }
   // scores far below 1 take their own way: they may be below fp32's range
   float w;
