@@ -24,6 +24,10 @@
 //    more SMs stream W whatever N is.  The low-rank term is a dot product of
 //    length R per output with each token's own rows of B, on mma.sync: 16 rows
 //    of B are the M side, and p as hi + lo, both bf16, two of the N columns.
+//    K = 7168, N = 3584 (51 MB of W), rank 16: one token 14.2 us, of which W
+//    takes 6.6 at the HBM rate, the prologue 2 and the clusters' sum 3 to 4; 32
+//    tokens with an adapter each (K = 3584, N = 7168) 18.1 with the shrink, 9.7
+//    of them W and the adapters; 256 tokens of rank 32 (N = 2048) 38.
 //  - adapter_tile_kernel (adapter_tile.cu), many tokens: bound by the tensor
 //    cores; the low-rank term is R more columns of K for each adapter that
 //    occurs in an output tile's rows.

@@ -14,21 +14,27 @@
 // Selection.  The k-th largest of the 32 lane maxima is a lower bound of the
 // k-th largest key: only experts at or above it can be selected.  They are
 // compacted (about k + 2 of 384 for logits of a router), one to a lane, and
-// ranked against one another with m shuffles, in place of k warp-wide argmax
-// rounds over all registers.
+// ranked against one another through shared memory, in place of k warp-wide
+// argmax rounds over all registers.  Where more than 32 are left (few lanes hold
+// the kept groups, k near 32) the range of keys is halved first.
 //
 // Rounding.  A key c = s + b in fp32 carries an error of some 1e-7, and two
 // experts are as near as that in about one token of a hundred.  The decisions
 // are those of 64-bit scores all the same: candidates within the slack of the
 // bound are kept, and where two that matter lie within the error of one
-// another the keys of the (few) candidates are evaluated again in 64 bits.
+// another the keys of the (few) candidates are evaluated again: sigmoid keys
+// as pairs of fp32 values (fine_key), what those leave open in 64 bits.
 // Without a bias the order of the scores is the order of the logits and no
 // rounding decides anything.  Unavailable experts (z or c -inf or NaN) rank
 // below all others, with weight 0; experts outside the kept groups are never
 // chosen.
 //
-// Bound: at T = 8192, E = 384 the kernel reads 12.6 MB (1.9 us at the HBM
-// rate); it is bound by instructions, not by bytes.
+// Bound: instructions and the length of a token's chain of warp-wide steps, not
+// bytes.  T = 8192, E = 384, 8 groups of which 4 stay, k = 8: 11.4 us for 12.7 MB
+// (1.9 us at the HBM rate); loads and keys alone are 4.9 of them, the groups 3.3.
+// A warp holds a token because the registers then hold all keys: 32 warps fit an
+// SM, and two rounds of them make the call.  Five CTAs of 8 warps to an SM spill
+// (12.7 us against 12.3 when measured), three are too few (13.1).
 #include <float.h>
 #include <math.h>
 
