@@ -407,3 +407,24 @@ def test_route_groups_of_scores_below_fp32(moe, E, k, groups, kept, dtype):
     for top in (-80.0, -89.0, -105.0, -200.0):
         z = top - logits(12, E, E + k).abs().to(dtype) * 4
         check_route(moe, z.to(dtype).contiguous(), k, groups=groups, topk_groups=kept)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("E,groups,kept,ties,target", [(384, 1, 1, 12, 2.0), (96, 1, 1, 30, 0.5),
+                                                       (200, 4, 4, 9, -3.0), (256, 8, 3, 16, 1.5),
+                                                       (640, 1, 1, 20, 40.0)])
+def test_route_near_ties_among_few(moe, E, groups, kept, ties, target, dtype, score):
+    """A few experts whose keys s + b agree to fp32's rounding, far above the
+    others: their order, different in every row, is that of 64 bits."""
+    T, k = 300, 8
+    z = logits(T, E, E + ties)
+    at = torch.randperm(E, generator=torch.Generator().manual_seed(ties))[:ties].to(DEV)
+    z[:, at] = logits(1, ties, 5)
+    z[:, at] *= 1 + torch.linspace(-1, 1, T, device=DEV).unsqueeze(1) * 2e-6
+    z = z.to(dtype)
+    zz = z[T // 2].double()
+    s = torch.sigmoid(zz) if score == "sigmoid" else torch.softmax(zz, 0)
+    bias = ranking_bias(E, 1) + (target - 6.0)
+    bias[at] = (target - s[at]).float()
+    check_route(moe, z.contiguous(), k, bias, score=score, groups=groups, topk_groups=kept)
