@@ -331,11 +331,13 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
     lowp[kLowWarps][threadIdx.x] = v;
   }
   tc_fence_before();
-  cluster_sync_all();
+  // tensor memory goes back before the wait for the other ranks (see kSmBytes)
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, sh.cols);
   }
+  cluster_sync_all();
   if (FUSED) {
     if (threadIdx.x < tokens * a.R) {
       const int id = checked_id(a.ids[threadIdx.x / a.R], a.adapters);

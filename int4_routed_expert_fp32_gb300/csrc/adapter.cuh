@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -22,6 +23,7 @@ struct AdapterArgs {
 };
 
 constexpr int kSplitTokens = 256;  // up to here adapter_split_kernel
+constexpr int kTileSmemLeast = 168 * 1024;  // above: a CTA of adapter_tile_kernel takes more
 
 // Whether the two kernels of a call with few tokens are laid out to share the SMs
 // (T <= kSplitTokens).  Low-rank work that is small beside W: 128 tokens of rank

@@ -267,11 +267,14 @@ __global__ void __launch_bounds__(kStThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync_all();
+  // Tensor memory goes back before the wait for the other ranks, which may still
+  // wait for theirs behind another kernel's CTA (see kSmBytes)
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, kStMaxCols);
   }
+  cluster_sync_all();
   // the ranks take the rows in turn: 4 values to a thread, summed in rank order
   const int quads = s.R / 4;
   for (int i = rank * kStThreads + threadIdx.x; i < kAdTile * quads; i += ranks * kStThreads) {
@@ -291,6 +294,38 @@ __global__ void __launch_bounds__(kStThreads, 1)
 }
 
 namespace {
+
+constexpr int kAlone = 198 * 1024;  // shared memory where no other kernel is to fit beside
+
+// A slot of `per` adapters' A and xrows rows of x; what the CTA needs beside them.
+constexpr int shrink_slot(int per, int R, int xrows) {
+  return (per * R + 15) / 16 * 2048 + xrows * 128;
+}
+
+constexpr int shrink_fixed(int R, int xrows) {
+  const int sums = xrows * R * 4, over = (kAdTile - xrows) * 128;
+  return (sums > over ? sums : over) + 1024;
+}
+
+constexpr int shrink_stages(int bytes, int per, int R, int xrows) {
+  const int n = (bytes - shrink_fixed(R, xrows)) / shrink_slot(per, R, xrows);
+  return n < 2 ? 2 : n > kStMaxStages ? kStMaxStages : n;
+}
+
+// Above kSplitTokens the tile kernel starts beside this one, takes all of an SM's
+// tensor memory and keeps it until this one has finished: a CTA of each must not
+// fit an SM together, whatever the rank.
+constexpr bool shrink_fills_sm() {
+  for (int R = 8; R <= 128; R += 8) {
+    const int per = kStMaxCols / R;
+    const int smem = shrink_stages(kAlone, per, R, kAdTile) * shrink_slot(per, R, kAdTile) +
+                     shrink_fixed(R, kAdTile);
+    if (smem + kTileSmemLeast + 2 * kSmCtaBytes <= kSmBytes) return false;
+  }
+  return true;
+}
+
+static_assert(shrink_fills_sm(), "a tile CTA could keep the tensor memory that the shrink waits for");
 
 }  // namespace
 
@@ -322,20 +357,16 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
   // these have gone (32 tokens of rank 32: 17 us against 27; with fewer adapters
   // still, x is read too often: 64 tokens of rank 64, 63 us against 41).
   s.xrows = (rows + 7) / 8 * 8;
-  const int fixed = std::max(s.xrows * s.R * 4, (kAdTile - s.xrows) * 128) + 1024;
-  auto slot = [&](int per) { return (per * s.R + 15) / 16 * 2048 + s.xrows * 128; };
-  auto slots = [&](int per, int bytes) { return (bytes - fixed) / slot(per); };
-  const int room = s.T <= 64 ? 50 * 1024 : 84 * 1024;
-  constexpr int kAlone = 198 * 1024;
-  const int beside = slots(s.per, room) >= 2 ? s.per : (s.per + 1) / 2;
-  if (s.T <= kSplitTokens && adapter_beside(s.T, s.R) && slots(beside, room) >= 2) {
+  const int fixed = shrink_fixed(s.R, s.xrows), room = s.T <= 64 ? 50 * 1024 : 84 * 1024;
+  auto two_fit = [&](int per) { return fixed + 2 * shrink_slot(per, s.R, s.xrows) <= room; };
+  const int beside = two_fit(s.per) ? s.per : (s.per + 1) / 2;
+  int bytes = kAlone;
+  if (s.T <= kSplitTokens && adapter_beside(s.T, s.R) && two_fit(beside)) {
     s.per = beside;
-    s.stages = slots(s.per, room);
-  } else {
-    s.stages = std::max(2, slots(s.per, kAlone));
+    bytes = room;
   }
-  s.stages = std::min(kStMaxStages, s.stages);
-  const int smem = s.stages * slot(s.per) + fixed;
+  s.stages = shrink_stages(bytes, s.per, s.R, s.xrows);
+  const int smem = s.stages * shrink_slot(s.per, s.R, s.xrows) + fixed;
   MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(adapter_shrink_tile_kernel), smem));
   const int ranks =
       adapter_cluster(reinterpret_cast<const void*>(adapter_shrink_tile_kernel), kStThreads, smem,

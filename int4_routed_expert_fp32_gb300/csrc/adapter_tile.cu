@@ -54,6 +54,8 @@ struct TileShape {
   static constexpr int kStageBytes = kTlABytes + kBBytes;
   static constexpr int kSmem = kTlStages * kStageBytes + 1024;
   static_assert(kBBytes % 1024 == 0 && BN % 32 == 0 && 2 * BN <= 512, "tile");
+  static_assert(fills_half_sm(kSmem), "CTAs of two pair kernels must not meet on an SM");
+  static_assert(kSmem >= kTileSmemLeast, "what the shrink kernel counts with");
 };
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {

@@ -70,6 +70,7 @@ constexpr uint32_t kPCols = 512;
 constexpr uint32_t kPACol = kPTN;               // A ring after the 256-column accumulator
 constexpr uint32_t kPASlot = kPBK / 2;          // 64 columns: 128 fp16 per row
 constexpr int kPSmem = kPStages * kPStageBytes + 1024 + 256;
+static_assert(fills_half_sm(kPSmem), "CTAs of two pair kernels must not meet on an SM");
 static_assert(kPStageBytes % 1024 == 0, "stage alignment");
 static_assert(kPDqWarps * 32 == kPM * (kPBK / kGroup), "one thread per row and group");
 static_assert((2 + kPDqWarps + 12) * 32 <= 1024, "threads per CTA");

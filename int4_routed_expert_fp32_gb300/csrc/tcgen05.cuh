@@ -7,6 +7,19 @@
 namespace moe {
 
 // ---- tensor memory
+//
+// tcgen05.alloc waits, without a limit, until the SM's other CTAs leave enough of
+// the 512 columns.  Kernels of several streams can meet on an SM in any order, so
+// no CTA may hold columns while it waits for a CTA that may itself be waiting for
+// columns:
+//  - cta_group::1 kernels free theirs before any wait for another CTA;
+//  - cta_group::2 kernels need their peer while they hold theirs (all of them). A
+//    CTA of one takes more than half of the SM's shared memory, so that two never
+//    meet on an SM; cta_group::1 CTAs beside it end by themselves.
+constexpr int kSmBytes = 228 * 1024;  // shared memory of an SM,
+constexpr int kSmCtaBytes = 1024;     // of which each CTA takes this beside its own
+
+constexpr bool fills_half_sm(int smem) { return 2 * (smem + kSmCtaBytes) > kSmBytes; }
 
 // Allocate `ncols` TMEM columns (power of two >= 32); one full warp executes
 // it; the TMEM address is written to *dst (shared memory).
