@@ -757,13 +757,14 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
     bool close = false;
     if constexpr (BIAS) {
       // the keys in descending order; neighbours within their error are not
-      // decided yet (equal infinities give NaN: their order is that of the ids)
+      // decided yet (infinite keys are: next to equal ones the ids decide)
       __syncwarp();
       if (lane < n) keys[rank] = key;
       __syncwarp();
       if (lane < n && lane > 0) {
         const float hi = key_value(keys[lane - 1]), lo = key_value(keys[lane]);
-        close = hi - lo <= near + kSlackStep * (fabsf(hi) + fabsf(lo)) && lane <= a.k;
+        close = hi < INFINITY && lo > -INFINITY && lane <= a.k &&
+                hi - lo <= near + kSlackStep * (fabsf(hi) + fabsf(lo));
       }
     }
     if constexpr (BIAS && !SOFTMAX) {
@@ -772,6 +773,7 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
         float low = 0.f;
         const float c = lane < n ? fine_key(my_z, my_b, low) : 0.f;
         key = lane < n ? order_key(my_z == -INFINITY ? -INFINITY : clean(c)) : 0;
+        if (key == kUnavail) low = 0.f;  // unavailable ones are equal, whatever their bias
         float* lows = fine[warp];
         keys[lane] = key;
         lows[lane] = low;
@@ -791,10 +793,11 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
         }
         __syncwarp();
         close = false;
-        if (lane < n && lane > 0)
-          close = (key_value(keys[lane - 1]) - key_value(keys[lane])) +
-                      (lows[lane - 1] - lows[lane]) <=
-                      kFineNear + 1e-14f * fabsf(key_value(keys[lane])) && lane <= a.k;
+        if (lane < n && lane > 0) {
+          const float hi = key_value(keys[lane - 1]), lo = key_value(keys[lane]);
+          close = hi < INFINITY && lo > -INFINITY && lane <= a.k &&
+                  (hi - lo) + (lows[lane - 1] - lows[lane]) <= kFineNear + 1e-14f * fabsf(lo);
+        }
       }
     }
     if constexpr (BIAS) {

@@ -175,6 +175,27 @@ def test_route_decides_like_64_bits(moe, score, groups, kept):
     check_route(moe, z.contiguous(), k, bias, score=score, groups=groups, topk_groups=kept)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,kept", [(24, 1, 1), (32, 1, 1), (64, 4, 2), (40, 5, 3)])
+def test_route_unavailable_experts_beside_near_ties(moe, score, E, groups, kept):
+    """Fewer than k experts left, some of them tied to fp32 rounding, the others
+    out by logits of -inf or NaN beside biases of every kind, or by biases of -inf
+    or NaN: those fill up the k in the order of their ids."""
+    rng = np.random.default_rng(E)
+    k = min(E // groups * kept, 20)
+    base = logits(1, E, 21)[0]
+    s = torch.sigmoid(base.double()) if score == "sigmoid" else torch.softmax(base.double(), 0)
+    bias = (1.0 - s).float()
+    other = torch.from_numpy(rng.permutation(E)[:E // 2])
+    kinds = torch.tensor([0.0, 0.1, -0.3, 1e-30, -1e-30, -INF, float("nan"), 2.0])
+    bias[other.to(DEV)] = kinds[torch.arange(E // 2) % 8].to(DEV)
+    z = base.repeat(60, 1)
+    for t in range(60):
+        out = torch.from_numpy(rng.permutation(E)[:int(rng.integers(E // 2, E + 1))]).to(DEV)
+        z[t, out] = -INF if t % 3 else float("nan")
+    check_route(moe, z.contiguous(), k, bias, score=score, groups=groups, topk_groups=kept)
+
+
 def test_route_large_logits_and_biases(moe):
     z = logits(64, 160, 5, std=40.0)
     bias = ranking_bias(160, 6, std=3.0)
