@@ -428,8 +428,10 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
 }
 
 // Asked of the runtime once for each kernel, cluster size and amount of shared
-// memory; what a device holds does not change.
-int adapter_cluster(const void* kernel, int threads, int smem, int clusters, int most) {
+// memory; what a device holds does not change.  A query that fails is an error
+// and is not kept: the cluster's size decides the order of the sums.
+cudaError_t adapter_cluster(const void* kernel, int threads, int smem, int clusters, int most,
+                            int* size) {
   struct Known {
     const void* kernel;
     int device, threads, smem, size, held;
@@ -437,36 +439,34 @@ int adapter_cluster(const void* kernel, int threads, int smem, int clusters, int
   static std::mutex mu;
   static std::vector<Known> known;
   int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess) return 1;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  for (int size = most; size > 1; --size) {
+  for (*size = most; *size > 1; --*size) {
     int held = -1;
     for (const Known& k : known)
       if (k.kernel == kernel && k.device == device && k.threads == threads && k.smem == smem &&
-          k.size == size)
+          k.size == *size)
         held = k.held;
     if (held < 0) {
       cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(size);
+      cfg.gridDim = dim3(*size);
       cfg.blockDim = dim3(threads);
       cfg.dynamicSmemBytes = smem;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = size;
+      attr[0].val.clusterDim.x = *size;
       attr[0].val.clusterDim.y = 1;
       attr[0].val.clusterDim.z = 1;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      held = 0;
-      if (cudaOccupancyMaxActiveClusters(&held, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        held = 0;
-      }
-      known.push_back(Known{kernel, device, threads, smem, size, held});
+      e = cudaOccupancyMaxActiveClusters(&held, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      known.push_back(Known{kernel, device, threads, smem, *size, held});
     }
-    if (held >= clusters) return size;
+    if (held >= clusters) return cudaSuccess;
   }
-  return 1;
+  return cudaSuccess;
 }
 
 namespace {
@@ -515,13 +515,11 @@ int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
   const int tiles = split_tiles(a.T, a.N);
   const int most = std::min({kSpMaxCluster, std::max(1, num_sms() / tiles), (a.K + 63) / 64});
   SplitShape sh = split_shape(a.T, a.R, most);
-  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern), static_cast<int>(sh.smem)));
-  const int held = adapter_cluster(reinterpret_cast<const void*>(kern), THREADS,
-                                   static_cast<int>(sh.smem), tiles, most);
-  if (held < most) {  // fewer ranks, more tokens to each
-    sh = split_shape(a.T, a.R, held);
-    MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern), static_cast<int>(sh.smem)));
-  }
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
+  int held = 1;
+  MOE_TRY_CUDA(adapter_cluster(reinterpret_cast<const void*>(kern), THREADS,
+                               static_cast<int>(sh.smem), tiles, most, &held));
+  if (held < most) sh = split_shape(a.T, a.R, held);  // fewer ranks, more tokens to each
   CUtensorMap mw, mx;
   if (!adapter_map_rows(&mw, a.w, a.N, a.K, 128) || !adapter_map_rows(&mx, a.x, a.T, a.K, sh.tb))
     return MOE_ERR_CUDA;

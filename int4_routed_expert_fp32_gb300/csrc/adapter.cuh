@@ -50,19 +50,21 @@ inline bool adapter_map_rows(CUtensorMap* m, const uint16_t* base, int rows, int
                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Dynamic shared memory of a kernel, and all of an SM's L1 as shared memory while it
+// Dynamic shared memory for a kernel, and all of an SM's L1 as shared memory while it
 // runs: the split in force is the first kernel's, and a CTA of the next one that
 // wants more of it waits until the SM is empty.
-inline cudaError_t adapter_smem(const void* kernel, int bytes) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+inline cudaError_t adapter_smem(const void* kernel) {
+  const cudaError_t e = allow_most_smem(kernel);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                               cudaSharedmemCarveoutMaxShared);
 }
 
-// The largest cluster (at most `most` CTAs) of which the device holds `clusters` at
-// a time, or 1: one cluster too many would wait for a whole other one to finish.
-int adapter_cluster(const void* kernel, int threads, int smem, int clusters, int most);
+// *size: the largest cluster (at most `most` CTAs) of which the device holds
+// `clusters` at a time, or 1: one cluster too many would wait for a whole other one
+// to finish.  After adapter_smem.
+cudaError_t adapter_cluster(const void* kernel, int threads, int smem, int clusters, int most,
+                            int* size);
 
 // Launch attributes: clusters of `ranks` CTAs, programmatic dependent of the
 // kernel before it in the stream.

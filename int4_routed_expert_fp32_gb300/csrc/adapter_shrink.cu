@@ -367,10 +367,11 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
   }
   s.stages = shrink_stages(bytes, s.per, s.R, s.xrows);
   const int smem = s.stages * shrink_slot(s.per, s.R, s.xrows) + fixed;
-  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(adapter_shrink_tile_kernel), smem));
-  const int ranks =
-      adapter_cluster(reinterpret_cast<const void*>(adapter_shrink_tile_kernel), kStThreads, smem,
-                      tiles * groups, std::min(kShMaxCluster, steps));
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(adapter_shrink_tile_kernel)));
+  int ranks = 1;
+  MOE_TRY_CUDA(adapter_cluster(reinterpret_cast<const void*>(adapter_shrink_tile_kernel),
+                               kStThreads, smem, tiles * groups, std::min(kShMaxCluster, steps),
+                               &ranks));
   CUtensorMap mx, ma;
   const uint64_t dims[3] = {static_cast<uint64_t>(s.K), static_cast<uint64_t>(s.R),
                             static_cast<uint64_t>(s.adapters)};

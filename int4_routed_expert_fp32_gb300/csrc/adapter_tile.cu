@@ -546,7 +546,7 @@ int launch_tile(const AdapterArgs& a, int* status, cudaStream_t st) {
                          CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_ERR_CUDA;
   auto kern = adapter_tile_kernel<BN, WIDE>;
-  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern), TileShape<BN>::kSmem));
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
   const long tiles = static_cast<long>((a.N + BN - 1) / BN) * ((a.T + kTlRows - 1) / kTlRows);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long>(tiles, num_sms() / 2)));

@@ -413,7 +413,7 @@ int launch_odd(const NormArgs& a, int threads, cudaStream_t s) {
   auto kern = block_norm_odd_kernel<XF32, VPT, THREADS>;
   const int smem = 3 * ((a.N + 7) / 8 * 8 + 8) * 2;
   if (smem > 48 * 1024)
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    MOE_TRY_CUDA(allow_most_smem(reinterpret_cast<const void*>(kern)));
   int fit = 1;
   MOE_TRY_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, threads, smem));
   kern<<<std::min(a.T, std::max(1, fit) * num_sms()), threads, smem, s>>>(a);
@@ -434,8 +434,7 @@ int launch_norm(const NormArgs& a, bool vec, bool dense, cudaStream_t s) {
     const size_t smem = static_cast<size_t>(a.N) * sizeof(float);
     auto kern = block_norm_any_kernel<XF32>;
     if (smem > 48 * 1024)
-      MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(smem)));
+      MOE_TRY_CUDA(allow_most_smem(reinterpret_cast<const void*>(kern)));
     const int threads = std::min(512, (a.N + 31) / 32 * 32);
     kern<<<a.T, threads, smem, s>>>(a);
     MOE_LAUNCH_CHECK();

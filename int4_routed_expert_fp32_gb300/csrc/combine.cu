@@ -163,8 +163,7 @@ static int launch_combine_t(const YT* y, const int32_t* inv_row, const float* w,
   if (gain) {
     const size_t smem = (size_t)D * sizeof(float);
     if (smem > 48 * 1024)
-      MOE_TRY_CUDA(cudaFuncSetAttribute(combine_kernel<YT, true>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      MOE_TRY_CUDA(allow_most_smem(reinterpret_cast<const void*>(&combine_kernel<YT, true>)));
     combine_kernel<YT, true><<<T, kCbThreads, smem, s>>>(y, inv_row, w, T, D, k, gain, eps, out,
                                                          status);
   } else {

@@ -1,7 +1,9 @@
 // Status word, device queries, tensor-map encoding, and the status /
 // self-test entry points of the C ABI.
 #include <atomic>
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include <cudaTypedefs.h>
 
@@ -49,6 +51,32 @@ int num_sms() {
     g_num_sms[d] = n;
   }
   return g_num_sms[d];
+}
+
+cudaError_t allow_most_smem(const void* kernel) {
+  // The amount is asked for once; the limit is set on every call, since a new
+  // context starts without it.
+  static std::map<std::pair<const void*, int>, int> most;
+  int device = 0, bytes = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    const auto it = most.find({kernel, device});
+    if (it != most.end()) bytes = it->second;
+  }
+  if (!bytes) {
+    cudaFuncAttributes f{};
+    int optin = 0;
+    e = cudaFuncGetAttributes(&f, kernel);
+    if (e == cudaSuccess)
+      e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+    if (e != cudaSuccess) return e;
+    bytes = optin - static_cast<int>(f.sharedSizeBytes);
+    std::lock_guard<std::mutex> lk(g_mu);
+    most[{kernel, device}] = bytes;
+  }
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 void note_cuda_error(cudaError_t e) { g_last_cuda_error = e; }

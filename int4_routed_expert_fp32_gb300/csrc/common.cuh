@@ -30,6 +30,11 @@ constexpr int64_t kDefaultWaitNs = 2000000000LL;  // 2 s per wait before giving 
 int* status_word();
 // Number of SMs of the current device (cached).
 int num_sms();
+// Lets a kernel whose calls ask for different amounts of dynamic shared memory have
+// all that the current device gives a CTA beside its static part.  The limit is
+// the function's, not the call's: set to one call's amount, it could be lowered
+// by another host thread before that call's launch.  Every thread sets this value.
+cudaError_t allow_most_smem(const void* kernel);
 // Record the last CUDA error for moe_check_error diagnostics.
 void note_cuda_error(cudaError_t e);
 // Count one kernel launch of this library (read by moe_launch_count).

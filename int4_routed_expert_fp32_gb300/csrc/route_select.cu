@@ -863,9 +863,6 @@ int launch_npl(const moe_route_config& cfg, const SelectArgs& a, int warps, size
                            : route_select_kernel<ZT, NPL, true, false>)
                    : (bias ? route_select_kernel<ZT, NPL, false, true>
                            : route_select_kernel<ZT, NPL, false, false>);
-  if (smem > 48 * 1024)
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem)));
   kern<<<(a.T + warps - 1) / warps, 32 * warps, smem, s>>>(a);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
@@ -920,6 +917,7 @@ int launch_route_select(const moe_route_config& cfg, const void* in, bool bf16, 
   const int sms = num_sms();
   int warps = T >= 16 * sms ? 8 : (T >= 4 * sms ? 2 : 1);
   const size_t per = static_cast<size_t>(a.E) * (kListBytes + (a.c > 16 ? 8 : 0));
+  static_assert(kMaxExperts * (kListBytes + 8) + 4 <= 40 * 1024, "one token's fits as it is");
   while (warps > 1 && warps * per > 40 * 1024) warps >>= 1;
   // a candidate list rounded up so that what follows it is 4-byte aligned
   const size_t smem = warps * per + 4;
