@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 from typing import Dict, Optional
@@ -320,15 +321,25 @@ SCORES = {"sigmoid": 0, "softmax": 1}
 GROUP_SCORES = {"top2": 0, "max": 1}
 
 
-@functools.lru_cache(maxsize=256)
 def _route_config(E: int, k: int, score: str, groups: int, topk_groups: Optional[int],
                   group_score: str, renorm: bool, scale: float):
+    """(config, k): the struct of these options.  They are turned into plain numbers
+    first, since a tensor's hash is its identity, not its value."""
+    k = operator.index(k)
+    groups = operator.index(groups)
+    topk_groups = groups if topk_groups is None else operator.index(topk_groups)
+    return _route_struct(E, k, score, groups, topk_groups, group_score, bool(renorm),
+                         float(scale)), k
+
+
+@functools.lru_cache(maxsize=256)
+def _route_struct(E: int, k: int, score: str, groups: int, topk_groups: int, group_score: str,
+                  renorm: bool, scale: float):
     if score not in SCORES:
         raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
     if group_score not in GROUP_SCORES:
         raise ValueError(f"group_score: expected one of {sorted(GROUP_SCORES)}, got {group_score!r}")
-    return ctypes.pointer(MoeRouteConfig(E, k, SCORES[score], groups,
-                                         groups if topk_groups is None else topk_groups,
+    return ctypes.pointer(MoeRouteConfig(E, k, SCORES[score], groups, topk_groups,
                                          GROUP_SCORES[group_score], int(renorm), scale))
 
 
@@ -350,7 +361,7 @@ def route_logits(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
         ld = _ld(logits)
     if bias is not None:
         _arg("bias", bias, (E,), torch.float32)
-    cfg = _route_config(E, k, score, groups, topk_groups, group_score, renorm, scale)
+    cfg, k = _route_config(E, k, score, groups, topk_groups, group_score, renorm, scale)
     dev = _device_of((logits, bias), ("logits", "bias"))
     idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
     w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
@@ -375,7 +386,7 @@ def route_grouped(x: torch.Tensor, w_router: torch.Tensor, k: int,
         _arg("bias", bias, (E,), torch.float32)
     if w_terms is not None:
         _arg("w_terms", w_terms, (3, E, H), torch.bfloat16)
-    cfg = _route_config(E, k, score, groups, topk_groups, group_score, renorm, scale)
+    cfg, k = _route_config(E, k, score, groups, topk_groups, group_score, renorm, scale)
     dev = _placed(x=x, w_router=w_router, bias=bias, w_terms=w_terms)
     idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
     w = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)

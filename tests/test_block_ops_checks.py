@@ -2,6 +2,7 @@
 the Python binding on host tensors, and by the C entry points before any launch
 (no GPU needed)."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -52,6 +53,39 @@ def test_route_grouped_binding(capi):
     raises("w_router: expected shape", r, bf16(4, 64), f32(16, 32), 2)
     raises("x: expected torch.bfloat16", r, f32(4, 64), f32(16, 64), 2)
     raises("w_terms: expected shape", r, bf16(4, 64), f32(16, 64), 2, w_terms=bf16(2, 16, 64))
+
+
+def test_route_options_are_read_anew_on_every_call(capi, monkeypatch):
+    """A scale (or another option) held in a tensor and changed in place between two
+    calls: the second call uses the new value."""
+    seen = []
+
+    def fake(cfg, *rest):
+        c = cfg.contents
+        seen.append((c.k, c.groups, c.topk_groups, c.renorm, c.scale))
+        return 0
+
+    names = ("moe_route_logits", "moe_route_grouped")
+    monkeypatch.setattr(capi, "lib", types.SimpleNamespace(
+        moe_route_grouped_workspace_size=lambda *a: 256, **{n: fake for n in names}))
+    monkeypatch.setattr(capi, "_device_of", lambda *a: torch.device("cpu"))
+    monkeypatch.setattr(capi, "_placed", lambda **k: torch.device("cpu"))
+    monkeypatch.setattr(capi, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(capi, "_stream", lambda: None)
+    scale, renorm = torch.tensor(2.5), torch.tensor(True)
+    k, groups, kept = torch.tensor(2), torch.tensor(4), torch.tensor(2)
+    calls = (lambda: capi.route_logits(f32(4, 16), k, groups=groups, topk_groups=kept,
+                                       renorm=renorm, scale=scale),
+             lambda: capi.route_grouped(bf16(4, 64), f32(16, 64), k, groups=groups,
+                                        topk_groups=kept, renorm=renorm, scale=scale))
+    for call in calls:
+        scale.fill_(2.5), renorm.fill_(True), k.fill_(2), groups.fill_(4), kept.fill_(2)
+        assert call()[0].shape == (4, 2)
+        scale.fill_(1.0), renorm.fill_(False), k.fill_(3), groups.fill_(8), kept.fill_(4)
+        assert call()[0].shape == (4, 3)
+    assert seen == 2 * [(2, 4, 2, 1, 2.5), (3, 8, 4, 0, 1.0)]
+    capi.route_logits(f32(4, 16), 2, scale=2)
+    assert seen[-1] == (2, 1, 1, 1, 2.0)
 
 
 def route_config(capi, **kw):
