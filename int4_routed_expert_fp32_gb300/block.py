@@ -7,6 +7,7 @@ adapters of many requests beside the latent projections:
     u      = adapter_linear(h, lat_down, ids)          (latent blocks)
     y      = combine(expert_ffn(dispatch(idx, u)), w)
     y      = adapter_linear(rmsnorm(y), lat_up, ids)   (latent blocks)
+    y     += shared_expert(h)                          (with shared_* weights)
     x, h   = block_norm(y, x, ...)                     norm, gate, residual, next norm
 
 The latent path is the one of the "Kimi K3 latent up-projection" page
@@ -33,7 +34,10 @@ class MoeBlock:
     weights   router_w fp32 [E, H], the stacked int4 experts (gate / up / down
               packed and scale), optionally router_bias fp32 [E]; for a latent
               block lat_down bf16 [L, H], lat_up bf16 [H, L] and optionally
-              lat_norm bf16 [L]
+              lat_norm bf16 [L]; for a shared expert shared_gate and shared_up
+              bf16 [I, H] and shared_down bf16 [H, I]; router_w_terms (from
+              ``router_prepare``; made here where it is missing).  Other names
+              are refused
     k, ...    routing options of ``route_grouped``
     adapters  {"lat_down": (A, B, scale), "lat_up": ...}: either, or none
     post_gain, next_gain, gate (a gain per channel, [H]), gate_sigmoid,
@@ -47,11 +51,23 @@ class MoeBlock:
                  post_gain: Optional[torch.Tensor] = None,
                  next_gain: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                  gate_sigmoid: bool = False, residual_scale: float = 1.0, eps: float = 1e-6):
-        self.weights = weights
+        extra = set(weights) - {n for n, _ in capi.MoeWeights._fields_}
+        if extra:
+            raise ValueError(f"unknown weight names: {sorted(extra)}")
+        for name in ("router_w", *capi.EXPERT_NAMES):
+            if name not in weights:
+                raise ValueError(f"{name} is required")
         self.experts = {n: weights[n] for n in capi.EXPERT_NAMES}
-        self.latent = weights.get("lat_down") is not None
-        if self.latent != (weights.get("lat_up") is not None):
+        self.weights = weights = {n: t for n, t in weights.items() if t is not None}
+        self.latent = "lat_down" in weights
+        if self.latent != ("lat_up" in weights):
             raise ValueError("lat_down and lat_up come together")
+        if "lat_norm" in weights and not self.latent:
+            raise ValueError("lat_norm belongs to a latent block (lat_down, lat_up)")
+        shared = [weights.get(n) for n in ("shared_gate", "shared_up", "shared_down")]
+        if len({t is None for t in shared}) > 1:
+            raise ValueError("shared_gate, shared_up and shared_down come together")
+        self.shared = None if shared[0] is None else shared
         self.adapters = dict(adapters or {})
         unknown = set(self.adapters) - ({"lat_down", "lat_up"} if self.latent else set())
         if unknown:
@@ -64,7 +80,9 @@ class MoeBlock:
                          gate_sigmoid=gate_sigmoid, scale=residual_scale, eps=eps)
         self.eps = eps
         # the router weight's bf16 terms, for calls of 512 tokens or more
-        self.w_terms = capi.router_prepare(weights["router_w"])
+        self.w_terms = weights.get("router_w_terms")
+        if self.w_terms is None:
+            self.w_terms = capi.router_prepare(weights["router_w"])
 
     def route(self, h: torch.Tensor):
         """(topk_idx, topk_w) of the block's input h bf16 [T, H]."""
@@ -90,7 +108,9 @@ class MoeBlock:
                             max_rows_per_expert=h.shape[0])
         y = capi.combine(y, d["inv_row"], w)
         if self.latent:
-            if self.weights.get("lat_norm") is not None:
+            if "lat_norm" in self.weights:
                 y = capi.rmsnorm(y, self.weights["lat_norm"], self.eps)
             y = self._project("lat_up", y, ids)
+        if self.shared is not None:
+            y = capi.shared_expert(h, *self.shared, out=y)
         return capi.block_norm(y, x, x_out=x_out, **self.norm)

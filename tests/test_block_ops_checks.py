@@ -253,3 +253,19 @@ def test_moe_block_checks_its_weights(capi, monkeypatch):
     raises("no projection for the adapters", MoeBlock, w, 2, adapters={"lat_up": ()})
     latent = {**w, "lat_down": bf16(32, 64), "lat_up": bf16(64, 32)}
     raises("no projection for the adapters", MoeBlock, latent, 2, adapters={"router": ()})
+
+
+def test_moe_block_refuses_weights_that_it_would_drop(capi, monkeypatch):
+    from int4_routed_expert_fp32_gb300.block import MoeBlock
+    monkeypatch.setattr(capi, "router_prepare", lambda w: None)
+    w = {n: f32(1) for n in capi.EXPERT_NAMES}
+    w["router_w"] = f32(16, 64)
+    assert MoeBlock({**w, "router_bias": None, "shared_gate": None}, 2).shared is None
+    raises("unknown weight names: .*'shared_gate_w'", MoeBlock, {**w, "shared_gate_w": None}, 2)
+    raises("lat_norm belongs to", MoeBlock, {**w, "lat_norm": bf16(32)}, 2)
+    raises("come together", MoeBlock, {**w, "shared_gate": bf16(32, 64)}, 2)
+    raises("come together", MoeBlock, {**w, "shared_gate": bf16(32, 64),
+                                       "shared_up": bf16(32, 64)}, 2)
+    raises("router_w is required", MoeBlock, {n: w[n] for n in capi.EXPERT_NAMES}, 2)
+    terms = bf16(3, 16, 64)
+    assert MoeBlock({**w, "router_w_terms": terms}, 2).w_terms is terms

@@ -126,3 +126,29 @@ def test_block_tokens_alone_are_the_batch(moe):
             d1, d2 = one[0] - x[t], x2[t] - x[t]
             assert float((d1 - d2).norm()) <= 8e-3 * float(d2.norm())
     assert moe.check_error() == 0
+
+
+@pytest.mark.parametrize("T,latent", [(1, False), (40, True), (600, True)])
+def test_block_with_a_shared_expert(moe, T, latent):
+    """The shared expert's output joins the routed ones' before the block norm, as in
+    the layer: with no norm, gate or adapters the stream's change is the layer's."""
+    w = wl.workload("tiny", name="block", T=T, H=512, L=256 if latent else 0, E=16, k=4, I=128,
+                    seed=9, norm_gain_std=0.1)
+    weights = device_weights(w, DEV)
+    g = torch.Generator().manual_seed(T)
+    for name, shape in (("shared_gate", (192, 512)), ("shared_up", (192, 512)),
+                        ("shared_down", (512, 192))):
+        weights[name] = (0.05 * torch.randn(*shape, generator=g)).to(BF16).to(DEV)
+    h = torch.randn(T, 512, generator=g).to(BF16).to(DEV)
+    x = torch.zeros(T, 512, device=DEV)
+    y, _ = moe.MoeBlock(weights, w.k).forward(x, h)
+    layer = moe.MoeLayer(T, 512, 16, w.k, 128, weights, L=w.L, I_shared=192)
+    want = layer.forward(h).double()
+    alone, _ = moe.MoeBlock({n: t for n, t in weights.items() if "shared" not in n},
+                            w.k).forward(x, h)
+    assert moe.check_error() == 0
+    part = (want - alone.double()).norm()
+    assert part > 0.05 * want.norm()             # it shows
+    # the latent norm's input is rounded here and not in the layer: 2^-8, and as
+    # much again in the up-projection's input
+    assert (y.double() - want).norm() <= 8e-3 * want.norm()
