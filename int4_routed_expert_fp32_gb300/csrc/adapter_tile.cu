@@ -23,7 +23,15 @@
 //
 // Per CTA: warp 0 (one thread) TMA; warp 1 of rank 0 issues the MMAs; warps
 // 2-5 the epilogue of the CTA's 128 rows; warps 6-9 the tile's list of
-// adapters and the A operands of its low-rank stages.  Every wait is bounded.
+// adapters and the A operands of its low-rank stages; warps 10 and up hand those
+// to the MMA warp.  Every wait on an mbarrier is bounded.
+//
+// Handing over.  The MMA warp of rank 0 reads what threads of rank 1 wrote to
+// their shared memory, so the chain from the writes to the MMA has a release and
+// an acquire at cluster scope.  Each takes some 0.4 us; done by the A warps or by
+// the MMA warp, one stage after the other, they make it 445 us in place of 357
+// (T = 8192, 8 adapters of rank 64 in every tile).  They are left to warps that take
+// the stages in turn.
 //
 // Measured: T = 8192, K = 3584, N = 7168, 8 adapters of rank 64: 241 us in this
 // kernel, 258 with the shrink before it (1.68 PFLOP/s; 1.79 in this kernel, where
@@ -44,8 +52,14 @@ namespace {
 constexpr int kTlRows = 256;                 // tokens of a tile, 128 to a CTA
 constexpr int kTlABytes = 128 * 64 * 2;      // the CTA's half of a stage's A
 constexpr int kTlStages = 6;
-constexpr int kTlThreads = 320;
 constexpr int kFillWarp0 = 6;
+constexpr int kPassWarp0 = 10;
+
+// Four warps hand over; two at ranks over 32, where a stage's MMAs take longer and
+// more threads would leave too few registers (T = 8192, 8 adapters of rank 64:
+// 362 us with two, 382 with four; T = 512, 64 of rank 16: 109 and 105).
+constexpr int pass_warps(bool wide) { return wide ? 2 : 4; }
+constexpr int tile_threads(bool wide) { return 32 * (kPassWarp0 + pass_warps(wide)); }
 
 template <int BN>
 struct TileShape {
@@ -57,11 +71,6 @@ struct TileShape {
   static_assert(fills_half_sm(kSmem), "CTAs of two pair kernels must not meet on an SM");
   static_assert(kSmem >= kTileSmemLeast, "what the shrink kernel counts with");
 };
-
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
-               : "memory");
-}
 
 // 2-D tensor copy into this CTA's shared memory whose completion is counted on
 // a barrier of either CTA of the pair (a shared::cluster address).
@@ -134,20 +143,23 @@ constexpr int kBadRing = 8;
 
 // WIDE: R > 32, a hi and a lo stage for every 64 columns of the rank.
 template <int BN, bool WIDE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 1)
     adapter_tile_kernel(const __grid_constant__ CUtensorMap mx,
                         const __grid_constant__ CUtensorMap mw,
                         const __grid_constant__ CUtensorMap mb, const AdapterArgs a, int* status,
                         long long wait_ns) {
   grid_launch_dependents();
   using S = TileShape<BN>;
+  constexpr int kThreads = tile_threads(WIDE), kPassWarps = pass_warps(WIDE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t full[kTlStages];   // rank 0: both CTAs' copies and A warps
+  __shared__ __align__(8) uint64_t full[kTlStages];   // rank 0: both CTAs' operands are there
   __shared__ __align__(8) uint64_t sfree[kTlStages];  // the stage's MMAs are done
   __shared__ __align__(8) uint64_t sgo[kTlStages];    // a low-rank stage's slot is free
   __shared__ __align__(8) uint64_t bland[kTlStages];  // and its B (this CTA's half) there
+  __shared__ __align__(8) uint64_t awrote[kTlStages];  // and its A, and B looked over
+  __shared__ __align__(8) uint64_t passed[kTlStages];  // rank 0: the same in rank 1
   __shared__ __align__(8) uint64_t accfull[2], accempty[2], listfull[2], listempty[2], mma_done;
   __shared__ uint32_t tmem_slot;
   __shared__ int cta_abort;
@@ -159,22 +171,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTlStages; ++s) {
-      mbar_init(&full[s], 9);  // rank 0's producer, and four A warps of each CTA
+      mbar_init(&full[s], 2);  // rank 0's producer, and the warp that hands over
       mbar_init(&sfree[s], 1);
       mbar_init(&sgo[s], 1);
       mbar_init(&bland[s], 1);
+      mbar_init(&awrote[s], 4);
+      mbar_init(&passed[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
       mbar_init(&accempty[b], 8);  // rank 0: the epilogue warps of both CTAs
       mbar_init(&listfull[b], 4);
-      mbar_init(&listempty[b], rank == 0 ? 6 : 5);  // producer, epilogue warps, rank 0's MMA warp
+      // producer, epilogue warps, warps 10 and up, rank 0's MMA warp
+      mbar_init(&listempty[b], 5 + kPassWarps + (rank == 0 ? 1 : 0));
     }
     mbar_init(&mma_done, 1);
     cta_abort = 0;
     fence_mbarrier_init();
   }
-  for (int i = threadIdx.x; i < kBadRing * kTlRows; i += kTlThreads) (&bad[0][0])[i] = 0;
+  for (int i = threadIdx.x; i < kBadRing * kTlRows; i += kThreads) (&bad[0][0])[i] = 0;
   if (warp == 1) {
     tmem_alloc_pair(&tmem_slot, 512);
     tmem_relinquish_pair();
@@ -213,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
           uint8_t* st = smem + s * S::kStageBytes;
           if (rank == 0) {
             mbar_arrive_expect_tx(&full[s], 2 * S::kStageBytes);
-            mbar_arrive_n(&full[s], 8);
+            mbar_arrive(&full[s]);
           }
           tma_pair_g2s_2d(st, &mx, full0 + 8u * s, k * 64, m0);
           tma_pair_g2s_2d(st + kTlABytes, &mw, full0 + 8u * s, k * 64, n0);
@@ -311,7 +326,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
                                        mbar_wait(&listfull[b], ph, wt)))
         break;
       tc_fence_after();
-      // adapters with a row of lora_b that is not finite: by hand, below
+      // adapters with a row of lora_b that is not finite: by hand, below (the other
+      // CTA's flags were written before the accumulator's last MMA)
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");
       const TileList& l = lists[b];
       const int d = l.of_row[32 * q + lane];
       const bool by_hand =
@@ -364,10 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&listempty[b]);
     }
-  } else {
+  } else if (warp < kPassWarp0) {
     // --------------------------- the tile's adapters and the low-rank A operand
     const int i = threadIdx.x - 32 * kFillWarp0;  // row of this CTA
-    const uint32_t leader_full = mapa_shared(full, 0);
     uint32_t it = 0, uc = 0, gpar = 0, bpar = 0;  // parities of sgo[s] and bland[s], bit s
     bool ok = true;
     grid_wait();  // the low-rank vectors are complete
@@ -431,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
       const int n = l.n;
       const int row = m0 + static_cast<int>(rank) * 128 + i;
       it += ksteps;
-      // Looks over the B of slot s and hands the stage to the MMA warp.
+      // Looks over the B of slot s, after which the stage's operands are there.
       auto finish = [&](int s, int d) {
         const bool got = mbar_wait(&bland[s], (bpar >> s) & 1u, wt);
         bpar ^= 1u << s;
@@ -458,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
         }
         fence_async_smem();  // this row of A and of B, for the MMAs
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(leader_full + 8u * s);
+        if (lane == 0) mbar_arrive(&awrote[s]);
         return true;
       };
       int last = -1, last_d = 0;  // the stage whose A is written and B not yet seen
@@ -517,6 +533,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTlThreads, 1)
       }
       if (ok && last >= 0) ok = finish(last, last_d);
     }
+  } else if (lane == 0) {
+    // ------------------- low-rank stages, every kPassWarps-th, to the MMA warp
+    const uint32_t leader_passed = mapa_shared(passed, 0);
+    uint32_t it = 0, uc = 0, par = 0, count = 0;  // par: parities of awrote[s] and passed[s]
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs, ++uc) {
+      const int b = uc & 1;
+      if (!mbar_wait(&listfull[b], (uc >> 1) & 1u, wt)) break;
+      const int stages = lists[b].n * blocks * parts;
+      mbar_arrive(&listempty[b]);
+      it += ksteps;
+      for (int e = 0; e < stages; ++e, ++it, ++count) {
+        const int s = it % kTlStages;
+        const uint32_t ph = (par >> s) & 1u;
+        par ^= 1u << s;
+        if (count % kPassWarps != static_cast<uint32_t>(warp - kPassWarp0)) continue;
+        if (!mbar_wait(&awrote[s], ph, wt) || (rank == 0 && !mbar_wait(&passed[s], ph, wt))) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) {
+          mbar_acquire_cluster(&passed[s], ph);
+          mbar_arrive(&full[s]);
+        } else {
+          mbar_arrive_remote_release(leader_passed + 8u * s);
+        }
+      }
+    }
   }
   // every MMA is done before rank 0 arrives, every copy landed and every
   // epilogue read its accumulators before either CTA passes
@@ -550,7 +594,7 @@ int launch_tile(const AdapterArgs& a, int* status, cudaStream_t st) {
   const long tiles = static_cast<long>((a.N + BN - 1) / BN) * ((a.T + kTlRows - 1) / kTlRows);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long>(tiles, num_sms() / 2)));
-  cfg.blockDim = dim3(kTlThreads);
+  cfg.blockDim = dim3(tile_threads(WIDE));
   cfg.dynamicSmemBytes = TileShape<BN>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
