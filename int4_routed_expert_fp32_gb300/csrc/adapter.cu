@@ -309,8 +309,9 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
   // tile [tokens][128 columns of y]
   __syncthreads();
   mbar_drain(&done, 0, status);  // complete: each reader observes it for itself
-  tc_fence_after();
   if (threadIdx.x == 64) fetch_wave(1);  // its buffer may be part of the ring
+  __syncwarp();
+  tc_fence_after();
   float* red = reinterpret_cast<float*>(smem);
   // this rank's low-rank vectors as bf16 hi and lo parts: [token][2][R]
   uint16_t* lows = FUSED ? lowv : reinterpret_cast<uint16_t*>(red + tb * 128);
@@ -388,6 +389,7 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
     const uint8_t* buf = smem + (w & 1 ? sh.buf1 : sh.buf0);
     // (not a wait that gives up with the CTA: the copies are in flight)
     if (slots > 0) mbar_drain(&bfull[w & 1], (w >> 1) & 1u, status);
+    __syncwarp();
     for (int j = j0 + warp; j < j1; j += kSpThreads / 32) {
       const int i = order[p0 + j], slot = slot_of[j];
       float4 o[kSpMaxCluster];
@@ -416,6 +418,7 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
               (static_cast<uint32_t>(f32_to_bf16_bits(v.w + s.w)) << 16);
         *reinterpret_cast<uint2*>(a.y + static_cast<size_t>(t0 + i) * a.N + n) = q;
       }
+      __syncwarp();  // whole again for the next token's MMAs
     }
     j0 = j1;
     if (w + 2 < waves) {  // the wave's buffer takes the one after next
@@ -424,6 +427,7 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
       if (threadIdx.x == 64) fetch_wave(w + 2);
     }
   }
+  __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its tile
 }
 

@@ -198,6 +198,7 @@ __device__ __forceinline__ void shrink_item(const uint16_t* x, const uint16_t* A
             if (16 * m + 8 * h < R) o[16 * m + 8 * h] = acc[m][n][2 * h + e];
       }
     }
+  __syncwarp();  // whole again for the next token's MMAs
 }
 
 }  // namespace moe

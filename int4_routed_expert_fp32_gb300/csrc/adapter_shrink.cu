@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
         if (!__any_sync(0xffffffffu, mine == d)) continue;
         for (int c = 0; c < s.R; c += 8) {
           uint32_t r[8];
+          __syncwarp();  // the lanes of other adapters went past the last stores
           tmem_ld8(tbase + (static_cast<uint32_t>(32 * q) << 16) + (d - d0) * s.R + c, r);
           tmem_ld_wait();
           if (mine == d) {
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     *reinterpret_cast<float4*>(s.low + static_cast<size_t>(t0 + row) * s.R + e) =
         make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
   }
+  __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its sums
 }
 

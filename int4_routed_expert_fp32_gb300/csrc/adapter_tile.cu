@@ -195,6 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
     tmem_relinquish_pair();
   }
   // both CTAs' barriers exist before either CTA arrives on the other's
+  __syncwarp();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -337,6 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
 #pragma unroll 1
       for (int c0 = 0; c0 < BN; c0 += 32) {
         uint32_t r[32];
+        __syncwarp();  // rows beyond T and rows done by hand took their own ways
         tmem_ld32(tbase + (static_cast<uint32_t>(32 * q) << 16) + b * BN + c0, r);
         tmem_ld_wait();
         if (c0 + 32 == BN) {  // the accumulator goes back to the MMA warp
@@ -570,6 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
   cluster_sync_all();
   if (warp == 1) {
     mbar_drain(&mma_done, 0, status);  // rank 0's last commit has arrived here too
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tbase, 512);
   }

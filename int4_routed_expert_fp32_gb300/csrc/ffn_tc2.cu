@@ -129,6 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(MODE), 
     tmem_relinquish_pair();
   }
   // both CTAs' barriers exist before either CTA arrives on the other's
+  __syncwarp();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -396,6 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(MODE), 
   tc_fence_before();
   __syncthreads();
   if (warp == 1) mbar_drain(mma_done, 0, p.status);
+  __syncwarp();
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
