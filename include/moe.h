@@ -628,6 +628,20 @@ int moe_int4_linear_stall_selftest(const void* x, const float* x_scale, const in
                                    int stall_stage, int64_t limit_ns, float* out, void* ws,
                                    size_t ws_bytes, void* stream);
 
+/* For tests: the exit paths of the adapter projection's kernels.  Runs
+ * moe_adapter_linear (same arguments) with a build of one kernel whose copies
+ * stop, and every wait of that kernel limited to `limit_ns` (1e3 .. 5e9) --
+ * `kernel` 0: the kernel of the low-rank vectors, before its copy stage
+ * `stall_stage` (counted per CTA from 0); 1: the projection kernel, likewise;
+ * 2: the projection kernel of few tokens, whose copies of lora_b never come.
+ * The call records MOE_ERR_TIMEOUT and y is not valid; later calls run
+ * normally.  MOE_ERR_UNSUPPORTED where a call of this size runs no such kernel. */
+int moe_adapter_linear_stall_selftest(const uint16_t* x, const uint16_t* w, const uint16_t* lora_a,
+                                      const uint16_t* lora_b, const int32_t* ids,
+                                      const float* scale, int T, int K, int N, int R, int adapters,
+                                      int kernel, int stall_stage, int64_t limit_ns, uint16_t* y,
+                                      void* ws, size_t ws_bytes, void* stream);
+
 /* Which tensor-core kernels run the act_bits 16 expert GEMMs of
  * moe_expert_ffn, moe_layer_forward and moe_int4_linear for prefill-shaped
  * batches.  enable != 0 (the default), where a cluster of two CTAs fits on

@@ -7,7 +7,8 @@ no fallback).  ``int4_routed_expert_fp32_gb300.build`` compiles it.
 """
 import importlib
 
-_BINDING = ("MoeConfig", "MoeError", "MoeLayer", "MoeWeights", "adapter_linear", "block_norm", "check_error", "combine",
+_BINDING = ("MoeConfig", "MoeError", "MoeLayer", "MoeWeights", "adapter_linear",
+            "adapter_linear_stall_selftest", "block_norm", "check_error", "combine",
             "dispatch", "dispatch_noalloc", "expert_ffn", "int4_linear", "int4_linear_partials",
             "int4_linear_stall_selftest", "int4_linear_int16", "quantize_rows_int16",
             "last_cuda_error", "launch_count",

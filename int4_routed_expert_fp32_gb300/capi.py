@@ -148,6 +148,10 @@ SIGNATURES = {
     "moe_adapter_linear": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
                                    c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_size_t,
                                    c_void_p]),
+    "moe_adapter_linear_stall_selftest": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                                  c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                                  c_int, c_int, c_int64, c_void_p, c_void_p,
+                                                  c_size_t, c_void_p]),
 }
 
 
@@ -736,13 +740,8 @@ def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None,
     return x_out, h_out
 
 
-def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
-                   ids: torch.Tensor, scale: Optional[torch.Tensor] = None,
-                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """y bf16 [T, N] = x w^T + scale[a] (x lora_a[a]^T) lora_b[a]^T with a =
-    ids[t] for each row t (-1: no adapter): x bf16 [T, K], w bf16 [N, K],
-    lora_a bf16 [adapters, R, K], lora_b bf16 [adapters, N, R], ids int32 [T],
-    scale fp32 [adapters] or None (moe_adapter_linear)."""
+def _adapter_args(x, w, lora_a, lora_b, ids, scale, out):
+    """(T, K, N, R, adapters, device) of ``adapter_linear``'s tensors, checked."""
     bf16 = torch.bfloat16
     T, K = _arg("x", x, x.shape if x.dim() == 2 else (None, None), bf16).shape
     N = _arg("w", w, (w.shape[0] if w.dim() == 2 else None, K), bf16).shape[0]
@@ -756,8 +755,19 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_
         _arg("out", out, (T, N), bf16)
     dev = _device_of((x, w, lora_a, lora_b, ids, scale, out),
                      ("x", "w", "lora_a", "lora_b", "ids", "scale", "out"))
+    return T, K, N, R, n, dev
+
+
+def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                   ids: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y bf16 [T, N] = x w^T + scale[a] (x lora_a[a]^T) lora_b[a]^T with a =
+    ids[t] for each row t (-1: no adapter): x bf16 [T, K], w bf16 [N, K],
+    lora_a bf16 [adapters, R, K], lora_b bf16 [adapters, N, R], ids int32 [T],
+    scale fp32 [adapters] or None (moe_adapter_linear)."""
+    T, K, N, R, n, dev = _adapter_args(x, w, lora_a, lora_b, ids, scale, out)
     if out is None:
-        out = torch.empty((T, N), dtype=bf16, device=dev)
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
     need = lib.moe_adapter_linear_workspace_size(T, K, N, R)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     rc = lib.moe_adapter_linear(
@@ -767,6 +777,20 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_
     if rc:
         _check("moe_adapter_linear", rc)
     return out
+
+
+def adapter_linear_stall_selftest(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor,
+                                  lora_b: torch.Tensor, ids: torch.Tensor, kernel: int,
+                                  stall_stage: int, limit_ns: int) -> None:
+    """Run adapter_linear with a build of one of its kernels whose copies stop before
+    stage ``stall_stage`` (tests of the exit paths; the device records
+    MOE_ERR_TIMEOUT, read with check_error())."""
+    T, K, N, R, n, dev = _adapter_args(x, w, lora_a, lora_b, ids, None, None)
+    out = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+    ws = _ws(lib.moe_adapter_linear_workspace_size(T, K, N, R), dev)
+    _check("moe_adapter_linear_stall_selftest", lib.moe_adapter_linear_stall_selftest(
+        _p(x), _p(w), _p(lora_a), _p(lora_b), _p(ids), None, T, K, N, R, n, kernel, stall_stage,
+        limit_ns, _p(out), _p(ws), ws.numel(), _stream()))
 
 
 def check_error() -> int:

@@ -141,11 +141,13 @@ __device__ __forceinline__ void expand_token(const uint16_t* b, int rows, int R,
 // memory at the end costs 1 us and more a token, measured.
 // Cluster (x = rank, y, z): rows 128 y of W, tokens tb z; rank j takes the
 // K steps [j n / cluster, (j + 1) n / cluster) of n = ceil(K / 64).
-template <bool FUSED, int THREADS>
+// STALL (tests only): the copies stop before stage stall_at, or (-1) those of B never
+// come.
+template <bool FUSED, int THREADS, bool STALL>
 __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
     adapter_split_kernel(const __grid_constant__ CUtensorMap mw,
                          const __grid_constant__ CUtensorMap mx, const AdapterArgs a,
-                         const SplitShape sh, int* status, long long wait_ns) {
+                         const SplitShape sh, int* status, long long wait_ns, int stall_at) {
   constexpr int kSpThreads = THREADS;
   constexpr int kLowWarps = THREADS / 32 - 2;  // warps 2 and up
   extern __shared__ uint8_t smem_raw[];
@@ -215,6 +217,7 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
     uint64_t* bar = &bfull[w & 1];
     uint8_t* buf = smem + (w & 1 ? sh.buf1 : sh.buf0);
     mbar_arrive_expect_tx(bar, (j1 - j0) * block);
+    if (STALL && stall_at < 0) return;
     for (int j = j0; j < j1; ++j)
       bulk_g2s(buf + (j - j0) * 256 * a.R,
                a.b + (static_cast<size_t>(slot_id[j]) * a.N + n0) * a.R, block, bar);
@@ -225,7 +228,9 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
       uint32_t it = 0;
       for (int k = s0; k < s1; ++k, ++it) {
         const int s = it % stages;
-        if (!mbar_wait(&empty[s], ((it / stages) & 1u) ^ 1u, wt)) break;
+        if ((STALL && static_cast<int>(it) == stall_at) ||
+            !mbar_wait(&empty[s], ((it / stages) & 1u) ^ 1u, wt))
+          break;
         uint8_t* st = smem + s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         tma_g2s_2d(st, &mw, &full[s], k * 64, n0);
@@ -382,15 +387,19 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
   // without an adapter)
   const int n = n0 + 4 * lane;
   const bool on = n < a.N;  // N % 8 == 0: all four columns or none
-  const int waves = max(1, (slots + sh.wave - 1) / sh.wave);
+  const int fetches = (slots + sh.wave - 1) / sh.wave, waves = max(1, fetches);
+  int issued = min(2, fetches);  // waves whose copies thread 64 has issued
   int j0 = 0;
+  bool ok = true;
   for (int w = 0; w < waves; ++w) {
     const int j1 = (w + 1) * sh.wave < slots ? slot_first[(w + 1) * sh.wave] : mine;
     const uint8_t* buf = smem + (w & 1 ? sh.buf1 : sh.buf0);
-    // (not a wait that gives up with the CTA: the copies are in flight)
-    if (slots > 0) mbar_drain(&bfull[w & 1], (w >> 1) & 1u, status);
-    __syncwarp();
-    for (int j = j0 + warp; j < j1; j += kSpThreads / 32) {
+    // A wave whose B does not come is left out with all after it, and no buffer is
+    // filled again: its barrier's phase is still open (the parity of the phase after
+    // next would read as complete, and another arrival is one too many).
+    ok = ok && __all_sync(0xffffffffu,
+                          slots == 0 || mbar_wait(&bfull[w & 1], (w >> 1) & 1u, wt));
+    for (int j = ok ? j0 + warp : j1; j < j1; j += kSpThreads / 32) {
       const int i = order[p0 + j], slot = slot_of[j];
       float4 o[kSpMaxCluster];
 #pragma unroll
@@ -424,9 +433,16 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
     if (w + 2 < waves) {  // the wave's buffer takes the one after next
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
-      if (threadIdx.x == 64) fetch_wave(w + 2);
+      if (threadIdx.x == 64 && ok) {
+        fetch_wave(w + 2);
+        issued = w + 3;
+      }
     }
   }
+  // the copies land before the CTA can leave; on the normal path they have
+  if (threadIdx.x == 64)
+    for (int w = max(0, issued - 2); w < issued; ++w)
+      mbar_drain(&bfull[w & 1], (w >> 1) & 1u, status);
   __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its tile
 }
@@ -511,9 +527,10 @@ SplitShape split_shape(int T, int R, int cluster) {
   return s;
 }
 
-template <bool FUSED, int THREADS>
-int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
-  auto kern = adapter_split_kernel<FUSED, THREADS>;
+template <bool FUSED, int THREADS, bool STALL = false>
+int launch_split(const AdapterArgs& a, int* status, cudaStream_t st,
+                 const AdapterStall* stall = nullptr) {
+  auto kern = adapter_split_kernel<FUSED, THREADS, STALL>;
   // at most one CTA to an SM (a second one on some would take twice the time),
   // and as many clusters as the device holds at once
   const int tiles = split_tiles(a.T, a.N);
@@ -535,7 +552,8 @@ int launch_split(const AdapterArgs& a, int* status, cudaStream_t st) {
   cudaLaunchAttribute attr[2];
   set_adapter_attrs(&cfg, attr, sh.cluster);
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, mw, mx, a, sh, status,
-                                  static_cast<long long>(kDefaultWaitNs)));
+                                  STALL ? stall->wait_ns : static_cast<long long>(kDefaultWaitNs),
+                                  !STALL ? 0 : stall->kernel == 2 ? -1 : stall->stage));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -553,11 +571,11 @@ extern "C" size_t moe_adapter_linear_workspace_size(int T, int K, int N, int R) 
   return align_up(static_cast<size_t>(T) * R * sizeof(float), 256);
 }
 
-extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* lora_a,
-                                  const uint16_t* lora_b, const int32_t* ids, const float* scale,
-                                  int T, int K, int N, int R, int adapters, uint16_t* y, void* ws,
-                                  size_t ws_bytes, void* stream) {
-  moe::Range range_("moe_adapter_linear");
+// moe_adapter_linear; stall: moe_adapter_linear_stall_selftest.
+static int adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* lora_a,
+                          const uint16_t* lora_b, const int32_t* ids, const float* scale, int T,
+                          int K, int N, int R, int adapters, uint16_t* y, void* ws,
+                          size_t ws_bytes, const AdapterStall* stall, void* stream) {
   if (T < 0 || K <= 0 || N <= 0 || R <= 0 || adapters <= 0) return MOE_ERR_INVALID;
   if (K % 32 != 0 || N % 8 != 0 || R % 8 != 0 || R > kMaxRank) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -584,10 +602,39 @@ extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const ui
   a.low = static_cast<float*>(ws);
   a.y = y;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (fused(T, R)) return launch_split<true, 256>(a, status, st);
-  const int rc = launch_adapter_shrink(a, status, st);
+  if (fused(T, R)) {
+    if (stall && stall->kernel != 0) return launch_split<true, 256, true>(a, status, st, stall);
+    return launch_split<true, 256>(a, status, st);
+  }
+  const int rc = launch_adapter_shrink(a, status, st, stall);
   if (rc) return rc;
   if (T > kSplitTokens) return launch_adapter_tile(a, status, st);
+  if (stall && stall->kernel != 0)
+    return adapter_beside(T, R) ? launch_split<false, 256, true>(a, status, st, stall)
+                                : launch_split<false, 512, true>(a, status, st, stall);
   return adapter_beside(T, R) ? launch_split<false, 256>(a, status, st)
                               : launch_split<false, 512>(a, status, st);
+}
+
+extern "C" int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* lora_a,
+                                  const uint16_t* lora_b, const int32_t* ids, const float* scale,
+                                  int T, int K, int N, int R, int adapters, uint16_t* y, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  moe::Range range_("moe_adapter_linear");
+  return adapter_linear(x, w, lora_a, lora_b, ids, scale, T, K, N, R, adapters, y, ws, ws_bytes,
+                        nullptr, stream);
+}
+
+extern "C" int moe_adapter_linear_stall_selftest(
+    const uint16_t* x, const uint16_t* w, const uint16_t* lora_a, const uint16_t* lora_b,
+    const int32_t* ids, const float* scale, int T, int K, int N, int R, int adapters, int kernel,
+    int stall_stage, int64_t limit_ns, uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  moe::Range range_("moe_adapter_linear_stall_selftest");
+  if (kernel < 0 || kernel > 2 || stall_stage < 0) return MOE_ERR_INVALID;
+  if (limit_ns < 1000 || limit_ns > 5000000000LL) return MOE_ERR_INVALID;
+  if ((kernel == 0 && fused(T, R)) || (kernel != 0 && T > kSplitTokens))
+    return MOE_ERR_UNSUPPORTED;  // no such kernel in this call
+  const AdapterStall stall{kernel, stall_stage, limit_ns};
+  return adapter_linear(x, w, lora_a, lora_b, ids, scale, T, K, N, R, adapters, y, ws, ws_bytes,
+                        &stall, stream);
 }

@@ -32,8 +32,17 @@ constexpr int kTileSmemLeast = 168 * 1024;  // above: a CTA of adapter_tile_kern
 // 3584), because little shared memory means few adapters to a pass over x.
 inline bool adapter_beside(int T, int R) { return T <= 64 || T * R <= 4096; }
 
+// For tests of the exit paths: the kernel whose copies stop (by a build of its own),
+// the stage before which they do, counted per CTA, and the limit of every wait.
+struct AdapterStall {
+  int kernel;  // 0: the shrink; 1: the projection; 2: the split kernel's copies of B
+  int stage;
+  long long wait_ns;
+};
+
 // low from x, a and scale (adapter_shrink.cu).  Triggers its dependents at once.
-int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st);
+int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st,
+                          const AdapterStall* stall = nullptr);
 
 // The projection with its low-rank term for many tokens (adapter_tile.cu),
 // launched as a programmatic dependent of the shrink.

@@ -120,11 +120,13 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 }  // namespace
 
 // Cluster (rank = x) of CTAs over tile y and passes z, z + gridDim.z, ...; ma:
-// [adapters][R][K], boxes of R rows of one adapter.
+// [adapters][R][K], boxes of R rows of one adapter.  STALL (tests only): the copies
+// stop before stage stall_at.
+template <bool STALL>
 __global__ void __launch_bounds__(kStThreads, 1)
     adapter_shrink_tile_kernel(const __grid_constant__ CUtensorMap mx,
                                const __grid_constant__ CUtensorMap ma, const ShrinkArgs s,
-                               long long wait_ns) {
+                               long long wait_ns, int stall_at) {
   if (threadIdx.x == 0) {
     prefetch_tensor_map(&mx);
     prefetch_tensor_map(&ma);
@@ -198,7 +200,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
         const uint32_t bytes = xbytes + (d1 - d0) * s.R * 128;
         for (int k = s0; k < s1; ++k, ++it) {
           const int i = it % stages;
-          if (!mbar_wait(&empty[i], ((it / stages) & 1u) ^ 1u, wt)) {
+          if ((STALL && static_cast<int>(it) == stall_at) ||
+              !mbar_wait(&empty[i], ((it / stages) & 1u) ^ 1u, wt)) {
             ok = false;
             break;
           }
@@ -331,7 +334,10 @@ static_assert(shrink_fills_sm(), "a tile CTA could keep the tensor memory that t
 
 }  // namespace
 
-int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
+int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st,
+                          const AdapterStall* stall) {
+  const bool stop = stall && stall->kernel == 0;
+  auto kern = stop ? adapter_shrink_tile_kernel<true> : adapter_shrink_tile_kernel<false>;
   ShrinkArgs s{};
   s.x = a.x;
   s.a = a.a;
@@ -369,11 +375,10 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
   }
   s.stages = shrink_stages(bytes, s.per, s.R, s.xrows);
   const int smem = s.stages * shrink_slot(s.per, s.R, s.xrows) + fixed;
-  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(adapter_shrink_tile_kernel)));
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
   int ranks = 1;
-  MOE_TRY_CUDA(adapter_cluster(reinterpret_cast<const void*>(adapter_shrink_tile_kernel),
-                               kStThreads, smem, tiles * groups, std::min(kShMaxCluster, steps),
-                               &ranks));
+  MOE_TRY_CUDA(adapter_cluster(reinterpret_cast<const void*>(kern), kStThreads, smem,
+                               tiles * groups, std::min(kShMaxCluster, steps), &ranks));
   CUtensorMap mx, ma;
   const uint64_t dims[3] = {static_cast<uint64_t>(s.K), static_cast<uint64_t>(s.R),
                             static_cast<uint64_t>(s.adapters)};
@@ -391,8 +396,9 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st) {
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   set_adapter_attrs(&cfg, attr, ranks);
-  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, adapter_shrink_tile_kernel, mx, ma, s,
-                                  static_cast<long long>(kDefaultWaitNs)));
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, mx, ma, s,
+                                  stop ? stall->wait_ns : static_cast<long long>(kDefaultWaitNs),
+                                  stop ? stall->stage : 0));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -269,3 +269,21 @@ def test_moe_block_refuses_weights_that_it_would_drop(capi, monkeypatch):
     raises("router_w is required", MoeBlock, {n: w[n] for n in capi.EXPERT_NAMES}, 2)
     terms = bf16(3, 16, 64)
     assert MoeBlock({**w, "router_w_terms": terms}, 2).w_terms is terms
+
+
+def test_adapter_stall_selftest_refusals(capi):
+    L, n = capi.lib, capi.launch_count()
+    bad, uns = capi.MOE_ERR_INVALID, capi.MOE_ERR_UNSUPPORTED
+
+    def call(T=9, R=8, kernel=1, stage=0, limit=20_000_000, x=FAKE, ws_bytes=1 << 30):
+        return L.moe_adapter_linear_stall_selftest(x, FAKE, FAKE, FAKE, FAKE, None, T, 64, 24, R, 3,
+                                                   kernel, stage, limit, FAKE, FAKE, ws_bytes,
+                                                   None)
+
+    for kw in (dict(kernel=-1), dict(kernel=3), dict(stage=-1), dict(limit=999),
+               dict(limit=5_000_000_001), dict(x=None), dict(T=-1)):
+        assert call(**kw) == bad, kw
+    for kw in (dict(T=1, R=16, kernel=0), dict(T=300, kernel=2), dict(R=12)):
+        assert call(**kw) == uns, kw
+    assert call(ws_bytes=0) == capi.MOE_ERR_WORKSPACE
+    assert capi.launch_count() == n

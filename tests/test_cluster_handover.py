@@ -28,8 +28,8 @@ def test_operands_written_by_threads_are_released_and_acquired_at_cluster_scope(
 
 
 ALIGNED = r"\b(tmem_ld\d+\(|tmem_dealloc\w*\(|cluster_sync_all\(|expand_token\()"
-WHOLE = r"\b(__syncwarp\(|__syncthreads\(|__all_sync\(|__any_sync\(|cluster_sync_all\()"
-APART = r"\bmbar_drain\(|\bmbar_wait\(|\bif \((?!warp\b|constexpr|w \+ 2|slots? >=? 0\)|r < ranks\))"
+WHOLE = r"\b(__syncwarp\(|__syncthreads\(|__all_sync\([^;{]*|__any_sync\(|cluster_sync_all\()"
+APART = r"\bmbar_drain\(|\bmbar_wait\(|\bif \((?!warp\b|constexpr|w \+ 2|threadIdx.x == 64 && ok|slots? >=? 0\)|r < ranks\))"
 
 
 @pytest.mark.parametrize("name", ["adapter_tile_kernel", "adapter_split_kernel",
@@ -54,5 +54,5 @@ def test_warps_are_whole_before_instructions_that_take_whole_warps(name):
         loop = body[body.index(head):]
         assert re.search(WHOLE, loop[:loop.index(op)])
     if name == "adapter_split_kernel":
-        loop = body[body.index("for (int j = j0 + warp"):]
+        loop = body[body.index("for (int j = ok ? j0 + warp"):]
         assert "__syncwarp();" in loop[loop.index("if (on)"):loop.index("j0 = j1")]
