@@ -608,7 +608,7 @@ static int adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* 
   }
   const int rc = launch_adapter_shrink(a, status, st, stall);
   if (rc) return rc;
-  if (T > kSplitTokens) return launch_adapter_tile(a, status, st);
+  if (T > kSplitTokens) return launch_adapter_tile(a, status, st, stall);
   if (stall && stall->kernel != 0)
     return adapter_beside(T, R) ? launch_split<false, 256, true>(a, status, st, stall)
                                 : launch_split<false, 512, true>(a, status, st, stall);
@@ -632,7 +632,7 @@ extern "C" int moe_adapter_linear_stall_selftest(
   moe::Range range_("moe_adapter_linear_stall_selftest");
   if (kernel < 0 || kernel > 2 || stall_stage < 0) return MOE_ERR_INVALID;
   if (limit_ns < 1000 || limit_ns > 5000000000LL) return MOE_ERR_INVALID;
-  if ((kernel == 0 && fused(T, R)) || (kernel != 0 && T > kSplitTokens))
+  if ((kernel == 0 && fused(T, R)) || (kernel == 2 && T > kSplitTokens))
     return MOE_ERR_UNSUPPORTED;  // no such kernel in this call
   const AdapterStall stall{kernel, stall_stage, limit_ns};
   return adapter_linear(x, w, lora_a, lora_b, ids, scale, T, K, N, R, adapters, y, ws, ws_bytes,

@@ -46,7 +46,8 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st,
 
 // The projection with its low-rank term for many tokens (adapter_tile.cu),
 // launched as a programmatic dependent of the shrink.
-int launch_adapter_tile(const AdapterArgs& a, int* status, cudaStream_t st);
+int launch_adapter_tile(const AdapterArgs& a, int* status, cudaStream_t st,
+                        const AdapterStall* stall = nullptr);
 
 // Tensor map of [rows][cols] bf16: boxes of 64 columns and box_rows rows, with
 // the 128-byte swizzle.

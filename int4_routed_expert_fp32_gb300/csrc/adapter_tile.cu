@@ -139,15 +139,26 @@ static_assert(sizeof(TileList) % 16 == 0, "ids is read in 16-byte vectors");
 // the epilogue look at the rows for itself.
 constexpr int kBadRing = 8;
 
+// On the error path of rank 1: its copies of x and W count on rank 0's barriers,
+// where those of a stage that rank 0 never armed cannot be waited for.  A copy takes
+// a microsecond or two; its issuer stays this long after the last.
+constexpr int64_t kSettleNs = 10000000;
+
+__device__ __forceinline__ void settle_copies() {
+  const uint64_t t0 = global_timer_ns();
+  while (static_cast<int64_t>(global_timer_ns() - t0) < kSettleNs) __nanosleep(10000);
+}
+
 }  // namespace
 
-// WIDE: R > 32, a hi and a lo stage for every 64 columns of the rank.
-template <int BN, bool WIDE>
+// WIDE: R > 32, a hi and a lo stage for every 64 columns of the rank.  STALL (tests
+// only): each CTA's copies stop before stage stall_at.
+template <int BN, bool WIDE, bool STALL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 1)
     adapter_tile_kernel(const __grid_constant__ CUtensorMap mx,
                         const __grid_constant__ CUtensorMap mw,
                         const __grid_constant__ CUtensorMap mb, const AdapterArgs a, int* status,
-                        long long wait_ns) {
+                        long long wait_ns, int stall_at) {
   grid_launch_dependents();
   using S = TileShape<BN>;
   constexpr int kThreads = tile_threads(WIDE), kPassWarps = pass_warps(WIDE);
@@ -216,13 +227,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
       prefetch_tensor_map(&mb);
       const uint32_t full0 = mapa_shared(full, 0);
       uint32_t it = 0, uc = 0;
+      uint32_t bused = 0, bpar = 0;  // slots that held a B, and the parity of the next use
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs, ++uc) {
         const int n0 = (t % tn) * BN + static_cast<int>(rank) * S::kBRows;
         const int m0 = (t / tn) * kTlRows + static_cast<int>(rank) * 128;
         for (int k = 0; k < ksteps; ++k, ++it) {
           const int s = it % kTlStages;
-          if (!mbar_wait(&sfree[s], ((it / kTlStages) & 1u) ^ 1u, wt)) {
+          if ((STALL && static_cast<int>(it) == stall_at) ||
+              !mbar_wait(&sfree[s], ((it / kTlStages) & 1u) ^ 1u, wt)) {
             ok = false;
             break;
           }
@@ -236,12 +249,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
         }
         if (!ok) break;
         const int b = uc & 1;
-        if (!mbar_wait(&listfull[b], (uc >> 1) & 1u, wt)) break;
+        if (!mbar_wait(&listfull[b], (uc >> 1) & 1u, wt)) {
+          ok = false;
+          break;
+        }
         const TileList& l = lists[b];
         const int stages = l.n * blocks * parts;
         for (int e = 0; e < stages; ++e, ++it) {
           const int s = it % kTlStages;
-          if (!mbar_wait(&sfree[s], ((it / kTlStages) & 1u) ^ 1u, wt)) {
+          if ((STALL && static_cast<int>(it) == stall_at) ||
+              !mbar_wait(&sfree[s], ((it / kTlStages) & 1u) ^ 1u, wt)) {
             ok = false;
             break;
           }
@@ -250,13 +267,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
           mbar_arrive_expect_tx(&bland[s], S::kBBytes);
           tma_g2s_3d(smem + s * S::kStageBytes + kTlABytes, &mb, &bland[s], 64 * blk, n0,
                      l.adapter[d]);
+          bused |= 1u << s;
+          bpar ^= 1u << s;
           if (rank == 0) mbar_arrive(&full[s]);
         }
         mbar_arrive(&listempty[b]);
       }
       // the issued copies land before the pair can leave: rank 0 sees both
-      // CTAs' on its barriers, and the closing cluster barrier holds rank 1
-      if (rank == 0) drain_ring(full, it, kTlStages, status);
+      // CTAs' on its barriers, and the closing cluster barrier holds rank 1.  B's land
+      // on the CTA's own; the A warps have seen them unless they gave up
+      for (int s = 0; s < kTlStages; ++s)
+        if ((bused >> s) & 1u) mbar_drain(&bland[s], ((bpar >> s) & 1u) ^ 1u, status);
+      if (rank == 0)
+        drain_ring(full, it, kTlStages, status);
+      else if (!ok)
+        settle_copies();
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
@@ -580,8 +605,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
 
 namespace {
 
-template <int BN, bool WIDE>
-int launch_tile(const AdapterArgs& a, int* status, cudaStream_t st) {
+template <int BN, bool WIDE, bool STALL = false>
+int launch_tile(const AdapterArgs& a, int* status, cudaStream_t st,
+                const AdapterStall* stall = nullptr) {
   CUtensorMap mx, mw, mb;
   const uint64_t dims[3] = {static_cast<uint64_t>(a.R), static_cast<uint64_t>(a.N),
                             static_cast<uint64_t>(a.adapters)};
@@ -592,7 +618,7 @@ int launch_tile(const AdapterArgs& a, int* status, cudaStream_t st) {
       !encode_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.b, dims, strides, box,
                          CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_ERR_CUDA;
-  auto kern = adapter_tile_kernel<BN, WIDE>;
+  auto kern = adapter_tile_kernel<BN, WIDE, STALL>;
   MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
   const long tiles = static_cast<long>((a.N + BN - 1) / BN) * ((a.T + kTlRows - 1) / kTlRows);
   cudaLaunchConfig_t cfg{};
@@ -603,14 +629,19 @@ int launch_tile(const AdapterArgs& a, int* status, cudaStream_t st) {
   cudaLaunchAttribute attr[2];
   set_adapter_attrs(&cfg, attr, 0);  // the cluster is the kernel's own
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, mx, mw, mb, a, status,
-                                  static_cast<long long>(kDefaultWaitNs)));
+                                  STALL ? stall->wait_ns : static_cast<long long>(kDefaultWaitNs),
+                                  STALL ? stall->stage : 0));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
 
 }  // namespace
 
-int launch_adapter_tile(const AdapterArgs& a, int* status, cudaStream_t st) {
+int launch_adapter_tile(const AdapterArgs& a, int* status, cudaStream_t st,
+                        const AdapterStall* stall) {
+  if (stall && stall->kernel == 1)  // one width of the two
+    return a.R > 32 ? launch_tile<192, true, true>(a, status, st, stall)
+                    : launch_tile<192, false, true>(a, status, st, stall);
   // the width whose last wave of tiles leaves fewer columns idle
   const long pairs = num_sms() / 2, tm = (a.T + kTlRows - 1) / kTlRows;
   auto cost = [&](long bn) {

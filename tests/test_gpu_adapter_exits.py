@@ -67,3 +67,10 @@ def test_split_projection_whose_copies_stop(moe, T, R, stage):
 @pytest.mark.parametrize("T,R,n", [(1, 16, 1), (8, 8, 5), (64, 64, 60), (200, 128, 150)])
 def test_split_projection_whose_low_rank_rows_never_come(moe, T, R, n):
     check(moe, inputs(T, 512, 264, R, n), 2, 0)
+
+
+# K = 2048 is 32 stages; after them come those of the adapters that the tile's rows use
+@pytest.mark.parametrize("stage", [0, 3, 31, 32, 33, 36])
+@pytest.mark.parametrize("T,N,R", [(300, 264, 16), (600, 520, 128), (4100, 4104, 16)])
+def test_tile_projection_whose_copies_stop(moe, T, N, R, stage):
+    check(moe, inputs(T, 2048, N, R, 5), 1, stage)
