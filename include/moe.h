@@ -488,7 +488,8 @@ int moe_block_norm(const moe_block_norm_args* args, void* stream);
  *   scale   fp32 [adapters] or NULL (1)
  * K % 32 == 0, N % 8 == 0, R % 8 == 0 and R <= 128, else MOE_ERR_UNSUPPORTED.
  * All tensors 16-byte aligned (ids and scale 4), ws 256 (NULL where the size is
- * 0: a few tokens of low rank need none). */
+ * 0: a few tokens of low rank need none).  y and ws share no byte with each other
+ * or with an input, else MOE_ERR_INVALID. */
 size_t moe_adapter_linear_workspace_size(int T, int K, int N, int R);
 int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* lora_a,
                        const uint16_t* lora_b, const int32_t* ids, const float* scale, int T, int K,

@@ -275,6 +275,16 @@ def _ld(t: torch.Tensor) -> int:
     return max(t.stride(0), cols) if rows > 1 else cols
 
 
+def _apart(name: str, out: torch.Tensor, **inputs: Optional[torch.Tensor]) -> None:
+    """Refuse an output that shares memory with an input (contiguous tensors)."""
+    a, n = out.data_ptr(), out.numel() * out.element_size()
+    for other, t in inputs.items():
+        if t is not None:
+            b, m = t.data_ptr(), t.numel() * t.element_size()
+            if n and m and a < b + m and b < a + n and t.device == out.device:
+                raise ValueError(f"{name} must not share memory with {other}")
+
+
 _DEVICES: Dict[int, torch.device] = {}
 
 
@@ -753,6 +763,7 @@ def _adapter_args(x, w, lora_a, lora_b, ids, scale, out):
         _arg("scale", scale, (n,), torch.float32)
     if out is not None:
         _arg("out", out, (T, N), bf16)
+        _apart("out", out, x=x, w=w, lora_a=lora_a, lora_b=lora_b, ids=ids, scale=scale)
     dev = _device_of((x, w, lora_a, lora_b, ids, scale, out),
                      ("x", "w", "lora_a", "lora_b", "ids", "scale", "out"))
     return T, K, N, R, n, dev
@@ -764,7 +775,8 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_
     """y bf16 [T, N] = x w^T + scale[a] (x lora_a[a]^T) lora_b[a]^T with a =
     ids[t] for each row t (-1: no adapter): x bf16 [T, K], w bf16 [N, K],
     lora_a bf16 [adapters, R, K], lora_b bf16 [adapters, N, R], ids int32 [T],
-    scale fp32 [adapters] or None (moe_adapter_linear)."""
+    scale fp32 [adapters] or None (moe_adapter_linear).  out must not share memory
+    with an input."""
     T, K, N, R, n, dev = _adapter_args(x, w, lora_a, lora_b, ids, scale, out)
     if out is None:
         out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)

@@ -585,6 +585,21 @@ static int adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* 
       !aligned(ids, 4) || !aligned(scale, 4) || !aligned(y, 16) || !aligned(ws, 256))
     return MOE_ERR_INVALID;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  // CTAs write y and the workspace while others still read the inputs
+  const size_t y_bytes = static_cast<size_t>(T) * N * 2;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } inputs[] = {{x, static_cast<size_t>(T) * K * 2},
+                {w, static_cast<size_t>(N) * K * 2},
+                {lora_a, static_cast<size_t>(adapters) * R * K * 2},
+                {lora_b, static_cast<size_t>(adapters) * N * R * 2},
+                {ids, static_cast<size_t>(T) * 4},
+                {scale, scale ? static_cast<size_t>(adapters) * 4 : 0}};
+  for (const auto& in : inputs)
+    if (overlap(in.p, in.bytes, y, y_bytes) || overlap(in.p, in.bytes, ws, need))
+      return MOE_ERR_INVALID;
+  if (overlap(y, y_bytes, ws, need)) return MOE_ERR_INVALID;
   int* status = status_word();
   if (!status) return MOE_ERR_CUDA;
   AdapterArgs a{};

@@ -42,6 +42,12 @@ void count_launch();
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two stretches of memory have a byte in common (empty ones have none).
+inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return np && nq && (a <= b ? b - a < np : a - b < nq);
+}
+
 // Names a stretch of host code (one C-ABI call, or one stage of the layer) in
 // a profiler's timeline: an NVTX range on the calling thread, open for the
 // object's lifetime.  Without an attached tool NVTX calls return at once;

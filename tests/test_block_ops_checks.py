@@ -287,3 +287,36 @@ def test_adapter_stall_selftest_refusals(capi):
         assert call(**kw) == uns, kw
     assert call(ws_bytes=0) == capi.MOE_ERR_WORKSPACE
     assert capi.launch_count() == n
+
+
+def test_adapter_linear_refuses_overlapping_memory(capi):
+    """CTAs write y while others read the inputs: y over any of them, or the workspace
+    over any, is refused (adjacent memory is not)."""
+    T, K, N, R, n = 9, 64, 64, 8, 3
+    sizes = dict(x=T * K * 2, w=N * K * 2, a=n * R * K * 2, b=n * N * R * 2, ids=T * 4,
+                 scale=n * 4, y=T * N * 2, ws=int(capi.lib.moe_adapter_linear_workspace_size(
+                     T, K, N, R)))
+    apart = {name: FAKE * (i + 1) for i, name in enumerate(sizes)}
+    n0 = capi.launch_count()
+
+    def call(**at):
+        p = {**apart, **at}
+        return capi.lib.moe_adapter_linear(p["x"], p["w"], p["a"], p["b"], p["ids"], p["scale"],
+                                           T, K, N, R, n, p["y"], p["ws"], sizes["ws"], None)
+
+    for name in sizes:
+        if name == "y":
+            continue
+        step = 256 if name == "ws" else 16
+        for y in (apart[name], apart[name] + (sizes[name] - 1) // step * step,
+                  apart[name] - (sizes["y"] - 1) // step * step):
+            assert call(y=y) == capi.MOE_ERR_INVALID, (name, y)
+        if name != "ws":
+            assert call(ws=apart[name]) == capi.MOE_ERR_INVALID, name
+    x = bf16(T, K)
+    w, a, b, ids = bf16(N, K), bf16(n, R, K), bf16(n, N, R), torch.zeros(T, dtype=torch.int32)
+    raises("out must not share memory with x", capi.adapter_linear, x, w, a, b, ids, out=x)
+    raises("out must not share memory with w", capi.adapter_linear, x, w, a, b, ids, out=w[5:5 + T])
+    both = bf16(2 * T, K)
+    raises(CUDA_ONLY, capi.adapter_linear, both[:T], w, a, b, ids, out=both[T:])
+    assert capi.launch_count() == n0
