@@ -486,8 +486,8 @@ int moe_block_norm(const moe_block_norm_args* args, void* stream);
  *   ids     int32 [T], any order and repetition; a value outside
  *           [-1, adapters) selects no adapter and records MOE_ERR_INVALID
  *   scale   fp32 [adapters] or NULL (1)
- * K % 32 == 0, N % 8 == 0, R % 8 == 0 and R <= 128, else MOE_ERR_UNSUPPORTED.
- * All tensors 16-byte aligned (ids and scale 4), ws 256 (NULL where the size is
+ * K % 32 == 0, N % 8 == 0, R % 8 == 0 and R <= 128, T and N at most 65535 * 128,
+ * else MOE_ERR_UNSUPPORTED.  All tensors 16-byte aligned (ids and scale 4), ws 256 (NULL where the size is
  * 0: a few tokens of low rank need none).  y and ws share no byte with each other
  * or with an input, else MOE_ERR_INVALID. */
 size_t moe_adapter_linear_workspace_size(int T, int K, int N, int R);

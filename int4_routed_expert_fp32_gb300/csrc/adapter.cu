@@ -47,6 +47,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxRank = 128;
+constexpr int kMaxExtent = 65535 * 128;  // tokens, and columns: blocks of 128 in a grid's y
 
 constexpr int kSpTokens = 128;   // tokens to a block, at most
 constexpr int kSpWBytes = 128 * 64 * 2;
@@ -578,6 +579,7 @@ static int adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* 
                           size_t ws_bytes, const AdapterStall* stall, void* stream) {
   if (T < 0 || K <= 0 || N <= 0 || R <= 0 || adapters <= 0) return MOE_ERR_INVALID;
   if (K % 32 != 0 || N % 8 != 0 || R % 8 != 0 || R > kMaxRank) return MOE_ERR_UNSUPPORTED;
+  if (T > kMaxExtent || N > kMaxExtent) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   const size_t need = moe_adapter_linear_workspace_size(T, K, N, R);
   if (!x || !w || !lora_a || !lora_b || !ids || !y || (need && !ws)) return MOE_ERR_INVALID;

@@ -320,3 +320,16 @@ def test_adapter_linear_refuses_overlapping_memory(capi):
     both = bf16(2 * T, K)
     raises(CUDA_ONLY, capi.adapter_linear, both[:T], w, a, b, ids, out=both[T:])
     assert capi.launch_count() == n0
+
+
+def test_adapter_linear_refuses_more_tokens_or_columns_than_a_grid_has(capi):
+    L, n = capi.lib, capi.launch_count()
+    far = 1 << 50   # apart from FAKE by more than any of these tensors is long
+
+    def call(T, N):
+        return L.moe_adapter_linear(FAKE, FAKE, FAKE, FAKE, FAKE, None, T, 64, N, 8, 3, far,
+                                    2 * far, 1 << 40, None)
+
+    for T, N in ((65535 * 128 + 1, 24), (2 ** 31 - 1, 24), (9, 65535 * 128 + 8)):
+        assert call(T, N) == capi.MOE_ERR_UNSUPPORTED, (T, N)
+    assert capi.launch_count() == n
