@@ -150,9 +150,10 @@ int moe_router_prepare(const float* w_router, int E, int H, uint16_t* w_terms, v
  *   the topk_groups best groups are kept, and of their experts the k with the
  *   largest c, in descending order (equal: lower id first, groups too)
  *   w = s (unbiased); w /= sum w + 1e-20 if renorm; w *= scale
- * The choice is that of 64-bit scores: fp32 scores decide where they can, and
- * experts whose fp32 keys are within their rounding of one another are
- * compared again in 64 bits.
+ * The choice is that of 64-bit scores: fp32 scores decide where they can.
+ * Experts whose fp32 keys are within their rounding of one another are compared
+ * again, biased sigmoid keys as unevaluated pairs of fp32 values, and in 64 bits
+ * what that leaves open and every other kind of key.
  * Unavailable experts: a logit of -inf or NaN, or a bias of -inf or NaN.  They
  * rank below every other expert of the kept groups, count nothing in a
  * group's score, and get weight 0 where they have to fill up the k (a row
@@ -487,9 +488,9 @@ int moe_block_norm(const moe_block_norm_args* args, void* stream);
  *           [-1, adapters) selects no adapter and records MOE_ERR_INVALID
  *   scale   fp32 [adapters] or NULL (1)
  * K % 32 == 0, N % 8 == 0, R % 8 == 0 and R <= 128, T and N at most 65535 * 128,
- * else MOE_ERR_UNSUPPORTED.  All tensors 16-byte aligned (ids and scale 4), ws 256 (NULL where the size is
- * 0: a few tokens of low rank need none).  y and ws share no byte with each other
- * or with an input, else MOE_ERR_INVALID. */
+ * else MOE_ERR_UNSUPPORTED.  All tensors 16-byte aligned (ids and scale 4), ws 256
+ * (NULL where the size is 0: a few tokens of low rank need none).  y and ws share
+ * no byte with each other or with an input, else MOE_ERR_INVALID. */
 size_t moe_adapter_linear_workspace_size(int T, int K, int N, int R);
 int moe_adapter_linear(const uint16_t* x, const uint16_t* w, const uint16_t* lora_a,
                        const uint16_t* lora_b, const int32_t* ids, const float* scale, int T, int K,

@@ -72,7 +72,7 @@ struct SplitShape {
 
 // By one warp: out[r] = p b[r]^T for the rows r < rows of b [rows][R] in shared
 // memory (0 up to 128), p given as hi[R] and lo[R].  A lane's 16-byte loads of b
-// (columns 8 (lane % 4) .. + 7 of 32) feed two MMAs, as in shrink_item.
+// (columns 8 (lane % 4) .. + 7 of 32) feed two MMAs, as in shrink_token.
 __device__ __forceinline__ void expand_token(const uint16_t* b, int rows, int R,
                                              const uint16_t* hi, float* out) {
   const int lane = threadIdx.x & 31;
@@ -168,7 +168,6 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
   __shared__ float lowp[kLowWarps + 1][kFusedLow];  // FUSED: the warps' sums, and the CTA's
   __shared__ __align__(16) uint16_t lowv[2 * kFusedLow];  // FUSED: as lows below
   __shared__ __align__(16) float lowout[kSpThreads / 32][128];  // a token's low-rank term
-  __shared__ int16_t low_rows[8];
   const Waiter wt{&cta_abort, status, wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -199,7 +198,6 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
     cta_abort = 0;
     fence_mbarrier_init();
   }
-  if (FUSED && threadIdx.x < 8) low_rows[threadIdx.x] = 0;
   if (warp == 1) {
     tmem_alloc(&tmem_slot, sh.cols);
     tmem_relinquish();
@@ -305,9 +303,9 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
         const uint16_t* x = a.x + static_cast<size_t>(t) * a.K;
         float* out = &lowp[w][t * a.R];
         if (a.R <= 16)
-          shrink_item<1, 1>(x, A, a.K, a.R, low_rows, 1, a0, a1, out);
+          shrink_token<1>(x, A, a.K, a.R, a0, a1, out);
         else
-          shrink_item<4, 1>(x, A, a.K, a.R, low_rows, 1, a0, a1, out);
+          shrink_token<4>(x, A, a.K, a.R, a0, a1, out);
       }
     }
   }

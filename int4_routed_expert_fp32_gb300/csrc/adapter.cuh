@@ -146,39 +146,29 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// By one warp, over the columns [k0, k1): out[p][j] = x[row p] A[j]^T for j < R
-// and the rows p < c <= 8 NT (the low bytes of rows).  The rows of A are the M side of m16n8k16 MMAs and the tokens the
-// N side.  A lane's 16-byte loads (columns 8 (lane % 4) .. + 7 of a 32-column
-// step) feed two MMAs, of which each takes the same columns of both operands,
-// in an order of its own that the sum does not see.
-template <int MT, int NT>
-__device__ __forceinline__ void shrink_item(const uint16_t* x, const uint16_t* A, int K,
-                                            int R, const int16_t* rows, int c, int k0, int k1,
-                                            float* out) {
+// By one warp, over the columns [k0, k1): out[j] = x A[j]^T for j < R <= 16 MT.  The
+// rows of A are the M side of m16n8k16 MMAs, x the first of the N columns.  A lane's
+// 16-byte loads (columns 8 (lane % 4) .. + 7 of a 32-column step) feed two MMAs, of
+// which each takes the same columns of both operands, in an order of its own that the
+// sum does not see.
+template <int MT>
+__device__ __forceinline__ void shrink_token(const uint16_t* x, const uint16_t* A, int K, int R,
+                                             int k0, int k1, float* out) {
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  float acc[MT][NT][4];
+  float acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
   const uint16_t* ap = A + static_cast<size_t>(g) * K + 8 * q;
-  const uint16_t* xp[NT];
-  bool xon[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    xon[n] = 8 * n + g < c;
-    xp[n] = x + static_cast<size_t>(xon[n] ? rows[8 * n + g] & 0xff : 0) * K + 8 * q;
-  }
+  const uint16_t* xp = x + 8 * q;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  constexpr int kUnroll = MT == 1 ? 8 : MT == 2 ? 4 : 2;  // ~100 registers of loads
+  constexpr int kUnroll = MT == 1 ? 8 : 2;  // ~100 registers of loads
 #pragma unroll kUnroll
   for (int k = k0; k < k1; k += 32) {
-    uint4 av[MT][2], xv[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xv[n] = xon[n] ? ldg16(xp[n] + k) : zero;
+    uint4 av[MT][2];
+    const uint4 xv = g == 0 ? ldg16(xp + k) : zero;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -187,27 +177,18 @@ __device__ __forceinline__ void shrink_item(const uint16_t* x, const uint16_t* A
         av[m][h] = r < R ? ldg16(ap + static_cast<size_t>(r) * K + k) : zero;
       }
 #pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      mma_bf16(acc[m], av[m][0].x, av[m][1].x, av[m][0].y, av[m][1].y, xv.x, xv.y);
+      mma_bf16(acc[m], av[m][0].z, av[m][1].z, av[m][0].w, av[m][1].w, xv.z, xv.w);
+    }
+  }
+  if (q == 0) {
+#pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma_bf16(acc[m][n], av[m][0].x, av[m][1].x, av[m][0].y, av[m][1].y, xv[n].x, xv[n].y);
-        mma_bf16(acc[m][n], av[m][0].z, av[m][1].z, av[m][0].w, av[m][1].w, xv[n].z, xv[n].w);
-      }
+      for (int h = 0; h < 2; ++h)
+        if (16 * m + 8 * h < R) out[16 * m + 8 * h + g] = acc[m][2 * h];
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int p = 8 * n + 2 * q + e;
-      if (p < c) {
-        float* o = out + p * R + g;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (16 * m + 8 * h < R) o[16 * m + 8 * h] = acc[m][n][2 * h + e];
-      }
-    }
   __syncwarp();  // whole again for the next token's MMAs
 }
 

@@ -28,8 +28,6 @@ constexpr int kAdTile = 128;
 constexpr int kShMaxCluster = 8;
 
 struct ShrinkArgs {
-  const uint16_t* x;
-  const uint16_t* a;
   const int32_t* ids;
   const float* scale;
   int T, K, R, adapters;
@@ -39,8 +37,9 @@ struct ShrinkArgs {
   int* status;
 };
 
-// The rows of a tile, sorted by adapter, and the work in them: item j is up to
-// `cut` rows row[at[j]] .. of one adapter id[j] (the low byte of row is the row).
+// The rows of a tile, sorted by adapter, and the adapters in it: item j is the
+// count[j] rows row[at[j]] .. of adapter id[j] (the low byte of row is the row; 0x100
+// marks an adapter's first).
 struct __align__(16) Items {
   int32_t ids[kAdTile];
   int16_t row[kAdTile];
@@ -50,10 +49,10 @@ struct __align__(16) Items {
   int n;
 };
 
-// Sorts the tile's rows and cuts them into items (all threads call).  A row's
+// Sorts the tile's rows and lists their adapters (all threads call).  A row's
 // place is counted against the other 127 rows, in their order.
-__device__ void make_items(Items& u, int cut, const int32_t* ids, int t0, int rows,
-                           int adapters, int* status, bool report) {
+__device__ void make_items(Items& u, const int32_t* ids, int t0, int rows, int adapters,
+                           int* status, bool report) {
   const int i = threadIdx.x;
   if (i < kAdTile) {
     int id = -1;
@@ -77,8 +76,8 @@ __device__ void make_items(Items& u, int cut, const int32_t* ids, int t0, int ro
         before += v[q] == id && j + q < i ? 1 : 0;
       }
     }
-    // `before` is the row's place among its adapter's: every cut-th opens an item
-    if (id >= 0) u.row[lower + before] = static_cast<int16_t>(before % cut == 0 ? i | 0x100 : i);
+    // `before` is the row's place among its adapter's
+    if (id >= 0) u.row[lower + before] = static_cast<int16_t>(before == 0 ? i | 0x100 : i);
   }
   __syncthreads();
   if (i < 32) {
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   }
   tc_fence_before();
   // the barriers in here cover the initialisation too
-  make_items(u, kAdTile, s.ids, t0, min(kAdTile, s.T - t0), s.adapters, s.status,
+  make_items(u, s.ids, t0, min(kAdTile, s.T - t0), s.adapters, s.status,
              rank == 0 && blockIdx.z == 0);
   tc_fence_after();
   const uint32_t tbase = tmem_slot;
@@ -339,8 +338,6 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st,
   const bool stop = stall && stall->kernel == 0;
   auto kern = stop ? adapter_shrink_tile_kernel<true> : adapter_shrink_tile_kernel<false>;
   ShrinkArgs s{};
-  s.x = a.x;
-  s.a = a.a;
   s.ids = a.ids;
   s.scale = a.scale;
   s.T = a.T;
@@ -385,8 +382,8 @@ int launch_adapter_shrink(const AdapterArgs& a, int* status, cudaStream_t st,
   const uint64_t strides[2] = {static_cast<uint64_t>(s.K) * 2,
                                static_cast<uint64_t>(s.K) * s.R * 2};
   const uint32_t box[3] = {64, static_cast<uint32_t>(s.R), 1};
-  if (!adapter_map_rows(&mx, s.x, s.T, s.K, s.xrows) ||
-      !encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, s.a, dims, strides, box,
+  if (!adapter_map_rows(&mx, a.x, s.T, s.K, s.xrows) ||
+      !encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.a, dims, strides, box,
                          CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
