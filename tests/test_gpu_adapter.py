@@ -220,3 +220,55 @@ def test_an_adapter_that_is_not_finite_reaches_its_own_tokens_only(moe, T, R):
     a[2] = float("nan")
     got = moe.adapter_linear(x, w, a, b, ids, scale)
     assert torch.equal(got[~own], clean[~own]) and torch.isnan(got[own]).all()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("T", [1, 4, 40, 100, 200, 700])
+def test_calls_that_depend_on_one_another(moe, T, graph):
+    """Each call's x is the output of the one before, and its ids and scale are written
+    just ahead of it: the kernels of a call may start before those of the call before
+    have ended, and read nothing that is not complete."""
+    R, n, steps = 16, 5, 6
+    widths = [2048, 1024, 2048, 512, 1056, 2048, 256]
+    g = torch.Generator().manual_seed(T)
+    layers, wanted = [], []
+    for i in range(steps):
+        K, N = widths[i], widths[i + 1]
+        x, w, a, b, ids, scale = inputs(T, K, N, R, n, "mixed", 40 + i)
+        layers.append((w, a, b, ids, scale))
+    x0 = torch.randn(T, widths[0], generator=g).to(BF16).to(DEV)
+    h = x0
+    for w, a, b, ids, scale in layers:
+        torch.cuda.synchronize()
+        h = moe.adapter_linear(h, w, a, b, ids, scale)
+        torch.cuda.synchronize()
+        wanted.append(h)
+    idle = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    now, s = idle.clone(), torch.zeros(n, device=DEV)
+
+    def chain():
+        out, h = [], x0
+        for w, a, b, ids, scale in layers:
+            now.copy_(ids)
+            s.copy_(scale)
+            h = moe.adapter_linear(h, w, a, b, now, s)
+            out.append(h)
+        now.copy_(idle)
+        s.zero_()
+        return out
+
+    got = chain()
+    if graph:
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            got = chain()
+        for _ in range(20):
+            captured.replay()
+    else:
+        for _ in range(20):
+            got = chain()
+    torch.cuda.synchronize()
+    assert moe.check_error() == 0
+    for i, (a, b) in enumerate(zip(got, wanted)):
+        assert torch.equal(a, b), i

@@ -241,6 +241,66 @@ def test_route_grouped_from_hidden_states(moe, T, score):
     assert np.abs(gw - rw[~near]).max() <= 1e-5
 
 
+def can_turn(z, idx, bias, d, score, groups, topk_groups, scale):
+    """The rows of finite logits z [T, E] whose choice some change of up to d in every
+    logit could turn.  A sigmoid score moves by at most d s (1 - s) (1 + d), a softmax
+    score by 2 d s (1 + d); two keys can change places when they are no further apart
+    than both can move, and two groups likewise with their two best."""
+    T, E = z.shape
+    if score == "sigmoid":
+        s = 1.0 / (1.0 + np.exp(-z))
+        move = 1.01 * d * s * (1.0 - s)
+    else:
+        e = np.exp(z - z.max(axis=1, keepdims=True))
+        s = e / e.sum(axis=1, keepdims=True)
+        move = 2.02 * d * s
+    key, shift = (z, np.full_like(z, d)) if bias is None else (s + bias, move)
+    near = np.zeros(T, dtype=bool)
+    for t in range(T):
+        inside = np.ones(E, dtype=bool)
+        if topk_groups < groups:
+            per = E // groups
+            best = [np.argsort(-key[t, g * per:(g + 1) * per])[:2] + g * per
+                    for g in range(groups)]
+            value = s[t] if bias is None else key[t]
+            score_of = np.array([value[b].sum() for b in best])
+            # each of the two may be another one after the change, no further off
+            slack = np.array([2.0 * 1.01 * move[t, g * per:(g + 1) * per].max()
+                              for g in range(groups)])
+            order = np.argsort(-score_of)
+            a, b = order[:topk_groups], order[topk_groups:]
+            near[t] |= bool((score_of[a][:, None] - score_of[b][None] <=
+                             slack[a][:, None] + slack[b][None]).any())
+            inside = np.isin(np.arange(E) // per, a)
+        own = np.nonzero(inside)[0]
+        o = own[np.argsort(-key[t, own])][:len(idx[t]) + 1]
+        near[t] |= bool((key[t, o[:-1]] - key[t, o[1:]] <= shift[t, o[:-1]] + shift[t, o[1:]]).any())
+    return near
+
+
+@pytest.mark.parametrize("T", [1, 31, 33, 511, 513])
+@pytest.mark.parametrize("H,E,k,groups,kept,score,biased", [
+    (7168, 384, 8, 8, 4, "sigmoid", True), (7168, 384, 8, 1, 1, "softmax", False),
+    (1088, 200, 6, 4, 2, "softmax", True), (64, 40, 5, 5, 3, "sigmoid", False),
+    (2048, 1024, 16, 1, 1, "sigmoid", True)])
+def test_route_grouped_on_other_routers(moe, T, H, E, k, groups, kept, score, biased):
+    """As above, on wide and narrow routers: many partial sums to a logit and one."""
+    g = torch.Generator().manual_seed(T + E)
+    x = torch.randn(T, H, generator=g).to(BF16)
+    W = torch.randn(E, H, generator=g) * (1.7 / H ** 0.5)
+    b = torch.randn(E, generator=g) * 0.01 if biased else None
+    kw = dict(score=score, groups=groups, topk_groups=kept, scale=2.5)
+    gi, gw = moe.route_grouped(x.to(DEV), W.to(DEV), k, None if b is None else b.to(DEV), **kw)
+    assert moe.check_error() == 0
+    z = x.double().numpy() @ W.double().numpy().T
+    bias = None if b is None else b.double().numpy()
+    ri, rw = route_ref(z, k, bias, **kw)
+    near = can_turn(z, ri, bias, 1e-5, **kw)
+    assert near.mean() < 0.2
+    assert np.array_equal(gi.cpu().numpy()[~near], ri[~near])
+    assert np.abs(gw.cpu().numpy()[~near] - rw[~near]).max() <= 2.5e-5
+
+
 # ---------------------------------------------------------------- block norm
 
 def norm_ref(y, x, post, gate, sigmoid, scale, pre, eps):
