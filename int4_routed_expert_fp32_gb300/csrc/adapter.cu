@@ -54,11 +54,15 @@ constexpr int kSpWBytes = 128 * 64 * 2;
 constexpr int kSpMaxCluster = 8;
 
 // Up to here the split kernel does the shrink itself: every output tile reads the
-// adapters' A again (T R of them in place of 128 rows of W a tile).
+// adapters' A again (T R of them in place of 128 rows of W a tile), one token after
+// the other.  One launch against two, us in a graph / issued one by one (K 7168, N
+// 3584): T 1, R 16: 14.9 / 15.8 against 14.7 / 22.6; T 2, R 32: 15.1 / 15.9 and
+// 14.8 / 24.0; T 4, R 16: 21.5 / 21.3 and 15.0 / 24.2; T 8, R 8: 29 / 29 and 15.2 /
+// 23.9.  K = N = 2048: T 4, R 16 9.1 / 14.7 and 9.3 / 24.0, T 8 11.6 and 9.9.
+constexpr int kFusedTokens = 4;
 constexpr int kFusedLow = 64;  // T R
 
-
-bool fused(int T, int R) { return T <= 8 && T * R <= kFusedLow; }
+bool fused(int T, int R) { return T <= kFusedTokens && T * R <= kFusedLow; }
 
 struct SplitShape {
   int tb;      // tokens to a block (the MMA's N), a multiple of 16

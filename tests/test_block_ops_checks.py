@@ -333,3 +333,13 @@ def test_adapter_linear_refuses_more_tokens_or_columns_than_a_grid_has(capi):
     for T, N in ((65535 * 128 + 1, 24), (2 ** 31 - 1, 24), (9, 65535 * 128 + 8)):
         assert call(T, N) == capi.MOE_ERR_UNSUPPORTED, (T, N)
     assert capi.launch_count() == n
+
+
+def test_adapter_linear_of_a_few_tokens_needs_no_workspace(capi):
+    """One launch up to four tokens of T R <= 64; above, the low-rank vectors of a launch
+    of their own."""
+    size = capi.lib.moe_adapter_linear_workspace_size
+    for T, R in ((1, 8), (1, 64), (2, 32), (4, 16)):
+        assert size(T, 7168, 3584, R) == 0, (T, R)
+    for T, R in ((1, 72), (2, 40), (4, 24), (5, 8), (8, 8), (9, 8)):
+        assert size(T, 7168, 3584, R) >= T * R * 4, (T, R)
