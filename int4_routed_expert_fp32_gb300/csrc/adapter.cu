@@ -58,7 +58,8 @@ constexpr int kSpMaxCluster = 8;
 // the other.  One launch against two, us in a graph / issued one by one (K 7168, N
 // 3584): T 1, R 16: 14.9 / 15.8 against 14.7 / 22.6; T 2, R 32: 15.1 / 15.9 and
 // 14.8 / 24.0; T 4, R 16: 21.5 / 21.3 and 15.0 / 24.2; T 8, R 8: 29 / 29 and 15.2 /
-// 23.9.  K = N = 2048: T 4, R 16 9.1 / 14.7 and 9.3 / 24.0, T 8 11.6 and 9.9.
+// 23.9.  K = N = 2048: T 4, R 16 9.1 / 14.7 and 9.3 / 24.0; T 8, R 8 11.5 / 14.6 and
+// 9.9 / 23.1.
 constexpr int kFusedTokens = 4;
 constexpr int kFusedLow = 64;  // T R
 

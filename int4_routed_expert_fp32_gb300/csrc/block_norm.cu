@@ -453,9 +453,12 @@ int launch_norm(const NormArgs& a, bool vec, bool dense, cudaStream_t s) {
   } else {
     // Few rows: as many threads as vectors (latency).  Many: about 224 threads
     // with more loads each in flight, which leaves more rows to an SM (8192 x
-    // 7168 with a gate: 4 vectors 91 us, 2 114, 1 117; 2049 x 3584 in fp32: 4
-    // vectors 20.5 us, 2 16.1).
-    const int want = a.T <= 2 * num_sms() ? 1 : nv >= 768 ? 4 : nv >= 384 ? 2 : 1;
+    // 7168 with a gate: 4 vectors 91 us, 2 114, 1 117).  A vector of an fp32
+    // stream is half as many again, and four of them spill: two at most (8192 x
+    // 7168 with a gate: 4 vectors 142 us, 2 128, 1 205; 2049 x 3584: 4 20.5, 2
+    // 15.4, 1 18.2; 8192 x 2048: 1 34.5; 305 x 7168: 4 7.8, 2 7.4).
+    const int wide = XF32 ? 2 : 4;
+    const int want = a.T <= 2 * num_sms() ? 1 : nv >= 768 ? wide : nv >= 384 ? 2 : 1;
     const int vpt = std::max(want, nv > 2048 ? 4 : nv > 1024 ? 2 : 1);
     const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
     if (vpt == 1 && threads <= 256)
@@ -466,10 +469,10 @@ int launch_norm(const NormArgs& a, bool vec, bool dense, cudaStream_t s) {
       block_norm_kernel<XF32, false, 2><<<a.T, threads, 0, s>>>(a);
     else if (vpt == 2)
       block_norm_kernel<XF32, false, 2, 1024><<<a.T, threads, 0, s>>>(a);
-    else if (threads <= 256)
-      block_norm_kernel<XF32, false, 4><<<a.T, threads, 0, s>>>(a);
-    else
+    else if (XF32 || threads > 256)
       block_norm_kernel<XF32, false, 4, 1024><<<a.T, threads, 0, s>>>(a);
+    else if constexpr (!XF32)
+      block_norm_kernel<false, false, 4><<<a.T, threads, 0, s>>>(a);
   }
   MOE_LAUNCH_CHECK();
   return MOE_OK;

@@ -367,6 +367,19 @@ def test_block_norm(moe, shape, gate, stream):
             check_norm(gh, h, hsize, BF16, 8e-6)
 
 
+@pytest.mark.parametrize("stream", [BF16, torch.float32])
+@pytest.mark.parametrize("N", [3136, 6144, 7168, 8192 + 8, 16384])
+def test_block_norm_wide_rows_of_many_tokens(moe, N, stream):
+    """More rows than two to an SM: the variants with several vectors to a thread."""
+    y, x, post, pre, gate = norm_inputs(310, N, stream, "full", N)
+    gx, gh = moe.block_norm(y, x, post_gain=post, gate=gate, gate_sigmoid=True, scale=0.37,
+                            pre_gain=pre, eps=1e-5)
+    assert moe.check_error() == 0
+    r, h, size, hsize = norm_ref(y, x, post, gate, True, 0.37, pre, 1e-5)
+    check_norm(gx, r, size, stream, 4e-6)
+    check_norm(gh, h, hsize, BF16, 8e-6)
+
+
 def test_block_norm_without_residual_is_rmsnorm(moe):
     y, _, _, pre, _ = norm_inputs(37, 512, None, "none", 3)
     x_out, h = moe.block_norm(y, pre_gain=pre, eps=1e-6)
