@@ -1,10 +1,9 @@
 // A shared projection with the low-rank adapters of many requests:
 //   y[t] = x[t] W^T + s_a (x[t] A_a^T) B_a^T,  a = ids[t]  (-1: no adapter),
 // x bf16 [T, K], W bf16 [N, K], A bf16 [adapters, R, K], B bf16 [adapters, N,
-// R], y bf16 [T, N]; fp32 accumulation, one rounding of the sum.  The
-// projections it stands beside are the latent ones and the shared expert's
-// ("Kimi K3 latent up-projection" page, KimiSparseMoeBlock listing); no page
-// has adapters.
+// R], y bf16 [T, N]; fp32 accumulation, one rounding of the sum.  MoeBlock has
+// it in place of the latent projections ("Kimi K3 latent up-projection" page,
+// KimiSparseMoeBlock listing); no page has adapters.
 //
 // Two launches.  The shrink (adapter_shrink.cu) forms p = s x A^T for each
 // token's own adapter, in fp32.  A projection kernel forms x W^T on the tensor cores and
@@ -17,6 +16,12 @@
 // Each kernel lets the next call's first kernel start early, and waits for its
 // predecessor before it reads anything.
 //
+// Lines between the kernels, us in a graph (K 7168, N 3584, R 16 but where said).
+// Split against tile kernel: T 256 of one adapter 35.6 against 36.2 (K 3584, N
+// 7168: 44.6 against 23.6), of 64 adapters 39.6 against 104; T 512 of one 55.5
+// against 36.3, of 8 64.7 against 40, of 64 81 against 105.  What decides is the
+// number of distinct adapters, which the host does not know.
+//
 //  - adapter_split_kernel, few tokens: bound by reading W.  128 rows of W are
 //    the MMA's M side and up to 128 tokens its N side; the K range is split
 //    over the CTAs of a cluster, which add their accumulators through
@@ -24,10 +29,10 @@
 //    more SMs stream W whatever N is.  The low-rank term is a dot product of
 //    length R per output with each token's own rows of B, on mma.sync: 16 rows
 //    of B are the M side, and p as hi + lo, both bf16, two of the N columns.
-//    K = 7168, N = 3584 (51 MB of W), rank 16: one token 14.2 us, of which W
-//    takes 6.6 at the HBM rate, the prologue 2 and the clusters' sum 3 to 4; 32
-//    tokens with an adapter each (K = 3584, N = 7168) 18.1 with the shrink, 9.7
-//    of them W and the adapters; 256 tokens of rank 32 (N = 2048) 38.
+//    K = 7168, N = 3584 (51 MB of W), rank 16: one token 14.4 to 15.2 us, of
+//    which W takes 6.6 at the HBM rate, the prologue 2 and the clusters' sum 3 to
+//    4; 32 tokens with an adapter each (K = 3584, N = 7168) 18.3 with the shrink,
+//    9.7 of them W and the adapters; 256 tokens of rank 32 (N = 2048) 38.7.
 //  - adapter_tile_kernel (adapter_tile.cu), many tokens: bound by the tensor
 //    cores; the low-rank term is R more columns of K for each adapter that
 //    occurs in an output tile's rows.

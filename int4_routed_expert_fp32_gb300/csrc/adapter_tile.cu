@@ -33,10 +33,11 @@
 // (T = 8192, 8 adapters of rank 64 in every tile).  They are left to warps that take
 // the stages in turn.
 //
-// Measured: T = 8192, K = 3584, N = 7168, 8 adapters of rank 64: 241 us in this
-// kernel, 258 with the shrink before it (1.68 PFLOP/s; 1.79 in this kernel, where
-// cuBLAS sustains 1.74).  T = 2047, K = 7168, N = 3584, 16 of rank 16: 79 us with
-// the shrink (1.34 PFLOP/s), about 60 of them here.
+// Measured with the shrink before it: T = 8192, K = 3584, N = 7168, 8 adapters of
+// rank 64, requests of consecutive tokens: 270 us (1.60 PFLOP/s), and 290 to 297 in
+// runs of 0.1 s and more, under the power cap (1.45 to 1.49, where cuBLAS sustains
+// 1.74).  T = 2047, K = 7168, N = 3584, 16 of rank 16: 81.5 us (1.30 PFLOP/s), about
+// 15 of them the shrink.
 #include <math.h>
 
 #include <algorithm>

@@ -31,10 +31,14 @@
 //
 // Bound: instructions and the length of a token's chain of warp-wide steps, not
 // bytes.  T = 8192, E = 384, 8 groups of which 4 stay, k = 8: 11.4 us for 12.7 MB
-// (1.9 us at the HBM rate); loads and keys alone are 4.9 of them, the groups 3.3.
+// (1.9 us at the HBM rate; 11 to 12 on one GPU or another); loads and keys alone are
+// 4.9 of them, the groups 3.3.
 // A warp holds a token because the registers then hold all keys: 32 warps fit an
-// SM, and two rounds of them make the call.  Five CTAs of 8 warps to an SM spill
-// (12.7 us against 12.3 when measured), three are too few (13.1).
+// SM, and two rounds of them make the call.  At four CTAs of 8 warps to an SM (64
+// registers) this variant stores 24 bytes a thread and loads 8 back; five spill more
+// (12.7 us against 12.3 when measured), three are too few (13.1).  Softmax with a bias
+// stores 96 and loads 304 there: 8192 x 384 in 8 groups 22 us.  A row with fewer
+// than k experts left has all the others as candidates: 94 us where every row has 6.
 #include <float.h>
 #include <math.h>
 
@@ -141,7 +145,7 @@ __device__ __forceinline__ float exp_diff(float a, float b) {
   return fmaf(e, lost, e);
 }
 
-// a + b = hi + lo, hi rounded to nearest.
+// a + b = hi + lo, hi rounded to nearest (Knuth's exact sum of two floats).
 __device__ __forceinline__ float two_sum(float a, float b, float& lo) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   lo = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
@@ -813,7 +817,9 @@ __global__ void __launch_bounds__(256, NPL <= 12 ? 4 : 3) route_select_kernel(co
     }
   }
 
-  // ---- weights of the selected, unbiased
+  // ---- weights of the selected, unbiased.  The divisions are the fast ones, off by
+  // up to two steps of fp32 each: the weights' error is 7e-8 (rms), and 5e-8 with
+  // rounded divisions, which take 3 to 5 % longer
   float zz = -INFINITY;
   if (rank < a.k) {
     zz = my_z;
