@@ -452,7 +452,6 @@ __global__ void __launch_bounds__(THREADS, FUSED || THREADS == 512 ? 1 : 2)
   if (threadIdx.x == 64)
     for (int w = max(0, issued - 2); w < issued; ++w)
       mbar_drain(&bfull[w & 1], (w >> 1) & 1u, status);
-  __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its tile
 }
 

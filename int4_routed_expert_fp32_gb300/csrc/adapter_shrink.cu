@@ -293,7 +293,6 @@ __global__ void __launch_bounds__(kStThreads, 1)
     *reinterpret_cast<float4*>(s.low + static_cast<size_t>(t0 + row) * s.R + e) =
         make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
   }
-  __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its sums
 }
 

@@ -207,7 +207,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(WIDE), 
     tmem_relinquish_pair();
   }
   // both CTAs' barriers exist before either CTA arrives on the other's
-  __syncwarp();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();

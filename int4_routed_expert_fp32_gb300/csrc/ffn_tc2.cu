@@ -70,7 +70,6 @@ constexpr uint32_t kPCols = 512;
 constexpr uint32_t kPACol = kPTN;               // A ring after the 256-column accumulator
 constexpr uint32_t kPASlot = kPBK / 2;          // 64 columns: 128 fp16 per row
 constexpr int kPSmem = kPStages * kPStageBytes + 1024 + 256;
-static_assert(fills_half_sm(kPSmem), "CTAs of two pair kernels must not meet on an SM");
 static_assert(kPStageBytes % 1024 == 0, "stage alignment");
 static_assert(kPDqWarps * 32 == kPM * (kPBK / kGroup), "one thread per row and group");
 static_assert((2 + kPDqWarps + 12) * 32 <= 1024, "threads per CTA");
@@ -129,7 +128,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(MODE), 
     tmem_relinquish_pair();
   }
   // both CTAs' barriers exist before either CTA arrives on the other's
-  __syncwarp();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -397,7 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(MODE), 
   tc_fence_before();
   __syncthreads();
   if (warp == 1) mbar_drain(mma_done, 0, p.status);
-  __syncwarp();
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();

@@ -193,9 +193,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
-// Every thread of both CTAs arrives and waits (release / acquire, cluster
-// scope); also a barrier for the threads of each CTA.
+// Every thread of the cluster's CTAs arrives and waits (release / acquire, cluster
+// scope); also a barrier for the threads of each CTA.  Whole warps execute it.
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }

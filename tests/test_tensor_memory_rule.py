@@ -43,6 +43,21 @@ def test_the_kernels_are_found():
         {name for _, name, _ in ONE}
 
 
+def test_ctas_of_two_pair_kernels_never_meet_on_an_sm():
+    """Those of the experts' pair kernel take more than half of an SM's shared memory
+    (the adapter projection's, by a static_assert, too)."""
+    pairs = {file for file, _, body in ALL if "tmem_alloc_pair(" in body}
+    assert pairs == {"ffn_tc2.cu", "adapter_tile.cu"}
+    with open(os.path.join(CSRC, "ffn_tc2.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    value = {}
+    for name, expr in re.findall(r"constexpr int (kP\w+) = ([^;]+);", text):
+        value[name] = eval(expr.replace("/", "//"), {}, value)
+    assert 2 * (value["kPSmem"] + 1024) > 228 * 1024
+    with open(os.path.join(CSRC, "adapter_tile.cu")) as f:
+        assert "static_assert(fills_half_sm(kSmem)" in f.read()
+
+
 @pytest.mark.parametrize("file,name,body", ONE, ids=[k[1] for k in ONE])
 def test_tensor_memory_is_freed_before_the_cluster_is_waited_for(file, name, body):
     alloc = body.index("tmem_alloc(")
