@@ -41,7 +41,6 @@
 
 #include <algorithm>
 #include <mutex>
-#include <vector>
 
 #include "adapter.cuh"
 #include "common.cuh"
@@ -464,18 +463,22 @@ cudaError_t adapter_cluster(const void* kernel, int threads, int smem, int clust
     const void* kernel;
     int device, threads, smem, size, held;
   };
+  constexpr int kRoom = 1024;  // beyond, the answer is not kept
   static std::mutex mu;
-  static std::vector<Known> known;
+  static Known known[kRoom];
+  static int kept = 0;
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   for (*size = most; *size > 1; --*size) {
     int held = -1;
-    for (const Known& k : known)
+    for (int i = 0; i < kept && held < 0; ++i) {
+      const Known& k = known[i];
       if (k.kernel == kernel && k.device == device && k.threads == threads && k.smem == smem &&
           k.size == *size)
         held = k.held;
+    }
     if (held < 0) {
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(*size);
@@ -490,7 +493,7 @@ cudaError_t adapter_cluster(const void* kernel, int threads, int smem, int clust
       cfg.numAttrs = 1;
       e = cudaOccupancyMaxActiveClusters(&held, kernel, &cfg);
       if (e != cudaSuccess) return e;
-      known.push_back(Known{kernel, device, threads, smem, *size, held});
+      if (kept < kRoom) known[kept++] = Known{kernel, device, threads, smem, *size, held};
     }
     if (held >= clusters) return cudaSuccess;
   }

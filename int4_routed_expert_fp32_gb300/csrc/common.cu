@@ -1,9 +1,7 @@
 // Status word, device queries, tensor-map encoding, and the status /
 // self-test entry points of the C ABI.
 #include <atomic>
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include <cudaTypedefs.h>
 
@@ -54,16 +52,22 @@ int num_sms() {
 }
 
 cudaError_t allow_most_smem(const void* kernel) {
-  // The amount is asked for once; the limit is set on every call, since a new
-  // context starts without it.
-  static std::map<std::pair<const void*, int>, int> most;
+  // The amount is asked for once (again by kernels that the table has no room for);
+  // the limit is set on every call, since a new context starts without it.
+  struct Most {
+    const void* kernel;
+    int device, bytes;
+  };
+  constexpr int kRoom = 256;
+  static Most most[kRoom];
+  static int kept = 0;
   int device = 0, bytes = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    const auto it = most.find({kernel, device});
-    if (it != most.end()) bytes = it->second;
+    for (int i = 0; i < kept && !bytes; ++i)
+      if (most[i].kernel == kernel && most[i].device == device) bytes = most[i].bytes;
   }
   if (!bytes) {
     cudaFuncAttributes f{};
@@ -74,7 +78,7 @@ cudaError_t allow_most_smem(const void* kernel) {
     if (e != cudaSuccess) return e;
     bytes = optin - static_cast<int>(f.sharedSizeBytes);
     std::lock_guard<std::mutex> lk(g_mu);
-    most[{kernel, device}] = bytes;
+    if (kept < kRoom) most[kept++] = Most{kernel, device, bytes};
   }
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }

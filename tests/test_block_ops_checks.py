@@ -343,3 +343,17 @@ def test_adapter_linear_of_a_few_tokens_needs_no_workspace(capi):
         assert size(T, 7168, 3584, R) == 0, (T, R)
     for T, R in ((1, 72), (2, 40), (4, 24), (5, 8), (8, 8), (9, 8)):
         assert size(T, 7168, 3584, R) >= T * R * 4, (T, R)
+
+
+def test_c_entries_keep_no_containers_that_throw():
+    """What a launch keeps sits in tables of fixed size: an exception would leave the
+    C entry."""
+    import glob
+    import os
+    from tests.test_tensor_memory_rule import CSRC
+    for path in glob.glob(os.path.join(CSRC, "*.cu*")):
+        with open(path) as f:
+            text = f.read()
+        for name in ("std::vector", "std::map", "std::unordered_map", "std::string",
+                     "std::function"):
+            assert name not in text, (os.path.basename(path), name)
