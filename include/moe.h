@@ -592,6 +592,46 @@ int moe_layer_pipe_submit(moe_layer_pipe* pipe, const uint16_t* x_host, uint16_t
 int moe_layer_pipe_join(moe_layer_pipe* pipe, void* stream);
 void moe_layer_pipe_destroy(moe_layer_pipe* pipe);
 
+/* ------------------------------------------------------------ few tokens -- */
+
+/* The routed experts of a few tokens (T <= 32; one token of one request, drafted
+ * tokens, a small decode batch) in two launches instead of dispatch, experts and
+ * combine (no page has this call; the arithmetic is moe_expert_ffn's and
+ * moe_combine's):
+ *   out[t] = bf16( sum_j topk_w[t, j] down_e( SiLU(gate_e x[t]) * up_e x[t] ) ),
+ *   e = topk_idx[t, j], j ascending, in fp32 with one rounding at the end (the
+ *   intermediate h is kept in fp16: a value beyond its range records
+ *   MOE_ERR_UNSUPPORTED).  x may have any bf16 value: a token is scaled by a
+ *   power of two on its way in and out.
+ *   x         bf16 [T, D];  out bf16 [T, D]
+ *   topk_idx  int32 [T, k]: any experts, in any order and repetition; an id outside
+ *             [0, E) adds nothing and records MOE_ERR_INVALID
+ *   topk_w    fp32 [T, k]
+ *   weights   as moe_expert_ffn, act_bits 16
+ * Each chosen expert's weights are read once for every 8 tokens that chose it.
+ * Equal calls give equal bits.  D % 64 == 0, I % 64 == 0, E <= 2048, k <= min(E, 32), else
+ * MOE_ERR_UNSUPPORTED.  x, out and packed weights 16-byte aligned, ws 256; out and ws
+ * share no byte with each other or with an input, else MOE_ERR_INVALID. */
+size_t moe_experts_few_workspace_size(int T, int D, int E, int k, int I);
+int moe_experts_few(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, int T, int D,
+                    int E, int k, int I, const int32_t* gate_packed, const uint16_t* gate_scale,
+                    const int32_t* up_packed, const uint16_t* up_scale, const int32_t* down_packed,
+                    const uint16_t* down_scale, uint16_t* out, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* The whole layer for a few tokens (cfg->T <= 32, act_bits 16) in the same two
+ * launches: the routing of moe_route (decided in 64 bits where fp32 keys are
+ * near one another; more than 16 of them near the border stay as fp32 has
+ * them), moe_experts_few, and with cfg->L > 0 the latent projections and norm,
+ * with cfg->I_shared > 0 the shared expert, as moe_layer_forward has them.  Between
+ * the steps values are kept in fp16 (u = the latent input, h; beyond fp16's
+ * range: MOE_ERR_UNSUPPORTED recorded) or as two bf16 parts (16 bits), sums in
+ * fp32; the output is rounded once.  Same sizes, alignment and memory rules as
+ * moe_experts_few (router_w 16-byte aligned); router_w_terms is not read. */
+size_t moe_layer_few_workspace_size(const moe_config* cfg);
+int moe_layer_few(const moe_config* cfg, const moe_weights* w, const uint16_t* x, uint16_t* out,
+                  void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------ status etc -- */
 
 /* Synchronises `stream`, then returns and clears the current device's
@@ -643,6 +683,17 @@ int moe_adapter_linear_stall_selftest(const uint16_t* x, const uint16_t* w, cons
                                       const float* scale, int T, int K, int N, int R, int adapters,
                                       int kernel, int stall_stage, int64_t limit_ns, uint16_t* y,
                                       void* ws, size_t ws_bytes, void* stream);
+
+/* For tests: the exit paths of the few tokens' kernel.  Runs moe_experts_few (same
+ * arguments) with a build of it whose weight copies stop before stage `stall_stage`
+ * (counted per CTA from 0), and every wait limited to `limit_ns` (1e3 .. 5e9).  The
+ * call records MOE_ERR_TIMEOUT and out is not valid; later calls run normally. */
+int moe_experts_few_stall_selftest(const uint16_t* x, const int32_t* topk_idx, const float* topk_w,
+                                   int T, int D, int E, int k, int I, const int32_t* gate_packed,
+                                   const uint16_t* gate_scale, const int32_t* up_packed,
+                                   const uint16_t* up_scale, const int32_t* down_packed,
+                                   const uint16_t* down_scale, int stall_stage, int64_t limit_ns,
+                                   uint16_t* out, void* ws, size_t ws_bytes, void* stream);
 
 /* Which tensor-core kernels run the act_bits 16 expert GEMMs of
  * moe_expert_ffn, moe_layer_forward and moe_int4_linear for prefill-shaped

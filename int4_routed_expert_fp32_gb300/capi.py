@@ -152,6 +152,17 @@ SIGNATURES = {
                                                   c_void_p, c_int, c_int, c_int, c_int, c_int,
                                                   c_int, c_int, c_int64, c_void_p, c_void_p,
                                                   c_size_t, c_void_p]),
+    "moe_experts_few_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "moe_experts_few": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_experts_few_stall_selftest": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
+                                               c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                               c_void_p, c_void_p, c_void_p, c_int, c_int64,
+                                               c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_layer_few_workspace_size": (c_size_t, [POINTER(MoeConfig)]),
+    "moe_layer_few": (c_int, [POINTER(MoeConfig), POINTER(MoeWeights), c_void_p, c_void_p, c_void_p,
+                              c_size_t, c_void_p]),
 }
 
 
@@ -803,6 +814,97 @@ def adapter_linear_stall_selftest(x: torch.Tensor, w: torch.Tensor, lora_a: torc
     _check("moe_adapter_linear_stall_selftest", lib.moe_adapter_linear_stall_selftest(
         _p(x), _p(w), _p(lora_a), _p(lora_b), _p(ids), None, T, K, N, R, n, kernel, stall_stage,
         limit_ns, _p(out), _p(ws), ws.numel(), _stream()))
+
+
+def _few_args(topk_idx, topk_w, x, experts, out):
+    """(T, D, E, k, I, device) of ``experts_few``'s tensors, checked."""
+    bf16 = torch.bfloat16
+    T, D = _arg("x", x, x.shape if x.dim() == 2 else (None, None), bf16).shape
+    k = _arg("topk_idx", topk_idx, (T, topk_idx.shape[1] if topk_idx.dim() == 2 else None),
+             torch.int32).shape[1]
+    _arg("topk_w", topk_w, (T, k), torch.float32)
+    E, I = _arg("gate_packed", experts.get("gate_packed"), (None, None, None), torch.int32).shape[:2]
+    _experts(experts, E, D, I)
+    if out is not None:
+        _arg("out", out, (T, D), bf16)
+    w = [experts[n] for n in EXPERT_NAMES]
+    dev = _device_of((x, topk_idx, topk_w, out, *w), ("x", "topk_idx", "topk_w", "out", *EXPERT_NAMES))
+    if out is not None:
+        _apart("out", out, x=x, topk_idx=topk_idx, topk_w=topk_w, **dict(zip(EXPERT_NAMES, w)))
+    return T, D, E, k, I, w, dev
+
+
+def experts_few(topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
+                experts: Dict[str, torch.Tensor],
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out bf16 [T, D] = sum over the k choices of topk_w * down(SiLU(gate x) * up x),
+    for at most 32 tokens x bf16 [T, D] with their routing topk_idx int32 [T, k] and
+    topk_w fp32 [T, k]: dispatch, experts and combine in two launches
+    (moe_experts_few).  ``experts``: a dict with the six expert tensors (others are
+    not read).  out must not share memory with an input."""
+    T, D, E, k, I, w, dev = _few_args(topk_idx, topk_w, x, experts, out)
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    need = lib.moe_experts_few_workspace_size(T, D, E, k, I)
+    ws = torch.empty(need or 256, dtype=torch.uint8, device=dev)
+    rc = lib.moe_experts_few(x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), T, D, E, k, I,
+                             *[t.data_ptr() for t in w], out.data_ptr(), ws.data_ptr(), need,
+                             _raw_stream(dev.index))
+    if rc:
+        _check("moe_experts_few", rc)
+    return out
+
+
+def experts_few_stall_selftest(topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
+                               experts: Dict[str, torch.Tensor], stall_stage: int,
+                               limit_ns: int) -> None:
+    """Run experts_few with a build of its kernel whose weight copies stop before stage
+    ``stall_stage`` (tests of the exit paths; the device records MOE_ERR_TIMEOUT,
+    read with check_error())."""
+    T, D, E, k, I, w, dev = _few_args(topk_idx, topk_w, x, experts, None)
+    out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    need = lib.moe_experts_few_workspace_size(T, D, E, k, I)
+    ws = _ws(need, dev)
+    _check("moe_experts_few_stall_selftest", lib.moe_experts_few_stall_selftest(
+        _p(x), _p(topk_idx), _p(topk_w), T, D, E, k, I, *[_p(t) for t in w], stall_stage, limit_ns,
+        _p(out), _p(ws), ws.numel(), _stream()))
+
+
+def layer_few(x: torch.Tensor, weights: Dict[str, torch.Tensor], k: int, renorm: bool = True,
+              eps: float = 1e-6, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The whole layer for at most 32 tokens x bf16 [T, H] in two launches: router, experts
+    and sum, with lat_down and lat_up (and lat_norm) the latent projections, with the
+    shared_* weights the shared expert (moe_layer_few).  ``weights``: those of
+    MoeLayer, act_bits 16.  out must not share memory with an input."""
+    T, H = _arg("x", x, x.shape if x.dim() == 2 else (None, None), torch.bfloat16).shape
+    k = operator.index(k)
+    gate, lat, shared = (weights.get(n) for n in ("gate_packed", "lat_down", "shared_gate"))
+    E, I = _arg("gate_packed", gate, (None, None, None), torch.int32).shape[:2]
+    L = 0 if lat is None else _arg("lat_down", lat, (None, H), torch.bfloat16).shape[0]
+    S = 0 if shared is None else _arg("shared_gate", shared, (None, H), torch.bfloat16).shape[0]
+    _check_layer_weights(weights, H, E, I, L, S)
+    for of, there, names in (("lat_down", L, ("lat_up", "lat_norm")),
+                             ("shared_gate", S, ("shared_up", "shared_down"))):
+        for n in names:
+            if not there and weights.get(n) is not None:
+                raise ValueError(f"{n} needs {of}")
+    w = {n: t for n, t in weights.items() if t is not None}
+    if out is not None:
+        _arg("out", out, (T, H), torch.bfloat16)
+    dev = _device_of((x, out, *w.values()), ("x", "out", *w))
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _apart("out", out, x=x, **w)
+    cfg = MoeConfig(T, H, E, k, I, L, 16, int(renorm), eps, S)
+    ptrs = MoeWeights(*[w[n].data_ptr() if n in w else None for n, _ in MoeWeights._fields_])
+    need = lib.moe_layer_few_workspace_size(ctypes.byref(cfg))
+    ws = torch.empty(need or 256, dtype=torch.uint8, device=dev)
+    rc = lib.moe_layer_few(ctypes.byref(cfg), ctypes.byref(ptrs), x.data_ptr(), out.data_ptr(),
+                           ws.data_ptr(), need, _raw_stream(dev.index))
+    if rc:
+        _check("moe_layer_few", rc)
+    return out
 
 
 def check_error() -> int:

@@ -1,0 +1,1355 @@
+// The routed experts of a few tokens (T <= 32) in two launches.
+//
+// What the work is: every weight of every chosen expert is read once and used
+// for a handful of tokens, so the HBM rate bounds it and everything else has
+// to hide behind the weights' stream.
+//
+//   few_front_kernel   the router's logits (one pass over its fp32 weight), x as
+//                      fp16 in the order of the packed nibbles, counters to zero
+//   few_kernel         one persistent CTA per SM.  Every CTA selects the experts
+//                      (the same arithmetic everywhere, cheaper than another
+//                      launch), then takes units of work in ticket order: 16
+//                      gate rows and the 16 up rows of the same columns, or 32
+//                      rows of a down projection, times the tokens (at most 4)
+//                      of one chunk of one expert.
+//
+// Tickets are taken in the order of the units, and a unit waits only for units
+// with lower tickets (a down projection for its expert's h).  Those are held by
+// CTAs that run, so the kernel ends whatever else holds SMs: no CTA waits for
+// one that has not started.
+//
+// Roles of a CTA: warp 0 copies weights into a ring (TMA), warp 1 their scales and the
+// tokens' rows (once the units they wait for are done), the last eight multiply, and
+// two between them take the finished segments in turn.  Twelve warps leave the
+// products the registers that they need.  The ring runs on
+// across units and phases, so the weights of a down projection arrive while
+// its h is still being computed.
+//
+// The products use m16n8k16 MMAs: 16 weight rows, 8 tokens.  At 8 tokens a
+// weight byte is worth 32 operations, a hundredth of what would make the tensor
+// cores matter; the cost is the conversion of the nibbles, the same for
+// any MMA, and tcgen05 would add the trip of the converted weights through
+// shared or tensor memory.
+#include "few.cuh"
+
+#include <cuda_fp16.h>
+
+#include "adapter.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int C = kFewColumns;
+constexpr int kMul = 8;                      // warps that multiply, each a share of K
+constexpr int kCopy = 2;                     // warps that copy: weights, the rest
+constexpr int kFinish = 2;                   // warps that take finished segments
+constexpr int kFirstMul = kCopy + kFinish;   // warps before the multiplying ones
+constexpr int kThreads = 32 * (kFirstMul + kMul);
+constexpr int kFrontThreads = 256;
+constexpr int kFrontExperts = 2;             // router rows of a CTA
+constexpr int kFrontLoads = 7;               // float4 of a router row held by a thread
+
+// Ring slot: weights (32 rows of C / 2 bytes: for each row block of 16, pieces of 128
+// bytes of its rows, swizzled), scales (32 rows, swizzled), rows of tokens: fp16
+// blocks with their start values, 64 bytes apart in the banks, or bf16 rows in
+// swizzled pieces like the weights.
+constexpr int kWeightBytes = 32 * C / 2;
+constexpr int kScaleBytes = 32 * C / 16;
+constexpr int kStarts = 2 * C;  // where a row's start values lie
+constexpr int kPitch4 = kFewBlock + 64;
+static_assert(kPitch4 % 128 == 64, "rows spread over the banks");
+__host__ __device__ constexpr int slot_bytes(int rows_bytes) {
+  return kWeightBytes + kScaleBytes + (rows_bytes + 1023) / 1024 * 1024;
+}
+// Room for the rows of tokens: of a chunk, or in 128-byte pieces of bf16 in two parts.
+__host__ __device__ __forceinline__ int rows_bytes(const FewArgs& a) {
+  const int four = (a.T < a.chunk ? a.T : a.chunk) * kPitch4;
+  const int two = a.L > 0 || a.S > 0 ? 2 * (a.T < kFewRows ? a.T : kFewRows) * (C / 2) : 0;
+  return four > two ? four : two;
+}
+
+constexpr int kMaxSlots = 12;
+constexpr int kAhead = 4;  // tickets a CTA holds
+
+// Partial sums of a finished segment for each finishing warp; at first the expert
+// masks of the lists.
+__host__ __device__ constexpr int sums_bytes(int tokens, int E) {
+  const int sums = kFinish * kMul * 2 * tokens * 16 * 4, masks = 6 * E;
+  return ((sums > masks ? sums : masks) + 15) / 16 * 16;
+}
+
+// One header per slot and per finishing warp.  A segment is what one chunk adds to
+// a unit.
+struct __align__(16) Header {
+  int kind;   // FewKind, | kLastSlot, | kLastSegment
+  int size;   // tokens, | columns of K << 16
+  int which;  // expert chunk, or chunk of tokens
+  int n0;     // first column of the output
+  __device__ __forceinline__ int rows() const { return size & 0xffff; }
+  __device__ __forceinline__ int cols() const { return size >> 16; }
+};
+constexpr int kLastSlot = 256;     // of its segment
+constexpr int kLastSegment = 512;  // of its unit
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                        float c2, float c3) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// The eight nibbles of a word as fp16 pairs (columns 0 4, 1 5, 2 6, 3 7), exactly but
+// for a constant: in the low mantissa bits of 1024.0 a nibble makes 1032 + q, in
+// bits 4-7 of 64.0 it makes 72 + q.  One shift and four three-input operations: as
+// those take one immediate, the second constant of each has to come from a
+// register that the compiler does not see through (else it makes two of them, 9.4
+// instructions a word against 5.8).
+struct Magic {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x64086408;" : "=r"(lo));
+    asm volatile("mov.b32 %0, 0x54805480;" : "=r"(hi));
+  }
+};
+
+__device__ __forceinline__ void nibbles(uint32_t w, const Magic& m, uint32_t (&q)[4]) {
+  const uint32_t w8 = w >> 8;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0x6a;" : "=r"(q[0]) : "r"(w), "r"(m.lo));  // (w & a) ^ b
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0x6a;" : "=r"(q[1]) : "r"(w), "r"(m.hi));
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0x6a;" : "=r"(q[2]) : "r"(w8), "r"(m.lo));
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0x6a;" : "=r"(q[3]) : "r"(w8), "r"(m.hi));
+}
+
+// So a product with the activations v starts from -(1032 sum of the even columns + 72
+// sum of the odd ones): what one value of column c adds to it.
+__device__ __forceinline__ float start_of(float v, int c) { return c & 1 ? -72.f * v : -1032.f * v; }
+
+// mbar_wait with its slow part out of line (the code of all roles shares the instruction
+// caches), and for the roles that run ahead or behind with a rest between two
+// looks: seven warps that look all the time take as many issue slots as the
+// products.
+__device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, Waiter w, uint32_t rest_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (rest_ns) __nanosleep(rest_ns);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (aborted(w)) return false;
+    if (static_cast<int64_t>(global_timer_ns() - t0) > w.limit_ns) {
+      give_up(w);
+      return false;
+    }
+  }
+}
+template <int REST = 0>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const Waiter& w) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) ok = wait_slowly(bar, parity, w, REST);
+  return __all_sync(0xffffffffu, ok);
+}
+constexpr int kRest = 100;  // ns
+
+__device__ __forceinline__ int load_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void add_release(int32_t* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
+// Columns of K (int4) or of the bf16 rows that one slot holds, and the length of K.
+__device__ __forceinline__ bool is_int4(int kind) { return kind == kFewGateUp || kind == kFewDown; }
+__device__ __forceinline__ int length_of(const FewArgs& a, int kind) {
+  switch (kind) {
+    case kFewLatDown:
+    case kFewSharedUp: return a.H;
+    case kFewGateUp: return a.D;
+    case kFewDown: return a.I;
+    case kFewSharedDown: return a.S;
+    default: return a.L;
+  }
+}
+
+// ------------------------------------------------------------------ prologue
+
+// CTAs below `routers` take kFrontExperts rows of the router, the next T a token
+// each; the last CTA of all clears the counters.
+__global__ void __launch_bounds__(kFrontThreads) few_front_kernel(const FewArgs a, int routers) {
+  grid_wait();
+  grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (static_cast<int>(blockIdx.x) == static_cast<int>(gridDim.x) - 1)
+    for (int i = tid; i < a.n_counters; i += kFrontThreads) a.counters[i] = 0;
+
+  if (static_cast<int>(blockIdx.x) < routers) {
+    // A thread holds its columns of the router's rows and meets every token with
+    // them: the weight is read once, from all SMs at once, and x comes from L2.
+    __shared__ float part[kFewTokens][kFrontExperts][kFrontThreads / 32];
+    const int e0 = blockIdx.x * kFrontExperts;
+    constexpr int kStep = 4 * kFrontThreads * kFrontLoads;
+    for (int h0 = 0; h0 < a.H; h0 += kStep) {
+      float4 w[kFrontExperts][kFrontLoads];
+#pragma unroll
+      for (int i = 0; i < kFrontLoads; ++i) {
+        const int c = h0 + 4 * (tid + i * kFrontThreads);
+#pragma unroll
+        for (int e = 0; e < kFrontExperts; ++e) {
+          w[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < a.H && e0 + e < a.E)
+            w[e][i] = __ldg(reinterpret_cast<const float4*>(a.router_w + (size_t)(e0 + e) * a.H + c));
+        }
+      }
+#pragma unroll 2
+      for (int t = 0; t < a.T; ++t) {
+        float z[kFrontExperts] = {};
+#pragma unroll
+        for (int i = 0; i < kFrontLoads; ++i) {
+          const int c = h0 + 4 * (tid + i * kFrontThreads);
+          uint2 v = make_uint2(0u, 0u);
+          if (c < a.H) v = __ldg(reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H + c));
+          const float x0 = __uint_as_float(v.x << 16), x1 = __uint_as_float(v.x & 0xffff0000u);
+          const float x2 = __uint_as_float(v.y << 16), x3 = __uint_as_float(v.y & 0xffff0000u);
+#pragma unroll
+          for (int e = 0; e < kFrontExperts; ++e) {
+            z[e] = fmaf(x0, w[e][i].x, z[e]);
+            z[e] = fmaf(x1, w[e][i].y, z[e]);
+            z[e] = fmaf(x2, w[e][i].z, z[e]);
+            z[e] = fmaf(x3, w[e][i].w, z[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kFrontExperts; ++e) {
+          const float v = warp_sum(z[e]);
+          if (lane == 0) part[t][e][warp] = h0 ? part[t][e][warp] + v : v;
+        }
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < a.T * kFrontExperts; i += kFrontThreads) {
+      const int t = i / kFrontExperts, e = i % kFrontExperts;
+      float z = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFrontThreads / 32; ++w) z += part[t][e][w];
+      if (e0 + e < a.E) a.logits[(size_t)t * a.E + e0 + e] = z;
+    }
+    return;
+  }
+
+  // x as fp16 in pair order, times the power of two that brings the token's
+  // largest value to [2^14, 2^15): bf16's 8 bits stay whole down to 2^-29 of it
+  const int t = static_cast<int>(blockIdx.x) - routers;
+  if (t >= a.T || a.L > 0) return;
+  __shared__ float top[kFrontThreads / 32];
+  const uint16_t* row = a.x + (size_t)t * a.H;
+  float m = 0.f;
+  for (int c = 8 * tid; c < a.H; c += 8 * kFrontThreads) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + c));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
+                         fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+  }
+  m = warp_max(m);
+  if (lane == 0) top[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kFrontThreads / 32; ++w) m = fmaxf(m, top[w]);
+  // exponent field of 2^(14 - floor(log2 m)), at most 2^126; 1 where m is 0 or not finite
+  const int field = static_cast<int>(__float_as_uint(m) >> 23);
+  const int up = m == 0.f || field == 255 ? 127 : min(127 + 14 + 127 - field, 253);
+  const float by = __uint_as_float(static_cast<uint32_t>(up) << 23);
+  if (tid == 0) a.x_unit[t] = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+  uint8_t* x16 = a.x16 + t * few_row_bytes(a.D);
+  for (int c0 = 0; c0 < a.H; c0 += 8 * kFrontThreads) {
+    const int c = c0 + 8 * tid;
+    float start = 0.f;
+    if (c < a.H) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + c));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      __half2 p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // columns i and i + 4
+        const uint32_t lo = (w[i >> 1] >> (16 * (i & 1))) << 16;
+        const uint32_t hi = (w[2 + (i >> 1)] >> (16 * (i & 1))) << 16;
+        p[i] = __floats2half2_rn(__uint_as_float(lo) * by, __uint_as_float(hi) * by);
+        start += start_of(__low2float(p[i]) + __high2float(p[i]), i);
+      }
+      *reinterpret_cast<uint4*>(x16 + few_value_at(c)) = *reinterpret_cast<const uint4*>(p);
+    }
+    start += __shfl_xor_sync(0xffffffffu, start, 1);  // 16 columns
+    if (c < a.H && !(tid & 1)) *reinterpret_cast<float*>(x16 + few_start_at(c)) = start;
+  }
+}
+
+// ----------------------------------------------------------------- selection
+
+// The chosen experts as lists in shared memory.  A row is one (token, expert) pair;
+// the rows of a chunk follow one another.
+struct Lists {
+  float* row_weight;  // [T k] weight of a row's output
+  float* weight;      // [T k] weights of the choices
+  uint32_t* tokens;   // [chunks] tokens, one bit each
+  uint16_t* row;      // [T k] rows of the choices (0xffff: none)
+  uint16_t* expert;   // [chunks]
+  uint16_t* row0;     // [chunks] first row
+  int* chunks;
+  uint32_t* in_group; // [kFewGroups] tokens of a group of chunks
+};
+
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// Keys closer than this are compared again in 64 bits: it is far above what the
+// fp32 logits, the sigmoid and the sum leave open, and met by one token in a thousand.
+constexpr float kNear = 2e-5f;
+
+// One token's view of the router.  Passed by value, as the kernels' arguments have to
+// stay in the constant bank: a reference that leaves the kernel turns every access
+// to them into a load from memory.
+struct Row {
+  const uint16_t* x;   // [H]
+  const float* z;      // [E] logits
+  const float* w;      // [E, H]
+  const float* bias;   // [E]
+  int H, E, k, renorm;
+};
+
+// sigmoid(x . w_e) + bias_e in 64 bits (every lane gets it).
+__device__ __noinline__ double key64(Row a, int e, int lane) {
+  double z = 0.0;
+  for (int c = lane; c < a.H; c += 32)
+    z += static_cast<double>(bf16_bits_to_f32(a.x[c])) *
+         static_cast<double>(a.w[(size_t)e * a.H + c]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  return 1.0 / (1.0 + exp(-z)) + static_cast<double>(a.bias[e]);
+}
+
+// fp32 key of one expert; NaN ranks last.
+__device__ __forceinline__ float key32(const Row& a, int e) {
+  const float r = 1.0f / (1.0f + expf(-__ldcg(a.z + e))) + __ldg(a.bias + e);
+  return r != r ? -INFINITY : r;
+}
+
+// Experts within kNear of the k-th key `low`, decided in 64 bits: lane j < k holds
+// choice j in descending order of fp32 keys and gets its final one.  More than 16
+// of them (a router with no preference) stay as fp32 has them.
+__device__ __noinline__ int select_near(Row a, int lane, int mine, float low) {
+  int mine_near = 0, n = 0, sure = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    const float r = e < a.E ? key32(a, e) : -INFINITY;
+    sure += __popc(__ballot_sync(0xffffffffu, r > low + kNear));
+    uint32_t near = __ballot_sync(0xffffffffu, r <= low + kNear && r >= low - kNear);
+    for (; near; near &= near - 1, ++n)
+      if (lane == (n & 31)) mine_near = e0 + __ffs(near) - 1;
+    if (n > 16) return mine;
+  }
+  double key = 0.0;
+  for (int i = 0; i < n; ++i) {
+    const double v = key64(a, __shfl_sync(0xffffffffu, mine_near, i), lane);
+    if (lane == i) key = v;
+  }
+  int rank = 0;  // ids ascend with the lane
+  for (int i = 0; i < n; ++i) {
+    const double v = __shfl_sync(0xffffffffu, key, i);
+    rank += v > key || (v == key && i < lane);
+  }
+  for (int i = 0; i < n; ++i) {
+    const int e = __shfl_sync(0xffffffffu, mine_near, i);
+    const int to = sure + __shfl_sync(0xffffffffu, rank, i);
+    if (to < a.k && lane == to) mine = e;
+  }
+  return mine;
+}
+
+// The k experts of token t with the largest sigmoid(z) + bias (equal: the lower id)
+// and their weights; one warp.
+__device__ __forceinline__ void select_token(const Row a, int lane, float* weight, uint16_t* id) {
+  constexpr int NPL = 16;  // experts of a lane whose keys stay in registers
+  uint32_t key[NPL];
+  uint64_t gone = 0;  // chosen ones among the others
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    key[i] = lane + 32 * i < a.E ? ordered(key32(a, lane + 32 * i)) : 0u;
+  uint32_t low = 0, next = 0;
+  int mine = 0;
+  for (int j = 0; j <= a.k && j < a.E; ++j) {  // one more than k: the best that stays out
+    uint32_t best = 0u;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    for (int i = NPL; lane + 32 * i < a.E; ++i) {
+      const uint32_t v = gone >> i & 1u ? 0u : ordered(key32(a, lane + 32 * i));
+      if (v > best) {
+        best = v;
+        at = i;
+      }
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    if (j == a.k) {
+      next = top;
+      break;
+    }
+    low = top;
+    const uint32_t e =
+        __reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(lane + 32 * at) : ~0u);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+    if ((e & 31u) == static_cast<uint32_t>(lane)) gone |= 1ull << (e >> 5);
+    if (lane == j) mine = static_cast<int>(e);
+  }
+  const float f_low = unordered(low), f_next = next ? unordered(next) : -INFINITY;
+  if (f_next > -INFINITY && f_low - f_next <= kNear) mine = select_near(a, lane, mine, f_low);
+  const float s = lane < a.k ? 1.0f / (1.0f + expf(-__ldcg(a.z + mine))) : 0.f;
+  const float sum = warp_sum(s);
+  if (lane < a.k) {
+    weight[lane] = a.renorm ? __fdiv_rn(s, sum + 1e-20f) : s;
+    id[lane] = static_cast<uint16_t>(mine);
+  }
+}
+
+// Chunks of a group, for at most kFewGroups groups.
+__device__ __forceinline__ int group_chunks(int chunks) {
+  return max(1, (chunks + kFewGroups - 1) / kFewGroups);
+}
+__device__ __forceinline__ int group_count(int chunks) {
+  return (chunks + group_chunks(chunks) - 1) / group_chunks(chunks);
+}
+
+__device__ __forceinline__ void mul_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kMul * 32) : "memory");
+}
+
+// The lists of a call, by the multiplying warps of every CTA: each token's choice,
+// a mask of tokens for each expert, chunks of at most a.chunk tokens in the
+// order of the experts.  scratch: E words and E halves.
+__device__ __forceinline__ void build_lists(const FewArgs& a, const Lists& ls, uint32_t* mask, uint16_t* base,
+                            uint64_t* listed, int tid) {
+  const int lane = tid & 31, warp = tid >> 5, pairs = a.T * a.k;
+  for (int e = tid; e < a.E; e += kMul * 32) mask[e] = 0u;
+  if (tid < kFewGroups) ls.in_group[tid] = 0u;
+  if (a.router_w) {
+    for (int t = warp; t < a.T; t += kMul)
+      select_token(Row{a.x + (size_t)t * a.H, a.logits + (size_t)t * a.E, a.router_w, a.router_bias,
+                       a.H, a.E, a.k, a.renorm},
+                   lane, ls.weight + t * a.k, ls.row + t * a.k);
+  } else {
+    for (int p = tid; p < pairs; p += kMul * 32) {
+      const int e = a.topk_idx[p];
+      const bool ok = e >= 0 && e < a.E;
+      if (!ok) record_status(a.status, MOE_ERR_INVALID);
+      ls.weight[p] = a.topk_w[p];
+      ls.row[p] = ok ? static_cast<uint16_t>(e) : 0xffffu;
+    }
+  }
+  mul_sync();
+  for (int p = tid; p < pairs; p += kMul * 32)
+    if (ls.row[p] != 0xffffu) atomicOr(&mask[ls.row[p]], 1u << (p / a.k));
+  mul_sync();
+  if (warp == 0) {
+    int rows = 0, chunks = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      uint32_t m = e < a.E ? mask[e] : 0u;
+      const int n = __popc(m), c = (n + a.chunk - 1) / a.chunk;
+      int sum = n | c << 16;  // rows and chunks before this expert, both below 2^16
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      int r = rows + (sum & 0xffff) - n, at = chunks + (sum >> 16) - c;
+      rows += __shfl_sync(0xffffffffu, sum, 31) & 0xffff;
+      chunks += __shfl_sync(0xffffffffu, sum, 31) >> 16;
+      if (e < a.E) base[e] = static_cast<uint16_t>(r);
+      for (int i = 0; i < c; ++i, ++at, r += a.chunk) {
+        uint32_t part = 0u;
+        for (int b = 0; b < a.chunk && m; ++b, m &= m - 1) part |= m & (0u - m);
+        ls.tokens[at] = part;
+        ls.expert[at] = static_cast<uint16_t>(e);
+        ls.row0[at] = static_cast<uint16_t>(r);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      *ls.chunks = chunks;
+      mbar_arrive(listed);  // the copies may start
+    }
+  }
+  for (int p = tid; p < pairs; p += kMul * 32) ls.row_weight[p] = 0.f;
+  mul_sync();
+  for (int p = tid; p < pairs; p += kMul * 32) {
+    const int e = ls.row[p];
+    if (e != 0xffff)
+      ls.row[p] = static_cast<uint16_t>(base[e] + __popc(mask[e] & ((1u << (p / a.k)) - 1u)));
+  }
+  const int chunks = *ls.chunks, per = group_chunks(chunks);
+  for (int i = tid; i < chunks; i += kMul * 32) atomicOr(&ls.in_group[i / per], ls.tokens[i]);
+  mul_sync();
+  if (tid < a.T)  // an expert that a token lists twice counts twice
+    for (int p = tid * a.k; p < (tid + 1) * a.k; ++p)
+      if (ls.row[p] != 0xffffu) ls.row_weight[ls.row[p]] += ls.weight[p];
+  if (chunks == 0)  // no valid choice at all: no unit will write the output
+    for (int i = blockIdx.x * kMul * 32 + tid; i < a.T * a.H; i += gridDim.x * kMul * 32)
+      a.out[i] = 0;
+  mul_sync();
+}
+
+__device__ __forceinline__ int nth_token(uint32_t tokens, int i) {
+  for (; i > 0; --i) tokens &= tokens - 1;
+  return __ffs(tokens) - 1;
+}
+
+// --------------------------------------------------------------------- units
+
+struct Counts {  // units of each kind, in ticket order
+  int n[kFewKinds];
+};
+
+__device__ __forceinline__ Counts count_units(const FewArgs& a, int chunks) {
+  const int tc = few_token_chunks(a.T);
+  Counts c;
+  c.n[kFewLatDown] = a.L / 32 * tc;
+  c.n[kFewSharedUp] = a.S / 16 * tc;
+  c.n[kFewGateUp] = chunks * (a.I / 16);
+  c.n[kFewDown] = group_count(chunks) * (a.D / 32);
+  c.n[kFewSharedDown] = a.S > 0 ? a.H / 32 * tc : 0;
+  c.n[kFewLatUp] = a.L > 0 ? a.H / 32 * tc : 0;
+  return c;
+}
+
+// The matrix of a unit's first row block.
+__device__ __forceinline__ int matrix_of(int kind) {
+  switch (kind) {
+    case kFewLatDown: return kFewLatDownW;
+    case kFewSharedUp: return kFewSharedGateW;
+    case kFewGateUp: return kFewGateW;
+    case kFewDown: return kFewDownW;
+    case kFewSharedDown: return kFewSharedDownW;
+    default: return kFewLatUpW;
+  }
+}
+
+// A role's place in the ring: slot, parity of its use, slots passed.  (A division by the
+// number of slots would cost more than the rest of a role's turn.)
+struct Place {
+  uint32_t s = 0, parity = 0, n = 0;
+  __device__ __forceinline__ void next(int slots) {
+    ++n;
+    if (++s == static_cast<uint32_t>(slots)) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Ring and buffers of a CTA.
+struct Ring {
+  uint8_t* slots;
+  int bytes;  // of a slot
+  int n;      // slots
+  int tokens; // bf16 rows between their two parts
+  Header* header;
+  uint64_t* full;
+  uint64_t* empty;
+  uint64_t* named;  // header written
+  __device__ __forceinline__ uint8_t* slot(uint32_t s) const { return slots + (size_t)s * bytes; }
+  __device__ __forceinline__ uint8_t* scales(uint32_t s) const { return slot(s) + kWeightBytes; }
+  __device__ __forceinline__ uint8_t* rows(uint32_t s) const {
+    return slot(s) + kWeightBytes + kScaleBytes;
+  }
+};
+
+// Where a row's scales of groups 2 g2, 2 g2 + 1 lie in its row block: rows of 128 bytes
+// whose 16-byte pieces are swizzled as TMA writes them.
+__device__ __forceinline__ uint32_t scale_at(int row, int g2) {
+  return row * 128 + (((g2 >> 2) ^ (row & 7)) << 4) + (g2 & 3) * 4;
+}
+
+// -------------------------------------------------------------------- copies
+
+template <bool STALL>
+__device__ __forceinline__ void copy_weights(const FewArgs& a, const FewMaps& maps, const Ring& ring,
+                             const Lists& ls, uint64_t* listed, int lane, const Waiter& wt) {
+  Place at;
+  bool ok = true, known = false;
+  Counts units = count_units(a, 0);
+  const int fixed = units.n[kFewLatDown] + units.n[kFewSharedUp];
+  const int tc = few_token_chunks(a.T);
+  // kAhead tickets at a time, so that a unit does not wait for its own
+  int ticket = lane < kAhead ? atomicAdd(a.counters, 1) : 0;
+  for (int turn = 0; ok; turn = (turn + 1) % kAhead) {
+    int u = __shfl_sync(0xffffffffu, ticket, turn);
+    if (lane == turn) ticket = atomicAdd(a.counters, 1);
+    if (u >= fixed && !known) {
+      known = true;
+      ok = wait_for<kRest>(listed, 0, wt);
+      if (!ok) break;
+      units = count_units(a, *ls.chunks);
+    }
+    Header h{kFewEnd, 0, 0, 0};
+    int row[2] = {0, 0}, end = 1;  // segments h.which .. end - 1
+#pragma unroll
+    for (int kind = 0; kind < kFewKinds; ++kind) {
+      if (h.kind != kFewEnd) break;
+      if (u >= units.n[kind]) {
+        u -= units.n[kind];
+        continue;
+      }
+      h.kind = kind;
+      if (kind == kFewGateUp) {
+        h.which = u / (a.I / 16);
+        h.n0 = (u - h.which * (a.I / 16)) * 16;
+        end = h.which + 1;
+      } else if (kind == kFewDown) {
+        const int group = u / (a.D / 32), per = group_chunks(*ls.chunks);
+        h.n0 = (u - group * (a.D / 32)) * 32;
+        h.which = group * per;
+        end = min(h.which + per, *ls.chunks);
+      } else {
+        h.n0 = u / tc * (kind == kFewSharedUp ? 16 : 32);
+        h.which = u % tc;
+        h.size = min(kFewRows, a.T - h.which * kFewRows);
+        end = h.which + 1;
+      }
+    }
+    const int kind = h.kind;
+    const bool four = is_int4(kind);
+    row[0] = h.n0;
+    row[1] = h.n0 + (kind == kFewGateUp || kind == kFewSharedUp ? 0 : 16);
+    const int w0 = matrix_of(kind), w1 = w0 + (kind == kFewGateUp || kind == kFewSharedUp);
+    const int K = kind == kFewEnd ? 1 : length_of(a, kind);
+    const int step = four ? C : C / 4, wide = four ? 256 : 64;  // columns of 128 bytes
+    for (; ok && h.which < end; ++h.which) {
+      int mat = 0;
+      if (four) {
+        h.size = __popc(ls.tokens[h.which]);
+        mat = ls.expert[h.which];
+      }
+      for (int k0 = 0; k0 < K; k0 += step, at.next(ring.n)) {
+        const uint32_t s = at.s;
+        if (STALL && static_cast<int>(at.n) == a.stall_at) {
+          ok = false;
+          break;
+        }
+        ok = wait_for<kRest>(&ring.empty[s], at.parity ^ 1u, wt);
+        if (!ok) break;
+        const int cols = min(step, K - k0);
+        if (lane == 0) {
+          Header q = h;
+          q.size |= cols << 16;
+          if (k0 + step >= K) q.kind |= h.which + 1 == end ? kLastSlot | kLastSegment : kLastSlot;
+          ring.header[s] = q;
+          mbar_arrive(&ring.named[s]);
+          if (kind == kFewEnd) {
+            mbar_arrive(&ring.full[s]);
+          } else {
+            // one thread issues all copies: operands that differ between lanes would
+            // be taken up one lane after another (200 cycles each)
+            const int pieces = cols / wide;
+            const bool tail = cols % wide != 0;
+            uint64_t* bar = &ring.full[s];
+            mbar_arrive_expect_tx(bar, (pieces + tail) * 2 * 2048);
+            uint8_t* dst = ring.slot(s);
+            if (pieces > 0) {
+              const CUtensorMap* m = cols == step ? maps.full : maps.rest;
+              tma_g2s_4d(dst, m + w0, bar, 0, row[0], k0 / wide, mat);
+              tma_g2s_4d(dst + kWeightBytes / 2, m + w1, bar, 0, row[1], k0 / wide, mat);
+            }
+            if (tail) {
+              dst += pieces * 2048;
+              const int word = (k0 + pieces * wide) / 8;
+              tma_g2s_3d(dst, maps.tail + w0, bar, word, row[0], mat);
+              tma_g2s_3d(dst + kWeightBytes / 2, maps.tail + w1, bar, word, row[1], mat);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (kind == kFewEnd) break;
+  }
+  // whatever ended the loop, no copy is still on its way when the CTA leaves
+  drain_ring(ring.full, at.n, ring.n, a.status);
+}
+
+// The scales of slot i of a segment.
+__device__ __forceinline__ void copy_scales(const FewArgs& a, const FewMaps& maps, const Ring& ring,
+                                            uint32_t s, int i, int kind, int mat, int n0, int lane) {
+  const bool lanes = !(a.tma_scale[0] && a.tma_scale[1]);  // every lane arrives on a slot
+  uint64_t* bar = &ring.full[s];
+  if (!is_int4(kind)) {
+    if (lanes || lane == 0) mbar_arrive(bar);
+    return;
+  }
+  const bool down = kind == kFewDown;
+  const int row1 = n0 + (down ? 16 : 0);
+  uint8_t* dst = ring.scales(s);
+  if (a.tma_scale[down]) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, kScaleBytes);
+      const CUtensorMap* m = maps.scale + (down ? kFewDownW : kFewGateW);
+      tma_g2s_3d(dst, m, bar, i * (C / kGroup), n0, mat);
+      tma_g2s_3d(dst + kScaleBytes / 2, m + !down, bar, i * (C / kGroup), row1, mat);
+    } else if (lanes) {
+      mbar_arrive(bar);
+    }
+  } else {
+    // rows of K / 16 bytes, not 16-byte aligned: 4 bytes (two groups) at a time
+    const int K = down ? a.I : a.D, N = down ? a.D : a.I, pairs = min(C, K - i * C) / 64;
+    for (int j = lane; j < 32 * pairs; j += 32) {
+      const int r = j / pairs, g2 = j - r * pairs, block = r >> 4;
+      const uint16_t* src = a.scale[down ? 2 : block] +
+                            ((size_t)mat * N + (block ? row1 : n0) + (r & 15)) * (K / kGroup) +
+                            i * (C / kGroup) + 2 * g2;
+      cp_async_4(dst + block * (kScaleBytes / 2) + scale_at(r & 15, g2), src);
+    }
+    cp_async_arrive_noinc(bar);
+  }
+}
+
+// Waits until counter `c` has reached `n`; false when the time ran out.
+__device__ __forceinline__ bool wait_count(const int32_t* c, int n, const Waiter& wt) {
+  if (load_acquire(c) >= n) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (load_acquire(c) < n) {
+    if (aborted(wt)) return false;
+    if (static_cast<int64_t>(global_timer_ns() - t0) > wt.limit_ns) {
+      give_up(wt);
+      return false;
+    }
+    __nanosleep(64);
+  }
+  return true;
+}
+
+// Scales and rows of tokens.
+__device__ __forceinline__ void copy_rest(const FewArgs& a, const FewMaps& maps, const Ring& ring,
+                                          const Lists& ls, int lane, const Waiter& wt) {
+  const int tc = few_token_chunks(a.T);
+  int known = 0;         // chunks whose h is known to be complete
+  uint32_t others = 0;   // kinds whose rows are
+  for (Place at;;) {
+    if (!wait_for<kRest>(&ring.named[at.s], at.parity, wt)) break;
+    const Header h = ring.header[at.s];
+    const int kind = h.kind & 255;
+    const int mat = is_int4(kind) ? ls.expert[h.which] : 0;
+    copy_scales(a, maps, ring, at.s, 0, kind, mat, h.n0, lane);  // these wait for nothing
+    if (kind == kFewEnd) {
+      if (lane == 0) mbar_arrive(&ring.full[at.s]);
+      return;
+    }
+    // the rows this segment reads have to be there
+    bool ok = true;
+    if (kind == kFewDown) {
+      if (h.which >= known) {
+        // this chunk, and what a look at the next ones shows at the same time
+        const int32_t* c = a.counters + kFewFixed + h.which;
+        const bool there = h.which + lane < a.T * a.k;
+        ok = wait_count(c, a.I / 16, wt);
+        const uint32_t done =
+            __ballot_sync(0xffffffffu, there && load_acquire(c + lane) >= a.I / 16);
+        known = h.which + (~done ? __ffs(~done) - 1 : 32);
+      }
+    } else if (!(others >> kind & 1u)) {
+      others |= 1u << kind;
+      if (kind == kFewGateUp && a.L > 0) ok = wait_count(a.counters + 1, a.L / 32 * tc, wt);
+      if (kind == kFewSharedDown) ok = wait_count(a.counters + 2, a.S / 16 * tc, wt);
+      if (kind == kFewLatUp) ok = wait_count(a.counters + 3, a.L / 32, wt);
+    }
+    if (!__all_sync(0xffffffffu, ok)) break;
+    __syncwarp();  // what one lane has seen holds for all
+    // written through the generic proxy, read by copies
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    const int K = length_of(a, kind), rows = h.rows();
+    const bool four = is_int4(kind);
+    const int64_t pitch = few_row_bytes(K);
+    const uint8_t* src = kind == kFewDown ? a.h16 + ls.row0[h.which] * pitch : a.x16;
+    const uint32_t tokens = kind == kFewGateUp ? ls.tokens[h.which] : (1u << rows) - 1u;
+    const bool two = kind == kFewSharedDown || kind == kFewLatUp;
+    const CUtensorMap* m = maps.rows + (kind == kFewSharedDown ? 1 : kind == kFewLatUp ? 2 : 0);
+    const int slots = (K + (four ? C : C / 4) - 1) / (four ? C : C / 4);
+#pragma unroll 1
+    for (int i = 0; i < slots; ++i, at.next(ring.n)) {
+      const uint32_t s = at.s;
+      if (i > 0) {
+        ok = wait_for<kRest>(&ring.named[s], at.parity, wt);
+        if (!ok) break;
+        copy_scales(a, maps, ring, s, i, kind, mat, h.n0, lane);
+      }
+      if (lane == 0) {
+        uint64_t* bar = &ring.full[s];
+        uint8_t* dst = ring.rows(s);
+        if (four) {
+          mbar_arrive_expect_tx(bar, rows * kFewBlock);
+          const uint8_t* from = src + i * kFewBlock;
+#pragma unroll 1
+          for (uint32_t m = tokens; m; m &= m - 1, dst += kPitch4)
+            bulk_g2s(dst, from + (__ffs(m) - 1) * pitch, kFewBlock, bar);
+        } else {
+          const int bytes = ring.tokens * (C / 2);
+          mbar_arrive_expect_tx(bar, two ? 2 * bytes : bytes);
+          tma_g2s_4d(dst, m, bar, 0, h.which * kFewRows, i * (C / 256), 0);
+          if (two) tma_g2s_4d(dst + bytes, m, bar, 0, h.which * kFewRows, i * (C / 256), 1);
+        }
+      }
+      __syncwarp();
+    }
+    if (!ok) break;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // a wait that ran out: nothing stays on its way
+}
+
+// ------------------------------------------------------------------ products
+
+// Row of a block that lane (g, t) reads as rows g and (+ 8) g + 8 of an MMA: so the 8
+// lanes of a 128-byte shared-memory access meet both halves of the swizzle.
+__device__ __forceinline__ int row_of(int g) { return g >> 1 | (g & 1) << 2; }
+
+// 128 columns (4 groups) of both row blocks and of up to 2 PAIRS tokens.
+//
+// A lane's 16-byte load of a row is one whole group, and the four lanes of a quad hold
+// four groups.  An MMA adds over the quad, so the groups are kept apart on the
+// other side: column n = 4 (token of the pair) + group of the B operand holds
+// that token's values of that group, and zeros where the quad's other lanes
+// hold another group.  Eight MMAs then give the partial sums of 16 rows, 4
+// groups and 2 tokens, 8 of them in each accumulator column, with the words
+// used as they were loaded and 4 scale products for 64 weights a lane.
+//
+// Columns of tokens that are not there hold whatever the slot does: no column reaches
+// another.  Lanes that are off keep the zeros they were given.
+struct Lane {
+  int g, t, r;
+  bool on;  // holds the B operand of its column's group
+  __device__ __forceinline__ explicit Lane(int lane)
+      : g(lane >> 2), t(lane & 3), r(row_of(lane >> 2)), on((lane >> 2 & 3) == (lane & 3)) {}
+};
+
+// Step `step` of a slot for the tokens of rows first, first + 1: adds to acc[block][0, 1]
+// (rows g and g + 8).
+__device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int cols, int first,
+                                          int room, const Lane& l, const Magic& magic, uint4 (&v)[4],
+                                          float (&acc)[2][2]) {
+  const uint8_t* x = slot + kWeightBytes + kScaleBytes;
+  const uint8_t* row = x + min(first + (l.g >> 2), room) * kPitch4 + step * 256 + l.t * 64;
+  if (l.on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint4*>(row)[i];
+  }
+  // two start values (16 columns each) of groups 2 (t & 1) and + 1, token t >> 1
+  const float4 s = *reinterpret_cast<const float4*>(x + min(first + (l.t >> 1), room) * kPitch4 +
+                                                    kStarts + step * 32 + (l.t & 1) * 16);
+  const float start0 = s.x + s.y, start1 = s.z + s.w;
+  const uint8_t* w =
+      slot + (step >> 1) * 2048 + l.r * 128 + ((((step & 1) << 2 | l.t) ^ (l.r & 7)) << 4);
+  const uint8_t* sc = slot + kWeightBytes + scale_at(l.r, 2 * step + (l.t & 1));
+  // the last step of a row may be half: its upper two groups add nothing
+  const bool there = step < cols / 128 || !(l.t & 1);
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const uint4 q0 = *reinterpret_cast<const uint4*>(w + b * (kWeightBytes / 2));
+    const uint4 q8 = *reinterpret_cast<const uint4*>(w + b * (kWeightBytes / 2) + 1024);
+    const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w8[4] = {q8.x, q8.y, q8.z, q8.w};
+    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(sc + b * (kScaleBytes / 2));
+    const uint32_t s8 = *reinterpret_cast<const uint32_t*>(sc + b * (kScaleBytes / 2) + 1024);
+    float c[4] = {start0, start1, start0, start1};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo[4], hi[4];
+      nibbles(w0[i], magic, lo);
+      nibbles(w8[i], magic, hi);
+      mma_f16(c, lo[0], hi[0], lo[1], hi[1], v[i].x, v[i].y, c[0], c[1], c[2], c[3]);
+      mma_f16(c, lo[2], hi[2], lo[3], hi[3], v[i].z, v[i].w, c[0], c[1], c[2], c[3]);
+    }
+    if (there) {
+      acc[b][0] = fmaf(__uint_as_float(s0 & 0xffff0000u), c[1],
+                       fmaf(__uint_as_float(s0 << 16), c[0], acc[b][0]));
+      acc[b][1] = fmaf(__uint_as_float(s8 & 0xffff0000u), c[3],
+                       fmaf(__uint_as_float(s8 << 16), c[2], acc[b][1]));
+    }
+  }
+}
+// Columns of bf16 weights, 16 at a time, and up to 8 tokens (in one or two parts).
+__device__ __forceinline__ void multiply16(const uint8_t* slot, int cols, int tokens, int planes,
+                                           int warp, int lane, const Lane& l, float (&acc)[2][4]) {
+  const int li = lane & 7;
+  const uint32_t w = smem_u32(slot) + ((lane & 8) + li) * 128;
+#pragma unroll 1
+  for (int p = warp; p < cols / 16; p += kMul) {
+    uint32_t wr[2][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      ldsm4(w + b * (kWeightBytes / 2) + (p >> 2) * 2048 + ((((p & 3) << 1 | lane >> 4) ^ li) << 4),
+            wr[b]);
+    // columns of tokens that are not there repeat the last one's
+    const int at = (p >> 2) * tokens + min(l.g, tokens - 1);
+    const uint8_t* x = slot + kWeightBytes + kScaleBytes + at * 128 + l.t * 4;
+    const int piece = (p & 3) << 1, turn = at & 7;
+#pragma unroll 1
+    for (int plane = 0; plane < planes; ++plane, x += tokens * (C / 2)) {
+      const uint32_t b0 = *reinterpret_cast<const uint32_t*>(x + ((piece ^ turn) << 4));
+      const uint32_t b1 = *reinterpret_cast<const uint32_t*>(x + (((piece | 1) ^ turn) << 4));
+#pragma unroll
+      for (int b = 0; b < 2; ++b) mma_bf16(acc[b], wr[b], b0, b1);
+    }
+  }
+}
+
+// Finished segments: partial sums [warp][block][token][16 rows] for each finishing
+// warp, and its weighted sums [token][32 columns] over the segments of a unit.
+struct Sums {
+  float* part;
+  float* unit;
+  int tokens;
+  Header* header;
+  uint64_t* full;
+  uint64_t* empty;
+  __device__ __forceinline__ float* at(int buf, int warp, int block, int token) const {
+    return part + (((buf * kMul + warp) * 2 + block) * tokens + token) * 16;
+  }
+};
+
+__device__ __forceinline__ void multiply(const FewArgs& a, const Ring& ring, const Sums& sums, int warp, int lane,
+                         const Waiter& wt) {
+  float pair0[2][2] = {}, pair1[2][2] = {}, acc[2][4] = {};
+  const Magic magic;
+  const Lane l(lane);
+  const int room = min(a.T, a.chunk) - 1;  // last row of tokens of a slot
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  int buf = 0;             // the finishing warp of this unit
+  uint32_t taken = 0;      // parity of its buffer, one bit a warp
+  for (Place at;; at.next(ring.n)) {
+    const uint32_t s = at.s;
+    if (!wait_for(&ring.full[s], at.parity, wt)) return;
+    const Header h = ring.header[s];
+    const int kind = h.kind & 255;
+    if (kind == kFewEnd) break;
+    const bool four = is_int4(kind);
+    const uint8_t* slot = ring.slot(s);
+    if (four) {
+      const int steps = (h.cols() + 127) / 128;
+#pragma unroll 1
+      for (int step = warp; step < steps; step += kMul) {
+        multiply4(slot, step, h.cols(), 0, room, l, magic, v, pair0);
+        if (h.rows() > 2) multiply4(slot, step, h.cols(), 2, room, l, magic, v, pair1);
+      }
+    } else {
+      multiply16(slot, h.cols(), ring.tokens, kind == kFewSharedDown || kind == kFewLatUp ? 2 : 1,
+                 warp, lane, l, acc);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ring.empty[s]);
+    if (h.kind & kLastSlot) {
+      if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u, wt)) return;
+      taken ^= 1u << buf;
+      const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (four) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            pair0[b][i] += __shfl_xor_sync(0xffffffffu, pair0[b][i], 1);
+            pair1[b][i] += __shfl_xor_sync(0xffffffffu, pair1[b][i], 1);
+          }
+          // lane t even holds token t / 2 of the first pair, t odd that of the second
+          const int token = 2 * (t & 1) + (t >> 1);
+          if (token < h.rows()) {
+            float* p = sums.at(buf, warp, b, token);
+            p[l.r] = t & 1 ? pair1[b][0] : pair0[b][0];
+            p[l.r + 8] = t & 1 ? pair1[b][1] : pair0[b][1];
+          }
+          pair0[b][0] = pair0[b][1] = pair1[b][0] = pair1[b][1] = 0.f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (2 * t + i < h.rows()) {
+              float* p = sums.at(buf, warp, b, 2 * t + i);
+              p[g] = acc[b][i];
+              p[g + 8] = acc[b][2 + i];
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
+        }
+      }
+      if (warp == 0 && lane == 0) sums.header[buf] = h;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums.full[buf]);
+      if (h.kind & kLastSegment) buf = (buf + 1) % kFinish;
+    }
+  }
+  for (buf = 0; buf < kFinish; ++buf) {  // tell the finishing warps
+    if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u, wt)) return;
+    if (warp == 0 && lane == 0) sums.header[buf].kind = kFewEnd;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sums.full[buf]);
+  }
+}
+
+// ----------------------------------------------------------------- finishing
+
+__device__ __forceinline__ float total(const Sums& sums, int buf, int block, int token, int row) {
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMul; ++i) v += sums.at(buf, i, block, token)[row];
+  return v;
+}
+
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// A value as the sum of two bf16 values: 16 bits of significand.
+__device__ __forceinline__ void store_parts(uint16_t* p, size_t plane, float v) {
+  const uint16_t hi = f32_to_bf16_bits(v);
+  p[0] = hi;
+  p[plane] = f32_to_bf16_bits(v - bf16_bits_to_f32(hi));
+}
+
+// Adds one to a counter after the warp's stores.
+__device__ __forceinline__ void count_done(int32_t* c, int lane) {
+  __syncwarp();
+  if (lane == 0) add_release(c, 1);
+}
+
+// The same; whether that made it `n`: then all other contributions can be read.
+__device__ __forceinline__ bool count_last(int32_t* c, int n, int lane) {
+  __syncwarp();
+  int old = 0;
+  if (lane == 0) old = add_acq_rel(c, 1);
+  old = __shfl_sync(0xffffffffu, old, 0);
+  if (old != n - 1) return false;
+  __threadfence();
+  return true;
+}
+
+// Column n0 + lane of every token: the groups' sums, in order, whichever order they
+// were computed in.
+template <class Store>
+__device__ __forceinline__ void combine(const FewArgs& a, const Lists& ls, int n0, int lane,
+                                        Store store) {
+  const int groups = group_count(*ls.chunks);
+  constexpr int kBatch = 2;  // tokens whose loads are on their way at a time
+  const float* y = a.y + n0 + lane;
+  for (int t0 = 0; t0 < a.T; t0 += kBatch) {
+    float v[kBatch][kFewGroups];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int g = 0; g < kFewGroups; ++g) {
+        v[i][g] = 0.f;
+        if (g < groups && t0 + i < a.T && (ls.in_group[g] >> (t0 + i) & 1u))
+          v[i][g] = __ldcg(y + ((size_t)g * a.T + t0 + i) * a.D);
+      }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (t0 + i >= a.T) break;
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < kFewGroups; ++g) sum += v[i][g];
+      store(t0 + i, sum);
+    }
+  }
+}
+
+// Column c of a row of fp16 values, and with the 16 lanes of a half warp the start value
+// of its 16 columns.
+__device__ __forceinline__ void store_f16(const FewArgs& a, uint8_t* row, int c, float v, int lane) {
+  if (!(fabsf(v) <= 65504.0f)) record_status(a.status, MOE_ERR_UNSUPPORTED);
+  const __half h = __float2half_rn(v);
+  *reinterpret_cast<uint16_t*>(row + few_value_at(pair_pos(c))) = __half_as_ushort(h);
+  float s = start_of(__half2float(h), c);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(lane & 16 ? 0xffff0000u : 0xffffu, s, o);
+  if (!(lane & 15)) *reinterpret_cast<float*>(row + few_start_at(c)) = s;
+}
+
+__device__ __forceinline__ void finish(const FewArgs& a, const Sums& sums, const Lists& ls, int buf, int lane,
+                       const Waiter& wt) {
+  const int tc = few_token_chunks(a.T);
+  const int chunks_room = a.T * a.k;
+  int32_t* tile_done = a.counters + kFewFixed + chunks_room;
+  int32_t* out_done = tile_done + a.D / 32;
+  bool first = true;  // segment of a down projection's unit
+  for (uint32_t n = 0;; ++n) {
+    if (!wait_for<kRest>(&sums.full[buf], n & 1u, wt)) return;
+    const Header h = sums.header[buf];
+    const int kind = h.kind & 255;
+    if (kind == kFewEnd) return;
+    const int r16 = lane & 15, half = lane >> 4;
+    auto release = [&] {  // the buffer is handed back as soon as it has been read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums.empty[buf]);
+    };
+    if (kind == kFewGateUp || kind == kFewSharedUp) {
+      for (int i = half; i < h.rows(); i += 2) {
+        float g = total(sums, buf, 0, i, r16), u = total(sums, buf, 1, i, r16);
+        const int c = h.n0 + r16;
+        if (kind == kFewGateUp) {
+          if (a.L == 0) {
+            const float unit = __ldcg(a.x_unit + nth_token(ls.tokens[h.which], i));
+            g *= unit;
+            u *= unit;
+          }
+          const size_t r = ls.row0[h.which] + i;
+          store_f16(a, a.h16 + r * few_row_bytes(a.I), c, gated(g, u), lane);
+        } else {
+          store_parts(a.hs + (size_t)(h.which * kFewRows + i) * a.S + c, (size_t)a.T * a.S,
+                      gated(g, u));
+        }
+      }
+      release();
+      count_done(kind == kFewGateUp ? a.counters + kFewFixed + h.which : a.counters + 2, lane);
+      continue;
+    }
+    const int c = h.n0 + lane;
+    if (kind == kFewLatDown) {
+      for (int i = 0; i < h.rows(); ++i) {
+        const size_t r = h.which * kFewRows + i;
+        store_f16(a, a.x16 + r * few_row_bytes(a.L), c, total(sums, buf, half, i, r16), lane);
+      }
+      release();
+      count_done(a.counters + 1, lane);
+      continue;
+    }
+    int32_t* done;
+    int n_done;
+    if (kind == kFewDown) {
+      const int group = h.which / group_chunks(*ls.chunks);
+      float* unit = sums.unit + (buf * a.T) * 32 + lane;  // a token's 32 columns
+      if (first)
+        for (int t = 0; t < a.T; ++t) unit[t * 32] = 0.f;
+      for (int i = 0; i < h.rows(); ++i) {
+        const int t = nth_token(ls.tokens[h.which], i);
+        unit[t * 32] = fmaf(ls.row_weight[ls.row0[h.which] + i], total(sums, buf, half, i, r16),
+                            unit[t * 32]);
+      }
+      first = (h.kind & kLastSegment) != 0;
+      if (!first) {
+        release();
+        continue;
+      }
+      for (uint32_t m = ls.in_group[group]; m; m &= m - 1) {
+        const int t = __ffs(m) - 1;
+        a.y[((size_t)group * a.T + t) * a.D + c] = unit[t * 32];
+      }
+    } else if (kind == kFewSharedDown) {
+      for (int i = 0; i < h.rows(); ++i)
+        a.ys[(size_t)(h.which * kFewRows + i) * a.H + c] = total(sums, buf, half, i, r16);
+    } else {
+      for (int i = 0; i < h.rows(); ++i) {
+        const int t = h.which * kFewRows + i;
+        float scale = 1.0f;
+        if (a.norm) {
+          float q = 0.f;
+          for (int j = lane; j < a.L / 32; j += 32) q += __ldcg(a.ssq + (size_t)j * a.T + t);
+          scale = rsqrtf(warp_sum(q) / static_cast<float>(a.L) + a.eps);
+        }
+        a.yl[(size_t)t * a.H + c] = total(sums, buf, half, i, r16) * scale;
+      }
+    }
+    release();
+    const bool whole = a.L > 0 && kind != kFewDown;  // a tile of the latent layer's output
+    if (whole) {
+      done = out_done + h.n0 / 32 * tc + h.which;
+      n_done = a.S > 0 ? 2 : 1;
+    } else {
+      done = tile_done + h.n0 / 32;
+      n_done = group_count(*ls.chunks) + (a.S > 0 && a.L == 0 ? tc : 0);
+    }
+    if (!count_last(done, n_done, lane)) continue;
+    if (whole) {
+      for (int i = 0; i < h.rows(); ++i) {
+        const size_t at = (size_t)(h.which * kFewRows + i) * a.H + c;
+        float v = __ldcg(a.yl + at);
+        if (a.S > 0) v += __ldcg(a.ys + at);
+        a.out[at] = f32_to_bf16_bits(v);
+      }
+    } else if (a.L == 0) {
+      combine(a, ls, h.n0, lane, [&](int t, float v) {
+        if (a.S > 0) v += __ldcg(a.ys + (size_t)t * a.H + c);
+        a.out[(size_t)t * a.H + c] = f32_to_bf16_bits(v);
+      });
+    } else {
+      const float gain = a.lat_norm && a.norm ? bf16_bits_to_f32(__ldg(a.lat_norm + c)) : 1.0f;
+      combine(a, ls, h.n0, lane, [&](int t, float v) {
+        store_parts(a.z + (size_t)t * a.L + c, (size_t)a.T * a.L, v * gain);
+        const float q = warp_sum(v * v);
+        if (lane == 0) a.ssq[(size_t)(h.n0 / 32) * a.T + t] = q;
+      });
+      count_done(a.counters + 3, lane);
+    }
+  }
+}
+
+// -------------------------------------------------------------------- kernel
+
+template <bool STALL>
+__global__ void __launch_bounds__(kThreads, 1)
+    few_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
+  extern __shared__ uint8_t raw[];
+  // aligned by an offset: through an integer the compiler would lose that this is shared
+  // memory, and every access would take the long way of generic addresses
+  uint8_t* smem = raw + (-smem_u32(raw) & 1023u);
+  const int tokens = min(a.T, kFewRows), pairs = a.T * a.k;
+  const int slot = slot_bytes(rows_bytes(a));
+  __shared__ __align__(16) Header slot_header[kMaxSlots];
+  __shared__ __align__(16) Header sum_header[kFinish];
+  __shared__ __align__(8) uint64_t bars[3 * kMaxSlots + 2 * kFinish + 1];
+  __shared__ int cta_abort, n_chunks;
+  __shared__ uint32_t in_group[kFewGroups];
+  const Ring ring{smem, slot, a.stages, tokens, slot_header, bars, bars + kMaxSlots,
+                     bars + 2 * kMaxSlots};
+  uint64_t* sum_bar = bars + 3 * kMaxSlots;
+  uint64_t* listed = sum_bar + 2 * kFinish;
+  uint8_t* rest = smem + (size_t)slot * a.stages;
+  uint32_t* mask = reinterpret_cast<uint32_t*>(rest);  // before the first unit is finished
+  float* part = reinterpret_cast<float*>(rest);
+  rest += sums_bytes(tokens, a.E);
+  const Sums sums{part, reinterpret_cast<float*>(rest), tokens, sum_header, sum_bar,
+                  sum_bar + kFinish};
+  rest += kFinish * a.T * 32 * 4;
+  Lists ls;
+  ls.chunks = &n_chunks;
+  ls.in_group = in_group;
+  ls.row_weight = reinterpret_cast<float*>(rest);
+  ls.weight = ls.row_weight + pairs;
+  ls.tokens = reinterpret_cast<uint32_t*>(ls.weight + pairs);
+  ls.row = reinterpret_cast<uint16_t*>(ls.tokens + pairs);
+  ls.expert = ls.row + pairs;
+  ls.row0 = ls.expert + pairs;
+
+  const Waiter wt{&cta_abort, a.status, a.wait_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      // the announcements of the weights, the rows and the scales (or of all its lanes)
+      mbar_init(&ring.full[s], 2 + (a.tma_scale[0] && a.tma_scale[1] ? 1 : 32));
+      mbar_init(&ring.empty[s], kMul);
+      mbar_init(&ring.named[s], 1);
+    }
+    for (int b = 0; b < kFinish; ++b) {
+      mbar_init(&sums.full[b], kMul);
+      mbar_init(&sums.empty[b], 1);
+    }
+    mbar_init(listed, 1);
+    cta_abort = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  grid_wait();  // the prologue's logits, rows and cleared counters
+
+  if (warp == 0) {
+    copy_weights<STALL>(a, maps, ring, ls, listed, lane, wt);
+  } else if (warp == 1) {
+    copy_rest(a, maps, ring, ls, lane, wt);
+  } else if (warp < kFirstMul) {
+    finish(a, sums, ls, warp - kCopy, lane, wt);
+  } else {
+    build_lists(a, ls, mask, reinterpret_cast<uint16_t*>(mask + a.E), listed,
+                threadIdx.x - 32 * kFirstMul);
+    multiply(a, ring, sums, warp - kFirstMul, lane, wt);
+  }
+}
+
+}  // namespace
+
+// --------------------------------------------------------------------- launch
+
+// Weighted sums of the finishing warps and the lists.
+static size_t lists_bytes(const FewArgs& a) {
+  return align_up((size_t)kFinish * a.T * 128 + (size_t)18 * a.T * a.k, 16);
+}
+
+// What the device gives a CTA, less the static part and the alignment of the ring.
+constexpr int kSmemRoom = 227 * 1024 - 2048;
+
+static size_t smem_rest(const FewArgs& a) {
+  return sums_bytes(a.T < kFewRows ? a.T : kFewRows, a.E) + lists_bytes(a);
+}
+static int slot_of(const FewArgs& a) { return slot_bytes(rows_bytes(a)); }
+
+// Two tokens where experts have one or so each, for one more slot; four where they
+// have more, which then share a pass over the weights.
+int few_chunk(const FewArgs& a) { return a.T * a.k > a.E ? kFewChunk : 2; }
+
+int few_stages(const FewArgs& a) {
+  const int n = (kSmemRoom - static_cast<int>(smem_rest(a))) / slot_of(a);
+  return n < kMaxSlots ? n : kMaxSlots;
+}
+
+template <bool STALL>
+static int launch_main(const FewArgs& a, const FewMaps& maps, int grid, cudaStream_t st) {
+  auto kern = few_kernel<STALL>;
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)slot_of(a) * a.stages + smem_rest(a) + 1024;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  set_adapter_attrs(&cfg, attr, 0);
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, maps, a));
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+int launch_few(const FewArgs& a, const FewMaps& maps, bool stall, cudaStream_t st) {
+  const int routers = a.router_w ? (a.E + kFrontExperts - 1) / kFrontExperts : 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(routers + (a.L > 0 ? 1 : a.T));
+  cfg.blockDim = dim3(kFrontThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  set_adapter_attrs(&cfg, attr, 0);
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(few_front_kernel)));
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, few_front_kernel, a, routers));
+  MOE_LAUNCH_CHECK();
+  // no more CTAs than there can be units
+  const int64_t tc = few_token_chunks(a.T);
+  const int64_t units = (a.L / 32 + a.S / 16 + a.H / 32 * 2) * tc +
+                        static_cast<int64_t>(a.T) * a.k * (a.I / 16 + a.D / 32);
+  const int grid = static_cast<int>(units < num_sms() ? units : num_sms());
+  return stall ? launch_main<true>(a, maps, grid, st) : launch_main<false>(a, maps, grid, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,112 @@
+// The routed experts of a few tokens in two launches: a prologue and one
+// persistent kernel (few.cu), shared with their entry points (few_api.cu).
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kFewTokens = 32;  // tokens of a call: one bit each in an expert's mask
+constexpr int kFewChunk = 4;    // most tokens that share one pass over an expert's weights
+constexpr int kFewRows = 8;     // tokens that share one pass over bf16 weights
+constexpr int kFewColumns = 2048;  // int4 columns of a ring slot
+
+constexpr int kFewGroups = 8;   // groups of chunks whose outputs are summed before they are stored
+
+// Kinds of work units.  A unit is 32 weight rows (16 gate rows and the 16 up rows of
+// the same columns) times the tokens of one chunk; a down projection's takes a group of chunks one after another.
+// Units are taken in this order.
+enum FewKind {
+  kFewLatDown = 0,   // u = x lat_down^T           bf16 weights
+  kFewSharedUp = 1,  // SiLU(x gate^T) * x up^T    bf16 weights
+  kFewGateUp = 2,    // h of one expert            int4 weights
+  kFewDown = 3,      // y of one expert            int4 weights
+  kFewSharedDown = 4,
+  kFewLatUp = 5,
+  kFewKinds = 6,
+  kFewEnd = 7
+};
+
+// Arguments of both kernels; pointers not used by a call are NULL.
+struct FewArgs {
+  // inputs
+  const uint16_t* x;         // bf16 [T, H]
+  const float* router_w;     // fp32 [E, H]; NULL: the choice is given
+  const float* router_bias;  // fp32 [E]
+  const int32_t* topk_idx;   // int32 [T, k], where the choice is given
+  const float* topk_w;       // fp32 [T, k]
+  const uint16_t* scale[3];  // bf16 scales of gate, up, down
+  const uint16_t* lat_norm;  // bf16 [L] or NULL
+  uint16_t* out;             // bf16 [T, H]
+  // sizes: D is the width the experts see, L where the layer is latent (else 0)
+  int T, H, E, k, I, L, D, S;
+  int renorm, norm;
+  float eps;
+  int tma_scale[2];  // scales of gate/up and of down by TMA (K % 256 == 0) or in 4-byte copies
+  // workspace
+  int32_t* counters;
+  int n_counters;
+  float* logits;     // fp32 [T, E]
+  uint8_t* x16;      // [T] rows of fp16 blocks (below): x times a power of two, or u
+  float* x_unit;     // fp32 [T]: what one unit of x16 stands for
+  uint8_t* h16;      // [T k] rows of fp16 blocks
+  float* y;          // fp32 [kFewGroups, T, D]: weighted sums of the chunks of a group
+  uint16_t* hs;      // bf16 [2, T, S]: high and low parts of the shared expert's h
+  float* ys;         // fp32 [T, H] shared expert's output
+  uint16_t* z;       // bf16 [2, T, L]: high and low parts of the combined rows times the gain
+  float* ssq;        // fp32 [L / 32, T] sums of squares
+  float* yl;         // fp32 [T, H] latent up-projection
+  int* status;
+  long long wait_ns;
+  int chunk;         // tokens of a chunk, 2 or kFewChunk
+  int stages;        // ring slots
+  int stall_at;      // tests only: the weight copies stop before this stage (-1: never)
+};
+
+// counters: [0] ticket, [1] u tiles done, [2] shared h tiles done, [3] z tiles
+// done, then one per chunk (T k), then one per 32 columns of D, then one per 32
+// columns of H and kFewRows tokens.
+constexpr int kFewFixed = 4;
+
+// Matrices with tensor maps; the first three are of packed int4.
+enum FewMatrix {
+  kFewGateW, kFewUpW, kFewDownW, kFewLatDownW, kFewLatUpW, kFewSharedGateW, kFewSharedUpW,
+  kFewSharedDownW, kFewMatrices
+};
+
+// A ring slot takes 16 rows of a matrix in one copy: `full` of a whole slot's
+// pieces of 128 bytes of K, `rest` of the whole pieces of the last slot of a row,
+// `tail` of the columns behind them (K no multiple of 256).
+struct FewMaps {
+  CUtensorMap full[kFewMatrices], rest[kFewMatrices], tail[3], scale[3];
+  CUtensorMap rows[3];  // tokens of the bf16 units: x, the shared expert's h, z
+};
+
+// A row of fp16 activations lies in blocks of kFewColumns columns in pair order, each
+// followed by its start values (few.cu), one fp32 for 16 columns.
+constexpr int kFewBlock = kFewColumns * 2 + kFewColumns / 16 * 4;
+__host__ __device__ inline int64_t few_row_bytes(int K) {
+  return static_cast<int64_t>((K + kFewColumns - 1) / kFewColumns) * kFewBlock;
+}
+// Row of column c and its 16-column group's start value.
+__host__ __device__ inline int64_t few_value_at(int c) {
+  return static_cast<int64_t>(c / kFewColumns) * kFewBlock + c % kFewColumns * 2;
+}
+__host__ __device__ inline int64_t few_start_at(int c) {
+  return static_cast<int64_t>(c / kFewColumns) * kFewBlock + kFewColumns * 2 +
+         c % kFewColumns / 16 * 4;
+}
+
+__host__ __device__ inline int few_token_chunks(int T) { return (T + kFewRows - 1) / kFewRows; }
+
+// Tokens of a chunk, and ring slots that fit into shared memory.
+int few_chunk(const FewArgs& a);
+int few_stages(const FewArgs& a);
+
+// Both launches (validated arguments, a workspace as few_api.cu carves it).
+int launch_few(const FewArgs& a, const FewMaps& maps, bool stall, cudaStream_t st);
+
+}  // namespace moe
