@@ -46,37 +46,42 @@ constexpr int kCopy = 2;                     // warps that copy: weights, the re
 constexpr int kFinish = 2;                   // warps that take finished segments
 constexpr int kFirstMul = kCopy + kFinish;   // warps before the multiplying ones
 constexpr int kThreads = 32 * (kFirstMul + kMul);
+constexpr int kCtas = 2;                     // of an SM: one waits while the other multiplies
 constexpr int kFrontThreads = 256;
 constexpr int kFrontExperts = 2;             // router rows of a CTA
 constexpr int kFrontLoads = 7;               // float4 of a router row held by a thread
 
 // Ring slot: weights (32 rows of C / 2 bytes: for each row block of 16, pieces of 128
 // bytes of its rows, swizzled), scales (32 rows, swizzled), rows of tokens: fp16
-// blocks with their start values, 64 bytes apart in the banks, or bf16 rows in
-// swizzled pieces like the weights.
+// blocks with their start values, or bf16 rows in swizzled pieces like the weights.
 constexpr int kWeightBytes = 32 * C / 2;
 constexpr int kScaleBytes = 32 * C / 16;
 constexpr int kStarts = 2 * C;  // where a row's start values lie
-constexpr int kPitch4 = kFewBlock + 64;
-static_assert(kPitch4 % 128 == 64, "rows spread over the banks");
+constexpr int kPitch4 = kFewBlock;
 __host__ __device__ constexpr int slot_bytes(int rows_bytes) {
   return kWeightBytes + kScaleBytes + (rows_bytes + 1023) / 1024 * 1024;
 }
-// Room for the rows of tokens: of a chunk, or in 128-byte pieces of bf16 in two parts.
+// Room for the rows of tokens: of a chunk, or in 128-byte pieces of bf16.
 __host__ __device__ __forceinline__ int rows_bytes(const FewArgs& a) {
-  const int four = (a.T < a.chunk ? a.T : a.chunk) * kPitch4;
-  const int two = a.L > 0 || a.S > 0 ? 2 * (a.T < kFewRows ? a.T : kFewRows) * (C / 2) : 0;
-  return four > two ? four : two;
+  const int four = (a.T < kFewChunk ? a.T : kFewChunk) * kPitch4;
+  const int two = a.L > 0 || a.S > 0 ? (a.T < kFewRows ? a.T : kFewRows) * (C / 2) : 0;
+  const int parts = a.L > 0 || a.S > 0 ? 2 * (a.T < kFewRows / 2 ? a.T : kFewRows / 2) * (C / 2) : 0;
+  const int wide = two > parts ? two : parts;
+  return four > wide ? four : wide;
 }
 
-constexpr int kMaxSlots = 12;
-constexpr int kAhead = 4;  // tickets a CTA holds
+constexpr int kMaxSlots = 8;
+constexpr int kAhead = 2;  // tickets a CTA holds
 
-// Partial sums of a finished segment for each finishing warp; at first the expert
-// masks of the lists.
-__host__ __device__ constexpr int sums_bytes(int tokens, int E) {
-  const int sums = kFinish * kMul * 2 * tokens * 16 * 4, masks = 6 * E;
-  return ((sums > masks ? sums : masks) + 15) / 16 * 16;
+// Partial sums of a finished segment for each finishing warp; at first what only the
+// making of the lists needs.
+__host__ __device__ __forceinline__ int sum_tokens(const FewArgs& a) {
+  const int most = a.L > 0 || a.S > 0 ? kFewRows : kFewChunk;
+  return a.T < most ? a.T : most;
+}
+__host__ __device__ __forceinline__ int sums_bytes(const FewArgs& a) {
+  const int sums = kFinish * kMul * 2 * sum_tokens(a) * 16 * 4, lists = 6 * (a.E + a.T * a.k);
+  return ((sums > lists ? sums : lists) + 15) / 16 * 16;
 }
 
 // One header per slot and per finishing warp.  A segment is what one chunk adds to
@@ -149,12 +154,15 @@ __device__ __forceinline__ float start_of(float v, int c) { return c & 1 ? -72.f
 // looks: seven warps that look all the time take as many issue slots as the
 // products.
 __device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, Waiter w, uint32_t rest_ns) {
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
+  uint64_t t0 = 0;
+  for (int i = 0;; ++i) {
     if (rest_ns) __nanosleep(rest_ns);
     if (mbar_try_wait(bar, parity)) return true;
+    if (i < 8) continue;  // reading the clock takes longer than most waits
     if (aborted(w)) return false;
-    if (static_cast<int64_t>(global_timer_ns() - t0) > w.limit_ns) {
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (static_cast<int64_t>(now - t0) > w.limit_ns) {
       give_up(w);
       return false;
     }
@@ -315,14 +323,81 @@ __global__ void __launch_bounds__(kFrontThreads) few_front_kernel(const FewArgs 
 // the rows of a chunk follow one another.
 struct Lists {
   float* row_weight;  // [T k] weight of a row's output
-  float* weight;      // [T k] weights of the choices
   uint32_t* tokens;   // [chunks] tokens, one bit each
-  uint16_t* row;      // [T k] rows of the choices (0xffff: none)
   uint16_t* expert;   // [chunks]
   uint16_t* row0;     // [chunks] first row
   int* chunks;
   uint32_t* in_group; // [kFewGroups] tokens of a group of chunks
 };
+
+// Ring and buffers of a CTA.
+struct Ring {
+  uint8_t* slots;
+  int bytes;  // of a slot
+  int n;      // slots
+  Header* header;
+  uint64_t* full;
+  uint64_t* empty;
+  uint64_t* named;  // header written
+  __device__ __forceinline__ uint8_t* slot(uint32_t s) const { return slots + s * bytes; }
+  __device__ __forceinline__ uint8_t* scales(uint32_t s) const { return slot(s) + kWeightBytes; }
+  __device__ __forceinline__ uint8_t* rows(uint32_t s) const {
+    return slot(s) + kWeightBytes + kScaleBytes;
+  }
+};
+
+// Finished segments: partial sums [warp][block][token][16 rows] for each finishing
+// warp, and its weighted sums [token][32 columns] over the segments of a unit.
+struct Sums {
+  float* part;
+  float* unit;
+  int tokens;
+  Header* header;
+  uint64_t* full;
+  uint64_t* empty;
+  __device__ __forceinline__ float* at(int buf, int warp, int block, int token) const {
+    return part + (((buf * kMul + warp) * 2 + block) * tokens + token) * 16;
+  }
+};
+
+// What the roles of a CTA share, at the start of its shared memory.  Each role is a
+// function of its own that reads this: so each gets the registers it needs, and the
+// compiler sees that everything lies in shared memory.
+struct __align__(16) Context {
+  FewArgs a;
+  Header slot_header[kMaxSlots];
+  Header sum_header[kFinish];
+  uint64_t full[kMaxSlots], empty[kMaxSlots], named[kMaxSlots];
+  uint64_t sum_full[kFinish], sum_empty[kFinish], listed;
+  uint32_t in_group[kFewGroups];
+  int cta_abort, chunks;
+  int ring_at, slot, sums_at, unit_at, lists_at;  // offsets into shared memory
+};
+extern __shared__ __align__(16) uint8_t few_smem[];
+
+__device__ __forceinline__ Context& context() { return *reinterpret_cast<Context*>(few_smem); }
+__device__ __forceinline__ Ring ring_of(Context& c) {
+  return Ring{few_smem + c.ring_at, c.slot, c.a.stages, c.slot_header, c.full, c.empty, c.named};
+}
+__device__ __forceinline__ Sums sums_of(Context& c) {
+  return Sums{reinterpret_cast<float*>(few_smem + c.sums_at),
+              reinterpret_cast<float*>(few_smem + c.unit_at), sum_tokens(c.a), c.sum_header,
+              c.sum_full, c.sum_empty};
+}
+__device__ __forceinline__ Lists lists_of(Context& c) {
+  const int pairs = c.a.T * c.a.k;
+  Lists ls;
+  ls.chunks = &c.chunks;
+  ls.in_group = c.in_group;
+  ls.row_weight = reinterpret_cast<float*>(few_smem + c.lists_at);
+  ls.tokens = reinterpret_cast<uint32_t*>(ls.row_weight + pairs);
+  ls.expert = reinterpret_cast<uint16_t*>(ls.tokens + pairs);
+  ls.row0 = ls.expert + pairs;
+  return ls;
+}
+__device__ __forceinline__ Waiter waiter_of(Context& c) {
+  return Waiter{&c.cta_abort, c.a.status, c.a.wait_ns};
+}
 
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t u = __float_as_uint(f);
@@ -461,10 +536,18 @@ __device__ __forceinline__ void mul_sync() {
 }
 
 // The lists of a call, by the multiplying warps of every CTA: each token's choice,
-// a mask of tokens for each expert, chunks of at most a.chunk tokens in the
-// order of the experts.  scratch: E words and E halves.
-__device__ __forceinline__ void build_lists(const FewArgs& a, const Lists& ls, uint32_t* mask, uint16_t* base,
-                            uint64_t* listed, int tid) {
+// a mask of tokens for each expert, chunks of at most kFewChunk tokens in the
+// order of the experts.  The sums' memory holds E words and E halves meanwhile.
+__device__ __noinline__ void build_lists(int tid) {
+  Context& cx = context();
+  const FewArgs& a = cx.a;
+  const Lists ls = lists_of(cx);
+  // tokens of an expert, weights of the choices, first row of an expert, rows of the
+  // choices (0xffff: none)
+  uint32_t* mask = reinterpret_cast<uint32_t*>(few_smem + cx.sums_at);
+  float* weight = reinterpret_cast<float*>(mask + a.E);
+  uint16_t* base = reinterpret_cast<uint16_t*>(weight + a.T * a.k);
+  uint16_t* row = base + a.E;
   const int lane = tid & 31, warp = tid >> 5, pairs = a.T * a.k;
   for (int e = tid; e < a.E; e += kMul * 32) mask[e] = 0u;
   if (tid < kFewGroups) ls.in_group[tid] = 0u;
@@ -472,26 +555,26 @@ __device__ __forceinline__ void build_lists(const FewArgs& a, const Lists& ls, u
     for (int t = warp; t < a.T; t += kMul)
       select_token(Row{a.x + (size_t)t * a.H, a.logits + (size_t)t * a.E, a.router_w, a.router_bias,
                        a.H, a.E, a.k, a.renorm},
-                   lane, ls.weight + t * a.k, ls.row + t * a.k);
+                   lane, weight + t * a.k, row + t * a.k);
   } else {
     for (int p = tid; p < pairs; p += kMul * 32) {
       const int e = a.topk_idx[p];
       const bool ok = e >= 0 && e < a.E;
       if (!ok) record_status(a.status, MOE_ERR_INVALID);
-      ls.weight[p] = a.topk_w[p];
-      ls.row[p] = ok ? static_cast<uint16_t>(e) : 0xffffu;
+      weight[p] = a.topk_w[p];
+      row[p] = ok ? static_cast<uint16_t>(e) : 0xffffu;
     }
   }
   mul_sync();
   for (int p = tid; p < pairs; p += kMul * 32)
-    if (ls.row[p] != 0xffffu) atomicOr(&mask[ls.row[p]], 1u << (p / a.k));
+    if (row[p] != 0xffffu) atomicOr(&mask[row[p]], 1u << (p / a.k));
   mul_sync();
   if (warp == 0) {
     int rows = 0, chunks = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
       uint32_t m = e < a.E ? mask[e] : 0u;
-      const int n = __popc(m), c = (n + a.chunk - 1) / a.chunk;
+      const int n = __popc(m), c = (n + kFewChunk - 1) / kFewChunk;
       int sum = n | c << 16;  // rows and chunks before this expert, both below 2^16
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -502,9 +585,9 @@ __device__ __forceinline__ void build_lists(const FewArgs& a, const Lists& ls, u
       rows += __shfl_sync(0xffffffffu, sum, 31) & 0xffff;
       chunks += __shfl_sync(0xffffffffu, sum, 31) >> 16;
       if (e < a.E) base[e] = static_cast<uint16_t>(r);
-      for (int i = 0; i < c; ++i, ++at, r += a.chunk) {
+      for (int i = 0; i < c; ++i, ++at, r += kFewChunk) {
         uint32_t part = 0u;
-        for (int b = 0; b < a.chunk && m; ++b, m &= m - 1) part |= m & (0u - m);
+        for (int b = 0; b < kFewChunk && m; ++b, m &= m - 1) part |= m & (0u - m);
         ls.tokens[at] = part;
         ls.expert[at] = static_cast<uint16_t>(e);
         ls.row0[at] = static_cast<uint16_t>(r);
@@ -513,22 +596,22 @@ __device__ __forceinline__ void build_lists(const FewArgs& a, const Lists& ls, u
     __syncwarp();
     if (lane == 0) {
       *ls.chunks = chunks;
-      mbar_arrive(listed);  // the copies may start
+      mbar_arrive(&cx.listed);  // the copies may start
     }
   }
   for (int p = tid; p < pairs; p += kMul * 32) ls.row_weight[p] = 0.f;
   mul_sync();
   for (int p = tid; p < pairs; p += kMul * 32) {
-    const int e = ls.row[p];
+    const int e = row[p];
     if (e != 0xffff)
-      ls.row[p] = static_cast<uint16_t>(base[e] + __popc(mask[e] & ((1u << (p / a.k)) - 1u)));
+      row[p] = static_cast<uint16_t>(base[e] + __popc(mask[e] & ((1u << (p / a.k)) - 1u)));
   }
   const int chunks = *ls.chunks, per = group_chunks(chunks);
   for (int i = tid; i < chunks; i += kMul * 32) atomicOr(&ls.in_group[i / per], ls.tokens[i]);
   mul_sync();
   if (tid < a.T)  // an expert that a token lists twice counts twice
     for (int p = tid * a.k; p < (tid + 1) * a.k; ++p)
-      if (ls.row[p] != 0xffffu) ls.row_weight[ls.row[p]] += ls.weight[p];
+      if (row[p] != 0xffffu) ls.row_weight[row[p]] += weight[p];
   if (chunks == 0)  // no valid choice at all: no unit will write the output
     for (int i = blockIdx.x * kMul * 32 + tid; i < a.T * a.H; i += gridDim.x * kMul * 32)
       a.out[i] = 0;
@@ -547,14 +630,14 @@ struct Counts {  // units of each kind, in ticket order
 };
 
 __device__ __forceinline__ Counts count_units(const FewArgs& a, int chunks) {
-  const int tc = few_token_chunks(a.T);
+  const int whole = few_chunks(a.T, kFewRows), half = few_chunks(a.T, kFewRows / 2);
   Counts c;
-  c.n[kFewLatDown] = a.L / 32 * tc;
-  c.n[kFewSharedUp] = a.S / 16 * tc;
+  c.n[kFewLatDown] = a.L / 32 * whole;
+  c.n[kFewSharedUp] = a.S / 16 * whole;
   c.n[kFewGateUp] = chunks * (a.I / 16);
   c.n[kFewDown] = group_count(chunks) * (a.D / 32);
-  c.n[kFewSharedDown] = a.S > 0 ? a.H / 32 * tc : 0;
-  c.n[kFewLatUp] = a.L > 0 ? a.H / 32 * tc : 0;
+  c.n[kFewSharedDown] = a.S > 0 ? a.H / 32 * half : 0;
+  c.n[kFewLatUp] = a.L > 0 ? a.H / 32 * half : 0;
   return c;
 }
 
@@ -583,23 +666,6 @@ struct Place {
   }
 };
 
-// Ring and buffers of a CTA.
-struct Ring {
-  uint8_t* slots;
-  int bytes;  // of a slot
-  int n;      // slots
-  int tokens; // bf16 rows between their two parts
-  Header* header;
-  uint64_t* full;
-  uint64_t* empty;
-  uint64_t* named;  // header written
-  __device__ __forceinline__ uint8_t* slot(uint32_t s) const { return slots + (size_t)s * bytes; }
-  __device__ __forceinline__ uint8_t* scales(uint32_t s) const { return slot(s) + kWeightBytes; }
-  __device__ __forceinline__ uint8_t* rows(uint32_t s) const {
-    return slot(s) + kWeightBytes + kScaleBytes;
-  }
-};
-
 // Where a row's scales of groups 2 g2, 2 g2 + 1 lie in its row block: rows of 128 bytes
 // whose 16-byte pieces are swizzled as TMA writes them.
 __device__ __forceinline__ uint32_t scale_at(int row, int g2) {
@@ -608,14 +674,16 @@ __device__ __forceinline__ uint32_t scale_at(int row, int g2) {
 
 // -------------------------------------------------------------------- copies
 
-template <bool STALL>
-__device__ __forceinline__ void copy_weights(const FewArgs& a, const FewMaps& maps, const Ring& ring,
-                             const Lists& ls, uint64_t* listed, int lane, const Waiter& wt) {
+__device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
+  Context& cx = context();
+  const FewArgs& a = cx.a;
+  const Ring ring = ring_of(cx);
+  const Lists ls = lists_of(cx);
+  const Waiter wt = waiter_of(cx);
   Place at;
   bool ok = true, known = false;
   Counts units = count_units(a, 0);
   const int fixed = units.n[kFewLatDown] + units.n[kFewSharedUp];
-  const int tc = few_token_chunks(a.T);
   // kAhead tickets at a time, so that a unit does not wait for its own
   int ticket = lane < kAhead ? atomicAdd(a.counters, 1) : 0;
   for (int turn = 0; ok; turn = (turn + 1) % kAhead) {
@@ -623,7 +691,7 @@ __device__ __forceinline__ void copy_weights(const FewArgs& a, const FewMaps& ma
     if (lane == turn) ticket = atomicAdd(a.counters, 1);
     if (u >= fixed && !known) {
       known = true;
-      ok = wait_for<kRest>(listed, 0, wt);
+      ok = wait_for<kRest>(&cx.listed, 0, wt);
       if (!ok) break;
       units = count_units(a, *ls.chunks);
     }
@@ -647,9 +715,10 @@ __device__ __forceinline__ void copy_weights(const FewArgs& a, const FewMaps& ma
         h.which = group * per;
         end = min(h.which + per, *ls.chunks);
       } else {
-        h.n0 = u / tc * (kind == kFewSharedUp ? 16 : 32);
-        h.which = u % tc;
-        h.size = min(kFewRows, a.T - h.which * kFewRows);
+        const int rows = few_rows_of(kind), chunks = few_chunks(a.T, rows);
+        h.n0 = u / chunks * (kind == kFewSharedUp ? 16 : 32);
+        h.which = u % chunks;
+        h.size = min(rows, a.T - h.which * rows);
         end = h.which + 1;
       }
     }
@@ -668,7 +737,7 @@ __device__ __forceinline__ void copy_weights(const FewArgs& a, const FewMaps& ma
       }
       for (int k0 = 0; k0 < K; k0 += step, at.next(ring.n)) {
         const uint32_t s = at.s;
-        if (STALL && static_cast<int>(at.n) == a.stall_at) {
+        if (static_cast<int>(at.n) == a.stall_at) {  // tests only
           ok = false;
           break;
         }
@@ -692,15 +761,15 @@ __device__ __forceinline__ void copy_weights(const FewArgs& a, const FewMaps& ma
             mbar_arrive_expect_tx(bar, (pieces + tail) * 2 * 2048);
             uint8_t* dst = ring.slot(s);
             if (pieces > 0) {
-              const CUtensorMap* m = cols == step ? maps.full : maps.rest;
+              const CUtensorMap* m = cols == step ? maps->full : maps->rest;
               tma_g2s_4d(dst, m + w0, bar, 0, row[0], k0 / wide, mat);
               tma_g2s_4d(dst + kWeightBytes / 2, m + w1, bar, 0, row[1], k0 / wide, mat);
             }
             if (tail) {
               dst += pieces * 2048;
               const int word = (k0 + pieces * wide) / 8;
-              tma_g2s_3d(dst, maps.tail + w0, bar, word, row[0], mat);
-              tma_g2s_3d(dst + kWeightBytes / 2, maps.tail + w1, bar, word, row[1], mat);
+              tma_g2s_3d(dst, maps->tail + w0, bar, word, row[0], mat);
+              tma_g2s_3d(dst + kWeightBytes / 2, maps->tail + w1, bar, word, row[1], mat);
             }
           }
         }
@@ -714,7 +783,7 @@ __device__ __forceinline__ void copy_weights(const FewArgs& a, const FewMaps& ma
 }
 
 // The scales of slot i of a segment.
-__device__ __forceinline__ void copy_scales(const FewArgs& a, const FewMaps& maps, const Ring& ring,
+__device__ __forceinline__ void copy_scales(const FewArgs& a, const FewMaps* maps, const Ring& ring,
                                             uint32_t s, int i, int kind, int mat, int n0, int lane) {
   const bool lanes = !(a.tma_scale[0] && a.tma_scale[1]);  // every lane arrives on a slot
   uint64_t* bar = &ring.full[s];
@@ -728,7 +797,7 @@ __device__ __forceinline__ void copy_scales(const FewArgs& a, const FewMaps& map
   if (a.tma_scale[down]) {
     if (lane == 0) {
       mbar_arrive_expect_tx(bar, kScaleBytes);
-      const CUtensorMap* m = maps.scale + (down ? kFewDownW : kFewGateW);
+      const CUtensorMap* m = maps->scale + (down ? kFewDownW : kFewGateW);
       tma_g2s_3d(dst, m, bar, i * (C / kGroup), n0, mat);
       tma_g2s_3d(dst + kScaleBytes / 2, m + !down, bar, i * (C / kGroup), row1, mat);
     } else if (lanes) {
@@ -764,9 +833,13 @@ __device__ __forceinline__ bool wait_count(const int32_t* c, int n, const Waiter
 }
 
 // Scales and rows of tokens.
-__device__ __forceinline__ void copy_rest(const FewArgs& a, const FewMaps& maps, const Ring& ring,
-                                          const Lists& ls, int lane, const Waiter& wt) {
-  const int tc = few_token_chunks(a.T);
+__device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
+  Context& cx = context();
+  const FewArgs& a = cx.a;
+  const Ring ring = ring_of(cx);
+  const Lists ls = lists_of(cx);
+  const Waiter wt = waiter_of(cx);
+  const int tc = few_chunks(a.T, kFewRows);
   int known = 0;         // chunks whose h is known to be complete
   uint32_t others = 0;   // kinds whose rows are
   for (Place at;;) {
@@ -807,7 +880,7 @@ __device__ __forceinline__ void copy_rest(const FewArgs& a, const FewMaps& maps,
     const uint8_t* src = kind == kFewDown ? a.h16 + ls.row0[h.which] * pitch : a.x16;
     const uint32_t tokens = kind == kFewGateUp ? ls.tokens[h.which] : (1u << rows) - 1u;
     const bool two = kind == kFewSharedDown || kind == kFewLatUp;
-    const CUtensorMap* m = maps.rows + (kind == kFewSharedDown ? 1 : kind == kFewLatUp ? 2 : 0);
+    const CUtensorMap* m = maps->rows + (kind == kFewSharedDown ? 1 : kind == kFewLatUp ? 2 : 0);
     const int slots = (K + (four ? C : C / 4) - 1) / (four ? C : C / 4);
 #pragma unroll 1
     for (int i = 0; i < slots; ++i, at.next(ring.n)) {
@@ -827,10 +900,10 @@ __device__ __forceinline__ void copy_rest(const FewArgs& a, const FewMaps& maps,
           for (uint32_t m = tokens; m; m &= m - 1, dst += kPitch4)
             bulk_g2s(dst, from + (__ffs(m) - 1) * pitch, kFewBlock, bar);
         } else {
-          const int bytes = ring.tokens * (C / 2);
+          const int most = few_rows_of(kind), bytes = min(a.T, most) * (C / 2);
           mbar_arrive_expect_tx(bar, two ? 2 * bytes : bytes);
-          tma_g2s_4d(dst, m, bar, 0, h.which * kFewRows, i * (C / 256), 0);
-          if (two) tma_g2s_4d(dst + bytes, m, bar, 0, h.which * kFewRows, i * (C / 256), 1);
+          tma_g2s_4d(dst, m, bar, 0, h.which * most, i * (C / 256), 0);
+          if (two) tma_g2s_4d(dst + bytes, m, bar, 0, h.which * most, i * (C / 256), 1);
         }
       }
       __syncwarp();
@@ -865,20 +938,17 @@ struct Lane {
       : g(lane >> 2), t(lane & 3), r(row_of(lane >> 2)), on((lane >> 2 & 3) == (lane & 3)) {}
 };
 
-// Step `step` of a slot for the tokens of rows first, first + 1: adds to acc[block][0, 1]
-// (rows g and g + 8).
-__device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int cols, int first,
-                                          int room, const Lane& l, const Magic& magic, uint4 (&v)[4],
-                                          float (&acc)[2][2]) {
-  const uint8_t* x = slot + kWeightBytes + kScaleBytes;
-  const uint8_t* row = x + min(first + (l.g >> 2), room) * kPitch4 + step * 256 + l.t * 64;
+// Step `step` of a slot: adds to acc[block][0, 1] (rows g and g + 8).
+__device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int cols, const Lane& l,
+                                          int x_at, int start_at, const Magic& magic, uint4 (&v)[4],
+                                          float (&acc)[2][4]) {
   if (l.on) {
+    const uint4* row = reinterpret_cast<const uint4*>(slot + x_at + step * 256);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint4*>(row)[i];
+    for (int i = 0; i < 4; ++i) v[i] = row[i];
   }
   // two start values (16 columns each) of groups 2 (t & 1) and + 1, token t >> 1
-  const float4 s = *reinterpret_cast<const float4*>(x + min(first + (l.t >> 1), room) * kPitch4 +
-                                                    kStarts + step * 32 + (l.t & 1) * 16);
+  const float4 s = *reinterpret_cast<const float4*>(slot + start_at + step * 32);
   const float start0 = s.x + s.y, start1 = s.z + s.w;
   const uint8_t* w =
       slot + (step >> 1) * 2048 + l.r * 128 + ((((step & 1) << 2 | l.t) ^ (l.r & 7)) << 4);
@@ -909,6 +979,7 @@ __device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int col
     }
   }
 }
+
 // Columns of bf16 weights, 16 at a time, and up to 8 tokens (in one or two parts).
 __device__ __forceinline__ void multiply16(const uint8_t* slot, int cols, int tokens, int planes,
                                            int warp, int lane, const Lane& l, float (&acc)[2][4]) {
@@ -935,83 +1006,68 @@ __device__ __forceinline__ void multiply16(const uint8_t* slot, int cols, int to
   }
 }
 
-// Finished segments: partial sums [warp][block][token][16 rows] for each finishing
-// warp, and its weighted sums [token][32 columns] over the segments of a unit.
-struct Sums {
-  float* part;
-  float* unit;
-  int tokens;
-  Header* header;
-  uint64_t* full;
-  uint64_t* empty;
-  __device__ __forceinline__ float* at(int buf, int warp, int block, int token) const {
-    return part + (((buf * kMul + warp) * 2 + block) * tokens + token) * 16;
-  }
-};
-
-__device__ __forceinline__ void multiply(const FewArgs& a, const Ring& ring, const Sums& sums, int warp, int lane,
-                         const Waiter& wt) {
-  float pair0[2][2] = {}, pair1[2][2] = {}, acc[2][4] = {};
+__device__ __noinline__ void multiply(int warp, int lane) {
+  Context& cx = context();
+  const FewArgs& a = cx.a;
+  const Ring ring = ring_of(cx);
+  const Sums sums = sums_of(cx);
+  const Waiter wt = waiter_of(cx);
+  // int4 units: [block][row g, g + 8], the groups of lane t odd and even still apart;
+  // bf16 units: [block] MMA accumulator
+  float acc[2][4] = {};
   const Magic magic;
   const Lane l(lane);
-  const int room = min(a.T, a.chunk) - 1;  // last row of tokens of a slot
+  const int room = min(a.T, kFewChunk) - 1, slots = ring.n;
+  const int x_at = kWeightBytes + kScaleBytes + min(l.g >> 2, room) * kPitch4 + l.t * 64;
+  const int start_at =
+      kWeightBytes + kScaleBytes + min(l.t >> 1, room) * kPitch4 + kStarts + (l.t & 1) * 16;
   uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
   int buf = 0;             // the finishing warp of this unit
   uint32_t taken = 0;      // parity of its buffer, one bit a warp
-  for (Place at;; at.next(ring.n)) {
+  for (Place at;; at.next(slots)) {
     const uint32_t s = at.s;
     if (!wait_for(&ring.full[s], at.parity, wt)) return;
     const Header h = ring.header[s];
     const int kind = h.kind & 255;
-    if (kind == kFewEnd) break;
-    const bool four = is_int4(kind);
     const uint8_t* slot = ring.slot(s);
-    if (four) {
+    if (is_int4(kind)) {
       const int steps = (h.cols() + 127) / 128;
 #pragma unroll 1
-      for (int step = warp; step < steps; step += kMul) {
-        multiply4(slot, step, h.cols(), 0, room, l, magic, v, pair0);
-        if (h.rows() > 2) multiply4(slot, step, h.cols(), 2, room, l, magic, v, pair1);
-      }
+      for (int step = warp; step < steps; step += kMul)
+        multiply4(slot, step, h.cols(), l, x_at, start_at, magic, v, acc);
     } else {
-      multiply16(slot, h.cols(), ring.tokens, kind == kFewSharedDown || kind == kFewLatUp ? 2 : 1,
-                 warp, lane, l, acc);
+      if (kind == kFewEnd) break;
+      const int most = few_rows_of(kind);
+      multiply16(slot, h.cols(), min(a.T, most), most == kFewRows ? 1 : 2, warp, lane, l, acc);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.empty[s]);
     if (h.kind & kLastSlot) {
       if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u, wt)) return;
       taken ^= 1u << buf;
-      const int g = lane >> 2, t = lane & 3;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        if (four) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            pair0[b][i] += __shfl_xor_sync(0xffffffffu, pair0[b][i], 1);
-            pair1[b][i] += __shfl_xor_sync(0xffffffffu, pair1[b][i], 1);
+        if (is_int4(kind)) {
+          acc[b][0] += __shfl_xor_sync(0xffffffffu, acc[b][0], 1);
+          acc[b][1] += __shfl_xor_sync(0xffffffffu, acc[b][1], 1);
+          if (!(l.t & 1) && (l.t >> 1) < h.rows()) {
+            float* p = sums.at(buf, warp, b, l.t >> 1);
+            p[l.r] = acc[b][0];
+            p[l.r + 8] = acc[b][1];
           }
-          // lane t even holds token t / 2 of the first pair, t odd that of the second
-          const int token = 2 * (t & 1) + (t >> 1);
-          if (token < h.rows()) {
-            float* p = sums.at(buf, warp, b, token);
-            p[l.r] = t & 1 ? pair1[b][0] : pair0[b][0];
-            p[l.r + 8] = t & 1 ? pair1[b][1] : pair0[b][1];
-          }
-          pair0[b][0] = pair0[b][1] = pair1[b][0] = pair1[b][1] = 0.f;
         } else {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (2 * t + i < h.rows()) {
-              float* p = sums.at(buf, warp, b, 2 * t + i);
-              p[g] = acc[b][i];
-              p[g + 8] = acc[b][2 + i];
+            if (2 * l.t + i < h.rows()) {
+              float* p = sums.at(buf, warp, b, 2 * l.t + i);
+              p[l.g] = acc[b][i];
+              p[l.g + 8] = acc[b][2 + i];
             }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
       }
       if (warp == 0 && lane == 0) sums.header[buf] = h;
       __syncwarp();
@@ -1103,9 +1159,13 @@ __device__ __forceinline__ void store_f16(const FewArgs& a, uint8_t* row, int c,
   if (!(lane & 15)) *reinterpret_cast<float*>(row + few_start_at(c)) = s;
 }
 
-__device__ __forceinline__ void finish(const FewArgs& a, const Sums& sums, const Lists& ls, int buf, int lane,
-                       const Waiter& wt) {
-  const int tc = few_token_chunks(a.T);
+__device__ __noinline__ void finish(int buf, int lane) {
+  Context& cx = context();
+  const FewArgs& a = cx.a;
+  const Sums sums = sums_of(cx);
+  const Lists ls = lists_of(cx);
+  const Waiter wt = waiter_of(cx);
+  const int halves = few_chunks(a.T, kFewRows / 2);
   const int chunks_room = a.T * a.k;
   int32_t* tile_done = a.counters + kFewFixed + chunks_room;
   int32_t* out_done = tile_done + a.D / 32;
@@ -1174,10 +1234,10 @@ __device__ __forceinline__ void finish(const FewArgs& a, const Sums& sums, const
       }
     } else if (kind == kFewSharedDown) {
       for (int i = 0; i < h.rows(); ++i)
-        a.ys[(size_t)(h.which * kFewRows + i) * a.H + c] = total(sums, buf, half, i, r16);
+        a.ys[(size_t)(h.which * (kFewRows / 2) + i) * a.H + c] = total(sums, buf, half, i, r16);
     } else {
       for (int i = 0; i < h.rows(); ++i) {
-        const int t = h.which * kFewRows + i;
+        const int t = h.which * (kFewRows / 2) + i;
         float scale = 1.0f;
         if (a.norm) {
           float q = 0.f;
@@ -1190,16 +1250,16 @@ __device__ __forceinline__ void finish(const FewArgs& a, const Sums& sums, const
     release();
     const bool whole = a.L > 0 && kind != kFewDown;  // a tile of the latent layer's output
     if (whole) {
-      done = out_done + h.n0 / 32 * tc + h.which;
+      done = out_done + h.n0 / 32 * halves + h.which;
       n_done = a.S > 0 ? 2 : 1;
     } else {
       done = tile_done + h.n0 / 32;
-      n_done = group_count(*ls.chunks) + (a.S > 0 && a.L == 0 ? tc : 0);
+      n_done = group_count(*ls.chunks) + (a.S > 0 && a.L == 0 ? halves : 0);
     }
     if (!count_last(done, n_done, lane)) continue;
     if (whole) {
       for (int i = 0; i < h.rows(); ++i) {
-        const size_t at = (size_t)(h.which * kFewRows + i) * a.H + c;
+        const size_t at = (size_t)(h.which * (kFewRows / 2) + i) * a.H + c;
         float v = __ldcg(a.yl + at);
         if (a.S > 0) v += __ldcg(a.ys + at);
         a.out[at] = f32_to_bf16_bits(v);
@@ -1223,71 +1283,59 @@ __device__ __forceinline__ void finish(const FewArgs& a, const Sums& sums, const
 
 // -------------------------------------------------------------------- kernel
 
-template <bool STALL>
-__global__ void __launch_bounds__(kThreads, 1)
-    few_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
-  extern __shared__ uint8_t raw[];
-  // aligned by an offset: through an integer the compiler would lose that this is shared
-  // memory, and every access would take the long way of generic addresses
-  uint8_t* smem = raw + (-smem_u32(raw) & 1023u);
-  const int tokens = min(a.T, kFewRows), pairs = a.T * a.k;
-  const int slot = slot_bytes(rows_bytes(a));
-  __shared__ __align__(16) Header slot_header[kMaxSlots];
-  __shared__ __align__(16) Header sum_header[kFinish];
-  __shared__ __align__(8) uint64_t bars[3 * kMaxSlots + 2 * kFinish + 1];
-  __shared__ int cta_abort, n_chunks;
-  __shared__ uint32_t in_group[kFewGroups];
-  const Ring ring{smem, slot, a.stages, tokens, slot_header, bars, bars + kMaxSlots,
-                     bars + 2 * kMaxSlots};
-  uint64_t* sum_bar = bars + 3 * kMaxSlots;
-  uint64_t* listed = sum_bar + 2 * kFinish;
-  uint8_t* rest = smem + (size_t)slot * a.stages;
-  uint32_t* mask = reinterpret_cast<uint32_t*>(rest);  // before the first unit is finished
-  float* part = reinterpret_cast<float*>(rest);
-  rest += sums_bytes(tokens, a.E);
-  const Sums sums{part, reinterpret_cast<float*>(rest), tokens, sum_header, sum_bar,
-                  sum_bar + kFinish};
-  rest += kFinish * a.T * 32 * 4;
-  Lists ls;
-  ls.chunks = &n_chunks;
-  ls.in_group = in_group;
-  ls.row_weight = reinterpret_cast<float*>(rest);
-  ls.weight = ls.row_weight + pairs;
-  ls.tokens = reinterpret_cast<uint32_t*>(ls.weight + pairs);
-  ls.row = reinterpret_cast<uint16_t*>(ls.tokens + pairs);
-  ls.expert = ls.row + pairs;
-  ls.row0 = ls.expert + pairs;
+// Offsets into a CTA's shared memory, behind the context.
+struct Layout {
+  int slot, sums, unit, lists;
+  __host__ __device__ __forceinline__ explicit Layout(const FewArgs& a) {
+    slot = slot_bytes(rows_bytes(a));
+    sums = sums_bytes(a);
+    unit = kFinish * a.T * 32 * 4;
+    lists = (12 * a.T * a.k + 15) / 16 * 16;
+  }
+  __host__ __device__ __forceinline__ int rest() const {
+    return static_cast<int>(sizeof(Context)) + sums + unit + lists;
+  }
+};
 
-  const Waiter wt{&cta_abort, a.status, a.wait_ns};
+__global__ void __launch_bounds__(kThreads, kCtas)
+    few_kernel(const __grid_constant__ FewMaps maps, const FewArgs args) {
+  Context& cx = context();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
+    const Layout lay(args);
+    cx.a = args;
+    cx.slot = lay.slot;
+    cx.sums_at = sizeof(Context);
+    cx.unit_at = cx.sums_at + lay.sums;
+    cx.lists_at = cx.unit_at + lay.unit;
+    const int end = lay.rest();
+    cx.ring_at = end + (-(smem_u32(few_smem) + end) & 1023u);
+    for (int s = 0; s < args.stages; ++s) {
       // the announcements of the weights, the rows and the scales (or of all its lanes)
-      mbar_init(&ring.full[s], 2 + (a.tma_scale[0] && a.tma_scale[1] ? 1 : 32));
-      mbar_init(&ring.empty[s], kMul);
-      mbar_init(&ring.named[s], 1);
+      mbar_init(&cx.full[s], 2 + (args.tma_scale[0] && args.tma_scale[1] ? 1 : 32));
+      mbar_init(&cx.empty[s], kMul);
+      mbar_init(&cx.named[s], 1);
     }
     for (int b = 0; b < kFinish; ++b) {
-      mbar_init(&sums.full[b], kMul);
-      mbar_init(&sums.empty[b], 1);
+      mbar_init(&cx.sum_full[b], kMul);
+      mbar_init(&cx.sum_empty[b], 1);
     }
-    mbar_init(listed, 1);
-    cta_abort = 0;
+    mbar_init(&cx.listed, 1);
+    cx.cta_abort = 0;
     fence_mbarrier_init();
   }
   __syncthreads();
   grid_wait();  // the prologue's logits, rows and cleared counters
 
   if (warp == 0) {
-    copy_weights<STALL>(a, maps, ring, ls, listed, lane, wt);
+    copy_weights(&maps, lane);
   } else if (warp == 1) {
-    copy_rest(a, maps, ring, ls, lane, wt);
+    copy_rest(&maps, lane);
   } else if (warp < kFirstMul) {
-    finish(a, sums, ls, warp - kCopy, lane, wt);
+    finish(warp - kCopy, lane);
   } else {
-    build_lists(a, ls, mask, reinterpret_cast<uint16_t*>(mask + a.E), listed,
-                threadIdx.x - 32 * kFirstMul);
-    multiply(a, ring, sums, warp - kFirstMul, lane, wt);
+    build_lists(threadIdx.x - 32 * kFirstMul);
+    multiply(warp - kFirstMul, lane);
   }
 }
 
@@ -1295,45 +1343,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------------- launch
 
-// Weighted sums of the finishing warps and the lists.
-static size_t lists_bytes(const FewArgs& a) {
-  return align_up((size_t)kFinish * a.T * 128 + (size_t)18 * a.T * a.k, 16);
-}
+// Shared memory of a CTA when two, or when one, share an SM, less the ring's alignment.
+constexpr int kRoomOfTwo = 113 * 1024 - 1024, kRoomOfOne = 227 * 1024 - 1024;
 
-// What the device gives a CTA, less the static part and the alignment of the ring.
-constexpr int kSmemRoom = 227 * 1024 - 2048;
-
-static size_t smem_rest(const FewArgs& a) {
-  return sums_bytes(a.T < kFewRows ? a.T : kFewRows, a.E) + lists_bytes(a);
-}
-static int slot_of(const FewArgs& a) { return slot_bytes(rows_bytes(a)); }
-
-// Two tokens where experts have one or so each, for one more slot; four where they
-// have more, which then share a pass over the weights.
-int few_chunk(const FewArgs& a) { return a.T * a.k > a.E ? kFewChunk : 2; }
-
+// Two slots at least; where two CTAs leave no room for that, one takes the SM.
 int few_stages(const FewArgs& a) {
-  const int n = (kSmemRoom - static_cast<int>(smem_rest(a))) / slot_of(a);
+  const Layout lay(a);
+  int n = (kRoomOfTwo - lay.rest()) / lay.slot;
+  if (n < 2) n = (kRoomOfOne - lay.rest()) / lay.slot;
   return n < kMaxSlots ? n : kMaxSlots;
 }
 
-template <bool STALL>
-static int launch_main(const FewArgs& a, const FewMaps& maps, int grid, cudaStream_t st) {
-  auto kern = few_kernel<STALL>;
-  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
+static int launch_main(const FewArgs& a, const FewMaps& maps, cudaStream_t st) {
+  MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(few_kernel)));
+  const Layout lay(a);
+  const int smem = lay.rest() + lay.slot * a.stages;
+  // no more CTAs than there can be units
+  const int64_t tc = few_chunks(a.T, kFewRows / 2);
+  const int64_t units = (a.L / 32 + a.S / 16 + a.H / 32 * 2) * tc +
+                        static_cast<int64_t>(a.T) * a.k * (a.I / 16 + a.D / 32);
+  const int64_t most = static_cast<int64_t>(num_sms()) * (smem <= kRoomOfTwo ? kCtas : 1);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(static_cast<unsigned>(units < most ? units : most));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)slot_of(a) * a.stages + smem_rest(a) + 1024;
+  cfg.dynamicSmemBytes = smem + 1024;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   set_adapter_attrs(&cfg, attr, 0);
-  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, maps, a));
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, few_kernel, maps, a));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
 
-int launch_few(const FewArgs& a, const FewMaps& maps, bool stall, cudaStream_t st) {
+int launch_few(const FewArgs& a, const FewMaps& maps, cudaStream_t st) {
   const int routers = a.router_w ? (a.E + kFrontExperts - 1) / kFrontExperts : 0;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(routers + (a.L > 0 ? 1 : a.T));
@@ -1344,12 +1386,7 @@ int launch_few(const FewArgs& a, const FewMaps& maps, bool stall, cudaStream_t s
   MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(few_front_kernel)));
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, few_front_kernel, a, routers));
   MOE_LAUNCH_CHECK();
-  // no more CTAs than there can be units
-  const int64_t tc = few_token_chunks(a.T);
-  const int64_t units = (a.L / 32 + a.S / 16 + a.H / 32 * 2) * tc +
-                        static_cast<int64_t>(a.T) * a.k * (a.I / 16 + a.D / 32);
-  const int grid = static_cast<int>(units < num_sms() ? units : num_sms());
-  return stall ? launch_main<true>(a, maps, grid, st) : launch_main<false>(a, maps, grid, st);
+  return launch_main(a, maps, st);
 }
 
 }  // namespace moe

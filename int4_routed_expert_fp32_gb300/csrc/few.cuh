@@ -10,8 +10,8 @@
 namespace moe {
 
 constexpr int kFewTokens = 32;  // tokens of a call: one bit each in an expert's mask
-constexpr int kFewChunk = 4;    // most tokens that share one pass over an expert's weights
-constexpr int kFewRows = 8;     // tokens that share one pass over bf16 weights
+constexpr int kFewChunk = 2;    // tokens that share one pass over an expert's weights
+constexpr int kFewRows = 8;     // tokens that share one pass over bf16 weights (4 in two parts)
 constexpr int kFewColumns = 2048;  // int4 columns of a ring slot
 
 constexpr int kFewGroups = 8;   // groups of chunks whose outputs are summed before they are stored
@@ -61,7 +61,6 @@ struct FewArgs {
   float* yl;         // fp32 [T, H] latent up-projection
   int* status;
   long long wait_ns;
-  int chunk;         // tokens of a chunk, 2 or kFewChunk
   int stages;        // ring slots
   int stall_at;      // tests only: the weight copies stop before this stage (-1: never)
 };
@@ -100,13 +99,16 @@ __host__ __device__ inline int64_t few_start_at(int c) {
          c % kFewColumns / 16 * 4;
 }
 
-__host__ __device__ inline int few_token_chunks(int T) { return (T + kFewRows - 1) / kFewRows; }
+__host__ __device__ inline int few_chunks(int T, int rows) { return (T + rows - 1) / rows; }
+// Tokens that share a pass over the weights of a bf16 kind.
+__host__ __device__ inline int few_rows_of(int kind) {
+  return kind == kFewSharedDown || kind == kFewLatUp ? kFewRows / 2 : kFewRows;
+}
 
-// Tokens of a chunk, and ring slots that fit into shared memory.
-int few_chunk(const FewArgs& a);
+// Ring slots that fit into shared memory.
 int few_stages(const FewArgs& a);
 
 // Both launches (validated arguments, a workspace as few_api.cu carves it).
-int launch_few(const FewArgs& a, const FewMaps& maps, bool stall, cudaStream_t st);
+int launch_few(const FewArgs& a, const FewMaps& maps, cudaStream_t st);
 
 }  // namespace moe

@@ -20,7 +20,7 @@ size_t carve(FewArgs* a, void* base) {
     return p;
   };
   const size_t T = a->T, P = T * a->k, D = a->D, H = a->H, L = a->L, S = a->S;
-  const size_t tc = few_token_chunks(a->T);
+  const size_t tc = few_chunks(a->T, kFewRows / 2);
   a->n_counters = static_cast<int>(kFewFixed + P + D / 32 + (L ? H / 32 * tc : 0));
   a->counters = static_cast<int32_t*>(take(4 * static_cast<size_t>(a->n_counters)));
   a->logits = static_cast<float*>(take(a->router_w ? 4 * T * a->E : 0));
@@ -74,10 +74,10 @@ bool weight_maps(FewMaps* m, int which, const void* w, bool four, uint64_t K,
 
 // bf16 rows of tokens [planes, T, K] as [planes, pieces, T, 128 bytes]: those of a pass
 // over a slot of weights in one copy.
-bool rows_map(CUtensorMap* m, const void* x, int T, uint64_t K, uint64_t planes) {
+bool rows_map(CUtensorMap* m, const void* x, int T, int most, uint64_t K, uint64_t planes) {
   const uint64_t dims[4] = {64, static_cast<uint64_t>(T), K / 64, planes};
   const uint64_t strides[3] = {K * 2, 128, K * 2 * T};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(T < kFewRows ? T : kFewRows),
+  const uint32_t box[4] = {64, static_cast<uint32_t>(T < most ? T : most),
                            kFewColumns / 256, 1};
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, x, dims, strides, box,
                            CU_TENSOR_MAP_SWIZZLE_128B);
@@ -128,7 +128,6 @@ int run(FewArgs a, const Experts& w, const moe_weights* layer, const Block* in, 
     if (overlap(in[i].p, in[i].bytes, a.out, out_bytes) || overlap(in[i].p, in[i].bytes, ws, need))
       return MOE_ERR_INVALID;
   if (overlap(a.out, out_bytes, ws, need)) return MOE_ERR_INVALID;
-  a.chunk = few_chunk(a);
   a.stages = few_stages(a);
   if (a.stages < 2) return MOE_ERR_UNSUPPORTED;
   a.status = status_word();
@@ -157,10 +156,10 @@ int run(FewArgs a, const Experts& w, const moe_weights* layer, const Block* in, 
     if (t.w && !weight_maps(&m, i, t.w, i < 3, t.K, t.rows, t.n)) return MOE_ERR_CUDA;
     if (t.scale && !scale_map(&m.scale[i], t.scale, t.K, t.rows, t.n)) return MOE_ERR_CUDA;
   }
-  if ((L || S) && !rows_map(&m.rows[0], a.x, a.T, H, 1)) return MOE_ERR_CUDA;
-  if (S && !rows_map(&m.rows[1], a.hs, a.T, S, 2)) return MOE_ERR_CUDA;
-  if (L && !rows_map(&m.rows[2], a.z, a.T, L, 2)) return MOE_ERR_CUDA;
-  return launch_few(a, m, stall_at >= 0, static_cast<cudaStream_t>(stream));
+  if ((L || S) && !rows_map(&m.rows[0], a.x, a.T, kFewRows, H, 1)) return MOE_ERR_CUDA;
+  if (S && !rows_map(&m.rows[1], a.hs, a.T, kFewRows / 2, S, 2)) return MOE_ERR_CUDA;
+  if (L && !rows_map(&m.rows[2], a.z, a.T, kFewRows / 2, L, 2)) return MOE_ERR_CUDA;
+  return launch_few(a, m, static_cast<cudaStream_t>(stream));
 }
 
 int experts_few(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, int T, int D,
