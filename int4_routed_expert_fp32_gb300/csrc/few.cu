@@ -72,6 +72,11 @@ __host__ __device__ __forceinline__ int rows_bytes(const FewArgs& a) {
 
 constexpr int kMaxSlots = 8;
 constexpr int kAhead = 2;  // tickets a CTA holds
+// The matrix of a unit's first row block, 4 bits a kind.
+constexpr uint32_t kFirstMatrix =
+    kFewLatDownW << 4 * kFewLatDown | kFewSharedGateW << 4 * kFewSharedUp |
+    kFewGateW << 4 * kFewGateUp | kFewDownW << 4 * kFewDown |
+    kFewSharedDownW << 4 * kFewSharedDown | kFewLatUpW << 4 * kFewLatUp;
 
 // Partial sums of a finished segment for each finishing warp; at first what only the
 // making of the lists needs.
@@ -176,6 +181,31 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const W
 }
 constexpr int kRest = 100;  // ns
 
+// Weights pass through L2 once and first make room again: else 200 MB of them a call would
+// push everything else out, the kernels' own code too, which then comes from HBM line
+// by line (10 us at the start of a call).
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void copy_once_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c1,
+                                             int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void copy_once_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                             int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ int load_acquire(const int32_t* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -193,7 +223,8 @@ __device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
 }
 
 // Columns of K (int4) or of the bf16 rows that one slot holds, and the length of K.
-__device__ __forceinline__ bool is_int4(int kind) { return kind == kFewGateUp || kind == kFewDown; }
+__device__ __forceinline__ bool is_int4(int kind) { return (kind | 1) == kFewDown; }
+static_assert(kFewGateUp == 2 && kFewDown == 3, "is_int4");
 __device__ __forceinline__ int length_of(const FewArgs& a, int kind) {
   switch (kind) {
     case kFewLatDown:
@@ -203,6 +234,16 @@ __device__ __forceinline__ int length_of(const FewArgs& a, int kind) {
     case kFewSharedDown: return a.S;
     default: return a.L;
   }
+}
+
+// Order of fp32 values as integers, above 0 for every value.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
 // ------------------------------------------------------------------ prologue
@@ -231,7 +272,7 @@ __global__ void __launch_bounds__(kFrontThreads) few_front_kernel(const FewArgs 
         for (int e = 0; e < kFrontExperts; ++e) {
           w[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (c < a.H && e0 + e < a.E)
-            w[e][i] = __ldg(reinterpret_cast<const float4*>(a.router_w + (size_t)(e0 + e) * a.H + c));
+            w[e][i] = __ldcs(reinterpret_cast<const float4*>(a.router_w + (size_t)(e0 + e) * a.H + c));
         }
       }
 #pragma unroll 2
@@ -265,7 +306,13 @@ __global__ void __launch_bounds__(kFrontThreads) few_front_kernel(const FewArgs 
       float z = 0.f;
 #pragma unroll
       for (int w = 0; w < kFrontThreads / 32; ++w) z += part[t][e][w];
-      if (e0 + e < a.E) a.logits[(size_t)t * a.E + e0 + e] = z;
+      if (e0 + e < a.E) {
+        const float score = 1.0f / (1.0f + expf(-z));
+        const float key = score + __ldg(a.router_bias + e0 + e);
+        const size_t at = (size_t)t * a.E + e0 + e;
+        a.scores[at] = score;
+        a.keys[at] = ordered(key != key ? -INFINITY : key);  // NaN ranks last
+      }
     }
     return;
   }
@@ -370,6 +417,7 @@ struct __align__(16) Context {
   uint64_t full[kMaxSlots], empty[kMaxSlots], named[kMaxSlots];
   uint64_t sum_full[kFinish], sum_empty[kFinish], listed;
   uint32_t in_group[kFewGroups];
+  int units[kFewKinds], each[kFewKinds];  // units of a kind; of them for one tile or chunk
   int cta_abort, chunks;
   int ring_at, slot, sums_at, unit_at, lists_at;  // offsets into shared memory
 };
@@ -399,45 +447,30 @@ __device__ __forceinline__ Waiter waiter_of(Context& c) {
   return Waiter{&c.cta_abort, c.a.status, c.a.wait_ns};
 }
 
-__device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-}
-
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
 // Keys closer than this are compared again in 64 bits: it is far above what the
 // fp32 logits, the sigmoid and the sum leave open, and met by one token in a thousand.
 constexpr float kNear = 2e-5f;
 
-// One token's view of the router.  Passed by value, as the kernels' arguments have to
-// stay in the constant bank: a reference that leaves the kernel turns every access
-// to them into a load from memory.
+// One token's view of the router.  Passed by value: a reference to the kernel's arguments
+// that leaves the kernel would turn every access to them into a load from memory.
 struct Row {
-  const uint16_t* x;   // [H]
-  const float* z;      // [E] logits
-  const float* w;      // [E, H]
-  const float* bias;   // [E]
-  int H, E, k, renorm;
+  const uint16_t* x;     // [H]
+  const uint32_t* key;   // [E]
+  const float* w;        // [E, H]
+  const float* bias;     // [E]
+  int H, E, k;
 };
 
 // sigmoid(x . w_e) + bias_e in 64 bits (every lane gets it).
 __device__ __noinline__ double key64(Row a, int e, int lane) {
   double z = 0.0;
+#pragma unroll 1
   for (int c = lane; c < a.H; c += 32)
     z += static_cast<double>(bf16_bits_to_f32(a.x[c])) *
          static_cast<double>(a.w[(size_t)e * a.H + c]);
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   return 1.0 / (1.0 + exp(-z)) + static_cast<double>(a.bias[e]);
-}
-
-// fp32 key of one expert; NaN ranks last.
-__device__ __forceinline__ float key32(const Row& a, int e) {
-  const float r = 1.0f / (1.0f + expf(-__ldcg(a.z + e))) + __ldg(a.bias + e);
-  return r != r ? -INFINITY : r;
 }
 
 // Experts within kNear of the k-th key `low`, decided in 64 bits: lane j < k holds
@@ -445,25 +478,30 @@ __device__ __forceinline__ float key32(const Row& a, int e) {
 // of them (a router with no preference) stay as fp32 has them.
 __device__ __noinline__ int select_near(Row a, int lane, int mine, float low) {
   int mine_near = 0, n = 0, sure = 0;
+#pragma unroll 1
   for (int e0 = 0; e0 < a.E; e0 += 32) {
     const int e = e0 + lane;
-    const float r = e < a.E ? key32(a, e) : -INFINITY;
+    const float r = e < a.E ? unordered(__ldcg(a.key + e)) : -INFINITY;
     sure += __popc(__ballot_sync(0xffffffffu, r > low + kNear));
     uint32_t near = __ballot_sync(0xffffffffu, r <= low + kNear && r >= low - kNear);
+#pragma unroll 1
     for (; near; near &= near - 1, ++n)
       if (lane == (n & 31)) mine_near = e0 + __ffs(near) - 1;
     if (n > 16) return mine;
   }
   double key = 0.0;
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const double v = key64(a, __shfl_sync(0xffffffffu, mine_near, i), lane);
     if (lane == i) key = v;
   }
   int rank = 0;  // ids ascend with the lane
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const double v = __shfl_sync(0xffffffffu, key, i);
     rank += v > key || (v == key && i < lane);
   }
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int e = __shfl_sync(0xffffffffu, mine_near, i);
     const int to = sure + __shfl_sync(0xffffffffu, rank, i);
@@ -472,17 +510,18 @@ __device__ __noinline__ int select_near(Row a, int lane, int mine, float low) {
   return mine;
 }
 
-// The k experts of token t with the largest sigmoid(z) + bias (equal: the lower id)
-// and their weights; one warp.
-__device__ __forceinline__ void select_token(const Row a, int lane, float* weight, uint16_t* id) {
+// The k experts with the largest keys (equal: the lower id); one warp, lane j < k gets
+// choice j.
+__device__ __noinline__ int select_token(Row a, int lane) {
   constexpr int NPL = 16;  // experts of a lane whose keys stay in registers
   uint32_t key[NPL];
   uint64_t gone = 0;  // chosen ones among the others
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
-    key[i] = lane + 32 * i < a.E ? ordered(key32(a, lane + 32 * i)) : 0u;
+    key[i] = lane + 32 * i < a.E ? __ldcg(a.key + lane + 32 * i) : 0u;
   uint32_t low = 0, next = 0;
   int mine = 0;
+#pragma unroll 1
   for (int j = 0; j <= a.k && j < a.E; ++j) {  // one more than k: the best that stays out
     uint32_t best = 0u;
     int at = 0;
@@ -492,8 +531,9 @@ __device__ __forceinline__ void select_token(const Row a, int lane, float* weigh
         best = key[i];
         at = i;
       }
+#pragma unroll 1
     for (int i = NPL; lane + 32 * i < a.E; ++i) {
-      const uint32_t v = gone >> i & 1u ? 0u : ordered(key32(a, lane + 32 * i));
+      const uint32_t v = gone >> i & 1u ? 0u : __ldcg(a.key + lane + 32 * i);
       if (v > best) {
         best = v;
         at = i;
@@ -515,12 +555,7 @@ __device__ __forceinline__ void select_token(const Row a, int lane, float* weigh
   }
   const float f_low = unordered(low), f_next = next ? unordered(next) : -INFINITY;
   if (f_next > -INFINITY && f_low - f_next <= kNear) mine = select_near(a, lane, mine, f_low);
-  const float s = lane < a.k ? 1.0f / (1.0f + expf(-__ldcg(a.z + mine))) : 0.f;
-  const float sum = warp_sum(s);
-  if (lane < a.k) {
-    weight[lane] = a.renorm ? __fdiv_rn(s, sum + 1e-20f) : s;
-    id[lane] = static_cast<uint16_t>(mine);
-  }
+  return mine;
 }
 
 // Chunks of a group, for at most kFewGroups groups.
@@ -548,29 +583,37 @@ __device__ __noinline__ void build_lists(int tid) {
   float* weight = reinterpret_cast<float*>(mask + a.E);
   uint16_t* base = reinterpret_cast<uint16_t*>(weight + a.T * a.k);
   uint16_t* row = base + a.E;
-  const int lane = tid & 31, warp = tid >> 5, pairs = a.T * a.k;
+  const int lane = tid & 31, warp = tid >> 5, k = a.k, pairs = a.T * k;
+#pragma unroll 1
   for (int e = tid; e < a.E; e += kMul * 32) mask[e] = 0u;
   if (tid < kFewGroups) ls.in_group[tid] = 0u;
-  if (a.router_w) {
-    for (int t = warp; t < a.T; t += kMul)
-      select_token(Row{a.x + (size_t)t * a.H, a.logits + (size_t)t * a.E, a.router_w, a.router_bias,
-                       a.H, a.E, a.k, a.renorm},
-                   lane, weight + t * a.k, row + t * a.k);
-  } else {
-    for (int p = tid; p < pairs; p += kMul * 32) {
-      const int e = a.topk_idx[p];
+  mul_sync();
+  // a warp a token, lane j its choice j
+#pragma unroll 1
+  for (int t = warp; t < a.T; t += kMul) {
+    int e = 0;
+    float w = 0.f;
+    if (a.router_w) {
+      e = select_token(Row{a.x + (size_t)t * a.H, a.keys + (size_t)t * a.E, a.router_w,
+                           a.router_bias, a.H, a.E, k}, lane);
+      if (lane < k) w = __ldcg(a.scores + (size_t)t * a.E + e);
+      if (a.renorm) w = __fdividef(w, warp_sum(w) + 1e-20f);
+    } else if (lane < k) {
+      e = a.topk_idx[t * k + lane];
+      w = a.topk_w[t * k + lane];
+    }
+    if (lane < k) {
       const bool ok = e >= 0 && e < a.E;
-      if (!ok) record_status(a.status, MOE_ERR_INVALID);
-      weight[p] = a.topk_w[p];
-      row[p] = ok ? static_cast<uint16_t>(e) : 0xffffu;
+      if (ok) atomicOr(&mask[e], 1u << t);
+      else record_status(a.status, MOE_ERR_INVALID);
+      weight[t * k + lane] = w;
+      row[t * k + lane] = ok ? static_cast<uint16_t>(e) : 0xffffu;
     }
   }
   mul_sync();
-  for (int p = tid; p < pairs; p += kMul * 32)
-    if (row[p] != 0xffffu) atomicOr(&mask[row[p]], 1u << (p / a.k));
-  mul_sync();
   if (warp == 0) {
     int rows = 0, chunks = 0;
+#pragma unroll 1
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
       uint32_t m = e < a.E ? mask[e] : 0u;
@@ -585,10 +628,13 @@ __device__ __noinline__ void build_lists(int tid) {
       rows += __shfl_sync(0xffffffffu, sum, 31) & 0xffff;
       chunks += __shfl_sync(0xffffffffu, sum, 31) >> 16;
       if (e < a.E) base[e] = static_cast<uint16_t>(r);
-      for (int i = 0; i < c; ++i, ++at, r += kFewChunk) {
-        uint32_t part = 0u;
-        for (int b = 0; b < kFewChunk && m; ++b, m &= m - 1) part |= m & (0u - m);
-        ls.tokens[at] = part;
+#pragma unroll 1
+      for (; m; ++at, r += kFewChunk) {
+        const uint32_t first = m & (0u - m);
+        m ^= first;
+        const uint32_t second = m & (0u - m);
+        m ^= second;
+        ls.tokens[at] = first | second;
         ls.expert[at] = static_cast<uint16_t>(e);
         ls.row0[at] = static_cast<uint16_t>(r);
       }
@@ -596,62 +642,38 @@ __device__ __noinline__ void build_lists(int tid) {
     __syncwarp();
     if (lane == 0) {
       *ls.chunks = chunks;
+      cx.units[kFewGateUp] = chunks * (a.I / 16);
+      cx.units[kFewDown] = group_count(chunks) * (a.D / 32);
       mbar_arrive(&cx.listed);  // the copies may start
     }
   }
+#pragma unroll 1
   for (int p = tid; p < pairs; p += kMul * 32) ls.row_weight[p] = 0.f;
   mul_sync();
-  for (int p = tid; p < pairs; p += kMul * 32) {
-    const int e = row[p];
-    if (e != 0xffff)
-      row[p] = static_cast<uint16_t>(base[e] + __popc(mask[e] & ((1u << (p / a.k)) - 1u)));
-  }
   const int chunks = *ls.chunks, per = group_chunks(chunks);
+#pragma unroll 1
   for (int i = tid; i < chunks; i += kMul * 32) atomicOr(&ls.in_group[i / per], ls.tokens[i]);
-  mul_sync();
-  if (tid < a.T)  // an expert that a token lists twice counts twice
-    for (int p = tid * a.k; p < (tid + 1) * a.k; ++p)
-      if (row[p] != 0xffffu) ls.row_weight[row[p]] += weight[p];
-  if (chunks == 0)  // no valid choice at all: no unit will write the output
+  if (tid < a.T) {  // an expert that a token lists twice counts twice
+#pragma unroll 1
+    for (int p = tid * k; p < (tid + 1) * k; ++p) {
+      const int e = row[p];
+      if (e != 0xffff) ls.row_weight[base[e] + __popc(mask[e] & ((1u << tid) - 1u))] += weight[p];
+    }
+  }
+  if (chunks == 0) {  // no valid choice at all: no unit will write the output
+#pragma unroll 1
     for (int i = blockIdx.x * kMul * 32 + tid; i < a.T * a.H; i += gridDim.x * kMul * 32)
       a.out[i] = 0;
+  }
   mul_sync();
 }
+static_assert(kFewChunk == 2, "the lists take two tokens at a time");
 
 __device__ __forceinline__ int nth_token(uint32_t tokens, int i) {
-  for (; i > 0; --i) tokens &= tokens - 1;
-  return __ffs(tokens) - 1;
+  return 31 - __clz(i ? tokens : tokens & (0u - tokens));
 }
 
 // --------------------------------------------------------------------- units
-
-struct Counts {  // units of each kind, in ticket order
-  int n[kFewKinds];
-};
-
-__device__ __forceinline__ Counts count_units(const FewArgs& a, int chunks) {
-  const int whole = few_chunks(a.T, kFewRows), half = few_chunks(a.T, kFewRows / 2);
-  Counts c;
-  c.n[kFewLatDown] = a.L / 32 * whole;
-  c.n[kFewSharedUp] = a.S / 16 * whole;
-  c.n[kFewGateUp] = chunks * (a.I / 16);
-  c.n[kFewDown] = group_count(chunks) * (a.D / 32);
-  c.n[kFewSharedDown] = a.S > 0 ? a.H / 32 * half : 0;
-  c.n[kFewLatUp] = a.L > 0 ? a.H / 32 * half : 0;
-  return c;
-}
-
-// The matrix of a unit's first row block.
-__device__ __forceinline__ int matrix_of(int kind) {
-  switch (kind) {
-    case kFewLatDown: return kFewLatDownW;
-    case kFewSharedUp: return kFewSharedGateW;
-    case kFewGateUp: return kFewGateW;
-    case kFewDown: return kFewDownW;
-    case kFewSharedDown: return kFewSharedDownW;
-    default: return kFewLatUpW;
-  }
-}
 
 // A role's place in the ring: slot, parity of its use, slots passed.  (A division by the
 // number of slots would cost more than the rest of a role's turn.)
@@ -680,61 +702,50 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
   const Ring ring = ring_of(cx);
   const Lists ls = lists_of(cx);
   const Waiter wt = waiter_of(cx);
+  const uint64_t once = evict_first();
   Place at;
   bool ok = true, known = false;
-  Counts units = count_units(a, 0);
-  const int fixed = units.n[kFewLatDown] + units.n[kFewSharedUp];
+  const int fixed = cx.units[kFewLatDown] + cx.units[kFewSharedUp];
   // kAhead tickets at a time, so that a unit does not wait for its own
   int ticket = lane < kAhead ? atomicAdd(a.counters, 1) : 0;
-  for (int turn = 0; ok; turn = (turn + 1) % kAhead) {
+#pragma unroll 1
+  for (int turn = 0; ok; turn ^= 1) {
     int u = __shfl_sync(0xffffffffu, ticket, turn);
     if (lane == turn) ticket = atomicAdd(a.counters, 1);
     if (u >= fixed && !known) {
       known = true;
       ok = wait_for<kRest>(&cx.listed, 0, wt);
       if (!ok) break;
-      units = count_units(a, *ls.chunks);
     }
+    int kind = 0;
+#pragma unroll 1
+    while (kind < kFewKinds && u >= cx.units[kind]) u -= cx.units[kind++];
     Header h{kFewEnd, 0, 0, 0};
-    int row[2] = {0, 0}, end = 1;  // segments h.which .. end - 1
-#pragma unroll
-    for (int kind = 0; kind < kFewKinds; ++kind) {
-      if (h.kind != kFewEnd) break;
-      if (u >= units.n[kind]) {
-        u -= units.n[kind];
-        continue;
-      }
-      h.kind = kind;
-      if (kind == kFewGateUp) {
-        h.which = u / (a.I / 16);
-        h.n0 = (u - h.which * (a.I / 16)) * 16;
-        end = h.which + 1;
-      } else if (kind == kFewDown) {
-        const int group = u / (a.D / 32), per = group_chunks(*ls.chunks);
-        h.n0 = (u - group * (a.D / 32)) * 32;
-        h.which = group * per;
-        end = min(h.which + per, *ls.chunks);
-      } else {
-        const int rows = few_rows_of(kind), chunks = few_chunks(a.T, rows);
-        h.n0 = u / chunks * (kind == kFewSharedUp ? 16 : 32);
-        h.which = u % chunks;
-        h.size = min(rows, a.T - h.which * rows);
-        end = h.which + 1;
-      }
-    }
-    const int kind = h.kind;
+    int end = 1;  // segments h.which .. end - 1
+    const bool pair = kind == kFewGateUp || kind == kFewSharedUp;  // two matrices
     const bool four = is_int4(kind);
-    row[0] = h.n0;
-    row[1] = h.n0 + (kind == kFewGateUp || kind == kFewSharedUp ? 0 : 16);
-    const int w0 = matrix_of(kind), w1 = w0 + (kind == kFewGateUp || kind == kFewSharedUp);
-    const int K = kind == kFewEnd ? 1 : length_of(a, kind);
-    const int step = four ? C : C / 4, wide = four ? 256 : 64;  // columns of 128 bytes
-    for (; ok && h.which < end; ++h.which) {
-      int mat = 0;
-      if (four) {
-        h.size = __popc(ls.tokens[h.which]);
-        mat = ls.expert[h.which];
+    int K = 1;
+    if (kind < kFewKinds) {
+      const int each = cx.each[kind], q = u / each, r = u - q * each;
+      const int tile = pair ? 16 : 32;
+      h = Header{kind, 0, four ? q : r, (four ? r : q) * tile};
+      end = h.which + 1;
+      if (kind == kFewDown) {
+        const int per = group_chunks(*ls.chunks);
+        h.which *= per;
+        end = min(h.which + per, *ls.chunks);
       }
+      K = length_of(a, kind);
+    }
+    const int w0 = kFirstMatrix >> 4 * kind & 15, w1 = w0 + pair;
+    const int row1 = h.n0 + (pair ? 0 : 16);
+    const int step = four ? C : C / 4, wide = four ? 256 : 64;  // columns of 128 bytes
+#pragma unroll 1
+    for (; ok && h.which < end; ++h.which) {
+      const int rows = few_rows_of(kind);
+      const int mat = four ? ls.expert[h.which] : 0;
+      const int size = four ? __popc(ls.tokens[h.which]) : min(rows, a.T - h.which * rows);
+#pragma unroll 1
       for (int k0 = 0; k0 < K; k0 += step, at.next(ring.n)) {
         const uint32_t s = at.s;
         if (static_cast<int>(at.n) == a.stall_at) {  // tests only
@@ -743,82 +754,46 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
         }
         ok = wait_for<kRest>(&ring.empty[s], at.parity ^ 1u, wt);
         if (!ok) break;
-        const int cols = min(step, K - k0);
         if (lane == 0) {
-          Header q = h;
-          q.size |= cols << 16;
-          if (k0 + step >= K) q.kind |= h.which + 1 == end ? kLastSlot | kLastSegment : kLastSlot;
-          ring.header[s] = q;
+          const int cols = min(step, K - k0);
+          const bool last = k0 + step >= K;
+          uint64_t* bar = &ring.full[s];
+          ring.header[s] = Header{h.kind | (last ? kLastSlot : 0) |
+                                      (last && h.which + 1 == end ? kLastSegment : 0),
+                                  size | cols << 16, h.which, h.n0};
           mbar_arrive(&ring.named[s]);
-          if (kind == kFewEnd) {
-            mbar_arrive(&ring.full[s]);
-          } else {
-            // one thread issues all copies: operands that differ between lanes would
-            // be taken up one lane after another (200 cycles each)
-            const int pieces = cols / wide;
-            const bool tail = cols % wide != 0;
-            uint64_t* bar = &ring.full[s];
-            mbar_arrive_expect_tx(bar, (pieces + tail) * 2 * 2048);
+          // one thread issues all copies: operands that differ between lanes would
+          // be taken up one lane after another (200 cycles each)
+          const int pieces = cols / wide;
+          const bool tail = four && cols % wide != 0;
+          mbar_arrive_expect_tx(bar, kind == kFewKinds ? 0 : (pieces + tail) * 2 * 2048);
+          if (kind < kFewKinds) {
             uint8_t* dst = ring.slot(s);
             if (pieces > 0) {
               const CUtensorMap* m = cols == step ? maps->full : maps->rest;
-              tma_g2s_4d(dst, m + w0, bar, 0, row[0], k0 / wide, mat);
-              tma_g2s_4d(dst + kWeightBytes / 2, m + w1, bar, 0, row[1], k0 / wide, mat);
+              copy_once_4d(dst, m + w0, bar, h.n0, k0 / wide, mat, once);
+              copy_once_4d(dst + kWeightBytes / 2, m + w1, bar, row1, k0 / wide, mat, once);
             }
             if (tail) {
               dst += pieces * 2048;
               const int word = (k0 + pieces * wide) / 8;
-              tma_g2s_3d(dst, maps->tail + w0, bar, word, row[0], mat);
-              tma_g2s_3d(dst + kWeightBytes / 2, maps->tail + w1, bar, word, row[1], mat);
+              copy_once_3d(dst, maps->tail + w0, bar, word, h.n0, mat, once);
+              copy_once_3d(dst + kWeightBytes / 2, maps->tail + w1, bar, word, row1, mat, once);
             }
           }
         }
         __syncwarp();
       }
     }
-    if (kind == kFewEnd) break;
+    if (kind == kFewKinds) break;
   }
   // whatever ended the loop, no copy is still on its way when the CTA leaves
   drain_ring(ring.full, at.n, ring.n, a.status);
 }
-
-// The scales of slot i of a segment.
-__device__ __forceinline__ void copy_scales(const FewArgs& a, const FewMaps* maps, const Ring& ring,
-                                            uint32_t s, int i, int kind, int mat, int n0, int lane) {
-  const bool lanes = !(a.tma_scale[0] && a.tma_scale[1]);  // every lane arrives on a slot
-  uint64_t* bar = &ring.full[s];
-  if (!is_int4(kind)) {
-    if (lanes || lane == 0) mbar_arrive(bar);
-    return;
-  }
-  const bool down = kind == kFewDown;
-  const int row1 = n0 + (down ? 16 : 0);
-  uint8_t* dst = ring.scales(s);
-  if (a.tma_scale[down]) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar, kScaleBytes);
-      const CUtensorMap* m = maps->scale + (down ? kFewDownW : kFewGateW);
-      tma_g2s_3d(dst, m, bar, i * (C / kGroup), n0, mat);
-      tma_g2s_3d(dst + kScaleBytes / 2, m + !down, bar, i * (C / kGroup), row1, mat);
-    } else if (lanes) {
-      mbar_arrive(bar);
-    }
-  } else {
-    // rows of K / 16 bytes, not 16-byte aligned: 4 bytes (two groups) at a time
-    const int K = down ? a.I : a.D, N = down ? a.D : a.I, pairs = min(C, K - i * C) / 64;
-    for (int j = lane; j < 32 * pairs; j += 32) {
-      const int r = j / pairs, g2 = j - r * pairs, block = r >> 4;
-      const uint16_t* src = a.scale[down ? 2 : block] +
-                            ((size_t)mat * N + (block ? row1 : n0) + (r & 15)) * (K / kGroup) +
-                            i * (C / kGroup) + 2 * g2;
-      cp_async_4(dst + block * (kScaleBytes / 2) + scale_at(r & 15, g2), src);
-    }
-    cp_async_arrive_noinc(bar);
-  }
-}
+static_assert(kAhead == 2, "tickets in turn");
 
 // Waits until counter `c` has reached `n`; false when the time ran out.
-__device__ __forceinline__ bool wait_count(const int32_t* c, int n, const Waiter& wt) {
+__device__ __noinline__ bool wait_count(const int32_t* c, int n, Waiter wt) {
   if (load_acquire(c) >= n) return true;
   const uint64_t t0 = global_timer_ns();
   while (load_acquire(c) < n) {
@@ -839,76 +814,121 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
   const Ring ring = ring_of(cx);
   const Lists ls = lists_of(cx);
   const Waiter wt = waiter_of(cx);
-  const int tc = few_chunks(a.T, kFewRows);
+  const uint64_t once = evict_first();
+  const bool lanes = !(a.tma_scale[0] && a.tma_scale[1]);  // every lane arrives on a slot
   int known = 0;         // chunks whose h is known to be complete
-  uint32_t others = 0;   // kinds whose rows are
-  for (Place at;;) {
-    if (!wait_for<kRest>(&ring.named[at.s], at.parity, wt)) break;
-    const Header h = ring.header[at.s];
+  uint32_t others = a.L > 0 ? 0u : 1u << kFewGateUp;  // kinds whose rows are
+  others |= 1u << kFewLatDown | 1u << kFewSharedUp;
+  int i = 0;  // slot of the segment
+  int mat = 0, K = 0;
+  int64_t pitch = 0;
+  const uint8_t* src = nullptr;
+#pragma unroll 1
+  for (Place at;; at.next(ring.n)) {
+    const uint32_t s = at.s;
+    if (!wait_for<kRest>(&ring.named[s], at.parity, wt)) break;
+    const Header h = ring.header[s];
     const int kind = h.kind & 255;
-    const int mat = is_int4(kind) ? ls.expert[h.which] : 0;
-    copy_scales(a, maps, ring, at.s, 0, kind, mat, h.n0, lane);  // these wait for nothing
+    const bool four = is_int4(kind), down = kind == kFewDown;
+    uint64_t* bar = &ring.full[s];
+    if (four && i == 0) {
+      mat = ls.expert[h.which];
+      K = down ? a.I : a.D;
+      pitch = few_row_bytes(K);
+      src = down ? a.h16 + ls.row0[h.which] * pitch : a.x16;
+    }
+    // scales, which wait for nothing
+    if (!four) {
+      if (lanes || lane == 0) mbar_arrive(bar);
+    } else {
+      const int row1 = h.n0 + (down ? 16 : 0);
+      uint8_t* dst = ring.scales(s);
+      if (a.tma_scale[down] == kScalesDense) {
+        // 16 whole rows at a time, one behind the other
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, 2 * K);
+          const int N = down ? a.D : a.I, per_row = K / kGroup;
+          const int64_t at = ((int64_t)mat * N + h.n0) * per_row;
+          bulk_g2s(dst, a.scale[down ? 2 : 0] + at, K, bar);
+          bulk_g2s(dst + kScaleBytes / 2, a.scale[down ? 2 : 1] + at + (down ? 16 * per_row : 0), K,
+                   bar);
+        } else if (lanes) {
+          mbar_arrive(bar);
+        }
+      } else if (a.tma_scale[down]) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, kScaleBytes);
+          const CUtensorMap* m = maps->scale + (down ? kFewDownW : kFewGateW);
+          copy_once_3d(dst, m, bar, i * (C / kGroup), h.n0, mat, once);
+          copy_once_3d(dst + kScaleBytes / 2, m + !down, bar, i * (C / kGroup), row1, mat, once);
+        } else if (lanes) {
+          mbar_arrive(bar);
+        }
+      } else {
+        // rows of K / 16 bytes, not 16-byte aligned: 4 bytes (two groups) at a time
+        const int N = down ? a.D : a.I, pairs = h.cols() / 64;
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+          const uint16_t* from = a.scale[down ? 2 : b] +
+                                 ((size_t)mat * N + (b ? row1 : h.n0)) * (K / kGroup) +
+                                 i * (C / kGroup);
+#pragma unroll 1
+          for (int j = lane; j < 16 * pairs; j += 32) {
+            const int r = j / pairs, g2 = j - r * pairs;
+            cp_async_4(dst + b * (kScaleBytes / 2) + scale_at(r, g2), from + r * (K / kGroup) + 2 * g2);
+          }
+        }
+        cp_async_arrive_noinc(bar);
+      }
+    }
     if (kind == kFewEnd) {
-      if (lane == 0) mbar_arrive(&ring.full[at.s]);
+      if (lane == 0) mbar_arrive(bar);
       return;
     }
     // the rows this segment reads have to be there
-    bool ok = true;
-    if (kind == kFewDown) {
-      if (h.which >= known) {
-        // this chunk, and what a look at the next ones shows at the same time
-        const int32_t* c = a.counters + kFewFixed + h.which;
-        const bool there = h.which + lane < a.T * a.k;
-        ok = wait_count(c, a.I / 16, wt);
-        const uint32_t done =
-            __ballot_sync(0xffffffffu, there && load_acquire(c + lane) >= a.I / 16);
+    if (i == 0 && (down ? h.which >= known : !(others >> kind & 1u))) {
+      const int32_t* c = a.counters + (down ? kFewFixed + h.which
+                                            : kind == kFewGateUp ? 1 : kind == kFewSharedDown ? 2 : 3);
+      const int whole = few_chunks(a.T, kFewRows);
+      const int n = down ? a.I / 16
+                         : kind == kFewGateUp ? a.L / 32 * whole
+                                              : kind == kFewSharedDown ? a.S / 16 * whole : a.L / 32;
+      const bool ok = wait_count(c, n, wt);
+      if (down) {
+        // and what a look at the next chunks shows at the same time
+        const bool there = h.which + lane < a.T * a.k && load_acquire(c + lane) >= n;
+        const uint32_t done = __ballot_sync(0xffffffffu, there);
         known = h.which + (~done ? __ffs(~done) - 1 : 32);
+      } else {
+        others |= 1u << kind;
       }
-    } else if (!(others >> kind & 1u)) {
-      others |= 1u << kind;
-      if (kind == kFewGateUp && a.L > 0) ok = wait_count(a.counters + 1, a.L / 32 * tc, wt);
-      if (kind == kFewSharedDown) ok = wait_count(a.counters + 2, a.S / 16 * tc, wt);
-      if (kind == kFewLatUp) ok = wait_count(a.counters + 3, a.L / 32, wt);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      __syncwarp();  // what one lane has seen holds for all
+      // written through the generic proxy, read by copies
+      asm volatile("fence.proxy.async.global;" ::: "memory");
     }
-    if (!__all_sync(0xffffffffu, ok)) break;
-    __syncwarp();  // what one lane has seen holds for all
-    // written through the generic proxy, read by copies
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    const int K = length_of(a, kind), rows = h.rows();
-    const bool four = is_int4(kind);
-    const int64_t pitch = few_row_bytes(K);
-    const uint8_t* src = kind == kFewDown ? a.h16 + ls.row0[h.which] * pitch : a.x16;
-    const uint32_t tokens = kind == kFewGateUp ? ls.tokens[h.which] : (1u << rows) - 1u;
-    const bool two = kind == kFewSharedDown || kind == kFewLatUp;
-    const CUtensorMap* m = maps->rows + (kind == kFewSharedDown ? 1 : kind == kFewLatUp ? 2 : 0);
-    const int slots = (K + (four ? C : C / 4) - 1) / (four ? C : C / 4);
+    if (lane == 0) {
+      uint8_t* dst = ring.rows(s);
+      if (four) {
+        const uint32_t tokens = ls.tokens[h.which];
+        mbar_arrive_expect_tx(bar, h.rows() * kFewBlock);
+        const uint8_t* from = src + i * kFewBlock;
 #pragma unroll 1
-    for (int i = 0; i < slots; ++i, at.next(ring.n)) {
-      const uint32_t s = at.s;
-      if (i > 0) {
-        ok = wait_for<kRest>(&ring.named[s], at.parity, wt);
-        if (!ok) break;
-        copy_scales(a, maps, ring, s, i, kind, mat, h.n0, lane);
-      }
-      if (lane == 0) {
-        uint64_t* bar = &ring.full[s];
-        uint8_t* dst = ring.rows(s);
-        if (four) {
-          mbar_arrive_expect_tx(bar, rows * kFewBlock);
-          const uint8_t* from = src + i * kFewBlock;
+        for (int r = 0; r < h.rows(); ++r)
+          bulk_g2s(dst + r * kPitch4, from + (down ? r : nth_token(tokens, r)) * pitch, kFewBlock,
+                   bar);
+      } else {
+        const int most = few_rows_of(kind), bytes = min(a.T, most) * (C / 2);
+        const int parts = most == kFewRows ? 1 : 2;
+        const CUtensorMap* m = maps->rows + (parts == 1 ? 0 : kind == kFewSharedDown ? 1 : 2);
+        mbar_arrive_expect_tx(bar, parts * bytes);
 #pragma unroll 1
-          for (uint32_t m = tokens; m; m &= m - 1, dst += kPitch4)
-            bulk_g2s(dst, from + (__ffs(m) - 1) * pitch, kFewBlock, bar);
-        } else {
-          const int most = few_rows_of(kind), bytes = min(a.T, most) * (C / 2);
-          mbar_arrive_expect_tx(bar, two ? 2 * bytes : bytes);
-          tma_g2s_4d(dst, m, bar, 0, h.which * most, i * (C / 256), 0);
-          if (two) tma_g2s_4d(dst + bytes, m, bar, 0, h.which * most, i * (C / 256), 1);
-        }
+        for (int p = 0; p < parts; ++p)
+          tma_g2s_4d(dst + p * bytes, m, bar, 0, h.which * most, i * (C / 256), p);
       }
-      __syncwarp();
     }
-    if (!ok) break;
+    __syncwarp();
+    i = (h.kind & kLastSlot) ? 0 : i + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // a wait that ran out: nothing stays on its way
 }
@@ -940,8 +960,8 @@ struct Lane {
 
 // Step `step` of a slot: adds to acc[block][0, 1] (rows g and g + 8).
 __device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int cols, const Lane& l,
-                                          int x_at, int start_at, const Magic& magic, uint4 (&v)[4],
-                                          float (&acc)[2][4]) {
+                                          int x_at, int start_at, bool dense, const Magic& magic,
+                                          uint4 (&v)[4], float (&acc)[2][4]) {
   if (l.on) {
     const uint4* row = reinterpret_cast<const uint4*>(slot + x_at + step * 256);
 #pragma unroll
@@ -952,7 +972,9 @@ __device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int col
   const float start0 = s.x + s.y, start1 = s.z + s.w;
   const uint8_t* w =
       slot + (step >> 1) * 2048 + l.r * 128 + ((((step & 1) << 2 | l.t) ^ (l.r & 7)) << 4);
-  const uint8_t* sc = slot + kWeightBytes + scale_at(l.r, 2 * step + (l.t & 1));
+  const int g2 = 2 * step + (l.t & 1), pitch = dense ? cols / 16 : 128;
+  const uint8_t* sc =
+      slot + kWeightBytes + (dense ? l.r * pitch + g2 * 4 : static_cast<int>(scale_at(l.r, g2)));
   // the last step of a row may be half: its upper two groups add nothing
   const bool there = step < cols / 128 || !(l.t & 1);
 #pragma unroll
@@ -961,7 +983,7 @@ __device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int col
     const uint4 q8 = *reinterpret_cast<const uint4*>(w + b * (kWeightBytes / 2) + 1024);
     const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w8[4] = {q8.x, q8.y, q8.z, q8.w};
     const uint32_t s0 = *reinterpret_cast<const uint32_t*>(sc + b * (kScaleBytes / 2));
-    const uint32_t s8 = *reinterpret_cast<const uint32_t*>(sc + b * (kScaleBytes / 2) + 1024);
+    const uint32_t s8 = *reinterpret_cast<const uint32_t*>(sc + b * (kScaleBytes / 2) + 8 * pitch);
     float c[4] = {start0, start1, start0, start1};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1024,6 +1046,7 @@ __device__ __noinline__ void multiply(int warp, int lane) {
   uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  const bool dense[2] = {a.tma_scale[0] == kScalesDense, a.tma_scale[1] == kScalesDense};
   int buf = 0;             // the finishing warp of this unit
   uint32_t taken = 0;      // parity of its buffer, one bit a warp
   for (Place at;; at.next(slots)) {
@@ -1036,7 +1059,7 @@ __device__ __noinline__ void multiply(int warp, int lane) {
       const int steps = (h.cols() + 127) / 128;
 #pragma unroll 1
       for (int step = warp; step < steps; step += kMul)
-        multiply4(slot, step, h.cols(), l, x_at, start_at, magic, v, acc);
+        multiply4(slot, step, h.cols(), l, x_at, start_at, dense[kind - kFewGateUp], magic, v, acc);
     } else {
       if (kind == kFewEnd) break;
       const int most = few_rows_of(kind);
@@ -1085,78 +1108,58 @@ __device__ __noinline__ void multiply(int warp, int lane) {
 
 // ----------------------------------------------------------------- finishing
 
-__device__ __forceinline__ float total(const Sums& sums, int buf, int block, int token, int row) {
-  float v = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMul; ++i) v += sums.at(buf, i, block, token)[row];
-  return v;
-}
-
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
-
-// A value as the sum of two bf16 values: 16 bits of significand.
-__device__ __forceinline__ void store_parts(uint16_t* p, size_t plane, float v) {
-  const uint16_t hi = f32_to_bf16_bits(v);
-  p[0] = hi;
-  p[plane] = f32_to_bf16_bits(v - bf16_bits_to_f32(hi));
-}
-
 // Adds one to a counter after the warp's stores.
 __device__ __forceinline__ void count_done(int32_t* c, int lane) {
   __syncwarp();
   if (lane == 0) add_release(c, 1);
 }
 
-// The same; whether that made it `n`: then all other contributions can be read.
-__device__ __forceinline__ bool count_last(int32_t* c, int n, int lane) {
-  __syncwarp();
-  int old = 0;
-  if (lane == 0) old = add_acq_rel(c, 1);
-  old = __shfl_sync(0xffffffffu, old, 0);
-  if (old != n - 1) return false;
-  __threadfence();
-  return true;
-}
-
-// Column n0 + lane of every token: the groups' sums, in order, whichever order they
-// were computed in.
-template <class Store>
-__device__ __forceinline__ void combine(const FewArgs& a, const Lists& ls, int n0, int lane,
-                                        Store store) {
-  const int groups = group_count(*ls.chunks);
+// Column n (of this lane) of every token: the groups' sums, in order, whichever order they
+// were computed in, and the shared expert's; for the latent path as two bf16 parts
+// with the gain, and their squares summed over the 32 columns.
+__device__ __noinline__ void combine(int n, int lane) {
+  Context& cx = context();
+  const FewArgs& a = cx.a;
+  const int groups = group_count(cx.chunks);
+  const bool latent = a.L > 0;
+  const float gain = latent && a.norm ? bf16_bits_to_f32(__ldg(a.lat_norm + n)) : 1.0f;
   constexpr int kBatch = 2;  // tokens whose loads are on their way at a time
-  const float* y = a.y + n0 + lane;
+#pragma unroll 1
   for (int t0 = 0; t0 < a.T; t0 += kBatch) {
-    float v[kBatch][kFewGroups];
+    float v[kBatch][kFewGroups], shared[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < kBatch; ++i) {
+      const bool there = t0 + i < a.T;
 #pragma unroll
       for (int g = 0; g < kFewGroups; ++g) {
         v[i][g] = 0.f;
-        if (g < groups && t0 + i < a.T && (ls.in_group[g] >> (t0 + i) & 1u))
-          v[i][g] = __ldcg(y + ((size_t)g * a.T + t0 + i) * a.D);
+        if (there && g < groups && (cx.in_group[g] >> (t0 + i) & 1u))
+          v[i][g] = __ldcg(a.y + ((size_t)g * a.T + t0 + i) * a.D + n);
       }
+      shared[i] = there && !latent && a.S > 0 ? __ldcg(a.ys + (size_t)(t0 + i) * a.H + n) : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (t0 + i >= a.T) break;
       float sum = 0.f;
 #pragma unroll
       for (int g = 0; g < kFewGroups; ++g) sum += v[i][g];
-      store(t0 + i, sum);
+      sum += shared[i];
+      const int t = t0 + i;
+      const float q = warp_sum(sum * sum);
+      if (t >= a.T) break;
+      if (!latent) {
+        a.out[(size_t)t * a.H + n] = f32_to_bf16_bits(sum);
+      } else {
+        if (lane == 0) a.ssq[(size_t)(n / 32) * a.T + t] = q;
+        // 16 bits of significand
+        uint16_t* p = a.z + (size_t)t * a.L + n;
+        const uint16_t high = f32_to_bf16_bits(sum * gain);
+        p[0] = high;
+        p[(size_t)a.T * a.L] = f32_to_bf16_bits(sum * gain - bf16_bits_to_f32(high));
+      }
     }
   }
-}
-
-// Column c of a row of fp16 values, and with the 16 lanes of a half warp the start value
-// of its 16 columns.
-__device__ __forceinline__ void store_f16(const FewArgs& a, uint8_t* row, int c, float v, int lane) {
-  if (!(fabsf(v) <= 65504.0f)) record_status(a.status, MOE_ERR_UNSUPPORTED);
-  const __half h = __float2half_rn(v);
-  *reinterpret_cast<uint16_t*>(row + few_value_at(pair_pos(c))) = __half_as_ushort(h);
-  float s = start_of(__half2float(h), c);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(lane & 16 ? 0xffff0000u : 0xffffu, s, o);
-  if (!(lane & 15)) *reinterpret_cast<float*>(row + few_start_at(c)) = s;
+  if (latent) count_done(a.counters + 3, lane);
 }
 
 __device__ __noinline__ void finish(int buf, int lane) {
@@ -1166,117 +1169,118 @@ __device__ __noinline__ void finish(int buf, int lane) {
   const Lists ls = lists_of(cx);
   const Waiter wt = waiter_of(cx);
   const int halves = few_chunks(a.T, kFewRows / 2);
-  const int chunks_room = a.T * a.k;
-  int32_t* tile_done = a.counters + kFewFixed + chunks_room;
+  int32_t* tile_done = a.counters + kFewFixed + a.T * a.k;
   int32_t* out_done = tile_done + a.D / 32;
+  const int r16 = lane & 15, half = lane >> 4;
+  float* unit = sums.unit + buf * a.T * 32 + lane;  // a token's 32 columns
   bool first = true;  // segment of a down projection's unit
+#pragma unroll 1
   for (uint32_t n = 0;; ++n) {
     if (!wait_for<kRest>(&sums.full[buf], n & 1u, wt)) return;
     const Header h = sums.header[buf];
     const int kind = h.kind & 255;
     if (kind == kFewEnd) return;
-    const int r16 = lane & 15, half = lane >> 4;
-    auto release = [&] {  // the buffer is handed back as soon as it has been read
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sums.empty[buf]);
-    };
-    if (kind == kFewGateUp || kind == kFewSharedUp) {
-      for (int i = half; i < h.rows(); i += 2) {
-        float g = total(sums, buf, 0, i, r16), u = total(sums, buf, 1, i, r16);
-        const int c = h.n0 + r16;
-        if (kind == kFewGateUp) {
-          if (a.L == 0) {
-            const float unit = __ldcg(a.x_unit + nth_token(ls.tokens[h.which], i));
-            g *= unit;
-            u *= unit;
+    const bool four = is_int4(kind), pair = kind == kFewGateUp || kind == kFewSharedUp;
+    const int c = h.n0 + (pair ? r16 : lane);
+    const int token0 = h.which * few_rows_of(kind);
+    const uint32_t tokens = four ? ls.tokens[h.which] : 0u;
+    const int row0 = four ? ls.row0[h.which] : 0;
+    if (kind == kFewDown && first) {
+#pragma unroll 1
+      for (int t = 0; t < a.T; ++t) unit[t * 32] = 0.f;
+    }
+#pragma unroll 1
+    for (int i = 0; i < h.rows(); ++i) {
+      const int t = four ? nth_token(tokens, i) : token0 + i;
+      float v = 0.f;
+      const float* part = sums.at(buf, 0, half, i) + r16;
+#pragma unroll
+      for (int w = 0; w < kMul; ++w) v += part[w * 2 * sums.tokens * 16];
+      const float other = __shfl_xor_sync(0xffffffffu, v, 16);  // of lanes below 16: up
+      if (pair || kind == kFewLatDown) {
+        // h, or u
+        if (pair) {
+          float g = v, u = other;
+          if (kind == kFewGateUp && a.L == 0) {
+            const float scale = __ldcg(a.x_unit + t);
+            g *= scale;
+            u *= scale;
           }
-          const size_t r = ls.row0[h.which] + i;
-          store_f16(a, a.h16 + r * few_row_bytes(a.I), c, gated(g, u), lane);
-        } else {
-          store_parts(a.hs + (size_t)(h.which * kFewRows + i) * a.S + c, (size_t)a.T * a.S,
-                      gated(g, u));
+          v = g / (1.0f + expf(-g)) * u;
         }
+        if (kind == kFewSharedUp) {
+          // two bf16 parts: 16 bits of significand
+          if (half == 0) {
+            uint16_t* p = a.hs + (size_t)t * a.S + c;
+            const uint16_t high = f32_to_bf16_bits(v);
+            p[0] = high;
+            p[(size_t)a.T * a.S] = f32_to_bf16_bits(v - bf16_bits_to_f32(high));
+          }
+        } else {
+          // fp16 in pair order, and the start value of each 16 columns
+          const bool mine = !pair || half == 0;
+          if (mine && !(fabsf(v) <= 65504.0f)) record_status(a.status, MOE_ERR_UNSUPPORTED);
+          const __half f = __float2half_rn(v);
+          uint8_t* row = pair ? a.h16 + (row0 + i) * few_row_bytes(a.I)
+                              : a.x16 + t * few_row_bytes(a.L);
+          if (mine)
+            *reinterpret_cast<uint16_t*>(row + few_value_at(pair_pos(c))) = __half_as_ushort(f);
+          float s = start_of(__half2float(f), c);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (mine && r16 == 0) *reinterpret_cast<float*>(row + few_start_at(c)) = s;
+        }
+      } else if (kind == kFewDown) {
+        unit[t * 32] = fmaf(ls.row_weight[row0 + i], v, unit[t * 32]);
+      } else {
+        float scale = 1.0f;
+        if (kind == kFewLatUp && a.norm) {
+          float q = 0.f;
+#pragma unroll 1
+          for (int j = lane; j < a.L / 32; j += 32) q += __ldcg(a.ssq + (size_t)j * a.T + t);
+          scale = rsqrtf(warp_sum(q) / static_cast<float>(a.L) + a.eps);
+        }
+        (kind == kFewLatUp ? a.yl : a.ys)[(size_t)t * a.H + c] = v * scale;
       }
-      release();
-      count_done(kind == kFewGateUp ? a.counters + kFewFixed + h.which : a.counters + 2, lane);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sums.empty[buf]);  // the buffer has been read
+    if (pair || kind == kFewLatDown) {
+      count_done(a.counters + (kind == kFewGateUp ? kFewFixed + h.which : kind == kFewLatDown ? 1 : 2),
+                 lane);
       continue;
     }
-    const int c = h.n0 + lane;
-    if (kind == kFewLatDown) {
-      for (int i = 0; i < h.rows(); ++i) {
-        const size_t r = h.which * kFewRows + i;
-        store_f16(a, a.x16 + r * few_row_bytes(a.L), c, total(sums, buf, half, i, r16), lane);
-      }
-      release();
-      count_done(a.counters + 1, lane);
-      continue;
-    }
-    int32_t* done;
-    int n_done;
     if (kind == kFewDown) {
-      const int group = h.which / group_chunks(*ls.chunks);
-      float* unit = sums.unit + (buf * a.T) * 32 + lane;  // a token's 32 columns
-      if (first)
-        for (int t = 0; t < a.T; ++t) unit[t * 32] = 0.f;
-      for (int i = 0; i < h.rows(); ++i) {
-        const int t = nth_token(ls.tokens[h.which], i);
-        unit[t * 32] = fmaf(ls.row_weight[ls.row0[h.which] + i], total(sums, buf, half, i, r16),
-                            unit[t * 32]);
-      }
       first = (h.kind & kLastSegment) != 0;
-      if (!first) {
-        release();
-        continue;
-      }
+      if (!first) continue;
+      const int group = h.which / group_chunks(*ls.chunks);
+#pragma unroll 1
       for (uint32_t m = ls.in_group[group]; m; m &= m - 1) {
         const int t = __ffs(m) - 1;
         a.y[((size_t)group * a.T + t) * a.D + c] = unit[t * 32];
       }
-    } else if (kind == kFewSharedDown) {
-      for (int i = 0; i < h.rows(); ++i)
-        a.ys[(size_t)(h.which * (kFewRows / 2) + i) * a.H + c] = total(sums, buf, half, i, r16);
-    } else {
-      for (int i = 0; i < h.rows(); ++i) {
-        const int t = h.which * (kFewRows / 2) + i;
-        float scale = 1.0f;
-        if (a.norm) {
-          float q = 0.f;
-          for (int j = lane; j < a.L / 32; j += 32) q += __ldcg(a.ssq + (size_t)j * a.T + t);
-          scale = rsqrtf(warp_sum(q) / static_cast<float>(a.L) + a.eps);
-        }
-        a.yl[(size_t)t * a.H + c] = total(sums, buf, half, i, r16) * scale;
-      }
     }
-    release();
+    // whoever brings the last contribution to 32 columns reads them all
     const bool whole = a.L > 0 && kind != kFewDown;  // a tile of the latent layer's output
-    if (whole) {
-      done = out_done + h.n0 / 32 * halves + h.which;
-      n_done = a.S > 0 ? 2 : 1;
-    } else {
-      done = tile_done + h.n0 / 32;
-      n_done = group_count(*ls.chunks) + (a.S > 0 && a.L == 0 ? halves : 0);
+    int32_t* done = whole ? out_done + h.n0 / 32 * halves + h.which : tile_done + h.n0 / 32;
+    const int all = whole ? (a.S > 0 ? 2 : 1)
+                          : group_count(*ls.chunks) + (a.S > 0 && a.L == 0 ? halves : 0);
+    __syncwarp();
+    int old = 0;
+    if (lane == 0) old = add_acq_rel(done, 1);
+    old = __shfl_sync(0xffffffffu, old, 0);
+    if (old != all - 1) continue;
+    __threadfence();
+    if (!whole) {
+      combine(c, lane);
+      continue;
     }
-    if (!count_last(done, n_done, lane)) continue;
-    if (whole) {
-      for (int i = 0; i < h.rows(); ++i) {
-        const size_t at = (size_t)(h.which * (kFewRows / 2) + i) * a.H + c;
-        float v = __ldcg(a.yl + at);
-        if (a.S > 0) v += __ldcg(a.ys + at);
-        a.out[at] = f32_to_bf16_bits(v);
-      }
-    } else if (a.L == 0) {
-      combine(a, ls, h.n0, lane, [&](int t, float v) {
-        if (a.S > 0) v += __ldcg(a.ys + (size_t)t * a.H + c);
-        a.out[(size_t)t * a.H + c] = f32_to_bf16_bits(v);
-      });
-    } else {
-      const float gain = a.lat_norm && a.norm ? bf16_bits_to_f32(__ldg(a.lat_norm + c)) : 1.0f;
-      combine(a, ls, h.n0, lane, [&](int t, float v) {
-        store_parts(a.z + (size_t)t * a.L + c, (size_t)a.T * a.L, v * gain);
-        const float q = warp_sum(v * v);
-        if (lane == 0) a.ssq[(size_t)(h.n0 / 32) * a.T + t] = q;
-      });
-      count_done(a.counters + 3, lane);
+#pragma unroll 1
+    for (int i = 0; i < h.rows(); ++i) {
+      const size_t at = (size_t)(token0 + i) * a.H + c;
+      float v = __ldcg(a.yl + at);
+      if (a.S > 0) v += __ldcg(a.ys + at);
+      a.out[at] = f32_to_bf16_bits(v);
     }
   }
 }
@@ -1304,6 +1308,17 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   if (threadIdx.x == 0) {
     const Layout lay(args);
     cx.a = args;
+    // units in ticket order, as tiles of chunks of tokens, or chunks of experts by tiles
+    const int whole = few_chunks(args.T, kFewRows), half = few_chunks(args.T, kFewRows / 2);
+    cx.each[kFewLatDown] = cx.each[kFewSharedUp] = whole;
+    cx.each[kFewSharedDown] = cx.each[kFewLatUp] = half;
+    cx.each[kFewGateUp] = args.I / 16;
+    cx.each[kFewDown] = args.D / 32;
+    cx.units[kFewLatDown] = args.L / 32 * whole;
+    cx.units[kFewSharedUp] = args.S / 16 * whole;
+    cx.units[kFewGateUp] = cx.units[kFewDown] = 0;  // when the lists are made
+    cx.units[kFewSharedDown] = args.S > 0 ? args.H / 32 * half : 0;
+    cx.units[kFewLatUp] = args.L > 0 ? args.H / 32 * half : 0;
     cx.slot = lay.slot;
     cx.sums_at = sizeof(Context);
     cx.unit_at = cx.sums_at + lay.sums;

@@ -30,6 +30,10 @@ enum FewKind {
   kFewEnd = 7
 };
 
+// Scales in 4-byte copies; by TMA (K a multiple of 256); or, of rows of at most a slot's
+// columns, 16 whole rows in one bulk copy.
+constexpr int kScalesWords = 0, kScalesTma = 1, kScalesDense = 2;
+
 // Arguments of both kernels; pointers not used by a call are NULL.
 struct FewArgs {
   // inputs
@@ -45,11 +49,12 @@ struct FewArgs {
   int T, H, E, k, I, L, D, S;
   int renorm, norm;
   float eps;
-  int tma_scale[2];  // scales of gate/up and of down by TMA (K % 256 == 0) or in 4-byte copies
+  int tma_scale[2];  // how the scales of gate/up and of down are copied, kScales*
   // workspace
   int32_t* counters;
   int n_counters;
-  float* logits;     // fp32 [T, E]
+  float* scores;     // fp32 [T, E] sigmoid of the logits
+  uint32_t* keys;    // [T, E] order of score + bias
   uint8_t* x16;      // [T] rows of fp16 blocks (below): x times a power of two, or u
   float* x_unit;     // fp32 [T]: what one unit of x16 stands for
   uint8_t* h16;      // [T k] rows of fp16 blocks

@@ -23,7 +23,8 @@ size_t carve(FewArgs* a, void* base) {
   const size_t tc = few_chunks(a->T, kFewRows / 2);
   a->n_counters = static_cast<int>(kFewFixed + P + D / 32 + (L ? H / 32 * tc : 0));
   a->counters = static_cast<int32_t*>(take(4 * static_cast<size_t>(a->n_counters)));
-  a->logits = static_cast<float*>(take(a->router_w ? 4 * T * a->E : 0));
+  a->scores = static_cast<float*>(take(a->router_w ? 4 * T * a->E : 0));
+  a->keys = static_cast<uint32_t*>(take(a->router_w ? 4 * T * a->E : 0));
   a->x16 = static_cast<uint8_t*>(take(T * few_row_bytes(a->D)));
   a->x_unit = static_cast<float*>(take(4 * T));
   a->h16 = static_cast<uint8_t*>(take(P * few_row_bytes(a->I)));
@@ -135,17 +136,21 @@ int run(FewArgs a, const Experts& w, const moe_weights* layer, const Block* in, 
   a.wait_ns = wait_ns;
   a.stall_at = stall_at;
   for (int i = 0; i < 3; ++i) a.scale[i] = w.scale[i];
-  a.tma_scale[0] = a.D % 256 == 0 && aligned(w.scale[0], 16) && aligned(w.scale[1], 16);
-  a.tma_scale[1] = a.I % 256 == 0 && aligned(w.scale[2], 16);
+  // every expert's rows begin on 16 bytes where the first one's do: 16 rows of K / 16 bytes
+  auto way = [](int K, bool on16) {
+    return !on16 ? kScalesWords : K % 256 == 0 ? kScalesTma : K <= kFewColumns ? kScalesDense : kScalesWords;
+  };
+  a.tma_scale[0] = way(a.D, aligned(w.scale[0], 16) && aligned(w.scale[1], 16));
+  a.tma_scale[1] = way(a.I, aligned(w.scale[2], 16));
   FewMaps m{};
   const uint64_t D = a.D, E = a.E, H = a.H, I = a.I, L = a.L, S = a.S;
   const struct {
     const void* w;
     const uint16_t* scale;
     uint64_t K, rows, n;
-  } mats[kFewMatrices] = {{w.packed[0], a.tma_scale[0] ? w.scale[0] : nullptr, D, I, E},
-                          {w.packed[1], a.tma_scale[0] ? w.scale[1] : nullptr, D, I, E},
-                          {w.packed[2], a.tma_scale[1] ? w.scale[2] : nullptr, I, D, E},
+  } mats[kFewMatrices] = {{w.packed[0], a.tma_scale[0] == kScalesTma ? w.scale[0] : nullptr, D, I, E},
+                          {w.packed[1], a.tma_scale[0] == kScalesTma ? w.scale[1] : nullptr, D, I, E},
+                          {w.packed[2], a.tma_scale[1] == kScalesTma ? w.scale[2] : nullptr, I, D, E},
                           {L ? layer->lat_down : nullptr, nullptr, H, L, 1},
                           {L ? layer->lat_up : nullptr, nullptr, L, H, 1},
                           {S ? layer->shared_gate : nullptr, nullptr, H, S, 1},
