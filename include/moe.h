@@ -594,12 +594,25 @@ void moe_layer_pipe_destroy(moe_layer_pipe* pipe);
 
 /* ------------------------------------------------------------ few tokens -- */
 
+/* One PackedInt4Linear on at most 16 rows (no expert segments, no workspace):
+ *   y[t] = bf16( x[t] W^T ),  W[n, c] = q[n, c] * scale[n, c / 32]
+ *   x         bf16, row t at x + t * x_ld elements (x_ld >= K, a multiple of 8): any
+ *             bf16 values, a row is scaled by a power of two on its way in and out
+ *   w_packed  int32 [N, K/8];  w_scale bf16 [N, K/32]: any N
+ *   y         bf16 [T, N]
+ * fp32 accumulation, one rounding; equal calls give equal bits.  Weights are read
+ * once.  T <= 16 and K % 32 == 0, else MOE_ERR_UNSUPPORTED (moe_int4_linear takes
+ * more rows).  x and w_packed 16-byte aligned, w_scale 4; y shares no byte with an
+ * input, else MOE_ERR_INVALID. */
+int moe_int4_matvec(const uint16_t* x, int64_t x_ld, const int32_t* w_packed,
+                    const uint16_t* w_scale, int T, int N, int K, uint16_t* y, void* stream);
+
 /* The routed experts of a few tokens (T <= 32; one token of one request, drafted
  * tokens, a small decode batch) in two launches instead of dispatch, experts and
  * combine (no page has this call; the arithmetic is moe_expert_ffn's and
  * moe_combine's):
  *   out[t] = bf16( sum_j topk_w[t, j] down_e( SiLU(gate_e x[t]) * up_e x[t] ) ),
- *   e = topk_idx[t, j], j ascending, in fp32 with one rounding at the end (the
+ *   e = topk_idx[t, j], summed in the order of the experts, in fp32 with one rounding at the end (the
  *   intermediate h is kept in fp16: a value beyond its range records
  *   MOE_ERR_UNSUPPORTED).  x may have any bf16 value: a token is scaled by a
  *   power of two on its way in and out.
@@ -608,7 +621,7 @@ void moe_layer_pipe_destroy(moe_layer_pipe* pipe);
  *             [0, E) adds nothing and records MOE_ERR_INVALID
  *   topk_w    fp32 [T, k]
  *   weights   as moe_expert_ffn, act_bits 16
- * Each chosen expert's weights are read once for every 8 tokens that chose it.
+ * Each chosen expert's weights are read once for every 2 tokens that chose it.
  * Equal calls give equal bits.  D % 64 == 0, I % 64 == 0, E <= 2048, k <= min(E, 32), else
  * MOE_ERR_UNSUPPORTED.  x, out and packed weights 16-byte aligned, ws 256; out and ws
  * share no byte with each other or with an input, else MOE_ERR_INVALID. */

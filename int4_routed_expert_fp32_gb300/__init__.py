@@ -10,7 +10,7 @@ import importlib
 _BINDING = ("MoeConfig", "MoeError", "MoeLayer", "MoeWeights", "adapter_linear",
             "adapter_linear_stall_selftest", "block_norm", "check_error", "combine",
             "dispatch", "dispatch_noalloc", "expert_ffn", "experts_few",
-            "experts_few_stall_selftest", "layer_few", "int4_linear", "int4_linear_partials",
+            "experts_few_stall_selftest", "int4_matvec", "layer_few", "int4_linear", "int4_linear_partials",
             "int4_linear_stall_selftest", "int4_linear_int16", "quantize_rows_int16",
             "last_cuda_error", "launch_count",
             "lib", "linear_bf16", "quantize_int4", "quantize_int8",

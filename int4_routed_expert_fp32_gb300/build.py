@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, "libmoe.so")
 SOURCES = ["common.cu", "router.cu", "dispatch.cu", "ffn_stream.cu", "ffn_tc.cu", "ffn_tc2.cu", "ffn_tc_q8.cu", "combine.cu",
            "gemm_bf16.cu", "layer.cu", "weights.cu", "shared.cu", "linear_i16.cu", "route_select.cu",
            "block_norm.cu", "adapter.cu", "adapter_shrink.cu",
-           "adapter_tile.cu", "few.cu", "few_api.cu"]
+           "adapter_tile.cu", "few.cu", "few_api.cu",
+           "int4_matvec.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE]

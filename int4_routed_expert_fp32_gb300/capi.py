@@ -152,6 +152,8 @@ SIGNATURES = {
                                                   c_void_p, c_int, c_int, c_int, c_int, c_int,
                                                   c_int, c_int, c_int64, c_void_p, c_void_p,
                                                   c_size_t, c_void_p]),
+    "moe_int4_matvec": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p,
+                                c_void_p]),
     "moe_experts_few_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "moe_experts_few": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
@@ -814,6 +816,29 @@ def adapter_linear_stall_selftest(x: torch.Tensor, w: torch.Tensor, lora_a: torc
     _check("moe_adapter_linear_stall_selftest", lib.moe_adapter_linear_stall_selftest(
         _p(x), _p(w), _p(lora_a), _p(lora_b), _p(ids), None, T, K, N, R, n, kernel, stall_stage,
         limit_ns, _p(out), _p(ws), ws.numel(), _stream()))
+
+
+def int4_matvec(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y bf16 [T, N] = x W^T for at most 16 rows x bf16 [T, K] (rows may lie apart, by a
+    multiple of 8 elements) and packed weights int32 [N, K/8] with scales bf16
+    [N, K/32], as ``quantize_int4`` makes them (moe_int4_matvec).  out must not share
+    memory with an input."""
+    bf16 = torch.bfloat16
+    T, K = _rows("x", x, x.shape if x.dim() == 2 else (None, None), bf16).shape
+    N = _arg("w_packed", w_packed, (w_packed.shape[0] if w_packed.dim() == 2 else None, K // 8),
+             torch.int32).shape[0]
+    _arg("w_scale", w_scale, (N, K // 32), bf16)
+    if out is not None:
+        _arg("out", out, (T, N), bf16)
+    dev = _device_of((x, w_packed, w_scale, out), ("x", "w_packed", "w_scale", "out"))
+    if out is None:
+        out = torch.empty((T, N), dtype=bf16, device=dev)
+    rc = lib.moe_int4_matvec(x.data_ptr(), _ld(x), w_packed.data_ptr(), w_scale.data_ptr(), T, N, K,
+                             out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check("moe_int4_matvec", rc)
+    return out
 
 
 def _few_args(topk_idx, topk_w, x, experts, out):
