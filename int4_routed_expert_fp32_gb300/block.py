@@ -10,6 +10,9 @@ adapters of many requests beside the latent projections:
     y     += shared_expert(h)                          (with shared_* weights)
     x, h   = block_norm(y, x, ...)                     norm, gate, residual, next norm
 
+With ``few_tokens`` a call of at most 32 tokens runs dispatch, experts and combine as
+one operator, ``experts_few``.
+
 The latent path is the one of the "Kimi K3 latent up-projection" page
 (KimiSparseMoeBlock.forward: router on the full width, down-projection, experts,
 norm, up-projection); groups, adapters, the norm after the block and its gate
@@ -42,6 +45,8 @@ class MoeBlock:
     adapters  {"lat_down": (A, B, scale), "lat_up": ...}: either, or none
     post_gain, next_gain, gate (a gain per channel, [H]), gate_sigmoid,
     residual_scale, eps: options of ``block_norm``
+    few_tokens  calls of at most 32 tokens through ``experts_few`` (the expert outputs
+              are then summed unrounded, so the bits differ from the other path's)
     """
 
     def __init__(self, weights: Dict[str, torch.Tensor], k: int, *, score: str = "sigmoid",
@@ -50,7 +55,8 @@ class MoeBlock:
                  adapters: Optional[Dict[str, Adapters]] = None,
                  post_gain: Optional[torch.Tensor] = None,
                  next_gain: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
-                 gate_sigmoid: bool = False, residual_scale: float = 1.0, eps: float = 1e-6):
+                 gate_sigmoid: bool = False, residual_scale: float = 1.0, eps: float = 1e-6,
+                 few_tokens: bool = False):
         extra = set(weights) - {n for n, _ in capi.MoeWeights._fields_}
         if extra:
             raise ValueError(f"unknown weight names: {sorted(extra)}")
@@ -79,6 +85,7 @@ class MoeBlock:
         self.norm = dict(post_gain=post_gain, pre_gain=next_gain, gate=gate,
                          gate_sigmoid=gate_sigmoid, scale=residual_scale, eps=eps)
         self.eps = eps
+        self.few_tokens = few_tokens
         # the router weight's bf16 terms, for calls of 512 tokens or more
         self.w_terms = weights.get("router_w_terms")
         if self.w_terms is None:
@@ -103,10 +110,13 @@ class MoeBlock:
         None: no adapters).  x_out may be x (in place)."""
         idx, w = self.route(h)
         u = self._project("lat_down", h, ids) if self.latent else h
-        d = capi.dispatch(idx, u, self.E, pairs=True)
-        y = capi.expert_ffn(d["x_sorted"], None, d["offsets"], self.experts, pairs=True,
-                            max_rows_per_expert=h.shape[0])
-        y = capi.combine(y, d["inv_row"], w)
+        if self.few_tokens and h.shape[0] <= capi.FEW_TOKENS:
+            y = capi.experts_few(idx, w, u, self.experts)
+        else:
+            d = capi.dispatch(idx, u, self.E, pairs=True)
+            y = capi.expert_ffn(d["x_sorted"], None, d["offsets"], self.experts, pairs=True,
+                                max_rows_per_expert=h.shape[0])
+            y = capi.combine(y, d["inv_row"], w)
         if self.latent:
             if "lat_norm" in self.weights:
                 y = capi.rmsnorm(y, self.weights["lat_norm"], self.eps)

@@ -841,6 +841,9 @@ def int4_matvec(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
     return out
 
 
+FEW_TOKENS = 32  # most tokens of experts_few and layer_few
+
+
 def _few_args(topk_idx, topk_w, x, experts, out):
     """(T, D, E, k, I, device) of ``experts_few``'s tensors, checked."""
     bf16 = torch.bfloat16
@@ -985,6 +988,17 @@ class MoeLayer:
             ctypes.byref(self.cfg), ctypes.byref(self.wstruct), _p(x), _p(out), _p(self.ws),
             self.ws.numel(), _stream()))
         return out
+
+    def forward_few(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """forward of any number of tokens up to 32 (whatever T the layer was made for)
+        in two launches: ``layer_few``.  act_bits 16 only."""
+        if self.cfg.act_bits != 16:
+            raise ValueError("forward_few needs act_bits 16")
+        c = self.cfg
+        drop = set() if c.L else {"lat_down", "lat_up", "lat_norm"}
+        drop |= set() if c.I_shared else {"shared_gate", "shared_up", "shared_down"}
+        return layer_few(x, {n: t for n, t in self.weights.items() if n not in drop}, c.k,
+                         renorm=bool(c.renorm), eps=c.eps, out=out)
 
     def forward_host(self, x_host: torch.Tensor, out_host: torch.Tensor) -> None:
         """x_host / out_host: CPU bf16 [T, H] (pinned for asynchronous copies)."""
