@@ -1,21 +1,23 @@
 // y = x W^T for packed int4 weights with a bf16 scale per 32 columns and at most 16 rows x.
 //
-// The weights are read once and bound the time from some MB on; below that it is
-// latency: launch, one trip to HBM, one reduction.  So a CTA takes 16-row blocks of W,
-// its eight warps split K (or, where K is short, the rows), and each warp copies its own
-// weights three steps ahead (cp.async, 8 KB of them on their way), on from one
-// block into the next.  What a warp copies it reads itself, so no warp waits for
-// another before the sums are joined.
+// The weights are read once and bound the time from some tens of MB on; below that it is
+// latency: launch, one trip to HBM, one reduction.  A cluster of CTAs takes blocks of
+// 32 rows of W and splits K; of a CTA's eight warps some split its columns, the others
+// have other blocks.  A warp copies its own weights two or three steps of 2 KB ahead
+// (cp.async), on from one block into the next.  What a warp copies it reads
+// itself, so no warp waits for another before the sums are joined: over the warps in
+// shared memory, over the cluster in that of its CTAs, both in a fixed order.
 //
-// The tokens are turned into fp16 in shared memory first, each scaled by a power of two
-// (exact), in the order in which a packed word pairs its nibbles; the weights'
-// first copies are under way meanwhile.  Where all of K does not fit, the CTA goes
-// through K in slices and keeps its sums in shared memory.
+// A CTA turns its columns of the tokens into fp16 in shared memory first, in the order in
+// which a packed word pairs its nibbles, each token's 128 columns scaled by a power of
+// two of their own (exact, undone in fp32); the weights' first copies are under way
+// meanwhile.  Where they do not fit, it goes through them in slices.
 //
 // Products: m16n8k16 MMAs on the nibbles as fp16, 1032 + q and 72 + q, exactly; the
 // accumulator starts from minus the constants' part (one value for a token and group),
 // and each group's sum is scaled and added in fp32.  One ldmatrix gives a lane the
-// words of two groups.
+// words of two groups; the two row tiles of a block share the tokens' fragments, whose
+// reads of shared memory cost more than the weights' own for 16 tokens.
 #include <cuda_fp16.h>
 
 #include "adapter.cuh"
@@ -27,12 +29,20 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kDepth = 3;              // steps of 128 columns a warp copies ahead
-constexpr int kStepWords = 16 * 64;    // 16 rows of 4 groups
-constexpr int kScalePitch = 12;        // 4 scales of a row, 4-byte pieces that hold them
-constexpr int kStepBytes = kStepWords + 16 * kScalePitch + 64;  // a multiple of 128
+constexpr int kTiles = 2;                        // row tiles of a block
+constexpr int kRows = 16 * kTiles;
+constexpr int kStepWords = kRows * 64;           // bytes of packed weights
+constexpr int kScalePitch = 12;                  // 4 scales of a row in 4-byte pieces
+constexpr int kStepBytes = kStepWords + kRows * kScalePitch;
 constexpr int kMaxTokens = 16;
-constexpr int kRoomForTokens = 60 * 1024;  // shared memory of a slice of x: two CTAs fit an SM
+constexpr int kMostBlocks = 16;                  // of a cluster: their sums are in shared memory
+constexpr int kMostCluster = 8;
+constexpr int kSumPitch = kRows + 4;             // lanes' tokens and rows in different banks
+constexpr int kPerSm = 113 * 1024;               // shared memory with which two CTAs fit an SM
+constexpr int kLoads = 4;                        // 16-byte loads of x under way in a thread
+
+// Steps of 128 columns that a warp copies ahead.  16 tokens need the room for themselves.
+__host__ __device__ constexpr int depth(int T) { return T <= 8 ? 3 : 2; }
 
 struct MatvecArgs {
   const uint16_t* x;
@@ -41,23 +51,31 @@ struct MatvecArgs {
   uint16_t* y;
   int64_t x_ld;
   int T, N, K;
-  int slice;   // columns of a slice, a multiple of 128
-  int split;   // warps that share a slice's columns
-  int blocks;  // 16-row blocks of a CTA
+  int slice;     // columns of a slice, a multiple of 128
+  int slices;    // of K: CTA r of a cluster has slices r, r + ranks, ...
+  int ranks;     // CTAs of a cluster
+  int split;     // warps that share a slice's columns
+  int blocks;    // blocks of a cluster
+  bool scales8;  // the scales of every 128 columns begin on 8 bytes
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                        float c2, float c3) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10,%11,%12,%13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "l"(policy)
                : "memory");
+}
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // Nibbles of a word as fp16 pairs (columns 0 4, 1 5, 2 6, 3 7): 1032 + q in the even
@@ -74,7 +92,7 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t lo, uint32_t hi, ui
 
 // Where one warp's work on a block and slice lies.
 struct Item {
-  int row0;   // first row of the block (N or more: none)
+  int row0;   // first row of the block
   int step0;  // first step of 128 columns, in the slice
   int steps;
   int col0;   // first column of the slice
@@ -84,30 +102,31 @@ struct Item {
 __host__ __device__ __forceinline__ int row_pitch(int slice) { return slice * 2 + 64; }
 
 struct Layout {
-  int start, steps, red, sums, total;
+  int start, unit, steps, red, sums, total;
   __host__ __device__ __forceinline__ explicit Layout(const MatvecArgs& a) {
     const int padded = (a.T + 7) / 8 * 8;
-    start = a.T * row_pitch(a.slice);                 // [slice / 32][padded] start values
-    steps = start + a.slice / kGroup * padded * 4;    // the warps' steps
-    red = steps + kWarps * kDepth * kStepBytes;       // [2][warp][16][padded]
-    sums = red + 2 * kWarps * 16 * padded * 4;        // [blocks][16][padded]
-    total = sums + (a.slice < a.K ? a.blocks * 16 * padded * 4 : 0);
+    start = a.T * row_pitch(a.slice);  // [slice / 32][padded / 2]: values of two tokens, twice
+    unit = start + a.slice / kGroup * padded * 8;  // [slice / 128][padded]: undoes their scaling
+    steps = unit + a.slice / 128 * padded * 4;     // the warps' steps
+    red = steps + kWarps * depth(a.T) * kStepBytes;  // [warp][T][kSumPitch]
+    sums = red + (a.split > 1 ? kWarps * a.T * kSumPitch * 4 : 0);  // [blocks][T][kSumPitch]
+    total = sums + a.blocks * a.T * kSumPitch * 4;
   }
 };
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t top[kMaxTokens];  // largest magnitude of a token in the slice
   const Layout lay(a);
-  constexpr int kPad = NB * 8;
+  constexpr int kPad = NB * 8, kDepth = depth(kPad);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int ks = warp & (a.split - 1), rb = warp / a.split, abreast = kWarps / a.split;
   const int groups = a.K / kGroup;
-  const int block0 = blockIdx.x * a.blocks;
-  const int blocks = min(a.blocks, (a.N + 15) / 16 - block0);
-  const int slices = (a.K + a.slice - 1) / a.slice;
-  const int turns = (blocks + abreast - 1) / abreast;  // of a slice
+  const int rank = a.ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int block0 = blockIdx.x / a.ranks * a.blocks;
+  const int blocks = min(a.blocks, (a.N + kRows - 1) / kRows - block0);
+  const int slices = (a.slices - rank + a.ranks - 1) / a.ranks;  // this CTA's
+  const int turns = (blocks + abreast - 1) / abreast;            // of a slice
   const uint64_t once = [] {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -120,12 +139,12 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
   auto item_of = [&](int turn) {  // turns count on over the slices
     Item it;
     const int sl = turn / turns, b = (turn - sl * turns) * abreast + rb;
-    it.col0 = sl * a.slice;
+    it.col0 = (rank + sl * a.ranks) * a.slice;
     const int steps = (min(a.slice, a.K - it.col0) + 127) / 128;
     const int each = (steps + a.split - 1) / a.split;
     it.step0 = ks * each;
     it.steps = sl < slices && b < blocks ? max(0, min(each, steps - it.step0)) : 0;
-    it.row0 = (block0 + b) * 16;
+    it.row0 = (block0 + b) * kRows;
     return it;
   };
   uint8_t* mine = smem + lay.steps + warp * kDepth * kStepBytes;
@@ -135,24 +154,29 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
     const int col = it.col0 + (it.step0 + j) * 128;
     const int first = col / kGroup;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * kTiles; ++h) {
       const int r = g + 8 * h, row = min(it.row0 + r, a.N - 1);
       if (first + t < groups)
         copy16(to + r * 64 + ((t ^ (r >> 1 & 3)) << 4),
                a.w + (int64_t)row * (a.K / 2) + col / 2 + t * 16, once);
     }
+    if (a.scales8) {
+      const int row = min(it.row0 + lane, a.N - 1);
+      copy8(to + kStepWords + lane * 8, a.scale + ((int64_t)row * groups + first) * 2);
+      return;
+    }
     // 8 bytes of scales of a row, which begin on 4 bytes or 2 behind them
+    const int row = min(it.row0 + lane, a.N - 1);
+    const int64_t at = ((int64_t)row * groups + first) * 2, word = at & ~3LL;
+    const int64_t end = min(at + 8, ((int64_t)row + 1) * groups * 2);  // of the row's scales
+    uint8_t* dst = mine + slot * kStepBytes + kStepWords + lane * kScalePitch;
 #pragma unroll 1
-    for (int p = lane; p < 48; p += 32) {
-      const int r = p & 15, piece = p >> 4, row = min(it.row0 + r, a.N - 1);
-      const int64_t at = ((int64_t)row * groups + first) * 2, word = (at & ~3LL) + 4 * piece;
-      const int64_t end = min(at + 8, ((int64_t)row + 1) * groups * 2);  // of the row's scales
-      uint8_t* dst = mine + slot * kStepBytes + kStepWords + r * kScalePitch + 4 * piece;
-      if (word >= end) continue;
-      if (word + 4 <= (int64_t)a.N * groups * 2)
-        cp_async_4(dst, a.scale + word);
+    for (int p = 0; p < 3 && word + 4 * p < end; ++p) {
+      if (word + 4 * p + 4 <= (int64_t)a.N * groups * 2)
+        cp_async_4(dst + 4 * p, a.scale + word + 4 * p);
       else  // the last scale of an odd number
-        *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(a.scale + word);
+        *reinterpret_cast<uint16_t*>(dst + 4 * p) =
+            *reinterpret_cast<const uint16_t*>(a.scale + word + 4 * p);
     }
   };
 
@@ -168,70 +192,77 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
   }
 
   float* start = reinterpret_cast<float*>(smem + lay.start);
+  float* unit = reinterpret_cast<float*>(smem + lay.unit);
+  float* red = reinterpret_cast<float*>(smem + lay.red);
+  float* sums = reinterpret_cast<float*>(smem + lay.sums);
   const int pitch = row_pitch(a.slice);
 #pragma unroll 1
   for (int turn = 0; turn < turns * slices; ++turn) {
     if (turn % turns == 0) {
-      // x of this slice as fp16 in pair order
+      // x of this slice as fp16 in pair order; 16 lanes have the 128 columns of a scale
       const int cols = min(a.slice, a.K - cur.col0);
-      __syncthreads();
-      if (tid < kMaxTokens) top[tid] = 0u;
-      __syncthreads();
-      const int pieces = cols / 8;
+      const int pieces = (cols + 127) / 128 * 16, all = a.T * pieces;
+      if (turn > 0) __syncthreads();  // the slice before has been read
 #pragma unroll 1
-      for (int k = 0; k < a.T; ++k) {
-        uint32_t m = 0u;
-#pragma unroll 1
-        for (int c = tid; c < pieces; c += kThreads) {
-          const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.x + k * a.x_ld + cur.col0 + 8 * c));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int base = tid; base - lane < all; base += kLoads * kThreads) {
+        uint4 v[kLoads];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            m = max(m, w[i] << 16 & 0x7fff0000u);
-            m = max(m, w[i] & 0x7fff0000u);
-          }
+        for (int l = 0; l < kLoads; ++l) {
+          const int i = base + l * kThreads, k = i / pieces, c = i - k * pieces;
+          v[l] = make_uint4(0u, 0u, 0u, 0u);
+          if (i < all && 8 * c < cols)
+            v[l] = __ldcg(reinterpret_cast<const uint4*>(a.x + k * a.x_ld + cur.col0 + 8 * c));
         }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0 && m) atomicMax(&top[k], m);
-      }
-      __syncthreads();
-#pragma unroll 1
-      for (int k = 0; k < a.T; ++k) {
-        // a power of two that brings the largest value to [2^14, 2^15), at most 2^126; 1 where
-        // it is 0 or not finite
-        const int field = static_cast<int>(top[k] >> 23);
-        const int up = top[k] == 0u || field == 255 ? 127 : min(127 + 14 + 127 - field, 253);
-        const float by = __uint_as_float(static_cast<uint32_t>(up) << 23);
-#pragma unroll 1
-        for (int c = tid; c < (pieces + 31) / 32 * 32; c += kThreads) {  // whole warps
-          float s = 0.f;
-          if (c < pieces) {
-            const uint4 v =
-                __ldcg(reinterpret_cast<const uint4*>(a.x + k * a.x_ld + cur.col0 + 8 * c));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            __half2 p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // columns i and i + 4
-              const uint32_t lo = (w[i >> 1] >> (16 * (i & 1))) << 16;
-              const uint32_t hi = (w[2 + (i >> 1)] >> (16 * (i & 1))) << 16;
-              p[i] = __floats2half2_rn(__uint_as_float(lo) * by, __uint_as_float(hi) * by);
-              s = fmaf(i & 1 ? -72.f : -1032.f, __low2float(p[i]) + __high2float(p[i]), s);
-            }
-            *reinterpret_cast<uint4*>(smem + k * pitch + 16 * c) = *reinterpret_cast<const uint4*>(p);
+        for (int l = 0; l < kLoads; ++l) {
+          const int i = base + l * kThreads, k = i / pieces, c = i - k * pieces;
+          const uint32_t w[4] = {v[l].x, v[l].y, v[l].z, v[l].w};
+          uint32_t m = 0u;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            m = max(m, w[j] << 16 & 0x7fff0000u);
+            m = max(m, w[j] & 0x7fff0000u);
+          }
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+          // a power of two that brings the largest value to [2^14, 2^15), at most 2^126; 1
+          // where it is 0 or not finite
+          const int field = static_cast<int>(m >> 23);
+          const int up = m == 0u || field == 255 ? 127 : min(127 + 14 + 127 - field, 253);
+          const float by = __uint_as_float(static_cast<uint32_t>(up) << 23);
+          __half2 p[4];
+          float s = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // columns j and j + 4
+            const uint32_t lo = (w[j >> 1] >> (16 * (j & 1))) << 16;
+            const uint32_t hi = (w[2 + (j >> 1)] >> (16 * (j & 1))) << 16;
+            p[j] = __floats2half2_rn(__uint_as_float(lo) * by, __uint_as_float(hi) * by);
+            s = fmaf(j & 1 ? -72.f : -1032.f, __low2float(p[j]) + __high2float(p[j]), s);
           }
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           s += __shfl_xor_sync(0xffffffffu, s, 2);
-          if (c < pieces && !(c & 3)) start[c / 4 * kPad + k] = s;
+          if (i < all) {
+            *reinterpret_cast<uint4*>(smem + k * pitch + 16 * c) = *reinterpret_cast<const uint4*>(p);
+            if (!(c & 3)) {
+              float* to = start + ((c >> 2) * (kPad / 2) + (k >> 1)) * 4 + (k & 1);
+              to[0] = s;
+              to[2] = s;
+            }
+            if (!(c & 15))
+              unit[(c >> 4) * kPad + k] = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+          }
         }
       }
       __syncthreads();
     }
     const Item next = item_of(turn + 1);
-    float acc[NB][4];
+    float acc[kTiles][NB][4];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+    for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
     const int steps = max(kDepth, cur.steps);
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
@@ -240,49 +271,89 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
       if (j < cur.steps) {
         const uint8_t* st = mine + slot * kStepBytes;
         const int step = cur.step0 + j, first = cur.col0 / kGroup + 4 * step;
-        // the lane's row of an ldmatrix tile, and scales of rows g and g + 8
-        const int r = (lane & 8) + (lane & 7);
-        const int64_t at0 = (int64_t)min(cur.row0 + g, a.N - 1) * groups + first;
-        const int64_t at8 = (int64_t)min(cur.row0 + g + 8, a.N - 1) * groups + first;
-        const uint8_t* s0 = st + kStepWords + g * kScalePitch + (at0 & 1) * 2;
-        const uint8_t* s8 = st + kStepWords + (g + 8) * kScalePitch + (at8 & 1) * 2;
+        // two words with the four scales of each of the lane's rows
+        uint32_t sc[2 * kTiles][2];
+#pragma unroll
+        for (int h = 0; h < 2 * kTiles; ++h) {
+          if (a.scales8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(st + kStepWords + (g + 8 * h) * 8);
+            sc[h][0] = v.x;
+            sc[h][1] = v.y;
+          } else {
+            const uint32_t* v =
+                reinterpret_cast<const uint32_t*>(st + kStepWords + (g + 8 * h) * kScalePitch);
+            const uint32_t row = min(cur.row0 + g + 8 * h, a.N - 1);
+            const uint32_t by = ((row & groups) + first & 1) * 16;
+            sc[h][0] = __funnelshift_r(v[0], v[1], by);
+            sc[h][1] = __funnelshift_r(v[1], v[2], by);
+          }
+        }
+        float part[kTiles][NB][4];
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[m][n][i] = 0.f;
 #pragma unroll
         for (int pair = 0; pair < 2; ++pair) {
           if (first + 2 * pair >= groups) break;
-          uint32_t wr[4];
-          const uint32_t from = smem_u32(st) + r * 64 + (((2 * pair + (lane >> 4)) ^ (r >> 1 & 3)) << 4);
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(wr[0]), "=r"(wr[1]), "=r"(wr[2]), "=r"(wr[3])
-                       : "r"(from)
-                       : "memory");
+          uint32_t wr[kTiles][4];
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) {
+            const int r = 16 * m + (lane & 15);
+            const uint32_t from =
+                smem_u32(st) + r * 64 + (((2 * pair + (lane >> 4)) ^ (r >> 1 & 3)) << 4);
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(wr[m][0]), "=r"(wr[m][1]), "=r"(wr[m][2]), "=r"(wr[m][3])
+                         : "r"(from)
+                         : "memory");
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int gr = 2 * pair + h;
             if (first + gr >= groups) break;
-            uint32_t lo[4], hi[4];
-            nibbles(wr[2 * h], magic_lo, magic_hi, lo);
-            nibbles(wr[2 * h + 1], magic_lo, magic_hi, hi);
-            const float f0 =
-                __uint_as_float(*reinterpret_cast<const uint16_t*>(s0 + 2 * gr) << 16);
-            const float f8 =
-                __uint_as_float(*reinterpret_cast<const uint16_t*>(s8 + 2 * gr) << 16);
+            // rows of tokens that are not there repeat the last one: no column of the
+            // product reaches another
+            uint4 v[NB];
+            float4 c[NB];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-              // rows of tokens that are not there repeat the last one: no column of the
-              // product reaches another
-              const uint4 v = *reinterpret_cast<const uint4*>(
-                  smem + min(8 * n + g, a.T - 1) * pitch + (4 * step + gr) * 64 + t * 16);
-              const float2 c =
-                  *reinterpret_cast<const float2*>(start + (4 * step + gr) * kPad + 8 * n + 2 * t);
-              float d[4] = {c.x, c.y, c.x, c.y};
-              mma_f16(d, lo[0], hi[0], lo[1], hi[1], v.x, v.y);
-              mma_f16(d, lo[2], hi[2], lo[3], hi[3], v.z, v.w);
-              acc[n][0] = fmaf(f0, d[0], acc[n][0]);
-              acc[n][1] = fmaf(f0, d[1], acc[n][1]);
-              acc[n][2] = fmaf(f8, d[2], acc[n][2]);
-              acc[n][3] = fmaf(f8, d[3], acc[n][3]);
+              v[n] = *reinterpret_cast<const uint4*>(smem + min(8 * n + g, a.T - 1) * pitch +
+                                                     (4 * step + gr) * 64 + t * 16);
+              c[n] = *reinterpret_cast<const float4*>(
+                  start + ((4 * step + gr) * (kPad / 2) + 4 * n + t) * 4);
+            }
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) {
+              uint32_t lo[4], hi[4];
+              nibbles(wr[m][2 * h], magic_lo, magic_hi, lo);
+              nibbles(wr[m][2 * h + 1], magic_lo, magic_hi, hi);
+              const uint32_t w0 = sc[2 * m][pair], w8 = sc[2 * m + 1][pair];
+              const float f0 = __uint_as_float(h ? w0 & 0xffff0000u : w0 << 16);
+              const float f8 = __uint_as_float(h ? w8 & 0xffff0000u : w8 << 16);
+#pragma unroll
+              for (int n = 0; n < NB; ++n) {
+                float d[4], e[4];
+                mma_f16(d, lo[0], hi[0], lo[1], hi[1], v[n].x, v[n].y, c[n].x, c[n].y, c[n].z,
+                        c[n].w);
+                mma_f16(e, lo[2], hi[2], lo[3], hi[3], v[n].z, v[n].w, d[0], d[1], d[2], d[3]);
+                part[m][n][0] = fmaf(f0, e[0], part[m][n][0]);
+                part[m][n][1] = fmaf(f0, e[1], part[m][n][1]);
+                part[m][n][2] = fmaf(f8, e[2], part[m][n][2]);
+                part[m][n][3] = fmaf(f8, e[3], part[m][n][3]);
+              }
             }
           }
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const float2 u = *reinterpret_cast<const float2*>(unit + step * kPad + 8 * n + 2 * t);
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[m][n][i] = fmaf(i & 1 ? u.y : u.x, part[m][n][i], acc[m][n][i]);
         }
       }
       __syncwarp();
@@ -294,77 +365,149 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
       asm volatile("cp.async.commit_group;" ::: "memory");
       slot = slot + 1 == kDepth ? 0 : slot + 1;
     }
-    float* red = reinterpret_cast<float*>(smem + lay.red) + (turn & 1) * kWarps * 16 * kPad;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      float* p = red + (warp * 16 + g) * kPad + 8 * n + 2 * t;
-      *reinterpret_cast<float2*>(p) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(p + 8 * kPad) = make_float2(acc[n][2], acc[n][3]);
-    }
-    __syncthreads();
-    // one thread an output: warps of a block in order, then the slices in order
+    // a block's sums: of its one warp, or of its warps in order; those of the slices in order
     const int sl = turn / turns, b0 = (turn - sl * turns) * abreast;
-    float* sums = reinterpret_cast<float*>(smem + lay.sums);
+    float* to = a.split > 1 ? red + warp * a.T * kSumPitch : sums + (b0 + rb) * a.T * kSumPitch;
+    if (a.split > 1 || b0 + rb < blocks) {
+      const bool add = a.split == 1 && sl > 0;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int k = 8 * n + 2 * t + i;
+          if (k >= a.T) continue;
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float* p = to + k * kSumPitch + 16 * m + 8 * h + g;
+              const float v = acc[m][n][2 * h + i];
+              *p = add ? *p + v : v;
+            }
+        }
+    }
+    if (a.split > 1) {
+      __syncthreads();
+      // a warp an output row's 32 values
 #pragma unroll 1
-    for (int i = tid; i < abreast * 16 * a.T; i += kThreads) {
-      const int r = i & 15, k = (i >> 4) % a.T, b = (i >> 4) / a.T;
-      if (b0 + b >= blocks) continue;
-      float v = 0.f;
-#pragma unroll 1
-      for (int w = 0; w < a.split; ++w) v += red[((b * a.split + w) * 16 + r) * kPad + k];
-      const int field = static_cast<int>(top[k] >> 23);
-      const int up = top[k] == 0u || field == 255 ? 127 : min(127 + 14 + 127 - field, 253);
-      v *= __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
-      if (slices > 1) {
-        float* sum = sums + ((b0 + b) * 16 + r) * kPad + k;
-        if (sl > 0) v += *sum;
-        *sum = v;
+      for (int q = warp; q < abreast * a.T; q += kWarps) {
+        const int b = q / a.T, k = q - b * a.T;
+        if (b0 + b >= blocks) continue;
+        const float* from = red + (b * a.split * a.T + k) * kSumPitch + lane;
+        float part[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) part[w] = w < a.split ? from[w * a.T * kSumPitch] : 0.f;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += part[w];
+        float* sum = sums + ((b0 + b) * a.T + k) * kSumPitch + lane;
+        *sum = sl > 0 ? *sum + v : v;
       }
-      const int row = (block0 + b0 + b) * 16 + r;
-      if (sl == slices - 1 && row < a.N) a.y[(int64_t)k * a.N + row] = f32_to_bf16_bits(v);
+      __syncthreads();
     }
     cur = next;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  // each CTA of the cluster has its share of the outputs, a warp 32 rows of one token
+  if (a.ranks > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+#pragma unroll 1
+  for (int q = rank * kWarps + warp; q < blocks * a.T; q += a.ranks * kWarps) {
+    float v = 0.f;
+    if (a.ranks > 1) {
+      const uint32_t at = smem_u32(sums + q * kSumPitch + lane);
+      float part[kMostCluster];
+#pragma unroll
+      for (int c = 0; c < kMostCluster; ++c) {
+        uint32_t from;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(min(c, a.ranks - 1)));
+        part[c] = ld_cluster_f1(from);
+      }
+#pragma unroll
+      for (int c = 0; c < kMostCluster; ++c) v += c < a.ranks ? part[c] : 0.f;
+    } else {
+      v = sums[q * kSumPitch + lane];
+    }
+    const int b = q / a.T, row = (block0 + b) * kRows + lane;
+    if (row < a.N) a.y[(int64_t)(q - b * a.T) * a.N + row] = f32_to_bf16_bits(v);
+  }
+  if (a.ranks > 1) cluster_sync_all();  // until every CTA has read this one's sums
 }
 
+// Clusters of 1, 2, 4 and 8 CTAs that the device holds at a time with two CTAs to an SM.
+template <int NB>
+const int* clusters_at_once() {
+  static const struct Held {
+    int n[4] = {0, 0, 0, 0};
+    Held() {
+      for (int i = 0; i < 4; ++i) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(kMostCluster);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kPerSm;
+        cudaLaunchAttribute attr[2];
+        set_adapter_attrs(&cfg, attr, 1 << i);
+        if (cudaOccupancyMaxActiveClusters(&n[i], int4_matvec_kernel<NB>, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          n[i] = 0;
+        }
+      }
+    }
+  } held;
+  return held.n;
+}
+
+// How the work is cut.  For each number of CTAs that share the columns (ranks) and of
+// warps that share a CTA's (split): the steps that a warp goes through, one more a turn
+// for the sums, what it costs to make x ready (16 bytes of it in each thread as much as a
+// step), and two for the sums over a cluster.  The fewest win.
 template <int NB>
 int launch(MatvecArgs a, cudaStream_t st) {
   auto kern = int4_matvec_kernel<NB>;
   MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
-  // as many columns as fit; at least 128
-  const int padded = NB * 8;
-  const int most = kRoomForTokens / (a.T * 2 + padded / 8) / 128 * 128;
-  const int all = (a.K + 127) / 128 * 128;
-  const int slices = (all + most - 1) / most;
-  a.slice = ((all / 128 + slices - 1) / slices) * 128;
-  // four steps a warp at least, else the warps have different rows
-  const int steps = a.slice / 128;
-  a.split = steps >= 32 ? 8 : steps >= 16 ? 4 : steps >= 8 ? 2 : 1;
-  const int n_blocks = (a.N + 15) / 16;
-  a.blocks = 1;
-  int ctas = 1;
-  const int want = Layout(a).total;
-  MOE_TRY_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kern, kThreads, want));
-  if (ctas < 1) return MOE_ERR_UNSUPPORTED;
-  const int grid = ctas * num_sms();
-  // whole rounds of the warps' blocks; with one slice a CTA's x costs little, and more CTAs
-  // than fit at a time are no loss
-  const int abreast = kWarps / a.split;
-  a.blocks = (n_blocks + grid - 1) / grid;
-  a.blocks = (a.blocks + abreast - 1) / abreast * abreast;
-  if (a.blocks < abreast) a.blocks = abreast;
-  if (a.blocks * abreast > 0 && n_blocks < abreast * num_sms()) a.blocks = abreast;
-  const Layout lay(a);
-  if (lay.total > 226 * 1024) return MOE_ERR_UNSUPPORTED;
+  const int* held = clusters_at_once<NB>();
+  const int steps = (a.K + 127) / 128, n_blocks = (a.N + kRows - 1) / kRows;
+  MatvecArgs best = a;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 4; ++i)
+    for (int split = 1; split <= kWarps; split *= 2) {
+      MatvecArgs b = a;
+      b.ranks = 1 << i;
+      b.split = split;
+      const int abreast = kWarps / split, clusters = held[i];
+      if (clusters < 1 || b.ranks > steps) continue;
+      b.blocks = max(abreast, (n_blocks + clusters - 1) / clusters);
+      const int waves = (b.blocks + kMostBlocks - 1) / kMostBlocks;
+      b.blocks = max(abreast, (n_blocks + clusters * waves - 1) / (clusters * waves));
+      // slices as few as fit, the same number in every CTA
+      int per = 0;
+      do {
+        ++per;
+        b.slice = (steps + per * b.ranks - 1) / (per * b.ranks) * 128;
+        b.slices = (a.K + b.slice - 1) / b.slice;
+      } while (Layout(b).total > kPerSm && b.slice > 128);
+      if (b.slices < b.ranks) continue;
+      const int turns = (b.blocks + abreast - 1) / abreast;
+      const int each = (b.slice / 128 + split - 1) / split;
+      const int64_t cost = static_cast<int64_t>(waves) *
+          (static_cast<int64_t>(per) * (turns * (each + 1) + b.slice / 8 * a.T / kThreads) +
+           (b.ranks > 1 ? 2 : 0));
+      if (cost >= least) continue;
+      least = cost;
+      best = b;
+    }
+  if (least == INT64_MAX) return MOE_ERR_CUDA;
+  const Layout lay(best);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((n_blocks + a.blocks - 1) / a.blocks);
+  cfg.gridDim = dim3((n_blocks + best.blocks - 1) / best.blocks * best.ranks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = lay.total;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  set_adapter_attrs(&cfg, attr, 0);
-  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+  set_adapter_attrs(&cfg, attr, best.ranks > 1 ? best.ranks : 0);
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kern, best));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -399,6 +542,7 @@ extern "C" int moe_int4_matvec(const uint16_t* x, int64_t x_ld, const int32_t* w
   a.T = T;
   a.N = N;
   a.K = K;
+  a.scales8 = K % 128 == 0 && aligned(w_scale, 8);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return T <= 8 ? launch<1>(a, st) : launch<2>(a, st);
 }
