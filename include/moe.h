@@ -597,12 +597,12 @@ void moe_layer_pipe_destroy(moe_layer_pipe* pipe);
 /* One PackedInt4Linear on at most 16 rows (no expert segments, no workspace):
  *   y[t] = bf16( x[t] W^T ),  W[n, c] = q[n, c] * scale[n, c / 32]
  *   x         bf16, row t at x + t * x_ld elements (x_ld >= K, a multiple of 8): any
- *             bf16 values, a row is scaled by a power of two on its way in and out
+ *             bf16 values, scaled by powers of two on their way in and out
  *   w_packed  int32 [N, K/8];  w_scale bf16 [N, K/32]: any N
  *   y         bf16 [T, N]
  * fp32 accumulation, one rounding; equal calls give equal bits.  Weights are read
- * once.  T <= 16 and K % 32 == 0, else MOE_ERR_UNSUPPORTED (moe_int4_linear takes
- * more rows).  x and w_packed 16-byte aligned, w_scale 4; y shares no byte with an
+ * once.  T <= 16, K % 32 == 0, K <= 2^20 and N <= 2^30, else MOE_ERR_UNSUPPORTED
+ * (moe_int4_linear takes more rows).  x and w_packed 16-byte aligned, w_scale 4; y shares no byte with an
  * input, else MOE_ERR_INVALID. */
 int moe_int4_matvec(const uint16_t* x, int64_t x_ld, const int32_t* w_packed,
                     const uint16_t* w_scale, int T, int N, int K, uint16_t* y, void* stream);

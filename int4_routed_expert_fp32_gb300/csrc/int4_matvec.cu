@@ -36,6 +36,7 @@ constexpr int kScalePitch = 12;                  // 4 scales of a row in 4-byte 
 constexpr int kStepBytes = kStepWords + kRows * kScalePitch;
 constexpr int kMaxTokens = 16;
 constexpr int kMostBlocks = 16;                  // of a cluster: their sums are in shared memory
+constexpr int kMostColumns = 1 << 20, kMostRows = 1 << 30;
 constexpr int kMostCluster = 8;
 constexpr int kSumPitch = kRows + 4;             // lanes' tokens and rows in different banks
 constexpr int kPerSm = 113 * 1024;               // shared memory with which two CTAs fit an SM
@@ -56,7 +57,6 @@ struct MatvecArgs {
   int ranks;     // CTAs of a cluster
   int split;     // warps that share a slice's columns
   int blocks;    // blocks of a cluster
-  bool scales8;  // the scales of every 128 columns begin on 8 bytes
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -90,12 +90,11 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t lo, uint32_t hi, ui
   asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0x6a;" : "=r"(q[3]) : "r"(w8), "r"(hi));
 }
 
-// Where one warp's work on a block and slice lies.
+// The steps of 128 columns of one warp, on a block and slice.
 struct Item {
   int row0;   // first row of the block
-  int step0;  // first step of 128 columns, in the slice
+  int col0;   // first column
   int steps;
-  int col0;   // first column of the slice
 };
 
 // Bytes of a token's row in shared memory: rows 64 bytes apart in the banks.
@@ -114,7 +113,7 @@ struct Layout {
   }
 };
 
-template <int NB>
+template <int NB, bool kScales8>
 __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const Layout lay(a);
@@ -139,68 +138,89 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
   auto item_of = [&](int turn) {  // turns count on over the slices
     Item it;
     const int sl = turn / turns, b = (turn - sl * turns) * abreast + rb;
-    it.col0 = (rank + sl * a.ranks) * a.slice;
-    const int steps = (min(a.slice, a.K - it.col0) + 127) / 128;
+    const int col0 = (rank + sl * a.ranks) * a.slice;
+    const int steps = (min(a.slice, a.K - col0) + 127) / 128;
     const int each = (steps + a.split - 1) / a.split;
-    it.step0 = ks * each;
-    it.steps = sl < slices && b < blocks ? max(0, min(each, steps - it.step0)) : 0;
+    it.steps = b < blocks ? max(0, min(each, steps - ks * each)) : 0;
     it.row0 = (block0 + b) * kRows;
+    it.col0 = col0 + ks * each * 128;
     return it;
   };
+  // The copies run ahead of the products through the same steps.  Where they are:
+  int to_turn = -1, to_steps = 0, to_rows = 0, to_groups = 0, to_slot = 0;
+  const uint8_t* to_w = nullptr;
+  int64_t to_scale = 0;  // byte offset
+  const int64_t rows8 = (int64_t)a.K * 4;  // bytes of 8 rows
   uint8_t* mine = smem + lay.steps + warp * kDepth * kStepBytes;
-  // Step j of an item: 16-byte pieces of rows swizzled by row / 2, and the scales.
-  auto load = [&](int slot, const Item& it, int j) {
-    const uint32_t to = smem_u32(mine) + slot * kStepBytes;
-    const int col = it.col0 + (it.step0 + j) * 128;
-    const int first = col / kGroup;
+  // The next step: 16-byte pieces of rows swizzled by row / 2, and the scales.  Rows
+  // behind the last and columns behind the last are left as they are.
+  auto load = [&] {
+    while (to_steps == 0) {
+      if (++to_turn >= turns * slices) {
+        to_steps = -1;
+        break;
+      }
+      const Item it = item_of(to_turn);
+      to_steps = it.steps;
+      to_rows = a.N - it.row0;
+      to_groups = groups - it.col0 / kGroup;
+      to_w = a.w + (int64_t)(it.row0 + g) * (a.K / 2) + it.col0 / 2 + t * 16;
+      to_scale = ((int64_t)(it.row0 + lane) * groups + it.col0 / kGroup) * 2;
+    }
+    if (to_steps > 0) {
+      uint8_t* st = mine + to_slot * kStepBytes;
+      const uint32_t to = smem_u32(st);
+      const uint8_t* w = to_w;
 #pragma unroll
-    for (int h = 0; h < 2 * kTiles; ++h) {
-      const int r = g + 8 * h, row = min(it.row0 + r, a.N - 1);
-      if (first + t < groups)
-        copy16(to + r * 64 + ((t ^ (r >> 1 & 3)) << 4),
-               a.w + (int64_t)row * (a.K / 2) + col / 2 + t * 16, once);
+      for (int h = 0; h < 2 * kTiles; ++h) {
+        const int r = g + 8 * h;
+        if (t < to_groups && r < to_rows) copy16(to + r * 64 + ((t ^ (r >> 1 & 3)) << 4), w, once);
+        w += rows8;
+      }
+      if (lane < to_rows) {
+        if (kScales8) {
+          copy8(to + kStepWords + lane * 8, a.scale + to_scale);
+        } else {
+          // at most 8 bytes, which begin on 4 bytes or 2 behind them
+          const int64_t word = to_scale & ~3LL, end = to_scale + 2 * min(to_groups, 4);
+          uint8_t* dst = st + kStepWords + lane * kScalePitch;
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            if (word + 4 * p >= end) continue;
+            if (word + 4 * p + 4 <= (int64_t)a.N * groups * 2)
+              cp_async_4(dst + 4 * p, a.scale + word + 4 * p);
+            else  // the last scale of an odd number
+              *reinterpret_cast<uint16_t*>(dst + 4 * p) =
+                  *reinterpret_cast<const uint16_t*>(a.scale + word + 4 * p);
+          }
+        }
+      }
+      to_w += 64;
+      to_scale += 8;
+      to_groups -= 4;
+      --to_steps;
+      to_slot = to_slot + 1 == kDepth ? 0 : to_slot + 1;
     }
-    if (a.scales8) {
-      const int row = min(it.row0 + lane, a.N - 1);
-      copy8(to + kStepWords + lane * 8, a.scale + ((int64_t)row * groups + first) * 2);
-      return;
-    }
-    // 8 bytes of scales of a row, which begin on 4 bytes or 2 behind them
-    const int row = min(it.row0 + lane, a.N - 1);
-    const int64_t at = ((int64_t)row * groups + first) * 2, word = at & ~3LL;
-    const int64_t end = min(at + 8, ((int64_t)row + 1) * groups * 2);  // of the row's scales
-    uint8_t* dst = mine + slot * kStepBytes + kStepWords + lane * kScalePitch;
-#pragma unroll 1
-    for (int p = 0; p < 3 && word + 4 * p < end; ++p) {
-      if (word + 4 * p + 4 <= (int64_t)a.N * groups * 2)
-        cp_async_4(dst + 4 * p, a.scale + word + 4 * p);
-      else  // the last scale of an odd number
-        *reinterpret_cast<uint16_t*>(dst + 4 * p) =
-            *reinterpret_cast<const uint16_t*>(a.scale + word + 4 * p);
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   grid_wait();  // x, or the weights, may come from the kernel before
   grid_launch_dependents();
   // the first copies of weights; x is made ready meanwhile
-  Item cur = item_of(0);
-  int slot = 0;
 #pragma unroll 1
-  for (int j = 0; j < kDepth; ++j) {
-    if (j < cur.steps) load(j, cur, j);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
+  for (int j = 0; j < kDepth; ++j) load();
 
   float* start = reinterpret_cast<float*>(smem + lay.start);
   float* unit = reinterpret_cast<float*>(smem + lay.unit);
   float* red = reinterpret_cast<float*>(smem + lay.red);
   float* sums = reinterpret_cast<float*>(smem + lay.sums);
   const int pitch = row_pitch(a.slice);
+  int slot = 0;
 #pragma unroll 1
   for (int turn = 0; turn < turns * slices; ++turn) {
     if (turn % turns == 0) {
       // x of this slice as fp16 in pair order; 16 lanes have the 128 columns of a scale
-      const int cols = min(a.slice, a.K - cur.col0);
+      const int col0 = (rank + turn / turns * a.ranks) * a.slice, cols = min(a.slice, a.K - col0);
       const int pieces = (cols + 127) / 128 * 16, all = a.T * pieces;
       if (turn > 0) __syncthreads();  // the slice before has been read
 #pragma unroll 1
@@ -211,11 +231,12 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
           const int i = base + l * kThreads, k = i / pieces, c = i - k * pieces;
           v[l] = make_uint4(0u, 0u, 0u, 0u);
           if (i < all && 8 * c < cols)
-            v[l] = __ldcg(reinterpret_cast<const uint4*>(a.x + k * a.x_ld + cur.col0 + 8 * c));
+            v[l] = __ldcg(reinterpret_cast<const uint4*>(a.x + k * a.x_ld + col0 + 8 * c));
         }
 #pragma unroll
         for (int l = 0; l < kLoads; ++l) {
           const int i = base + l * kThreads, k = i / pieces, c = i - k * pieces;
+          if (i - lane >= all) break;  // of the whole warp
           const uint32_t w[4] = {v[l].x, v[l].y, v[l].z, v[l].w};
           uint32_t m = 0u;
 #pragma unroll
@@ -255,7 +276,15 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
       }
       __syncthreads();
     }
-    const Item next = item_of(turn + 1);
+    const Item cur = item_of(turn);
+    const int first = (cur.col0 / 128 - (rank + turn / turns * a.ranks) * (a.slice / 128));  // step
+    const uint8_t* xs[NB];  // the lane's fragments of the step, of tokens 8n + g
+#pragma unroll
+    for (int n = 0; n < NB; ++n)  // a token that is not there is the last one: no column of
+      xs[n] = smem + min(8 * n + g, a.T - 1) * pitch + first * 256 + t * 16;  // the product
+    const float* cs = start + first * (8 * kPad) + t * 4;                     // reaches another
+    const float* us = unit + first * kPad + 2 * t;
+    int left = groups - cur.col0 / kGroup;
     float acc[kTiles][NB][4];
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
@@ -263,107 +292,95 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-    const int steps = max(kDepth, cur.steps);
 #pragma unroll 1
-    for (int j = 0; j < steps; ++j) {
+    for (int j = 0; j < cur.steps; ++j) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
       __syncwarp();
-      if (j < cur.steps) {
-        const uint8_t* st = mine + slot * kStepBytes;
-        const int step = cur.step0 + j, first = cur.col0 / kGroup + 4 * step;
-        // two words with the four scales of each of the lane's rows
-        uint32_t sc[2 * kTiles][2];
+      const uint8_t* st = mine + slot * kStepBytes;
+      // two words with the four scales of each of the lane's rows
+      uint32_t sc[2 * kTiles][2];
 #pragma unroll
-        for (int h = 0; h < 2 * kTiles; ++h) {
-          if (a.scales8) {
-            const uint2 v = *reinterpret_cast<const uint2*>(st + kStepWords + (g + 8 * h) * 8);
-            sc[h][0] = v.x;
-            sc[h][1] = v.y;
-          } else {
-            const uint32_t* v =
-                reinterpret_cast<const uint32_t*>(st + kStepWords + (g + 8 * h) * kScalePitch);
-            const uint32_t row = min(cur.row0 + g + 8 * h, a.N - 1);
-            const uint32_t by = ((row & groups) + first & 1) * 16;
-            sc[h][0] = __funnelshift_r(v[0], v[1], by);
-            sc[h][1] = __funnelshift_r(v[1], v[2], by);
+      for (int h = 0; h < 2 * kTiles; ++h) {
+        if (kScales8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(st + kStepWords + (g + 8 * h) * 8);
+          sc[h][0] = v.x;
+          sc[h][1] = v.y;
+        } else {
+          const uint32_t* v =
+              reinterpret_cast<const uint32_t*>(st + kStepWords + (g + 8 * h) * kScalePitch);
+          const int odd = ((cur.row0 + g + 8 * h & groups) + groups - left & 1) * 16;
+          sc[h][0] = __funnelshift_r(v[0], v[1], odd);
+          sc[h][1] = __funnelshift_r(v[1], v[2], odd);
+          // groups behind the last: x is zero there, whatever the words are, which must not
+          // meet a scale that is not finite
+          if (left < 4) {
+            if (left < 2) sc[h][0] &= 0xffffu;
+            sc[h][1] = left < 3 ? 0u : sc[h][1] & 0xffffu;
           }
         }
-        float part[kTiles][NB][4];
+      }
+      float part[kTiles][NB][4];  // set by the first group
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
+      for (int pair = 0; pair < 2; ++pair) {
+        uint32_t wr[kTiles][4];
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
+        for (int m = 0; m < kTiles; ++m) {
+          const int r = 16 * m + (lane & 15);
+          const uint32_t from =
+              smem_u32(st) + r * 64 + (((2 * pair + (lane >> 4)) ^ (r >> 1 & 3)) << 4);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(wr[m][0]), "=r"(wr[m][1]), "=r"(wr[m][2]), "=r"(wr[m][3])
+                       : "r"(from)
+                       : "memory");
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[m][n][i] = 0.f;
+        for (int h = 0; h < 2; ++h) {
+          const int gr = 2 * pair + h;
+          uint4 v[NB];
+          float4 c[NB];
 #pragma unroll
-        for (int pair = 0; pair < 2; ++pair) {
-          if (first + 2 * pair >= groups) break;
-          uint32_t wr[kTiles][4];
-#pragma unroll
-          for (int m = 0; m < kTiles; ++m) {
-            const int r = 16 * m + (lane & 15);
-            const uint32_t from =
-                smem_u32(st) + r * 64 + (((2 * pair + (lane >> 4)) ^ (r >> 1 & 3)) << 4);
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(wr[m][0]), "=r"(wr[m][1]), "=r"(wr[m][2]), "=r"(wr[m][3])
-                         : "r"(from)
-                         : "memory");
+          for (int n = 0; n < NB; ++n) {
+            v[n] = *reinterpret_cast<const uint4*>(xs[n] + gr * 64);
+            c[n] = *reinterpret_cast<const float4*>(cs + gr * (2 * kPad) + 16 * n);
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int gr = 2 * pair + h;
-            if (first + gr >= groups) break;
-            // rows of tokens that are not there repeat the last one: no column of the
-            // product reaches another
-            uint4 v[NB];
-            float4 c[NB];
+          for (int m = 0; m < kTiles; ++m) {
+            uint32_t lo[4], hi[4];
+            nibbles(wr[m][2 * h], magic_lo, magic_hi, lo);
+            nibbles(wr[m][2 * h + 1], magic_lo, magic_hi, hi);
+            const uint32_t w0 = sc[2 * m][pair], w8 = sc[2 * m + 1][pair];
+            const float f0 = __uint_as_float(h ? w0 & 0xffff0000u : w0 << 16);
+            const float f8 = __uint_as_float(h ? w8 & 0xffff0000u : w8 << 16);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-              v[n] = *reinterpret_cast<const uint4*>(smem + min(8 * n + g, a.T - 1) * pitch +
-                                                     (4 * step + gr) * 64 + t * 16);
-              c[n] = *reinterpret_cast<const float4*>(
-                  start + ((4 * step + gr) * (kPad / 2) + 4 * n + t) * 4);
-            }
+              float d[4], e[4];
+              mma_f16(d, lo[0], hi[0], lo[1], hi[1], v[n].x, v[n].y, c[n].x, c[n].y, c[n].z, c[n].w);
+              mma_f16(e, lo[2], hi[2], lo[3], hi[3], v[n].z, v[n].w, d[0], d[1], d[2], d[3]);
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
-              uint32_t lo[4], hi[4];
-              nibbles(wr[m][2 * h], magic_lo, magic_hi, lo);
-              nibbles(wr[m][2 * h + 1], magic_lo, magic_hi, hi);
-              const uint32_t w0 = sc[2 * m][pair], w8 = sc[2 * m + 1][pair];
-              const float f0 = __uint_as_float(h ? w0 & 0xffff0000u : w0 << 16);
-              const float f8 = __uint_as_float(h ? w8 & 0xffff0000u : w8 << 16);
-#pragma unroll
-              for (int n = 0; n < NB; ++n) {
-                float d[4], e[4];
-                mma_f16(d, lo[0], hi[0], lo[1], hi[1], v[n].x, v[n].y, c[n].x, c[n].y, c[n].z,
-                        c[n].w);
-                mma_f16(e, lo[2], hi[2], lo[3], hi[3], v[n].z, v[n].w, d[0], d[1], d[2], d[3]);
-                part[m][n][0] = fmaf(f0, e[0], part[m][n][0]);
-                part[m][n][1] = fmaf(f0, e[1], part[m][n][1]);
-                part[m][n][2] = fmaf(f8, e[2], part[m][n][2]);
-                part[m][n][3] = fmaf(f8, e[3], part[m][n][3]);
+              for (int i = 0; i < 4; ++i) {
+                const float f = i < 2 ? f0 : f8;
+                part[m][n][i] = gr == 0 ? f * e[i] : fmaf(f, e[i], part[m][n][i]);
               }
             }
           }
         }
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const float2 u = *reinterpret_cast<const float2*>(unit + step * kPad + 8 * n + 2 * t);
-#pragma unroll
-          for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[m][n][i] = fmaf(i & 1 ? u.y : u.x, part[m][n][i], acc[m][n][i]);
-        }
       }
-      __syncwarp();
-      const int ahead = j + kDepth;
-      if (ahead < cur.steps)
-        load(slot, cur, ahead);
-      else if (ahead >= steps && ahead - steps < next.steps)
-        load(slot, next, ahead - steps);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const float2 u = *reinterpret_cast<const float2*>(us + 8 * n);
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[m][n][i] = fmaf(i & 1 ? u.y : u.x, part[m][n][i], acc[m][n][i]);
+        xs[n] += 256;
+      }
+      cs += 8 * kPad;
+      us += kPad;
+      left -= 4;
       slot = slot + 1 == kDepth ? 0 : slot + 1;
+      __syncwarp();
+      load();
     }
     // a block's sums: of its one warp, or of its warps in order; those of the slices in order
     const int sl = turn / turns, b0 = (turn - sl * turns) * abreast;
@@ -405,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
       }
       __syncthreads();
     }
-    cur = next;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   // each CTA of the cluster has its share of the outputs, a warp 32 rows of one token
@@ -437,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
 }
 
 // Clusters of 1, 2, 4 and 8 CTAs that the device holds at a time with two CTAs to an SM.
-template <int NB>
+template <int NB, bool kScales8>
 const int* clusters_at_once() {
   static const struct Held {
     int n[4] = {0, 0, 0, 0};
@@ -449,7 +465,7 @@ const int* clusters_at_once() {
         cfg.dynamicSmemBytes = kPerSm;
         cudaLaunchAttribute attr[2];
         set_adapter_attrs(&cfg, attr, 1 << i);
-        if (cudaOccupancyMaxActiveClusters(&n[i], int4_matvec_kernel<NB>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n[i], int4_matvec_kernel<NB, kScales8>, &cfg) != cudaSuccess) {
           cudaGetLastError();
           n[i] = 0;
         }
@@ -460,14 +476,18 @@ const int* clusters_at_once() {
 }
 
 // How the work is cut.  For each number of CTAs that share the columns (ranks) and of
-// warps that share a CTA's (split): the steps that a warp goes through, one more a turn
-// for the sums, what it costs to make x ready (16 bytes of it in each thread as much as a
-// step), and two for the sums over a cluster.  The fewest win.
-template <int NB>
+// warps that share a CTA's (split), the time in steps of about 0.1 us: the steps that a
+// warp goes through, one more a turn for the sums, two for every 16 bytes of x that a
+// thread makes ready, and what a cluster costs to start and to join.  The fewest win.
+// Measured, ranks and split: one row of 7168 x 7168, 1 and 8: 12.8 us, 4 and 2: 14.0; 3
+// rows of 3585 x 2080, 1 and 8: 6.2, 4 and 4: 7.7; 16 rows of 16384 x 7168, 8 and 1: 32,
+// 4 and 1: 38, 2 and 1: 46; 2 rows of 1160 x 13216, 4 and 8: 10.3, 2 and 8: 11.5.
+template <int NB, bool kScales8>
 int launch(MatvecArgs a, cudaStream_t st) {
-  auto kern = int4_matvec_kernel<NB>;
+  auto kern = int4_matvec_kernel<NB, kScales8>;
   MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
-  const int* held = clusters_at_once<NB>();
+  const int joined[4] = {0, 5, 8, 12};
+  const int* held = (clusters_at_once<NB, kScales8>());
   const int steps = (a.K + 127) / 128, n_blocks = (a.N + kRows - 1) / kRows;
   MatvecArgs best = a;
   int64_t least = INT64_MAX;
@@ -492,8 +512,7 @@ int launch(MatvecArgs a, cudaStream_t st) {
       const int turns = (b.blocks + abreast - 1) / abreast;
       const int each = (b.slice / 128 + split - 1) / split;
       const int64_t cost = static_cast<int64_t>(waves) *
-          (static_cast<int64_t>(per) * (turns * (each + 1) + b.slice / 8 * a.T / kThreads) +
-           (b.ranks > 1 ? 2 : 0));
+          (static_cast<int64_t>(per) * (turns * (each + 1) + b.slice / 4 * a.T / kThreads) + joined[i]);
       if (cost >= least) continue;
       least = cost;
       best = b;
@@ -523,7 +542,8 @@ extern "C" int moe_int4_matvec(const uint16_t* x, int64_t x_ld, const int32_t* w
                                void* stream) {
   moe::Range range_("moe_int4_matvec");
   if (T < 0 || N <= 0 || K <= 0 || x_ld < K) return MOE_ERR_INVALID;
-  if (T > kMaxTokens || K % kGroup != 0 || x_ld % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (T > kMaxTokens || K % kGroup != 0 || K > kMostColumns || N > kMostRows || x_ld % 8 != 0)
+    return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w_packed || !w_scale || !y) return MOE_ERR_INVALID;
   if (!aligned(x, 16) || !aligned(w_packed, 16) || !aligned(w_scale, 4) || !aligned(y, 2))
@@ -542,7 +562,9 @@ extern "C" int moe_int4_matvec(const uint16_t* x, int64_t x_ld, const int32_t* w
   a.T = T;
   a.N = N;
   a.K = K;
-  a.scales8 = K % 128 == 0 && aligned(w_scale, 8);
+  // whether the scales of every 128 columns begin on 8 bytes
+  const bool scales8 = K % 128 == 0 && aligned(w_scale, 8);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return T <= 8 ? launch<1>(a, st) : launch<2>(a, st);
+  if (T <= 8) return scales8 ? launch<1, true>(a, st) : launch<1, false>(a, st);
+  return scales8 ? launch<2, true>(a, st) : launch<2, false>(a, st);
 }
