@@ -49,6 +49,8 @@ constexpr int kThreads = 32 * (kFirstMul + kMul);
 constexpr int kCtas = 2;                     // of an SM: one waits while the other multiplies
 constexpr int kFrontThreads = 256;
 constexpr int kFrontExperts = 2;             // router rows of a CTA
+constexpr int kFrontTokens = 4;              // tokens at a time
+static_assert(kFrontTokens * kFrontExperts == 8, "sums over the warp");
 constexpr int kFrontLoads = 7;               // float4 of a router row held by a thread
 
 // Ring slot: weights (32 rows of C / 2 bytes: for each row block of 16, pieces of 128
@@ -275,28 +277,51 @@ __global__ void __launch_bounds__(kFrontThreads) few_front_kernel(const FewArgs 
             w[e][i] = __ldcs(reinterpret_cast<const float4*>(a.router_w + (size_t)(e0 + e) * a.H + c));
         }
       }
-#pragma unroll 2
-      for (int t = 0; t < a.T; ++t) {
-        float z[kFrontExperts] = {};
+      // kFrontTokens at a time, their loads on the way together (32 tokens, 384 experts of
+      // 7168: 23 us two at a time, XX four)
+#pragma unroll 1
+      for (int t0 = 0; t0 < a.T; t0 += kFrontTokens) {
+        float z[kFrontTokens * kFrontExperts] = {};
 #pragma unroll
         for (int i = 0; i < kFrontLoads; ++i) {
           const int c = h0 + 4 * (tid + i * kFrontThreads);
-          uint2 v = make_uint2(0u, 0u);
-          if (c < a.H) v = __ldg(reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H + c));
-          const float x0 = __uint_as_float(v.x << 16), x1 = __uint_as_float(v.x & 0xffff0000u);
-          const float x2 = __uint_as_float(v.y << 16), x3 = __uint_as_float(v.y & 0xffff0000u);
+          uint2 v[kFrontTokens];
 #pragma unroll
-          for (int e = 0; e < kFrontExperts; ++e) {
-            z[e] = fmaf(x0, w[e][i].x, z[e]);
-            z[e] = fmaf(x1, w[e][i].y, z[e]);
-            z[e] = fmaf(x2, w[e][i].z, z[e]);
-            z[e] = fmaf(x3, w[e][i].w, z[e]);
+          for (int t = 0; t < kFrontTokens; ++t) {
+            v[t] = make_uint2(0u, 0u);
+            if (c < a.H && t0 + t < a.T)
+              v[t] = __ldg(reinterpret_cast<const uint2*>(a.x + (size_t)(t0 + t) * a.H + c));
+          }
+#pragma unroll
+          for (int t = 0; t < kFrontTokens; ++t) {
+            const float x0 = __uint_as_float(v[t].x << 16), x1 = __uint_as_float(v[t].x & 0xffff0000u);
+            const float x2 = __uint_as_float(v[t].y << 16), x3 = __uint_as_float(v[t].y & 0xffff0000u);
+#pragma unroll
+            for (int e = 0; e < kFrontExperts; ++e) {
+              float& to = z[t * kFrontExperts + e];
+              to = fmaf(x0, w[e][i].x, to);
+              to = fmaf(x1, w[e][i].y, to);
+              to = fmaf(x2, w[e][i].z, to);
+              to = fmaf(x3, w[e][i].w, to);
+            }
           }
         }
+        // sums over the warp, half of the values in each half of the lanes at every step:
+        // lane 4 j gets value j
 #pragma unroll
-        for (int e = 0; e < kFrontExperts; ++e) {
-          const float v = warp_sum(z[e]);
-          if (lane == 0) part[t][e][warp] = h0 ? part[t][e][warp] + v : v;
+        for (int o = 16, n = kFrontTokens * kFrontExperts / 2; n > 0; o >>= 1, n >>= 1)
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const bool upper = lane & o;
+            const float give = upper ? z[i] : z[i + n];
+            z[i] = (upper ? z[i + n] : z[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        z[0] += __shfl_xor_sync(0xffffffffu, z[0], 2);
+        z[0] += __shfl_xor_sync(0xffffffffu, z[0], 1);
+        const int t = t0 + lane / 4 / kFrontExperts;
+        if (!(lane & 3) && t < a.T) {
+          float* to = &part[t][lane / 4 % kFrontExperts][warp];
+          *to = h0 ? *to + z[0] : z[0];
         }
       }
     }
@@ -373,8 +398,6 @@ struct Lists {
   uint32_t* tokens;   // [chunks] tokens, one bit each
   uint16_t* expert;   // [chunks]
   uint16_t* row0;     // [chunks] first row
-  int* chunks;
-  uint32_t* in_group; // [kFewGroups] tokens of a group of chunks
 };
 
 // Ring and buffers of a CTA.
@@ -416,9 +439,11 @@ struct __align__(16) Context {
   Header sum_header[kFinish];
   uint64_t full[kMaxSlots], empty[kMaxSlots], named[kMaxSlots];
   uint64_t sum_full[kFinish], sum_empty[kFinish], listed;
-  uint32_t in_group[kFewGroups];
+  uint32_t in_group[kFewGroups];    // tokens of a group of chunks
+  uint32_t groups_of[kFewTokens];   // groups of a token
+  int scan[kMul];
   int units[kFewKinds], each[kFewKinds];  // units of a kind; of them for one tile or chunk
-  int cta_abort, chunks;
+  int cta_abort, chunks, per_group, groups;
   int ring_at, slot, sums_at, unit_at, lists_at;  // offsets into shared memory
 };
 extern __shared__ __align__(16) uint8_t few_smem[];
@@ -435,8 +460,6 @@ __device__ __forceinline__ Sums sums_of(Context& c) {
 __device__ __forceinline__ Lists lists_of(Context& c) {
   const int pairs = c.a.T * c.a.k;
   Lists ls;
-  ls.chunks = &c.chunks;
-  ls.in_group = c.in_group;
   ls.row_weight = reinterpret_cast<float*>(few_smem + c.lists_at);
   ls.tokens = reinterpret_cast<uint32_t*>(ls.row_weight + pairs);
   ls.expert = reinterpret_cast<uint16_t*>(ls.tokens + pairs);
@@ -558,12 +581,14 @@ __device__ __noinline__ int select_token(Row a, int lane) {
   return mine;
 }
 
-// Chunks of a group, for at most kFewGroups groups.
-__device__ __forceinline__ int group_chunks(int chunks) {
-  return max(1, (chunks + kFewGroups - 1) / kFewGroups);
-}
-__device__ __forceinline__ int group_count(int chunks) {
-  return (chunks + group_chunks(chunks) - 1) / group_chunks(chunks);
+// Chunks of a group: at most kFewGroups groups; more chunks to a group, up to a slot of
+// weights, as long as every CTA has four units.  Fewer and larger groups leave CTAs
+// without work at the end (32 tokens of 7168, 8 groups: 95 of 890 us), more and smaller
+// ones have more sums to store.
+__device__ __forceinline__ int group_chunks(const FewArgs& a, int chunks) {
+  const int least = max(1, (chunks + kFewGroups - 1) / kFewGroups);
+  const int whole = min(kFewColumns / a.I, chunks * (a.D / 32) / (4 * static_cast<int>(gridDim.x)));
+  return max(least, whole);
 }
 
 __device__ __forceinline__ void mul_sync() {
@@ -586,7 +611,10 @@ __device__ __noinline__ void build_lists(int tid) {
   const int lane = tid & 31, warp = tid >> 5, k = a.k, pairs = a.T * k;
 #pragma unroll 1
   for (int e = tid; e < a.E; e += kMul * 32) mask[e] = 0u;
-  if (tid < kFewGroups) ls.in_group[tid] = 0u;
+#pragma unroll 1
+  for (int p = tid; p < pairs; p += kMul * 32) ls.row_weight[p] = 0.f;
+  if (tid < kFewGroups) cx.in_group[tid] = 0u;
+  if (tid < kFewTokens) cx.groups_of[tid] = 0u;
   mul_sync();
   // a warp a token, lane j its choice j
 #pragma unroll 1
@@ -611,48 +639,60 @@ __device__ __noinline__ void build_lists(int tid) {
     }
   }
   mul_sync();
-  if (warp == 0) {
-    int rows = 0, chunks = 0;
+  // rows and chunks before a thread's experts, both below 2^16
+  const int each = (a.E + kMul * 32 - 1) / (kMul * 32), e0 = tid * each;
+  int sum = 0;
 #pragma unroll 1
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      uint32_t m = e < a.E ? mask[e] : 0u;
-      const int n = __popc(m), c = (n + kFewChunk - 1) / kFewChunk;
-      int sum = n | c << 16;  // rows and chunks before this expert, both below 2^16
+  for (int e = e0; e < min(e0 + each, a.E); ++e) {
+    const int n = __popc(mask[e]);
+    sum += n | (n + kFewChunk - 1) / kFewChunk << 16;
+  }
+  int before = -sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      int r = rows + (sum & 0xffff) - n, at = chunks + (sum >> 16) - c;
-      rows += __shfl_sync(0xffffffffu, sum, 31) & 0xffff;
-      chunks += __shfl_sync(0xffffffffu, sum, 31) >> 16;
-      if (e < a.E) base[e] = static_cast<uint16_t>(r);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  before += sum;
+  if (lane == 31) cx.scan[warp] = sum;
+  mul_sync();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kMul; ++w) {
+    const int v = cx.scan[w];
+    if (w < warp) before += v;
+    all += v;
+  }
+  const int chunks = all >> 16, per = group_chunks(a, chunks);
+  int at = before >> 16, r = before & 0xffff;
 #pragma unroll 1
-      for (; m; ++at, r += kFewChunk) {
-        const uint32_t first = m & (0u - m);
-        m ^= first;
-        const uint32_t second = m & (0u - m);
-        m ^= second;
-        ls.tokens[at] = first | second;
-        ls.expert[at] = static_cast<uint16_t>(e);
-        ls.row0[at] = static_cast<uint16_t>(r);
-      }
-    }
-    __syncwarp();
-    if (lane == 0) {
-      *ls.chunks = chunks;
-      cx.units[kFewGateUp] = chunks * (a.I / 16);
-      cx.units[kFewDown] = group_count(chunks) * (a.D / 32);
-      mbar_arrive(&cx.listed);  // the copies may start
+  for (int e = e0; e < min(e0 + each, a.E); ++e) {
+    base[e] = static_cast<uint16_t>(r);
+#pragma unroll 1
+    for (uint32_t m = mask[e]; m; ++at) {
+      const uint32_t first = m & (0u - m);
+      m ^= first;
+      const uint32_t second = m & (0u - m);
+      m ^= second;
+      ls.tokens[at] = first | second;
+      ls.expert[at] = static_cast<uint16_t>(e);
+      ls.row0[at] = static_cast<uint16_t>(r);
+      r += second ? 2 : 1;
+      const int group = at / per;
+      atomicOr(&cx.in_group[group], first | second);
+      atomicOr(&cx.groups_of[__ffs(first) - 1], 1u << group);
+      if (second) atomicOr(&cx.groups_of[__ffs(second) - 1], 1u << group);
     }
   }
-#pragma unroll 1
-  for (int p = tid; p < pairs; p += kMul * 32) ls.row_weight[p] = 0.f;
+  if (tid == 0) {
+    cx.chunks = chunks;
+    cx.per_group = per;
+    cx.groups = (chunks + per - 1) / per;
+    cx.units[kFewGateUp] = chunks * (a.I / 16);
+    cx.units[kFewDown] = cx.groups * (a.D / 32);
+  }
   mul_sync();
-  const int chunks = *ls.chunks, per = group_chunks(chunks);
-#pragma unroll 1
-  for (int i = tid; i < chunks; i += kMul * 32) atomicOr(&ls.in_group[i / per], ls.tokens[i]);
+  if (tid == 0) mbar_arrive(&cx.listed);  // the copies may start
   if (tid < a.T) {  // an expert that a token lists twice counts twice
 #pragma unroll 1
     for (int p = tid * k; p < (tid + 1) * k; ++p) {
@@ -731,9 +771,8 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
       h = Header{kind, 0, four ? q : r, (four ? r : q) * tile};
       end = h.which + 1;
       if (kind == kFewDown) {
-        const int per = group_chunks(*ls.chunks);
-        h.which *= per;
-        end = min(h.which + per, *ls.chunks);
+        h.which *= cx.per_group;
+        end = min(h.which + cx.per_group, cx.chunks);
       }
       K = length_of(a, kind);
     }
@@ -1120,30 +1159,39 @@ __device__ __forceinline__ void count_done(int32_t* c, int lane) {
 __device__ __noinline__ void combine(int n, int lane) {
   Context& cx = context();
   const FewArgs& a = cx.a;
-  const int groups = group_count(cx.chunks);
   const bool latent = a.L > 0;
   const float gain = latent && a.norm ? bf16_bits_to_f32(__ldg(a.lat_norm + n)) : 1.0f;
-  constexpr int kBatch = 2;  // tokens whose loads are on their way at a time
+  constexpr int kBatch = 2, kLoads = 8;  // tokens at a time, loads of each that are on their way
 #pragma unroll 1
   for (int t0 = 0; t0 < a.T; t0 += kBatch) {
-    float v[kBatch][kFewGroups], shared[kBatch];
+    uint32_t m[kBatch];
+    float total[kBatch], shared[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const bool there = t0 + i < a.T;
-#pragma unroll
-      for (int g = 0; g < kFewGroups; ++g) {
-        v[i][g] = 0.f;
-        if (there && g < groups && (cx.in_group[g] >> (t0 + i) & 1u))
-          v[i][g] = __ldcg(a.y + ((size_t)g * a.T + t0 + i) * a.D + n);
-      }
+      m[i] = there ? cx.groups_of[t0 + i] : 0u;
+      total[i] = 0.f;
       shared[i] = there && !latent && a.S > 0 ? __ldcg(a.ys + (size_t)(t0 + i) * a.H + n) : 0.f;
     }
+#pragma unroll 1
+    do {
+      float v[kBatch][kLoads];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) {
+          v[i][l] = 0.f;
+          if (m[i]) v[i][l] = __ldcg(a.y + ((size_t)(__ffs(m[i]) - 1) * a.T + t0 + i) * a.D + n);
+          m[i] &= m[i] - 1;
+        }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) total[i] += v[i][l];
+    } while (m[0] | m[1]);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      float sum = 0.f;
-#pragma unroll
-      for (int g = 0; g < kFewGroups; ++g) sum += v[i][g];
-      sum += shared[i];
+      const float sum = total[i] + shared[i];
       const int t = t0 + i;
       const float q = warp_sum(sum * sum);
       if (t >= a.T) break;
@@ -1174,6 +1222,7 @@ __device__ __noinline__ void finish(int buf, int lane) {
   const int r16 = lane & 15, half = lane >> 4;
   float* unit = sums.unit + buf * a.T * 32 + lane;  // a token's 32 columns
   bool first = true;  // segment of a down projection's unit
+  const float x_unit = a.L == 0 && lane < a.T ? __ldcg(a.x_unit + lane) : 1.f;  // of token `lane`
 #pragma unroll 1
   for (uint32_t n = 0;; ++n) {
     if (!wait_for<kRest>(&sums.full[buf], n & 1u, wt)) return;
@@ -1202,7 +1251,7 @@ __device__ __noinline__ void finish(int buf, int lane) {
         if (pair) {
           float g = v, u = other;
           if (kind == kFewGateUp && a.L == 0) {
-            const float scale = __ldcg(a.x_unit + t);
+            const float scale = __shfl_sync(0xffffffffu, x_unit, t);
             g *= scale;
             u *= scale;
           }
@@ -1253,9 +1302,9 @@ __device__ __noinline__ void finish(int buf, int lane) {
     if (kind == kFewDown) {
       first = (h.kind & kLastSegment) != 0;
       if (!first) continue;
-      const int group = h.which / group_chunks(*ls.chunks);
+      const int group = h.which / cx.per_group;
 #pragma unroll 1
-      for (uint32_t m = ls.in_group[group]; m; m &= m - 1) {
+      for (uint32_t m = cx.in_group[group]; m; m &= m - 1) {
         const int t = __ffs(m) - 1;
         a.y[((size_t)group * a.T + t) * a.D + c] = unit[t * 32];
       }
@@ -1264,7 +1313,7 @@ __device__ __noinline__ void finish(int buf, int lane) {
     const bool whole = a.L > 0 && kind != kFewDown;  // a tile of the latent layer's output
     int32_t* done = whole ? out_done + h.n0 / 32 * halves + h.which : tile_done + h.n0 / 32;
     const int all = whole ? (a.S > 0 ? 2 : 1)
-                          : group_count(*ls.chunks) + (a.S > 0 && a.L == 0 ? halves : 0);
+                          : cx.groups + (a.S > 0 && a.L == 0 ? halves : 0);
     __syncwarp();
     int old = 0;
     if (lane == 0) old = add_acq_rel(done, 1);

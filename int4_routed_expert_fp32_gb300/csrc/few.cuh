@@ -14,7 +14,7 @@ constexpr int kFewChunk = 2;    // tokens that share one pass over an expert's w
 constexpr int kFewRows = 8;     // tokens that share one pass over bf16 weights (4 in two parts)
 constexpr int kFewColumns = 2048;  // int4 columns of a ring slot
 
-constexpr int kFewGroups = 8;   // groups of chunks whose outputs are summed before they are stored
+constexpr int kFewGroups = 32;   // groups of chunks whose outputs are summed before they are stored
 
 // Kinds of work units.  A unit is 32 weight rows (16 gate rows and the 16 up rows of
 // the same columns) times the tokens of one chunk; a down projection's takes a group of chunks one after another.
@@ -58,7 +58,7 @@ struct FewArgs {
   uint8_t* x16;      // [T] rows of fp16 blocks (below): x times a power of two, or u
   float* x_unit;     // fp32 [T]: what one unit of x16 stands for
   uint8_t* h16;      // [T k] rows of fp16 blocks
-  float* y;          // fp32 [kFewGroups, T, D]: weighted sums of the chunks of a group
+  float* y;          // fp32 [groups, T, D]: weighted sums of the chunks of a group
   uint16_t* hs;      // bf16 [2, T, S]: high and low parts of the shared expert's h
   float* ys;         // fp32 [T, H] shared expert's output
   uint16_t* z;       // bf16 [2, T, L]: high and low parts of the combined rows times the gain

@@ -28,7 +28,7 @@ size_t carve(FewArgs* a, void* base) {
   a->x16 = static_cast<uint8_t*>(take(T * few_row_bytes(a->D)));
   a->x_unit = static_cast<float*>(take(4 * T));
   a->h16 = static_cast<uint8_t*>(take(P * few_row_bytes(a->I)));
-  a->y = static_cast<float*>(take(4 * kFewGroups * T * D));
+  a->y = static_cast<float*>(take(4 * (P < kFewGroups ? P : kFewGroups) * T * D));
   a->hs = static_cast<uint16_t*>(take(4 * T * S));
   a->ys = static_cast<float*>(take(S ? 4 * T * H : 0));
   a->z = static_cast<uint16_t*>(take(4 * T * L));
