@@ -1153,61 +1153,85 @@ __device__ __forceinline__ void count_done(int32_t* c, int lane) {
   if (lane == 0) add_release(c, 1);
 }
 
-// Column n (of this lane) of every token: the groups' sums, in order, whichever order they
+// 32 columns from n0 on of every token: the groups' sums, in order, whichever order they
 // were computed in, and the shared expert's; for the latent path as two bf16 parts
-// with the gain, and their squares summed over the 32 columns.
-__device__ __noinline__ void combine(int n, int lane) {
+// with the gain, and their squares summed over the 32 columns.  Eight lanes have a token,
+// four columns each: what the last unit of a call is waited for by (32 tokens two at a
+// time, a column a lane: 28 us at the end of a call; 16 tokens: 12, now XX).
+__device__ __noinline__ void combine(int n0, int lane) {
   Context& cx = context();
   const FewArgs& a = cx.a;
   const bool latent = a.L > 0;
-  const float gain = latent && a.norm ? bf16_bits_to_f32(__ldg(a.lat_norm + n)) : 1.0f;
-  constexpr int kBatch = 2, kLoads = 8;  // tokens at a time, loads of each that are on their way
+  const int n = n0 + 4 * (lane & 7);
+  constexpr int kLoads = 8;  // on their way at a time
 #pragma unroll 1
-  for (int t0 = 0; t0 < a.T; t0 += kBatch) {
-    uint32_t m[kBatch];
-    float total[kBatch], shared[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const bool there = t0 + i < a.T;
-      m[i] = there ? cx.groups_of[t0 + i] : 0u;
-      total[i] = 0.f;
-      shared[i] = there && !latent && a.S > 0 ? __ldcg(a.ys + (size_t)(t0 + i) * a.H + n) : 0.f;
-    }
+  for (int t0 = 0; t0 < a.T; t0 += 4) {
+    const int t = t0 + (lane >> 3);
+    const bool there = t < a.T;
+    uint32_t m = there ? cx.groups_of[t] : 0u;
+    const float* y = a.y + (size_t)t * a.D + n;
+    const size_t next = (size_t)a.T * a.D;  // group
+    float4 shared = make_float4(0.f, 0.f, 0.f, 0.f), sum = shared;
+    if (there && !latent && a.S > 0)
+      shared = __ldcg(reinterpret_cast<const float4*>(a.ys + (size_t)t * a.H + n));
 #pragma unroll 1
     do {
-      float v[kBatch][kLoads];
+      float4 v[kLoads];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l) {
-          v[i][l] = 0.f;
-          if (m[i]) v[i][l] = __ldcg(a.y + ((size_t)(__ffs(m[i]) - 1) * a.T + t0 + i) * a.D + n);
-          m[i] &= m[i] - 1;
-        }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l) total[i] += v[i][l];
-    } while (m[0] | m[1]);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float sum = total[i] + shared[i];
-      const int t = t0 + i;
-      const float q = warp_sum(sum * sum);
-      if (t >= a.T) break;
-      if (!latent) {
-        a.out[(size_t)t * a.H + n] = f32_to_bf16_bits(sum);
-      } else {
-        if (lane == 0) a.ssq[(size_t)(n / 32) * a.T + t] = q;
-        // 16 bits of significand
-        uint16_t* p = a.z + (size_t)t * a.L + n;
-        const uint16_t high = f32_to_bf16_bits(sum * gain);
-        p[0] = high;
-        p[(size_t)a.T * a.L] = f32_to_bf16_bits(sum * gain - bf16_bits_to_f32(high));
+      for (int l = 0; l < kLoads; ++l) {
+        v[l] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (m) v[l] = __ldcg(reinterpret_cast<const float4*>(y + (__ffs(m) - 1) * next));
+        m &= m - 1;
       }
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) {
+        sum.x += v[l].x;
+        sum.y += v[l].y;
+        sum.z += v[l].z;
+        sum.w += v[l].w;
+      }
+    } while (__any_sync(0xffffffffu, m != 0u));
+    float r[4] = {sum.x + shared.x, sum.y + shared.y, sum.z + shared.z, sum.w + shared.w};
+    if (!latent) {
+      if (there)
+        *reinterpret_cast<uint2*>(a.out + (size_t)t * a.H + n) =
+            make_uint2(f32_to_bf16_bits(r[0]) | static_cast<uint32_t>(f32_to_bf16_bits(r[1])) << 16,
+                       f32_to_bf16_bits(r[2]) | static_cast<uint32_t>(f32_to_bf16_bits(r[3])) << 16);
+      continue;
     }
+    float q = fmaf(r[0], r[0], fmaf(r[1], r[1], fmaf(r[2], r[2], r[3] * r[3])));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+    if (!there) continue;
+    if (!(lane & 7)) a.ssq[(size_t)(n0 / 32) * a.T + t] = q;
+    uint32_t high[4], low[4];  // 16 bits of significand
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (a.norm) r[i] *= bf16_bits_to_f32(__ldg(a.lat_norm + n + i));
+      high[i] = f32_to_bf16_bits(r[i]);
+      low[i] = f32_to_bf16_bits(r[i] - bf16_bits_to_f32(static_cast<uint16_t>(high[i])));
+    }
+    uint16_t* z = a.z + (size_t)t * a.L + n;
+    *reinterpret_cast<uint2*>(z) = make_uint2(high[0] | high[1] << 16, high[2] | high[3] << 16);
+    *reinterpret_cast<uint2*>(z + (size_t)a.T * a.L) =
+        make_uint2(low[0] | low[1] << 16, low[2] | low[3] << 16);
   }
   if (latent) count_done(a.counters + 3, lane);
+}
+
+// What the rows of the latent layer's norm are divided by: lane t gets token t's.
+__device__ __noinline__ float norms(int lane) {
+  const FewArgs& a = context().a;
+  float mine = 0.f;
+#pragma unroll 2
+  for (int t = 0; t < a.T; ++t) {
+    float q = 0.f;
+#pragma unroll 4
+    for (int j = lane; j < a.L / 32; j += 32) q += __ldcg(a.ssq + (size_t)j * a.T + t);
+    q = warp_sum(q);
+    if (lane == t) mine = rsqrtf(q / static_cast<float>(a.L) + a.eps);
+  }
+  return mine;
 }
 
 __device__ __noinline__ void finish(int buf, int lane) {
@@ -1222,6 +1246,8 @@ __device__ __noinline__ void finish(int buf, int lane) {
   const int r16 = lane & 15, half = lane >> 4;
   float* unit = sums.unit + buf * a.T * 32 + lane;  // a token's 32 columns
   bool first = true;  // segment of a down projection's unit
+  bool normed = false;
+  float norm = 1.f;  // of token `lane`
   const float x_unit = a.L == 0 && lane < a.T ? __ldcg(a.x_unit + lane) : 1.f;  // of token `lane`
 #pragma unroll 1
   for (uint32_t n = 0;; ++n) {
@@ -1234,6 +1260,10 @@ __device__ __noinline__ void finish(int buf, int lane) {
     const int token0 = h.which * few_rows_of(kind);
     const uint32_t tokens = four ? ls.tokens[h.which] : 0u;
     const int row0 = four ? ls.row0[h.which] : 0;
+    if (kind == kFewLatUp && a.norm && !normed) {  // every sum of squares is there by now
+      norm = norms(lane);
+      normed = true;
+    }
     if (kind == kFewDown && first) {
 #pragma unroll 1
       for (int t = 0; t < a.T; ++t) unit[t * 32] = 0.f;
@@ -1282,14 +1312,16 @@ __device__ __noinline__ void finish(int buf, int lane) {
       } else if (kind == kFewDown) {
         unit[t * 32] = fmaf(ls.row_weight[row0 + i], v, unit[t * 32]);
       } else {
-        float scale = 1.0f;
-        if (kind == kFewLatUp && a.norm) {
-          float q = 0.f;
-#pragma unroll 1
-          for (int j = lane; j < a.L / 32; j += 32) q += __ldcg(a.ssq + (size_t)j * a.T + t);
-          scale = rsqrtf(warp_sum(q) / static_cast<float>(a.L) + a.eps);
+        const size_t at = (size_t)t * a.H + c;
+        if (kind == kFewLatUp) {
+          if (a.norm) v *= __shfl_sync(0xffffffffu, norm, t);
+          if (a.S == 0)
+            a.out[at] = f32_to_bf16_bits(v);
+          else
+            a.yl[at] = v;
+        } else {
+          a.ys[at] = v;
         }
-        (kind == kFewLatUp ? a.yl : a.ys)[(size_t)t * a.H + c] = v * scale;
       }
     }
     __syncwarp();
@@ -1309,10 +1341,11 @@ __device__ __noinline__ void finish(int buf, int lane) {
         a.y[((size_t)group * a.T + t) * a.D + c] = unit[t * 32];
       }
     }
+    if (kind == kFewLatUp && a.S == 0) continue;
     // whoever brings the last contribution to 32 columns reads them all
     const bool whole = a.L > 0 && kind != kFewDown;  // a tile of the latent layer's output
     int32_t* done = whole ? out_done + h.n0 / 32 * halves + h.which : tile_done + h.n0 / 32;
-    const int all = whole ? (a.S > 0 ? 2 : 1)
+    const int all = whole ? 2
                           : cx.groups + (a.S > 0 && a.L == 0 ? halves : 0);
     __syncwarp();
     int old = 0;
@@ -1321,15 +1354,13 @@ __device__ __noinline__ void finish(int buf, int lane) {
     if (old != all - 1) continue;
     __threadfence();
     if (!whole) {
-      combine(c, lane);
+      combine(h.n0, lane);
       continue;
     }
 #pragma unroll 1
     for (int i = 0; i < h.rows(); ++i) {
       const size_t at = (size_t)(token0 + i) * a.H + c;
-      float v = __ldcg(a.yl + at);
-      if (a.S > 0) v += __ldcg(a.ys + at);
-      a.out[at] = f32_to_bf16_bits(v);
+      a.out[at] = f32_to_bf16_bits(__ldcg(a.yl + at) + __ldcg(a.ys + at));
     }
   }
 }

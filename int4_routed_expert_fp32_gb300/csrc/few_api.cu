@@ -33,7 +33,7 @@ size_t carve(FewArgs* a, void* base) {
   a->ys = static_cast<float*>(take(S ? 4 * T * H : 0));
   a->z = static_cast<uint16_t*>(take(4 * T * L));
   a->ssq = static_cast<float*>(take(4 * T * (L / 32)));
-  a->yl = static_cast<float*>(take(L ? 4 * T * H : 0));
+  a->yl = static_cast<float*>(take(L && S ? 4 * T * H : 0));
   return off;
 }
 
