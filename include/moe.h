@@ -622,8 +622,8 @@ int moe_int4_matvec(const uint16_t* x, int64_t x_ld, const int32_t* w_packed,
  *   topk_w    fp32 [T, k]
  *   weights   as moe_expert_ffn, act_bits 16
  * Each chosen expert's weights are read once for every 2 tokens that chose it.
- * Equal calls give equal bits.  D % 64 == 0, I % 64 == 0, E <= 2048, k <= min(E, 32), else
- * MOE_ERR_UNSUPPORTED.  x, out and packed weights 16-byte aligned, ws 256; out and ws
+ * Equal calls give equal bits.  D % 64 == 0, I % 64 == 0, both at most 2^20, E <= 2048,
+ * k <= min(E, 32), else MOE_ERR_UNSUPPORTED.  x, out and packed weights 16-byte aligned, ws 256; out and ws
  * share no byte with each other or with an input, else MOE_ERR_INVALID. */
 size_t moe_experts_few_workspace_size(int T, int D, int E, int k, int I);
 int moe_experts_few(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, int T, int D,
@@ -698,8 +698,8 @@ int moe_adapter_linear_stall_selftest(const uint16_t* x, const uint16_t* w, cons
                                       void* ws, size_t ws_bytes, void* stream);
 
 /* For tests: the exit paths of the few tokens' kernel.  Runs moe_experts_few (same
- * arguments) with a build of it whose weight copies stop before stage `stall_stage`
- * (counted per CTA from 0), and every wait limited to `limit_ns` (1e3 .. 5e9).  The
+ * arguments) with weight copies that stop before slot `stall_stage` of every CTA (counted
+ * from 0; an argument of the kernel that other calls give as -1), and every wait limited to `limit_ns` (1e3 .. 5e9).  The
  * call records MOE_ERR_TIMEOUT and out is not valid; later calls run normally. */
 int moe_experts_few_stall_selftest(const uint16_t* x, const int32_t* topk_idx, const float* topk_w,
                                    int T, int D, int E, int k, int I, const int32_t* gate_packed,

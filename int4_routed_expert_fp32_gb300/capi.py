@@ -49,6 +49,9 @@ class MoeWeights(ctypes.Structure):
         "shared_down", "router_w_terms")]
 
 
+WEIGHT_NAMES = tuple(n for n, _ in MoeWeights._fields_)
+
+
 class MoeRouteConfig(ctypes.Structure):
     _fields_ = [("E", c_int32), ("k", c_int32), ("score", c_int32), ("groups", c_int32),
                 ("topk_groups", c_int32), ("group_score", c_int32), ("renorm", c_int32),
@@ -886,9 +889,9 @@ def experts_few(topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
 def experts_few_stall_selftest(topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
                                experts: Dict[str, torch.Tensor], stall_stage: int,
                                limit_ns: int) -> None:
-    """Run experts_few with a build of its kernel whose weight copies stop before stage
-    ``stall_stage`` (tests of the exit paths; the device records MOE_ERR_TIMEOUT,
-    read with check_error())."""
+    """Run experts_few with weight copies that stop before the ``stall_stage``-th slot of
+    each CTA (tests of the exit paths; the device records MOE_ERR_TIMEOUT, read with
+    check_error())."""
     T, D, E, k, I, w, dev = _few_args(topk_idx, topk_w, x, experts, None)
     out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
     need = lib.moe_experts_few_workspace_size(T, D, E, k, I)
@@ -916,16 +919,20 @@ def layer_few(x: torch.Tensor, weights: Dict[str, torch.Tensor], k: int, renorm:
         for n in names:
             if not there and weights.get(n) is not None:
                 raise ValueError(f"{n} needs {of}")
-    w = {n: t for n, t in weights.items() if t is not None}
+    w = [weights.get(n) for n in WEIGHT_NAMES]
     if out is not None:
         _arg("out", out, (T, H), torch.bfloat16)
-    dev = _device_of((x, out, *w.values()), ("x", "out", *w))
+    dev = _device_of((x, out, *w), ("x", "out", *WEIGHT_NAMES))
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     else:
-        _apart("out", out, x=x, **w)
-    cfg = MoeConfig(T, H, E, k, I, L, 16, int(renorm), eps, S)
-    ptrs = MoeWeights(*[w[n].data_ptr() if n in w else None for n, _ in MoeWeights._fields_])
+        _apart("out", out, x=x, **dict(zip(WEIGHT_NAMES, w)))
+    ptrs = MoeWeights(*[None if t is None else t.data_ptr() for t in w])
+    return _layer_few(MoeConfig(T, H, E, k, I, L, 16, int(renorm), eps, S), ptrs, x, out, dev)
+
+
+def _layer_few(cfg: MoeConfig, ptrs: MoeWeights, x: torch.Tensor, out: torch.Tensor,
+               dev: torch.device) -> torch.Tensor:
     need = lib.moe_layer_few_workspace_size(ctypes.byref(cfg))
     ws = torch.empty(need or 256, dtype=torch.uint8, device=dev)
     rc = lib.moe_layer_few(ctypes.byref(cfg), ctypes.byref(ptrs), x.data_ptr(), out.data_ptr(),
@@ -995,10 +1002,16 @@ class MoeLayer:
         if self.cfg.act_bits != 16:
             raise ValueError("forward_few needs act_bits 16")
         c = self.cfg
-        drop = set() if c.L else {"lat_down", "lat_up", "lat_norm"}
-        drop |= set() if c.I_shared else {"shared_gate", "shared_up", "shared_down"}
-        return layer_few(x, {n: t for n, t in self.weights.items() if n not in drop}, c.k,
-                         renorm=bool(c.renorm), eps=c.eps, out=out)
+        T = _arg("x", x, (None, c.H), torch.bfloat16).shape[0]
+        if out is not None:
+            _arg("out", out, (T, c.H), torch.bfloat16)
+        dev = _device_of((x, out), ("x", "out"))
+        if dev != self.device:
+            raise ValueError(f"x is on {dev}; the layer's weights are on {self.device}")
+        if out is None:
+            out = torch.empty_like(x)
+        cfg = MoeConfig(T, c.H, c.E, c.k, c.I, c.L, 16, c.renorm, c.eps, c.I_shared)
+        return _layer_few(cfg, self.wstruct, x, out, dev)
 
     def forward_host(self, x_host: torch.Tensor, out_host: torch.Tensor) -> None:
         """x_host / out_host: CPU bf16 [T, H] (pinned for asynchronous copies)."""
@@ -1125,7 +1138,7 @@ def _check_layer_weights(w: Dict[str, torch.Tensor], H: int, E: int, I: int, L: 
     """Every pointer of moe_weights against the layout the configuration
     implies (the experts read the latent width L when L > 0)."""
     bf16 = torch.bfloat16
-    extra = set(w) - {n for n, _ in MoeWeights._fields_}
+    extra = set(w).difference(WEIGHT_NAMES)
     if extra:
         raise ValueError(f"unknown weight names: {sorted(extra)}")
     _arg("router_w", w.get("router_w"), (E, H), torch.float32)

@@ -6,12 +6,12 @@
 //
 //   few_front_kernel   the router's logits (one pass over its fp32 weight), x as
 //                      fp16 in the order of the packed nibbles, counters to zero
-//   few_kernel         one persistent CTA per SM.  Every CTA selects the experts
+//   few_kernel         two persistent CTAs per SM.  Every CTA selects the experts
 //                      (the same arithmetic everywhere, cheaper than another
 //                      launch), then takes units of work in ticket order: 16
-//                      gate rows and the 16 up rows of the same columns, or 32
-//                      rows of a down projection, times the tokens (at most 4)
-//                      of one chunk of one expert.
+//                      gate rows and the 16 up rows of the same columns, times the
+//                      tokens (at most 2) of one chunk of one expert, or 32 rows of
+//                      the down projections of a group of chunks, one after another.
 //
 // Tickets are taken in the order of the units, and a unit waits only for units
 // with lower tickets (a down projection for its expert's h).  Those are held by
@@ -20,16 +20,23 @@
 //
 // Roles of a CTA: warp 0 copies weights into a ring (TMA), warp 1 their scales and the
 // tokens' rows (once the units they wait for are done), the last eight multiply, and
-// two between them take the finished segments in turn.  Twelve warps leave the
-// products the registers that they need.  The ring runs on
-// across units and phases, so the weights of a down projection arrive while
-// its h is still being computed.
+// two between them take the finished segments in turn.  Twelve warps and two CTAs leave
+// 80 registers to a thread.  The ring runs on across units and phases, so the weights of
+// a down projection arrive while its h is still being computed.  A slot holds 36 KB: half
+// as much, in twice as many slots, costs more at every slot than it hides (32 tokens, 384
+// experts of 7168 x 2048: 991 us against 850).
 //
-// The products use m16n8k16 MMAs: 16 weight rows, 8 tokens.  At 8 tokens a
+// The products use m16n8k16 MMAs: 16 weight rows, 8 columns.  At 8 tokens a
 // weight byte is worth 32 operations, a hundredth of what would make the tensor
 // cores matter; the cost is the conversion of the nibbles, the same for
 // any MMA, and tcgen05 would add the trip of the converted weights through
-// shared or tensor memory.
+// shared or tensor memory.  An SM takes 1100 cycles for a slot's products (an MMA of
+// this form 8 cycles of a quarter of it, the logic operations that turn nibbles into fp16
+// 2 each), HBM 1570: near enough to one another that they do not overlap fully.
+//
+// Measured (graphs of calls; behind it the bytes at the measured copy rate): the layer of
+// one token, 8 of 384 experts, 7168 x 2048: 53 us, 31; of 32 tokens: 850 us, 689; 6 tokens of 3584 x 1024, experts alone: 51 us, 20; 16 tokens of 256 x 128:
+// 26 us, the latency of its steps.
 #include "few.cuh"
 
 #include <cuda_fp16.h>
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kFrontThreads) few_front_kernel(const FewArgs 
         }
       }
       // kFrontTokens at a time, their loads on the way together (32 tokens, 384 experts of
-      // 7168: 23 us two at a time, XX four)
+      // 7168: 23 us two at a time, 14 four)
 #pragma unroll 1
       for (int t0 = 0; t0 < a.T; t0 += kFrontTokens) {
         float z[kFrontTokens * kFrontExperts] = {};
@@ -1157,7 +1164,7 @@ __device__ __forceinline__ void count_done(int32_t* c, int lane) {
 // were computed in, and the shared expert's; for the latent path as two bf16 parts
 // with the gain, and their squares summed over the 32 columns.  Eight lanes have a token,
 // four columns each: what the last unit of a call is waited for by (32 tokens two at a
-// time, a column a lane: 28 us at the end of a call; 16 tokens: 12, now XX).
+// time, a column a lane: 28 us at the end of a call, so 15; 16 tokens: 12 and 8).
 __device__ __noinline__ void combine(int n0, int lane) {
   Context& cx = context();
   const FewArgs& a = cx.a;
@@ -1222,16 +1229,23 @@ __device__ __noinline__ void combine(int n0, int lane) {
 // What the rows of the latent layer's norm are divided by: lane t gets token t's.
 __device__ __noinline__ float norms(int lane) {
   const FewArgs& a = context().a;
-  float mine = 0.f;
-#pragma unroll 2
-  for (int t = 0; t < a.T; ++t) {
-    float q = 0.f;
-#pragma unroll 4
-    for (int j = lane; j < a.L / 32; j += 32) q += __ldcg(a.ssq + (size_t)j * a.T + t);
-    q = warp_sum(q);
-    if (lane == t) mine = rsqrtf(q / static_cast<float>(a.L) + a.eps);
+  int lanes = 1;  // of a row of sums, a power of two: lane t has token t % lanes
+  while (lanes < a.T) lanes *= 2;
+  const int t = lane & (lanes - 1), step = 32 / lanes;
+  constexpr int kLoads = 8;
+  float q = 0.f;
+#pragma unroll 1
+  for (int j = lane / lanes; j < a.L / 32; j += kLoads * step) {
+    float v[kLoads];
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l)
+      v[l] = t < a.T && j + l * step < a.L / 32 ? __ldcg(a.ssq + (size_t)(j + l * step) * a.T + t) : 0.f;
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) q += v[l];
   }
-  return mine;
+#pragma unroll 1
+  for (int o = lanes; o < 32; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+  return rsqrtf(q / static_cast<float>(a.L) + a.eps);
 }
 
 __device__ __noinline__ void finish(int buf, int lane) {

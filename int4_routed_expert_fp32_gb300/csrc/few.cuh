@@ -9,12 +9,13 @@
 
 namespace moe {
 
+constexpr int kFewWidth = 1 << 20;  // largest width: units are counted in 32 bits
 constexpr int kFewTokens = 32;  // tokens of a call: one bit each in an expert's mask
 constexpr int kFewChunk = 2;    // tokens that share one pass over an expert's weights
 constexpr int kFewRows = 8;     // tokens that share one pass over bf16 weights (4 in two parts)
 constexpr int kFewColumns = 2048;  // int4 columns of a ring slot
 
-constexpr int kFewGroups = 32;   // groups of chunks whose outputs are summed before they are stored
+constexpr int kFewGroups = 32;  // groups of chunks whose outputs are summed before they are stored
 
 // Kinds of work units.  A unit is 32 weight rows (16 gate rows and the 16 up rows of
 // the same columns) times the tokens of one chunk; a down projection's takes a group of chunks one after another.

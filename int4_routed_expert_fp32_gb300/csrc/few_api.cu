@@ -41,8 +41,8 @@ bool sizes_ok(int T, int D, int E, int k, int I, int* rc) {
   *rc = MOE_ERR_INVALID;
   if (T < 0 || D <= 0 || E <= 0 || k <= 0 || I <= 0) return false;
   *rc = MOE_ERR_UNSUPPORTED;
-  return T <= kFewTokens && D % 64 == 0 && I % 64 == 0 && E <= kMaxExperts && k <= E &&
-         k <= kMaxTopK;
+  return T <= kFewTokens && D % 64 == 0 && I % 64 == 0 && D <= kFewWidth && I <= kFewWidth &&
+         E <= kMaxExperts && k <= E && k <= kMaxTopK;
 }
 
 // Weights [n, rows, K] of 4 bits (words) or bf16 as [n, pieces, rows, 128 bytes]:
@@ -241,7 +241,9 @@ static bool layer_sizes(const moe_config* c, FewArgs* a, int* rc) {
   if (!c || c->H <= 0 || c->L < 0 || c->I_shared < 0 || !(c->eps >= 0.f)) return false;
   if (!sizes_ok(c->T, c->L > 0 ? c->L : c->H, c->E, c->k, c->I, rc)) return false;
   *rc = MOE_ERR_UNSUPPORTED;
-  if (c->H % 64 || c->I_shared % 64 || c->act_bits != 16) return false;
+  if (c->H % 64 || c->I_shared % 64 || c->H > kFewWidth || c->I_shared > kFewWidth ||
+      c->act_bits != 16)
+    return false;
   a->T = c->T;
   a->H = c->H;
   a->E = c->E;

@@ -20,6 +20,8 @@
 // reads of shared memory cost more than the weights' own for 16 tokens.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "adapter.cuh"
 #include "common.cuh"
 
@@ -452,27 +454,28 @@ __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const MatvecAr
   if (a.ranks > 1) cluster_sync_all();  // until every CTA has read this one's sums
 }
 
-// Clusters of 1, 2, 4 and 8 CTAs that the device holds at a time with two CTAs to an SM.
+// n[i]: clusters of 2^i CTAs that the device holds at a time with two CTAs to an SM, asked
+// once for a device; a question that fails is an error and is not kept.
 template <int NB, bool kScales8>
-const int* clusters_at_once() {
-  static const struct Held {
-    int n[4] = {0, 0, 0, 0};
-    Held() {
-      for (int i = 0; i < 4; ++i) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(kMostCluster);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kPerSm;
-        cudaLaunchAttribute attr[2];
-        set_adapter_attrs(&cfg, attr, 1 << i);
-        if (cudaOccupancyMaxActiveClusters(&n[i], int4_matvec_kernel<NB, kScales8>, &cfg) != cudaSuccess) {
-          cudaGetLastError();
-          n[i] = 0;
-        }
-      }
-    }
-  } held;
-  return held.n;
+cudaError_t clusters_at_once(int (&n)[4]) {
+  constexpr int kDevices = 32;
+  static std::atomic<int> known[kDevices][4];
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+    n[i] = device < kDevices ? known[device][i].load(std::memory_order_relaxed) : 0;
+    if (n[i] > 0) continue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kMostCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kPerSm;
+    cudaLaunchAttribute attr[2];
+    set_adapter_attrs(&cfg, attr, 1 << i);
+    e = cudaOccupancyMaxActiveClusters(&n[i], int4_matvec_kernel<NB, kScales8>, &cfg);
+    if (e == cudaSuccess && device < kDevices)
+      known[device][i].store(n[i], std::memory_order_relaxed);
+  }
+  return e;
 }
 
 // How the work is cut.  For each number of CTAs that share the columns (ranks) and of
@@ -487,7 +490,8 @@ int launch(MatvecArgs a, cudaStream_t st) {
   auto kern = int4_matvec_kernel<NB, kScales8>;
   MOE_TRY_CUDA(adapter_smem(reinterpret_cast<const void*>(kern)));
   const int joined[4] = {0, 5, 8, 12};
-  const int* held = (clusters_at_once<NB, kScales8>());
+  int held[4];
+  MOE_TRY_CUDA((clusters_at_once<NB, kScales8>(held)));
   const int steps = (a.K + 127) / 128, n_blocks = (a.N + kRows - 1) / kRows;
   MatvecArgs best = a;
   int64_t least = INT64_MAX;

@@ -138,7 +138,8 @@ def experts_args(capi, **kw):
 SIZES = [(dict(T=-1), "INVALID"), (dict(D=0), "INVALID"), (dict(E=0), "INVALID"),
          (dict(k=0), "INVALID"), (dict(I=0), "INVALID"), (dict(T=33), "UNSUPPORTED"),
          (dict(D=96), "UNSUPPORTED"), (dict(I=96), "UNSUPPORTED"), (dict(E=2049), "UNSUPPORTED"),
-         (dict(k=5), "UNSUPPORTED"), (dict(E=64, k=33), "UNSUPPORTED")]
+         (dict(k=5), "UNSUPPORTED"), (dict(E=64, k=33), "UNSUPPORTED"),
+         (dict(D=(1 << 20) + 64), "UNSUPPORTED"), (dict(I=(1 << 20) + 64), "UNSUPPORTED")]
 
 
 @pytest.mark.parametrize("kw,code", SIZES + [
@@ -191,7 +192,9 @@ def layer_call(capi, cfg=None, weights=None, x=FAKE, out=FAKE << 20, ws=FAKE << 
                                      for s, c in SIZES] + [
     (dict(H=0), "INVALID"), (dict(L=-64), "INVALID"), (dict(I_shared=-1), "INVALID"),
     (dict(eps=-1.0), "INVALID"), (dict(eps=float("nan")), "INVALID"), (dict(H=96), "UNSUPPORTED"),
-    (dict(L=32), "UNSUPPORTED"), (dict(I_shared=32), "UNSUPPORTED"),
+    (dict(L=32), "UNSUPPORTED"),
+    (dict(H=(1 << 20) + 64), "UNSUPPORTED"), (dict(L=(1 << 20) + 64), "UNSUPPORTED"),
+    (dict(I_shared=(1 << 20) + 64), "UNSUPPORTED"), (dict(I_shared=32), "UNSUPPORTED"),
     (dict(act_bits=8), "UNSUPPORTED")])
 def test_layer_size_refusals(capi, kw, code):
     n = capi.launch_count()
@@ -220,17 +223,22 @@ def test_layer_pointer_refusals(capi):
     assert capi.launch_count() == n
 
 
-def test_layer_object_and_block(capi, monkeypatch):
-    """forward_few hands layer_few the weights of the layer's own parts, and refuses
-    8-bit activations."""
+def test_layer_object(capi, monkeypatch):
+    """forward_few hands on the layer's own weights and sizes with the call's tokens, and
+    refuses 8-bit activations, another width and host tensors."""
     L = capi.MoeLayer.__new__(capi.MoeLayer)
-    L.weights = layer(L=64, S=64)
+    L.wstruct, L.device = capi.MoeWeights(), torch.device("cpu")
+    L.cfg = capi.MoeConfig(100, 64, 4, 2, 128, 64, 16, 0, 1e-5, 64)
+    raises(CUDA_ONLY, L.forward_few, bf16(3, 64))
+    raises("x: expected shape", L.forward_few, bf16(3, 128))
+    raises("out: expected shape", L.forward_few, bf16(3, 64), out=bf16(100, 64))
     seen = []
-    monkeypatch.setattr(capi, "layer_few", lambda x, w, k, **o: seen.append((sorted(w), k, o)))
-    for lat, shared in ((64, 64), (0, 0)):
-        L.cfg = capi.MoeConfig(100, 64, 4, 2, 128, lat, 16, 0, 1e-5, shared)
-        L.forward_few(bf16(3, 64))
-    assert seen[0][0] == sorted(L.weights) and seen[1][0] == sorted(layer())
-    assert seen[0][1] == 2 and seen[0][2]["renorm"] is False
+    monkeypatch.setattr(capi, "_device_of", lambda *a: torch.device("cpu"))
+    monkeypatch.setattr(capi, "_layer_few", lambda cfg, w, x, out, dev: seen.append((cfg, w, out)))
+    L.forward_few(bf16(3, 64))
+    cfg, w, out = seen[0]
+    got = [getattr(cfg, n) for n, _ in capi.MoeConfig._fields_]
+    want = [getattr(L.cfg, n) for n, _ in capi.MoeConfig._fields_]
+    assert cfg.T == 3 and got[1:] == want[1:] and w is L.wstruct and out.shape == (3, 64)
     L.cfg.act_bits = 8
     raises("act_bits 16", L.forward_few, bf16(3, 64))
