@@ -326,9 +326,10 @@ EXPERT_NAMES = ("gate_packed", "gate_scale", "up_packed", "up_scale", "down_pack
 
 def _experts(experts: Dict[str, torch.Tensor], E: int, D: int, I: int) -> None:
     """Gate/up [E, I, D/8] + [E, I, D/32]; down [E, D, I/8] + [E, D, I/32]."""
-    for proj, (N, K) in (("gate", (I, D)), ("up", (I, D)), ("down", (D, I))):
-        _arg(f"{proj}_packed", experts.get(f"{proj}_packed"), (E, N, K // 8), torch.int32)
-        _arg(f"{proj}_scale", experts.get(f"{proj}_scale"), (E, N, K // 32), torch.bfloat16)
+    for packed, scale, N, K in (("gate_packed", "gate_scale", I, D), ("up_packed", "up_scale", I, D),
+                                ("down_packed", "down_scale", D, I)):
+        _arg(packed, experts.get(packed), (E, N, K // 8), torch.int32)
+        _arg(scale, experts.get(scale), (E, N, K // 32), torch.bfloat16)
 
 
 # ------------------------------------------------------------------ stages
@@ -828,9 +829,13 @@ def int4_matvec(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
     [N, K/32], as ``quantize_int4`` makes them (moe_int4_matvec).  out must not share
     memory with an input."""
     bf16 = torch.bfloat16
-    T, K = _rows("x", x, x.shape if x.dim() == 2 else (None, None), bf16).shape
-    N = _arg("w_packed", w_packed, (w_packed.shape[0] if w_packed.dim() == 2 else None, K // 8),
-             torch.int32).shape[0]
+    if x is not None and x.dim() == 2 and x.dtype is bf16 and x.stride(1) == 1 \
+            and x.stride(0) >= x.shape[1]:
+        T, K = x.shape  # the common case
+    else:
+        T, K = _rows("x", x, (None, None), bf16).shape
+    N = _sizes("w_packed", w_packed, 2, torch.int32)[0]
+    _arg("w_packed", w_packed, (N, K // 8), torch.int32)
     _arg("w_scale", w_scale, (N, K // 32), bf16)
     if out is not None:
         _arg("out", out, (T, N), bf16)
@@ -847,14 +852,21 @@ def int4_matvec(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
 FEW_TOKENS = 32  # most tokens of experts_few and layer_few
 
 
+def _sizes(name: str, t: Optional[torch.Tensor], dims: int, dtype) -> torch.Size:
+    """Shape of a contiguous tensor of ``dims`` dimensions, checked as ``_arg`` does."""
+    if t is not None and t.dim() == dims and t.dtype is dtype and t.is_contiguous():
+        return t.shape
+    return _arg(name, t, (None,) * dims, dtype).shape
+
+
 def _few_args(topk_idx, topk_w, x, experts, out):
     """(T, D, E, k, I, device) of ``experts_few``'s tensors, checked."""
     bf16 = torch.bfloat16
-    T, D = _arg("x", x, x.shape if x.dim() == 2 else (None, None), bf16).shape
-    k = _arg("topk_idx", topk_idx, (T, topk_idx.shape[1] if topk_idx.dim() == 2 else None),
-             torch.int32).shape[1]
+    T, D = _sizes("x", x, 2, bf16)
+    k = _sizes("topk_idx", topk_idx, 2, torch.int32)[1]
+    _arg("topk_idx", topk_idx, (T, k), torch.int32)
     _arg("topk_w", topk_w, (T, k), torch.float32)
-    E, I = _arg("gate_packed", experts.get("gate_packed"), (None, None, None), torch.int32).shape[:2]
+    E, I = _sizes("gate_packed", experts.get("gate_packed"), 3, torch.int32)[:2]
     _experts(experts, E, D, I)
     if out is not None:
         _arg("out", out, (T, D), bf16)
@@ -907,12 +919,12 @@ def layer_few(x: torch.Tensor, weights: Dict[str, torch.Tensor], k: int, renorm:
     and sum, with lat_down and lat_up (and lat_norm) the latent projections, with the
     shared_* weights the shared expert (moe_layer_few).  ``weights``: those of
     MoeLayer, act_bits 16.  out must not share memory with an input."""
-    T, H = _arg("x", x, x.shape if x.dim() == 2 else (None, None), torch.bfloat16).shape
+    T, H = _sizes("x", x, 2, torch.bfloat16)
     k = operator.index(k)
     gate, lat, shared = (weights.get(n) for n in ("gate_packed", "lat_down", "shared_gate"))
-    E, I = _arg("gate_packed", gate, (None, None, None), torch.int32).shape[:2]
-    L = 0 if lat is None else _arg("lat_down", lat, (None, H), torch.bfloat16).shape[0]
-    S = 0 if shared is None else _arg("shared_gate", shared, (None, H), torch.bfloat16).shape[0]
+    E, I = _sizes("gate_packed", gate, 3, torch.int32)[:2]
+    L = 0 if lat is None else _sizes("lat_down", lat, 2, torch.bfloat16)[0]
+    S = 0 if shared is None else _sizes("shared_gate", shared, 2, torch.bfloat16)[0]
     _check_layer_weights(weights, H, E, I, L, S)
     for of, there, names in (("lat_down", L, ("lat_up", "lat_norm")),
                              ("shared_gate", S, ("shared_up", "shared_down"))):
