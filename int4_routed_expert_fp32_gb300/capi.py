@@ -50,6 +50,7 @@ class MoeWeights(ctypes.Structure):
 
 
 WEIGHT_NAMES = tuple(n for n, _ in MoeWeights._fields_)
+_WEIGHT_SET = frozenset(WEIGHT_NAMES)
 
 
 class MoeRouteConfig(ctypes.Structure):
@@ -887,7 +888,7 @@ def experts_few(topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
     not read).  out must not share memory with an input."""
     T, D, E, k, I, w, dev = _few_args(topk_idx, topk_w, x, experts, out)
     if out is None:
-        out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(x)
     need = lib.moe_experts_few_workspace_size(T, D, E, k, I)
     ws = torch.empty(need or 256, dtype=torch.uint8, device=dev)
     rc = lib.moe_experts_few(x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), T, D, E, k, I,
@@ -936,7 +937,7 @@ def layer_few(x: torch.Tensor, weights: Dict[str, torch.Tensor], k: int, renorm:
         _arg("out", out, (T, H), torch.bfloat16)
     dev = _device_of((x, out, *w), ("x", "out", *WEIGHT_NAMES))
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(x)
     else:
         _apart("out", out, x=x, **dict(zip(WEIGHT_NAMES, w)))
     ptrs = MoeWeights(*[None if t is None else t.data_ptr() for t in w])
@@ -1150,9 +1151,8 @@ def _check_layer_weights(w: Dict[str, torch.Tensor], H: int, E: int, I: int, L: 
     """Every pointer of moe_weights against the layout the configuration
     implies (the experts read the latent width L when L > 0)."""
     bf16 = torch.bfloat16
-    extra = set(w).difference(WEIGHT_NAMES)
-    if extra:
-        raise ValueError(f"unknown weight names: {sorted(extra)}")
+    if not w.keys() <= _WEIGHT_SET:
+        raise ValueError(f"unknown weight names: {sorted(set(w) - _WEIGHT_SET)}")
     _arg("router_w", w.get("router_w"), (E, H), torch.float32)
     _arg("router_bias", w.get("router_bias"), (E,), torch.float32)
     _experts(w, E, L if L else H, I)
