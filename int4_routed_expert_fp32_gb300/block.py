@@ -10,8 +10,12 @@ adapters of many requests beside the latent projections:
     y     += shared_expert(h)                          (with shared_* weights)
     x, h   = block_norm(y, x, ...)                     norm, gate, residual, next norm
 
-With ``few_tokens`` a call of at most 32 tokens runs dispatch, experts and combine as
-one operator, ``experts_few``.
+With ``few_tokens`` a call of at most 32 tokens, with 1.5 tokens to an expert or fewer on
+average, runs dispatch, experts and combine as one operator, ``experts_few``.  It reads an
+expert's weights once for every two tokens; the other path, once for 16.  Whole layers,
+this way and the other, us: 8 of 384 experts of 7168 x 2048, 1 token 54 and 97, 24 tokens
+672 and 752; 8 of 128 experts of 4096 x 1536, 24 tokens 277 and 280, 32 tokens 351 and 307;
+2 of 8 experts of 4096 x 14336, 8 tokens 179 and 205, 16 tokens 297 and 206.
 
 The latent path is the one of the "Kimi K3 latent up-projection" page
 (KimiSparseMoeBlock.forward: router on the full width, down-projection, experts,
@@ -45,7 +49,7 @@ class MoeBlock:
     adapters  {"lat_down": (A, B, scale), "lat_up": ...}: either, or none
     post_gain, next_gain, gate (a gain per channel, [H]), gate_sigmoid,
     residual_scale, eps: options of ``block_norm``
-    few_tokens  calls of at most 32 tokens through ``experts_few`` (the expert outputs
+    few_tokens  calls of few tokens (above) through ``experts_few`` (the expert outputs
               are then summed unrounded, so the bits differ from the other path's)
     """
 
@@ -110,7 +114,8 @@ class MoeBlock:
         None: no adapters).  x_out may be x (in place)."""
         idx, w = self.route(h)
         u = self._project("lat_down", h, ids) if self.latent else h
-        if self.few_tokens and h.shape[0] <= capi.FEW_TOKENS:
+        if (self.few_tokens and h.shape[0] <= capi.FEW_TOKENS
+                and 2 * idx.numel() <= 3 * self.E):
             y = capi.experts_few(idx, w, u, self.experts)
         else:
             d = capi.dispatch(idx, u, self.E, pairs=True)

@@ -262,13 +262,15 @@ def test_block_with_few_tokens(moe):
     gain = torch.ones(256, dtype=BF16, device=DEV)
     args = dict(k=4, groups=4, topk_groups=2, score="softmax", route_scale=1.5, next_gain=gain)
     plain, few = moe.MoeBlock(w, **args), moe.MoeBlock(w, few_tokens=True, **args)
-    for T in (1, 7, 32, 40):
+    for T in (1, 6, 7, 40):  # 24 choices of 16 experts: the most that go this way
         x = torch.randn(T, 256, generator=g).to(DEV)
         h = moe.rmsnorm(x.to(BF16), gain, 1e-6)
         (a, ah), (b, bh) = plain.forward(x, h), few.forward(x, h)
-        if T > 32:
+        if T > 6:
             assert torch.equal(a, b) and torch.equal(ah, bh)
+            continue
         # three roundings to bf16 on the plain path, two on the other
+        assert not torch.equal(a, b)
         assert float((a - b).norm() / (a - x).norm()) <= 5 * 2.0**-8
 
 

@@ -53,7 +53,8 @@ def check(y, x, packed, scale):
 
 SIZES = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 33, 160), (1, 300, 128), (4, 47, 1056),
          (5, 100, 2080), (8, 64, 256), (9, 40, 4128), (16, 130, 7168), (7, 31, 16384), (16, 20, 16384),
-         (1, 5001, 32), (2, 2450, 1024), (13, 4999, 288), (1, 129, 28672 + 32)]
+         (1, 5001, 32), (2, 2450, 1024), (13, 4999, 288), (1, 129, 28672 + 32),
+         (2, 3, 1 << 20), (16, 2, (1 << 20) - 96), (1, 1 << 20, 32)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES)
