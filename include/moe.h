@@ -633,7 +633,7 @@ int moe_experts_few(const uint16_t* x, const int32_t* topk_idx, const float* top
                     void* stream);
 
 /* The whole layer for a few tokens (cfg->T <= 32, act_bits 16) in the same two
- * launches: the routing of moe_route (decided in 64 bits where fp32 keys are
+ * launches: the routing of moe_route (decided again, as in 64 bits, where fp32 keys are
  * near one another; more than 16 of them near the border stay as fp32 has
  * them), moe_experts_few, and with cfg->L > 0 the latent projections and norm,
  * with cfg->I_shared > 0 the shared expert, as moe_layer_forward has them.  Between

@@ -245,6 +245,21 @@ def test_padded_rows_and_experts_out_of_service(moe):
     assert not moe.layer_few(x, w, 3)[2:4].any()
 
 
+def test_rows_that_are_not_finite_stay_by_themselves(moe):
+    """NaN, infinities and values whose logits overflow, with equal experts at the border."""
+    g = torch.Generator().manual_seed(15)
+    w = layer_weights(g, 256, 12, 64, L=128, S=64)
+    w["router_w"][5] = w["router_w"][2]
+    x = torch.randn(6, 256, generator=g).to(BF16).to(DEV)
+    clean = moe.layer_few(x, w, 3)
+    bad = x.clone()
+    bad[1, 7], bad[2, 9], bad[4] = float("nan"), float("inf"), 3e38
+    y = moe.layer_few(bad, w, 3)
+    assert moe.check_error() == moe.capi.MOE_ERR_UNSUPPORTED
+    assert torch.equal(y[[0, 3, 5]], clean[[0, 3, 5]])
+    assert not torch.isfinite(y[[1, 2, 4]].float()).all(dim=1).any()
+
+
 def test_agrees_with_the_layer(moe):
     g = torch.Generator().manual_seed(13)
     w = layer_weights(g, 512, 16, 128, L=256, S=128, norm=True)
