@@ -201,7 +201,8 @@ LAYERS = [dict(T=1, H=64, E=4, k=2, I=64), dict(T=1, H=2048, E=64, k=8, I=256),
           dict(T=4, H=512, E=16, k=4, I=128, S=192), dict(T=19, H=256, E=12, k=3, I=64, S=448),
           dict(T=1, H=512, E=8, k=2, I=64, L=128), dict(T=8, H=1024, E=8, k=3, I=192, L=576, norm=True),
           dict(T=13, H=192, E=6, k=2, I=64, L=320, norm=True, S=128),
-          dict(T=32, H=576, E=5, k=2, I=320, L=64, S=64)]
+          dict(T=32, H=576, E=5, k=2, I=320, L=64, S=64),
+          dict(T=32, H=64, E=2048, k=32, I=64), dict(T=3, H=128, E=513, k=31, I=64, S=64)]
 
 
 @pytest.mark.parametrize("c", LAYERS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
@@ -347,6 +348,36 @@ def test_calls_on_two_streams_at_once(moe):
     assert moe.check_error() == 0
     for i in range(2):
         assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+@pytest.mark.parametrize("c", [LAYERS[1], LAYERS[7], LAYERS[9], LAYERS[10], LAYERS[12]],
+                         ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_nothing_is_written_beyond_the_output_and_the_workspace(moe, c):
+    """Both between guards of a fixed pattern, the workspace of exactly the stated size."""
+    import ctypes
+    capi = moe.capi
+    g = torch.Generator().manual_seed(31)
+    w = layer_weights(g, c["H"], c["E"], c["I"], c.get("L", 0), c.get("S", 0), c.get("norm", False))
+    x = torch.randn(c["T"], c["H"], generator=g).to(BF16).to(DEV)
+    want = moe.layer_few(x, w, c["k"])
+    cfg = capi.MoeConfig(c["T"], c["H"], c["E"], c["k"], c["I"], c.get("L", 0), 16, 1, 1e-6,
+                         c.get("S", 0))
+    ptrs = capi.MoeWeights(*[w[n].data_ptr() if n in w else None for n in capi.WEIGHT_NAMES])
+    need = capi.lib.moe_layer_few_workspace_size(ctypes.byref(cfg))
+    guard, out_bytes = 65536, want.numel() * 2
+    ws = torch.full((need + 2 * guard,), 0xA5, dtype=torch.uint8, device=DEV)
+    out = torch.full((out_bytes + 2 * guard,), 0xA5, dtype=torch.uint8, device=DEV)
+    before = x.clone()
+    for _ in range(2):  # the second on what the first left
+        rc = capi.lib.moe_layer_few(ctypes.byref(cfg), ctypes.byref(ptrs), x.data_ptr(),
+                                    out.data_ptr() + guard, ws.data_ptr() + guard, need,
+                                    torch.cuda.current_stream().cuda_stream)
+        assert rc == capi.MOE_OK
+        torch.cuda.synchronize()
+        for t, n in ((ws, need), (out, out_bytes)):
+            assert bool((t[:guard] == 0xA5).all()) and bool((t[guard + n:] == 0xA5).all())
+        got = out[guard:guard + out_bytes].view(BF16).reshape(want.shape)
+        assert torch.equal(got, want) and torch.equal(x, before)
 
 
 @pytest.mark.parametrize("stage", [0, 1, 2])
