@@ -234,6 +234,7 @@ __device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
 // Columns of K (int4) or of the bf16 rows that one slot holds, and the length of K.
 __device__ __forceinline__ bool is_int4(int kind) { return (kind | 1) == kFewDown; }
 static_assert(kFewGateUp == 2 && kFewDown == 3, "is_int4");
+static_assert(C / 128 <= 2 * kMul && kMul == 8, "at most two steps a warp and slot");
 __device__ __forceinline__ int length_of(const FewArgs& a, int kind) {
   switch (kind) {
     case kFewLatDown:
@@ -1039,32 +1040,26 @@ struct Lane {
       : g(lane >> 2), t(lane & 3), r(row_of(lane >> 2)), on((lane >> 2 & 3) == (lane & 3)) {}
 };
 
-// Step `step` of a slot: adds to acc[block][0, 1] (rows g and g + 8).
-__device__ __forceinline__ void multiply4(const uint8_t* slot, int step, int cols, const Lane& l,
-                                          int x_at, int start_at, bool dense, const Magic& magic,
-                                          uint4 (&v)[4], float (&acc)[2][4]) {
-  if (l.on) {
-    const uint4* row = reinterpret_cast<const uint4*>(slot + x_at + step * 256);
+// One step: adds to acc[block][0, 1] (rows g and g + 8).  w, x, start, scale: where the lane
+// reads; rows8: bytes between the scales of 8 rows; there: the lane's two columns are of
+// groups that the row has.
+__device__ __forceinline__ void multiply4(const uint8_t* w, const uint8_t* x, const uint8_t* start,
+                                          const uint8_t* scale, int rows8, bool there, bool on,
+                                          const Magic& magic, uint4 (&v)[4], float (&acc)[2][4]) {
+  if (on) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = row[i];
+    for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint4*>(x)[i];
   }
   // two start values (16 columns each) of groups 2 (t & 1) and + 1, token t >> 1
-  const float4 s = *reinterpret_cast<const float4*>(slot + start_at + step * 32);
+  const float4 s = *reinterpret_cast<const float4*>(start);
   const float start0 = s.x + s.y, start1 = s.z + s.w;
-  const uint8_t* w =
-      slot + (step >> 1) * 2048 + l.r * 128 + ((((step & 1) << 2 | l.t) ^ (l.r & 7)) << 4);
-  const int g2 = 2 * step + (l.t & 1), pitch = dense ? cols / 16 : 128;
-  const uint8_t* sc =
-      slot + kWeightBytes + (dense ? l.r * pitch + g2 * 4 : static_cast<int>(scale_at(l.r, g2)));
-  // the last step of a row may be half: its upper two groups add nothing
-  const bool there = step < cols / 128 || !(l.t & 1);
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const uint4 q0 = *reinterpret_cast<const uint4*>(w + b * (kWeightBytes / 2));
     const uint4 q8 = *reinterpret_cast<const uint4*>(w + b * (kWeightBytes / 2) + 1024);
     const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w8[4] = {q8.x, q8.y, q8.z, q8.w};
-    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(sc + b * (kScaleBytes / 2));
-    const uint32_t s8 = *reinterpret_cast<const uint32_t*>(sc + b * (kScaleBytes / 2) + 8 * pitch);
+    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(scale + b * (kScaleBytes / 2));
+    const uint32_t s8 = *reinterpret_cast<const uint32_t*>(scale + b * (kScaleBytes / 2) + rows8);
     float c[4] = {start0, start1, start0, start1};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1121,13 +1116,18 @@ __device__ __noinline__ void multiply(int warp, int lane) {
   const Magic magic;
   const Lane l(lane);
   const int room = min(a.T, kFewChunk) - 1, slots = ring.n;
-  const int x_at = kWeightBytes + kScaleBytes + min(l.g >> 2, room) * kPitch4 + l.t * 64;
-  const int start_at =
-      kWeightBytes + kScaleBytes + min(l.t >> 1, room) * kPitch4 + kStarts + (l.t & 1) * 16;
+  // Where the lane reads in a slot for its warp's first step, columns 128 warp and on; what
+  // can be known before the slots: eight instructions more in a step are 8 % of a call.
+  const int w_at =
+      (warp >> 1) * 2048 + l.r * 128 + ((((warp & 1) << 2 | l.t) ^ (l.r & 7)) << 4);
+  const int scales_at = kWeightBytes + static_cast<int>(scale_at(l.r, 2 * warp + (l.t & 1)));
+  const int x_at =
+      kWeightBytes + kScaleBytes + min(l.g >> 2, room) * kPitch4 + warp * 256 + l.t * 64;
+  const int start_at = kWeightBytes + kScaleBytes + min(l.t >> 1, room) * kPitch4 + kStarts +
+                       warp * 32 + (l.t & 1) * 16;
   uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-  const bool dense[2] = {a.tma_scale[0] == kScalesDense, a.tma_scale[1] == kScalesDense};
   int buf = 0;             // the finishing warp of this unit
   uint32_t taken = 0;      // parity of its buffer, one bit a warp
   for (Place at;; at.next(slots)) {
@@ -1137,10 +1137,24 @@ __device__ __noinline__ void multiply(int warp, int lane) {
     const int kind = h.kind & 255;
     const uint8_t* slot = ring.slot(s);
     if (is_int4(kind)) {
-      const int steps = (h.cols() + 127) / 128;
+      const int cols = h.cols();
+      const uint8_t *w = slot + w_at, *x = slot + x_at, *start = slot + start_at;
+      const bool dense = a.tma_scale[kind - kFewGateUp] == kScalesDense;
+      int scale = scales_at, rows8 = 1024;
+      if (dense) {  // rows of cols / 16 bytes
+        scale = kWeightBytes + l.r * (cols >> 4) + 8 * warp + (l.t & 1) * 4;
+        rows8 = cols >> 1;
+      }
 #pragma unroll 1
-      for (int step = warp; step < steps; step += kMul)
-        multiply4(slot, step, h.cols(), l, x_at, start_at, dense[kind - kFewGateUp], magic, v, acc);
+      for (int c0 = 128 * warp; c0 < cols; c0 += 128 * kMul) {
+        // the last step of a row may be half: its upper two groups add nothing
+        multiply4(w, x, start, slot + scale, rows8, c0 + 128 <= cols || !(l.t & 1), l.on, magic, v,
+                  acc);
+        w += kMul / 2 * 2048;
+        x += kMul * 256;
+        start += kMul * 32;
+        scale = dense ? scale + 8 * kMul : scale ^ 64;  // four pieces on, which are swizzled
+      }
     } else {
       if (kind == kFewEnd) break;
       const int most = few_rows_of(kind);
