@@ -24,7 +24,7 @@
 // 80 registers to a thread.  The ring runs on across units and phases, so the weights of
 // a down projection arrive while its h is still being computed.  A slot holds 36 KB: half
 // as much, in twice as many slots, costs more at every slot than it hides (32 tokens, 384
-// experts of 7168 x 2048: 991 us against 850).
+// experts of 7168 x 2048: 991 us against 862).
 //
 // The products use m16n8k16 MMAs: 16 weight rows, 8 columns.  At 8 tokens a
 // weight byte is worth 32 operations, a hundredth of what would make the tensor
@@ -35,8 +35,9 @@
 // 2 each), HBM 1570: near enough to one another that they do not overlap fully.
 //
 // Measured (graphs of calls; behind it the bytes at the measured copy rate): the layer of
-// one token, 8 of 384 experts, 7168 x 2048: 53 us, 31; of 32 tokens: 850 us, 689; 6 tokens of 3584 x 1024, experts alone: 51 us, 20; 16 tokens of 256 x 128:
-// 26 us, the latency of its steps.
+// one token, 8 of 384 experts, 7168 x 2048: 52 us, 31; of 32 tokens: 828 us, 689; 6
+// tokens of 3584 x 1024, experts alone: 50 us, 20; 16 tokens of 256 x 128: 26 us, the
+// latency of its steps.
 #include "few.cuh"
 
 #include <cuda_fp16.h>
@@ -184,9 +185,8 @@ __device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, Waiter 
 }
 template <int REST = 0>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const Waiter& w) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) ok = wait_slowly(bar, parity, w, REST);
-  return __all_sync(0xffffffffu, ok);
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_slowly(bar, parity, w, REST));
 }
 constexpr int kRest = 100;  // ns
 
