@@ -1082,22 +1082,25 @@ __device__ __forceinline__ void multiply4(const uint8_t* w, const uint8_t* x, co
 __device__ __forceinline__ void multiply16(const uint8_t* slot, int cols, int tokens, int planes,
                                            int warp, int lane, const Lane& l, float (&acc)[2][4]) {
   const int li = lane & 7;
-  const uint32_t w = smem_u32(slot) + ((lane & 8) + li) * 128;
+  // of the warp's first 16 columns; the next ones lie two pieces on, at the same place in them
+  uint32_t w = smem_u32(slot) + (warp >> 2) * 2048 + ((lane & 8) + li) * 128 +
+               ((((warp & 3) << 1 | lane >> 4) ^ li) << 4);
+  // columns of tokens that are not there repeat the last one's
+  int at = (warp >> 2) * tokens + min(l.g, tokens - 1);
+  const uint8_t* rows = slot + kWeightBytes + kScaleBytes + l.t * 4;
+  const int piece = (warp & 3) << 1;
 #pragma unroll 1
-  for (int p = warp; p < cols / 16; p += kMul) {
+  for (int c0 = 16 * warp; c0 < cols; c0 += 16 * kMul, w += kMul / 4 * 2048, at += kMul / 4 * tokens) {
     uint32_t wr[2][4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-      ldsm4(w + b * (kWeightBytes / 2) + (p >> 2) * 2048 + ((((p & 3) << 1 | lane >> 4) ^ li) << 4),
-            wr[b]);
-    // columns of tokens that are not there repeat the last one's
-    const int at = (p >> 2) * tokens + min(l.g, tokens - 1);
-    const uint8_t* x = slot + kWeightBytes + kScaleBytes + at * 128 + l.t * 4;
-    const int piece = (p & 3) << 1, turn = at & 7;
-#pragma unroll 1
-    for (int plane = 0; plane < planes; ++plane, x += tokens * (C / 2)) {
-      const uint32_t b0 = *reinterpret_cast<const uint32_t*>(x + ((piece ^ turn) << 4));
-      const uint32_t b1 = *reinterpret_cast<const uint32_t*>(x + (((piece | 1) ^ turn) << 4));
+    for (int b = 0; b < 2; ++b) ldsm4(w + b * (kWeightBytes / 2), wr[b]);
+    const uint8_t* x = rows + at * 128 + ((piece ^ (at & 6)) << 4);
+    const int odd = (at & 1) << 4;
+#pragma unroll
+    for (int plane = 0; plane < 2; ++plane, x += tokens * (C / 2)) {
+      if (plane == planes) break;
+      const uint32_t b0 = *reinterpret_cast<const uint32_t*>(x + odd);
+      const uint32_t b1 = *reinterpret_cast<const uint32_t*>(x + (odd ^ 16));
 #pragma unroll
       for (int b = 0; b < 2; ++b) mma_bf16(acc[b], wr[b], b0, b1);
     }
