@@ -164,32 +164,6 @@ __device__ __forceinline__ void nibbles(uint32_t w, const Magic& m, uint32_t (&q
 // sum of the odd ones): what one value of column c adds to it.
 __device__ __forceinline__ float start_of(float v, int c) { return c & 1 ? -72.f * v : -1032.f * v; }
 
-// mbar_wait with its slow part out of line (the code of all roles shares the instruction
-// caches), and for the roles that run ahead or behind with a rest between two
-// looks: seven warps that look all the time take as many issue slots as the
-// products.
-__device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, Waiter w, uint32_t rest_ns) {
-  uint64_t t0 = 0;
-  for (int i = 0;; ++i) {
-    if (rest_ns) __nanosleep(rest_ns);
-    if (mbar_try_wait(bar, parity)) return true;
-    if (i < 8) continue;  // reading the clock takes longer than most waits
-    if (aborted(w)) return false;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (static_cast<int64_t>(now - t0) > w.limit_ns) {
-      give_up(w);
-      return false;
-    }
-  }
-}
-template <int REST = 0>
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const Waiter& w) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_slowly(bar, parity, w, REST));
-}
-constexpr int kRest = 100;  // ns
-
 // Weights pass through L2 once and first make room again: else 200 MB of them a call would
 // push everything else out, the kernels' own code too, which then comes from HBM line
 // by line (10 us at the start of a call).
@@ -477,6 +451,33 @@ __device__ __forceinline__ Lists lists_of(Context& c) {
 __device__ __forceinline__ Waiter waiter_of(Context& c) {
   return Waiter{&c.cta_abort, c.a.status, c.a.wait_ns};
 }
+
+// mbar_wait with its slow part out of line (the code of all roles shares the instruction
+// caches), and for the roles that run ahead or behind with a rest between two
+// looks: seven warps that look all the time take as many issue slots as the
+// products.
+__device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, uint32_t rest_ns) {
+  const Waiter w = waiter_of(context());
+  uint64_t t0 = 0;
+  for (int i = 0;; ++i) {
+    if (rest_ns) __nanosleep(rest_ns);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (i < 8) continue;  // reading the clock takes longer than most waits
+    if (aborted(w)) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (static_cast<int64_t>(now - t0) > w.limit_ns) {
+      give_up(w);
+      return false;
+    }
+  }
+}
+template <int REST = 0>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_slowly(bar, parity, REST));
+}
+constexpr int kRest = 100;  // ns
 
 // Keys closer than this are compared again in 64 bits: it is far above what the
 // fp32 logits, the sigmoid and the sum leave open, and met by one token in a thousand.
@@ -781,7 +782,6 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
   const FewArgs& a = cx.a;
   const Ring ring = ring_of(cx);
   const Lists ls = lists_of(cx);
-  const Waiter wt = waiter_of(cx);
   const uint64_t once = evict_first();
   Place at;
   bool ok = true, known = false;
@@ -794,7 +794,7 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
     if (lane == turn) ticket = atomicAdd(a.counters, 1);
     if (u >= fixed && !known) {
       known = true;
-      ok = wait_for<kRest>(&cx.listed, 0, wt);
+      ok = wait_for<kRest>(&cx.listed, 0);
       if (!ok) break;
     }
     int kind = 0;
@@ -831,7 +831,7 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
           ok = false;
           break;
         }
-        ok = wait_for<kRest>(&ring.empty[s], at.parity ^ 1u, wt);
+        ok = wait_for<kRest>(&ring.empty[s], at.parity ^ 1u);
         if (!ok) break;
         if (lane == 0) {
           const int cols = min(step, K - k0);
@@ -872,8 +872,9 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
 static_assert(kAhead == 2, "tickets in turn");
 
 // Waits until counter `c` has reached `n`; false when the time ran out.
-__device__ __noinline__ bool wait_count(const int32_t* c, int n, Waiter wt) {
+__device__ __noinline__ bool wait_count(const int32_t* c, int n) {
   if (load_acquire(c) >= n) return true;
+  const Waiter wt = waiter_of(context());
   const uint64_t t0 = global_timer_ns();
   while (load_acquire(c) < n) {
     if (aborted(wt)) return false;
@@ -892,7 +893,6 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
   const FewArgs& a = cx.a;
   const Ring ring = ring_of(cx);
   const Lists ls = lists_of(cx);
-  const Waiter wt = waiter_of(cx);
   const uint64_t once = evict_first();
   const bool lanes = !(a.tma_scale[0] && a.tma_scale[1]);  // every lane arrives on a slot
   int known = 0;         // chunks whose h is known to be complete
@@ -905,7 +905,7 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
 #pragma unroll 1
   for (Place at;; at.next(ring.n)) {
     const uint32_t s = at.s;
-    if (!wait_for<kRest>(&ring.named[s], at.parity, wt)) break;
+    if (!wait_for<kRest>(&ring.named[s], at.parity)) break;
     const Header h = ring.header[s];
     const int kind = h.kind & 255;
     const bool four = is_int4(kind), down = kind == kFewDown;
@@ -975,7 +975,7 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
       const int n = down ? a.I / 16
                          : kind == kFewGateUp ? a.L / 32 * whole
                                               : kind == kFewSharedDown ? a.S / 16 * whole : a.L / 32;
-      const bool ok = wait_count(c, n, wt);
+      const bool ok = wait_count(c, n);
       if (down) {
         // and what a look at the next chunks shows at the same time
         const bool there = h.which + lane < a.T * a.k && load_acquire(c + lane) >= n;
@@ -1112,7 +1112,6 @@ __device__ __noinline__ void multiply(int warp, int lane) {
   const FewArgs& a = cx.a;
   const Ring ring = ring_of(cx);
   const Sums sums = sums_of(cx);
-  const Waiter wt = waiter_of(cx);
   // int4 units: [block][row g, g + 8], the groups of lane t odd and even still apart;
   // bf16 units: [block] MMA accumulator
   float acc[2][4] = {};
@@ -1135,7 +1134,7 @@ __device__ __noinline__ void multiply(int warp, int lane) {
   uint32_t taken = 0;      // parity of its buffer, one bit a warp
   for (Place at;; at.next(slots)) {
     const uint32_t s = at.s;
-    if (!wait_for(&ring.full[s], at.parity, wt)) return;
+    if (!wait_for(&ring.full[s], at.parity)) return;
     const Header h = ring.header[s];
     const int kind = h.kind & 255;
     const uint8_t* slot = ring.slot(s);
@@ -1166,7 +1165,7 @@ __device__ __noinline__ void multiply(int warp, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.empty[s]);
     if (h.kind & kLastSlot) {
-      if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u, wt)) return;
+      if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u)) return;
       taken ^= 1u << buf;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
@@ -1197,7 +1196,7 @@ __device__ __noinline__ void multiply(int warp, int lane) {
     }
   }
   for (buf = 0; buf < kFinish; ++buf) {  // tell the finishing warps
-    if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u, wt)) return;
+    if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u)) return;
     if (warp == 0 && lane == 0) sums.header[buf].kind = kFewEnd;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sums.full[buf]);
@@ -1305,7 +1304,6 @@ __device__ __noinline__ void finish(int buf, int lane) {
   const FewArgs& a = cx.a;
   const Sums sums = sums_of(cx);
   const Lists ls = lists_of(cx);
-  const Waiter wt = waiter_of(cx);
   const int halves = few_chunks(a.T, kFewRows / 2);
   int32_t* tile_done = a.counters + kFewFixed + a.T * a.k;
   int32_t* out_done = tile_done + a.D / 32;
@@ -1317,7 +1315,7 @@ __device__ __noinline__ void finish(int buf, int lane) {
   const float x_unit = a.L == 0 && lane < a.T ? __ldcg(a.x_unit + lane) : 1.f;  // of token `lane`
 #pragma unroll 1
   for (uint32_t n = 0;; ++n) {
-    if (!wait_for<kRest>(&sums.full[buf], n & 1u, wt)) return;
+    if (!wait_for<kRest>(&sums.full[buf], n & 1u)) return;
     const Header h = sums.header[buf];
     const int kind = h.kind & 255;
     if (kind == kFewEnd) return;
