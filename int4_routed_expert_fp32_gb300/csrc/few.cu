@@ -35,7 +35,7 @@
 // 2 each), HBM 1570: near enough to one another that they do not overlap fully.
 //
 // Measured (graphs of calls; behind it the bytes at the measured copy rate): the layer of
-// one token, 8 of 384 experts, 7168 x 2048: 52 us, 31; of 32 tokens: 828 us, 689; 6
+// one token, 8 of 384 experts, 7168 x 2048: 52 us, 31; of 32 tokens: 819 us, 689; 6
 // tokens of 3584 x 1024, experts alone: 50 us, 20; 16 tokens of 256 x 128: 26 us, the
 // latency of its steps.
 #include "few.cuh"
