@@ -13,10 +13,10 @@
 //                      tokens (at most 2) of one chunk of one expert, or 32 rows of
 //                      the down projections of a group of chunks, one after another.
 //
-// Tickets are taken in the order of the units, and a unit waits only for units
-// with lower tickets (a down projection for its expert's h).  Those are held by
-// CTAs that run, so the kernel ends whatever else holds SMs: no CTA waits for
-// one that has not started.
+// Tickets are taken in the order of the units, a CTA works on its own in ascending
+// order, and a unit waits only for units with lower tickets (a down projection for
+// its expert's h).  Those are held by CTAs that run, so the kernel ends whatever
+// else holds SMs: no CTA waits for one that has not started.
 //
 // Roles of a CTA: warp 0 copies weights into a ring (TMA), warp 1 their scales and the
 // tokens' rows (once the units they wait for are done), the last eight multiply, and
@@ -786,12 +786,15 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
   Place at;
   bool ok = true, known = false;
   const int fixed = cx.units[kFewLatDown] + cx.units[kFewSharedUp];
-  // kAhead tickets at a time, so that a unit does not wait for its own
-  int ticket = lane < kAhead ? atomicAdd(a.counters, 1) : 0;
+  // kAhead tickets at a time, so that a unit does not wait for its own.  One thread takes
+  // them all: its atomics on one address follow one another in program order, so the CTA
+  // works on its units in ticket order.
+  int ticket = lane == 0 ? atomicAdd(a.counters, kAhead) : 0, later = ticket + 1;
 #pragma unroll 1
-  for (int turn = 0; ok; turn ^= 1) {
-    int u = __shfl_sync(0xffffffffu, ticket, turn);
-    if (lane == turn) ticket = atomicAdd(a.counters, 1);
+  while (ok) {
+    int u = __shfl_sync(0xffffffffu, ticket, 0);
+    ticket = later;
+    if (lane == 0) later = atomicAdd(a.counters, 1);
     if (u >= fixed && !known) {
       known = true;
       ok = wait_for<kRest>(&cx.listed, 0);
@@ -869,7 +872,7 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
   // whatever ended the loop, no copy is still on its way when the CTA leaves
   drain_ring(ring.full, at.n, ring.n, a.status);
 }
-static_assert(kAhead == 2, "tickets in turn");
+static_assert(kAhead == 2, "ticket and later");
 
 // Waits until counter `c` has reached `n`; false when the time ran out.
 __device__ __noinline__ bool wait_count(const int32_t* c, int n) {

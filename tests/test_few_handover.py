@@ -1,0 +1,36 @@
+"""Orders that the kernel of a few tokens relies on are stated in its source (no GPU
+needed: what is looked at is the source).
+
+A unit of work waits only for units with lower tickets, and a CTA works on its tickets
+in the order in which it holds them; so a CTA has to hold them in ascending order, or
+two of them could wait for one another.
+"""
+import os
+import re
+
+from tests.test_tensor_memory_rule import CSRC
+
+with open(os.path.join(CSRC, "few.cu")) as f:
+    TEXT = re.sub(r"//[^\n]*", "", f.read())
+
+
+def function(name):
+    """Body of a function of few.cu, without comments."""
+    start = TEXT.index("{", re.search(r"\b%s\([^;{]*\)\s*{" % name, TEXT).start())
+    depth, at = 0, start
+    while True:
+        depth += {"{": 1, "}": -1}.get(TEXT[at], 0)
+        at += 1
+        if depth == 0:
+            return TEXT[start:at]
+
+
+def test_one_thread_takes_every_ticket():
+    """Atomics of one thread on one address follow its program order; those of several
+    lanes of an instruction have no order that CUDA states."""
+    body = function("copy_weights")
+    takes = re.findall(r"([^;{}]*)atomicAdd\(a\.counters, (\w+)\)", body)
+    assert [n for _, n in takes] == ["kAhead", "1"]
+    for head, _ in takes:
+        assert re.search(r"if \(lane == 0\)|lane == 0 \?", head), head
+    assert len(re.findall(r"\bcounters\b", body)) == len(takes)
