@@ -910,6 +910,7 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
     const uint32_t s = at.s;
     if (!wait_for<kRest>(&ring.named[s], at.parity)) break;
     const Header h = ring.header[s];
+    __syncwarp();  // lane 0's arrivals let the slot and its header be written again
     const int kind = h.kind & 255;
     const bool four = is_int4(kind), down = kind == kFewDown;
     uint64_t* bar = &ring.full[s];

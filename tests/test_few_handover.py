@@ -8,6 +8,8 @@ two of them could wait for one another.
 import os
 import re
 
+import pytest
+
 from tests.test_tensor_memory_rule import CSRC
 
 with open(os.path.join(CSRC, "few.cu")) as f:
@@ -34,3 +36,14 @@ def test_one_thread_takes_every_ticket():
     for head, _ in takes:
         assert re.search(r"if \(lane == 0\)|lane == 0 \?", head), head
     assert len(re.findall(r"\bcounters\b", body)) == len(takes)
+
+
+@pytest.mark.parametrize("role,header", [("copy_rest", "ring.header[s]"), ("multiply", "ring.header[s]"),
+                                         ("finish", "sums.header[buf]")])
+def test_a_header_is_read_by_the_whole_warp_before_the_slot_moves_on(role, header):
+    """A lane's arrival on a slot's barrier is what lets the slot be used again, its
+    header too: the other lanes have read theirs by then."""
+    body = function(role)
+    read = body.index("const Header h = " + header)
+    arrive = re.search(r"\bmbar_arrive\w*\(|\bcp_async_arrive\w*\(", body[read:])
+    assert "__syncwarp();" in body[read:read + arrive.start()]
