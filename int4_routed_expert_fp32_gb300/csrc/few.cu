@@ -633,6 +633,7 @@ __device__ __forceinline__ int group_chunks(const FewArgs& a, int chunks) {
 }
 
 __device__ __forceinline__ void mul_sync() {
+  __syncwarp();  // whose lanes come from loops of different lengths
   asm volatile("bar.sync 1, %0;" ::"n"(kMul * 32) : "memory");
 }
 

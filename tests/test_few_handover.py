@@ -47,3 +47,9 @@ def test_a_header_is_read_by_the_whole_warp_before_the_slot_moves_on(role, heade
     read = body.index("const Header h = " + header)
     arrive = re.search(r"\bmbar_arrive\w*\(|\bcp_async_arrive\w*\(", body[read:])
     assert "__syncwarp();" in body[read:read + arrive.start()]
+
+
+def test_warps_are_whole_at_the_barrier_of_the_lists():
+    """bar.sync takes whole warps, whose lanes come from loops of different lengths."""
+    body = function("mul_sync")
+    assert body.index("__syncwarp();") < body.index("bar.sync")
