@@ -612,9 +612,10 @@ int moe_int4_matvec(const uint16_t* x, int64_t x_ld, const int32_t* w_packed,
  * combine (no page has this call; the arithmetic is moe_expert_ffn's and
  * moe_combine's):
  *   out[t] = bf16( sum_j topk_w[t, j] down_e( SiLU(gate_e x[t]) * up_e x[t] ) ),
- *   e = topk_idx[t, j], summed in the order of the experts, in fp32 with one rounding at the end (the
- *   intermediate h is kept in fp16: a value beyond its range records
- *   MOE_ERR_UNSUPPORTED).  x may have any bf16 value: a token is scaled by a
+ *   e = topk_idx[t, j], summed in the order of the experts, in fp32 with one rounding at the end.
+ *   The intermediate h is kept in fp16, 16 columns that are all below 2^-11 times a
+ *   power of two; a value above its range, or not finite, records
+ *   MOE_ERR_UNSUPPORTED.  x may have any bf16 value: a token is scaled by a
  *   power of two on its way in and out.
  *   x         bf16 [T, D];  out bf16 [T, D]
  *   topk_idx  int32 [T, k]: any experts, in any order and repetition; an id outside
@@ -637,8 +638,8 @@ int moe_experts_few(const uint16_t* x, const int32_t* topk_idx, const float* top
  * near one another; more than 16 of them near the border stay as fp32 has
  * them), moe_experts_few, and with cfg->L > 0 the latent projections and norm,
  * with cfg->I_shared > 0 the shared expert, as moe_layer_forward has them.  Between
- * the steps values are kept in fp16 (u = the latent input, h; beyond fp16's
- * range: MOE_ERR_UNSUPPORTED recorded) or as two bf16 parts (16 bits), sums in
+ * the steps values are kept in fp16 (u = the latent input, h; small ones scaled; beyond
+ * its range: MOE_ERR_UNSUPPORTED recorded) or as two bf16 parts (16 bits), sums in
  * fp32; the output is rounded once.  Same sizes, alignment and memory rules as
  * moe_experts_few (router_w 16-byte aligned); router_w_terms is not read. */
 size_t moe_layer_few_workspace_size(const moe_config* cfg);

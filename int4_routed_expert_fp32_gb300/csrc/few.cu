@@ -102,7 +102,7 @@ __host__ __device__ __forceinline__ int sums_bytes(const FewArgs& a) {
 // One header per slot and per finishing warp.  A segment is what one chunk adds to
 // a unit.
 struct __align__(16) Header {
-  int kind;   // FewKind, | kLastSlot, | kLastSegment
+  int kind;   // FewKind, | kScaled, | kLastSlot, | kLastSegment
   int size;   // tokens, | columns of K << 16
   int which;  // expert chunk, or chunk of tokens
   int n0;     // first column of the output
@@ -111,6 +111,12 @@ struct __align__(16) Header {
 };
 constexpr int kLastSlot = 256;     // of its segment
 constexpr int kLastSegment = 512;  // of its unit
+// Added to the kind of a segment whose activations have units of their own (so that it is
+// not is_int4: only multiply() meets it); then the slot's place in its segment stands above
+// the other bits.  Set by the warp that copies the rows.
+constexpr int kScaled = 128, kSlotShift = 11;
+static_assert(kFewEnd < kScaled, "kinds");
+static_assert(kFewWidth / kFewColumns <= 1 << (31 - kSlotShift), "the slot's place");
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
@@ -380,6 +386,7 @@ struct Lists {
   uint32_t* tokens;   // [chunks] tokens, one bit each
   uint16_t* expert;   // [chunks]
   uint16_t* row0;     // [chunks] first row
+  uint32_t* scaled;   // [T k] bits: a chunk's h has units of its own (the copying warp's)
 };
 
 // Ring and buffers of a CTA.
@@ -446,6 +453,7 @@ __device__ __forceinline__ Lists lists_of(Context& c) {
   ls.tokens = reinterpret_cast<uint32_t*>(ls.row_weight + pairs);
   ls.expert = reinterpret_cast<uint16_t*>(ls.tokens + pairs);
   ls.row0 = ls.expert + pairs;
+  ls.scaled = reinterpret_cast<uint32_t*>(ls.row0 + pairs);
   return ls;
 }
 __device__ __forceinline__ Waiter waiter_of(Context& c) {
@@ -659,7 +667,10 @@ __device__ __noinline__ void build_lists(int tid) {
 #pragma unroll 1
   for (int e = tid; e < a.E; e += kMul * 32) mask[e] = 0u;
 #pragma unroll 1
-  for (int p = tid; p < pairs; p += kMul * 32) ls.row_weight[p] = 0.f;
+  for (int p = tid; p < pairs; p += kMul * 32) {
+    ls.row_weight[p] = 0.f;
+    if (!(p & 31)) ls.scaled[p >> 5] = 0u;
+  }
   if (tid < kFewGroups) cx.in_group[tid] = 0u;
   if (tid < kFewTokens) cx.groups_of[tid] = 0u;
   mul_sync();
@@ -880,20 +891,21 @@ __device__ __noinline__ void copy_weights(const FewMaps* maps, int lane) {
 }
 static_assert(kAhead == 2, "ticket and later");
 
-// Waits until counter `c` has reached `n`; false when the time ran out.
-__device__ __noinline__ bool wait_count(const int32_t* c, int n) {
-  if (load_acquire(c) >= n) return true;
+// Waits until counter `c` has reached `n`; its value, or -1 when the time ran out.
+__device__ __noinline__ int wait_count(const int32_t* c, int n) {
+  int v = load_acquire(c);
+  if ((v & kFewCount) >= n) return v;
   const Waiter wt = waiter_of(context());
   const uint64_t t0 = global_timer_ns();
-  while (load_acquire(c) < n) {
-    if (aborted(wt)) return false;
+  while (((v = load_acquire(c)) & kFewCount) < n) {
+    if (aborted(wt)) return -1;
     if (static_cast<int64_t>(global_timer_ns() - t0) > wt.limit_ns) {
       give_up(wt);
-      return false;
+      return -1;
     }
     __nanosleep(64);
   }
-  return true;
+  return v;
 }
 
 // Scales and rows of tokens.
@@ -907,6 +919,8 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
   int known = 0;         // chunks whose h is known to be complete
   uint32_t others = a.L > 0 ? 0u : 1u << kFewGateUp;  // kinds whose rows are
   others |= 1u << kFewLatDown | 1u << kFewSharedUp;
+  bool u_scaled = false, scaled = false;  // u, the segment: units of their own
+  bool any_scaled = false;                // or any chunk
   int i = 0;  // slot of the segment
   int mat = 0, K = 0;
   int64_t pitch = 0;
@@ -985,16 +999,23 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
       const int n = down ? a.I / 16
                          : kind == kFewGateUp ? a.L / 32 * whole
                                               : kind == kFewSharedDown ? a.S / 16 * whole : a.L / 32;
-      const bool ok = wait_count(c, n);
+      const int count = wait_count(c, n);
       if (down) {
         // and what a look at the next chunks shows at the same time
-        const bool there = h.which + lane < a.T * a.k && load_acquire(c + lane) >= n;
+        const int chunk = h.which + lane, v = chunk < a.T * a.k ? load_acquire(c + lane) : 0;
+        const bool there = (v & kFewCount) >= n;
         const uint32_t done = __ballot_sync(0xffffffffu, there);
         known = h.which + (~done ? __ffs(~done) - 1 : 32);
+        if (there && (v & kFewScaled)) {
+          any_scaled = true;
+          atomicOr(&ls.scaled[chunk >> 5], 1u << (chunk & 31));
+        }
       } else {
         others |= 1u << kind;
+        if (kind == kFewGateUp && (count & kFewScaled)) u_scaled = any_scaled = true;
       }
-      if (!__all_sync(0xffffffffu, ok)) break;
+      any_scaled = __any_sync(0xffffffffu, any_scaled);
+      if (!__all_sync(0xffffffffu, count >= 0)) break;
       __syncwarp();  // what one lane has seen holds for all
       // written through the generic proxy, read by copies
       asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -1003,6 +1024,10 @@ __device__ __noinline__ void copy_rest(const FewMaps* maps, int lane) {
       uint8_t* dst = ring.rows(s);
       if (four) {
         const uint32_t tokens = ls.tokens[h.which];
+        if (any_scaled) {
+          if (i == 0) scaled = down ? ls.scaled[h.which >> 5] >> (h.which & 31) & 1u : u_scaled;
+          if (scaled) ring.header[s].kind = h.kind | kScaled | i << kSlotShift;
+        }
         mbar_arrive_expect_tx(bar, h.rows() * kFewBlock);
         const uint8_t* from = src + i * kFewBlock;
 #pragma unroll 1
@@ -1088,6 +1113,131 @@ __device__ __forceinline__ void multiply4(const uint8_t* w, const uint8_t* x, co
   }
 }
 
+// A multiplying warp's place in the ring and among the buffers of the finishing warps.
+struct Turn {
+  Place at;
+  int buf = 0;         // the finishing warp of this unit
+  uint32_t taken = 0;  // parity of its buffer, one bit a warp
+  static_assert(kMaxSlots == 8 && kFinish == 2, "packing");
+  __device__ __forceinline__ explicit Turn(int packed) {  // 0: the first
+    at.s = packed & 7;
+    at.parity = packed >> 3 & 1;
+    buf = packed >> 4 & 1;
+    taken = packed >> 5 & 3;
+  }
+  static __device__ __forceinline__ int pack(const Place& at, int buf, uint32_t taken) {
+    return at.s | at.parity << 3 | buf << 4 | taken << 5;
+  }
+};
+
+// A warp's steps through the slots of a segment in which 16 columns of a row have a unit of
+// their own, from the slot where multiply() stopped, which has been waited for; where that
+// goes on, or -1.  The products of a group's halves are made apart, and together too: with
+// one unit for both halves a token gets the bits that it gets from multiply4, so that they
+// do not depend on the other token.  Few calls come here, and the units come from L2.
+__device__ __noinline__ int multiply_scaled(int warp, int lane, int from) {
+  Context& cx = context();
+  const FewArgs& a = cx.a;
+  const Ring ring = ring_of(cx);
+  const Sums sums = sums_of(cx);
+  const Lists ls = lists_of(cx);
+  Turn m(from);
+  const Lane l(lane);
+  const Magic magic;
+  const int token = l.t >> 1, room = min(a.T, kFewChunk) - 1;
+  float acc[2][2] = {};  // [block][row g, g + 8]
+#pragma unroll 1
+  for (;;) {
+    const Header h = ring.header[m.at.s];
+    const uint8_t* slot = ring.slot(m.at.s);
+    const bool down = (h.kind & (kScaled - 1)) == kFewDown;
+    const int cols = h.cols();
+    const float* units = nullptr;  // of the lane's two groups
+    if (token < h.rows()) {
+      const int row = down ? ls.row0[h.which] + token : nth_token(ls.tokens[h.which], token);
+      units = (down ? a.h_unit + (size_t)row * (a.I / 16) : a.u_unit + (size_t)row * (a.L / 16)) +
+              (h.kind >> kSlotShift) * (C / 16) + (l.t & 1) * 4;
+    }
+    const uint8_t* rows = slot + kWeightBytes + kScaleBytes;
+    const bool dense = a.tma_scale[down] == kScalesDense;
+#pragma unroll 1
+    for (int c0 = 128 * warp; c0 < cols; c0 += 128 * kMul) {
+      const bool there = c0 + 128 <= cols || !(l.t & 1);
+      const float4 u = there && units ? __ldcg(reinterpret_cast<const float4*>(units + c0 / 16))
+                                      : make_float4(1.f, 1.f, 1.f, 1.f);
+      uint4 v[4];
+      const uint8_t* x = rows + min(l.g >> 2, room) * kPitch4 + c0 * 2 + l.t * 64;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = l.on ? reinterpret_cast<const uint4*>(x)[i] : make_uint4(0u, 0u, 0u, 0u);
+      const float4 start = *reinterpret_cast<const float4*>(
+          rows + min(token, room) * kPitch4 + kStarts + c0 / 4 + (l.t & 1) * 16);
+      const int piece = c0 / 256 * 2048 + ((((c0 / 128 & 1) << 2 | l.t) ^ (l.r & 7)) << 4);
+      const int g2 = c0 / 64 + (l.t & 1);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint8_t* w = slot + b * (kWeightBytes / 2) + piece + l.r * 128;
+        const uint8_t* scale = slot + kWeightBytes + b * (kScaleBytes / 2);
+        const uint4 q0 = *reinterpret_cast<const uint4*>(w);
+        const uint4 q8 = *reinterpret_cast<const uint4*>(w + 1024);
+        const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w8[4] = {q8.x, q8.y, q8.z, q8.w};
+        float all[4] = {start.x + start.y, start.z + start.w, start.x + start.y, start.z + start.w};
+        float half[2][4] = {{start.x, start.z, start.x, start.z}, {start.y, start.w, start.y, start.w}};
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t lo[4], hi[4];
+          nibbles(w0[i], magic, lo);
+          nibbles(w8[i], magic, hi);
+          float(&c)[4] = half[i >> 1];
+          mma_f16(all, lo[0], hi[0], lo[1], hi[1], v[i].x, v[i].y, all[0], all[1], all[2], all[3]);
+          mma_f16(all, lo[2], hi[2], lo[3], hi[3], v[i].z, v[i].w, all[0], all[1], all[2], all[3]);
+          mma_f16(c, lo[0], hi[0], lo[1], hi[1], v[i].x, v[i].y, c[0], c[1], c[2], c[3]);
+          mma_f16(c, lo[2], hi[2], lo[3], hi[3], v[i].z, v[i].w, c[0], c[1], c[2], c[3]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float first = u.x == u.y ? u.x * all[2 * r]
+                                         : fmaf(u.x, half[0][2 * r], u.y * half[1][2 * r]);
+          const float second = u.z == u.w ? u.z * all[2 * r + 1]
+                                          : fmaf(u.z, half[0][2 * r + 1], u.w * half[1][2 * r + 1]);
+          const uint32_t sc = *reinterpret_cast<const uint32_t*>(
+              dense ? scale + (l.r + 8 * r) * (cols >> 4) + g2 * 4 : scale + scale_at(l.r + 8 * r, g2));
+          if (there)
+            acc[b][r] = fmaf(__uint_as_float(sc & 0xffff0000u), second,
+                             fmaf(__uint_as_float(sc << 16), first, acc[b][r]));
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ring.empty[m.at.s]);
+    m.at.next(ring.n);
+    if (h.kind & kLastSlot) {
+      if (!wait_for(&sums.empty[m.buf], (m.taken >> m.buf & 1u) ^ 1u)) return -1;
+      m.taken ^= 1u << m.buf;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) acc[b][r] += __shfl_xor_sync(0xffffffffu, acc[b][r], 1);
+        if (!(l.t & 1) && token < h.rows()) {
+          float* p = sums.at(m.buf, warp, b, token);
+          p[l.r] = acc[b][0];
+          p[l.r + 8] = acc[b][1];
+        }
+      }
+      if (warp == 0 && lane == 0) {
+        sums.header[m.buf] = h;
+        sums.header[m.buf].kind = h.kind & ~kScaled;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums.full[m.buf]);
+      if (h.kind & kLastSegment) m.buf ^= 1;
+      return Turn::pack(m.at, m.buf, m.taken);
+    }
+    if (!wait_for(&ring.full[m.at.s], m.at.parity)) return -1;
+  }
+}
+
 // Columns of bf16 weights, 16 at a time, and up to 8 tokens (in one or two parts).
 __device__ __forceinline__ void multiply16(const uint8_t* slot, int cols, int tokens, int planes,
                                            int warp, int lane, const Lane& l, float (&acc)[2][4]) {
@@ -1117,7 +1267,9 @@ __device__ __forceinline__ void multiply16(const uint8_t* slot, int cols, int to
   }
 }
 
-__device__ __noinline__ void multiply(int warp, int lane) {
+// Products of all slots; stops at a segment of multiply_scaled, and returns where, or -1.  (A
+// call from inside the loop takes registers from it: 32 tokens 905 us, without 815 to 825.)
+__device__ __noinline__ int multiply(int warp, int lane, int from) {
   Context& cx = context();
   const FewArgs& a = cx.a;
   const Ring ring = ring_of(cx);
@@ -1140,11 +1292,18 @@ __device__ __noinline__ void multiply(int warp, int lane) {
   uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-  int buf = 0;             // the finishing warp of this unit
-  uint32_t taken = 0;      // parity of its buffer, one bit a warp
-  for (Place at;; at.next(slots)) {
+  Place at;
+  int buf = 0;
+  uint32_t taken = 0;
+  if (from) {
+    const Turn m(from);
+    at = m.at;
+    buf = m.buf;
+    taken = m.taken;
+  }
+  for (;; at.next(slots)) {
     const uint32_t s = at.s;
-    if (!wait_for(&ring.full[s], at.parity)) return;
+    if (!wait_for(&ring.full[s], at.parity)) return -1;
     const Header h = ring.header[s];
     const int kind = h.kind & 255;
     const uint8_t* slot = ring.slot(s);
@@ -1169,13 +1328,14 @@ __device__ __noinline__ void multiply(int warp, int lane) {
       }
     } else {
       if (kind == kFewEnd) break;
+      if (kind & kScaled) return Turn::pack(at, buf, taken);  // the first slot of a segment
       const int most = few_rows_of(kind);
       multiply16(slot, h.cols(), min(a.T, most), most == kFewRows ? 1 : 2, warp, lane, l, acc);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.empty[s]);
     if (h.kind & kLastSlot) {
-      if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u)) return;
+      if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u)) return -1;
       taken ^= 1u << buf;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
@@ -1206,19 +1366,24 @@ __device__ __noinline__ void multiply(int warp, int lane) {
     }
   }
   for (buf = 0; buf < kFinish; ++buf) {  // tell the finishing warps
-    if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u)) return;
+    if (!wait_for(&sums.empty[buf], (taken >> buf & 1u) ^ 1u)) return -1;
     if (warp == 0 && lane == 0) sums.header[buf].kind = kFewEnd;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sums.full[buf]);
   }
+  return -1;
 }
 
 // ----------------------------------------------------------------- finishing
 
-// Adds one to a counter after the warp's stores.
-__device__ __forceinline__ void count_done(int32_t* c, int lane) {
+// Adds one to a counter after the warp's stores; with `scaled` its bit is set first, so that
+// whoever sees the count sees that too.
+__device__ __forceinline__ void count_done(int32_t* c, int lane, bool scaled = false) {
   __syncwarp();
-  if (lane == 0) add_release(c, 1);
+  if (lane == 0) {
+    if (scaled) atomicOr(c, kFewScaled);
+    add_release(c, 1);
+  }
 }
 
 // 32 columns from n0 on of every token: the groups' sums, in order, whichever order they
@@ -1342,6 +1507,7 @@ __device__ __noinline__ void finish(int buf, int lane) {
 #pragma unroll 1
       for (int t = 0; t < a.T; ++t) unit[t * 32] = 0.f;
     }
+    bool scaled = false;  // columns with a unit of their own
 #pragma unroll 1
     for (int i = 0; i < h.rows(); ++i) {
       const int t = four ? nth_token(tokens, i) : token0 + i;
@@ -1370,9 +1536,21 @@ __device__ __noinline__ void finish(int buf, int lane) {
             p[(size_t)a.T * a.S] = f32_to_bf16_bits(v - bf16_bits_to_f32(high));
           }
         } else {
-          // fp16 in pair order, and the start value of each 16 columns
+          // fp16 in pair order, and the unit and the start value of each 16 columns
           const bool mine = !pair || half == 0;
           if (mine && !(fabsf(v) <= 65504.0f)) record_status(a.status, MOE_ERR_UNSUPPORTED);
+          const uint32_t top =
+              __reduce_max_sync(0xffffffffu, mine ? __float_as_uint(fabsf(v)) : 0u);
+          float by_one = 1.f;
+          if (top > 0u && top < __float_as_uint(kFewSmallest)) {
+            const uint32_t up = min(127u + 14u + 127u - (top >> 23), 253u);
+            v *= __uint_as_float(up << 23);
+            by_one = __uint_as_float((254u - up) << 23);
+            scaled = true;
+          }
+          float* units = pair ? a.h_unit + (size_t)(row0 + i) * (a.I / 16)
+                              : a.u_unit + (size_t)t * (a.L / 16);
+          if (mine && r16 == 0) units[c / 16] = by_one;
           const __half f = __float2half_rn(v);
           uint8_t* row = pair ? a.h16 + (row0 + i) * few_row_bytes(a.I)
                               : a.x16 + t * few_row_bytes(a.L);
@@ -1402,7 +1580,7 @@ __device__ __noinline__ void finish(int buf, int lane) {
     if (lane == 0) mbar_arrive(&sums.empty[buf]);  // the buffer has been read
     if (pair || kind == kFewLatDown) {
       count_done(a.counters + (kind == kFewGateUp ? kFewFixed + h.which : kind == kFewLatDown ? 1 : 2),
-                 lane);
+                 lane, scaled);
       continue;
     }
     if (kind == kFewDown) {
@@ -1448,7 +1626,8 @@ struct Layout {
     slot = slot_bytes(rows_bytes(a));
     sums = sums_bytes(a);
     unit = kFinish * a.T * 32 * 4;
-    lists = (12 * a.T * a.k + 15) / 16 * 16;
+    const int pairs = a.T * a.k;
+    lists = (12 * pairs + (pairs + 31) / 32 * 4 + 15) / 16 * 16;
   }
   __host__ __device__ __forceinline__ int rest() const {
     return static_cast<int>(sizeof(Context)) + sums + unit + lists;
@@ -1504,7 +1683,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     finish(warp - kCopy, lane);
   } else {
     build_lists(threadIdx.x - 32 * kFirstMul);
-    multiply(warp - kFirstMul, lane);
+    const int mul = warp - kFirstMul;
+    for (int at = 0; at >= 0;) {
+      at = multiply(mul, lane, at);
+      if (at >= 0) at = multiply_scaled(mul, lane, at);
+    }
   }
 }
 

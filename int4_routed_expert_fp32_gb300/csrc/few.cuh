@@ -58,7 +58,9 @@ struct FewArgs {
   uint32_t* keys;    // [T, E] order of score + bias
   uint8_t* x16;      // [T] rows of fp16 blocks (below): x times a power of two, or u
   float* x_unit;     // fp32 [T]: what one unit of x16 stands for
+  float* u_unit;     // fp32 [T, L / 16]: what one unit of 16 columns of u stands for
   uint8_t* h16;      // [T k] rows of fp16 blocks
+  float* h_unit;     // fp32 [T k, I / 16]: the same of h
   float* y;          // fp32 [groups, T, D]: weighted sums of the chunks of a group
   uint16_t* hs;      // bf16 [2, T, S]: high and low parts of the shared expert's h
   float* ys;         // fp32 [T, H] shared expert's output
@@ -73,8 +75,16 @@ struct FewArgs {
 
 // counters: [0] ticket, [1] u tiles done, [2] shared h tiles done, [3] z tiles
 // done, then one per chunk (T k), then one per 32 columns of D, then one per 32
-// columns of H and kFewRows tokens.
+// columns of H and kFewRows / 2 tokens.  Those of u and of the chunks keep in a bit
+// of their own whether a tile has a unit other than 1.
 constexpr int kFewFixed = 4;
+constexpr int kFewScaled = 1 << 30, kFewCount = kFewScaled - 1;
+
+// h and u are stored as fp16.  h goes as the square of x, and u has the size of its weights
+// and x, so both may lie anywhere: 16 columns (32 of u) whose largest value is below this
+// are stored times the power of two that brings it to [2^14, 2^15).  Others are stored
+// as they are: fp16's step of 2^-24 below its normal range then costs 2^-12 of them at most.
+constexpr float kFewSmallest = 0x1p-11f;
 
 // Matrices with tensor maps; the first three are of packed int4.
 enum FewMatrix {

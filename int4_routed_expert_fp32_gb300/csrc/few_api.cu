@@ -27,7 +27,9 @@ size_t carve(FewArgs* a, void* base) {
   a->keys = static_cast<uint32_t*>(take(a->router_w ? 4 * T * a->E : 0));
   a->x16 = static_cast<uint8_t*>(take(T * few_row_bytes(a->D)));
   a->x_unit = static_cast<float*>(take(4 * T));
+  a->u_unit = static_cast<float*>(take(4 * T * (L / 16)));
   a->h16 = static_cast<uint8_t*>(take(P * few_row_bytes(a->I)));
+  a->h_unit = static_cast<float*>(take(4 * P * (a->I / 16)));
   a->y = static_cast<float*>(take(4 * (P < kFewGroups ? P : kFewGroups) * T * D));
   a->hs = static_cast<uint16_t*>(take(4 * T * S));
   a->ys = static_cast<float*>(take(S ? 4 * T * H : 0));

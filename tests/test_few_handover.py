@@ -39,6 +39,7 @@ def test_one_thread_takes_every_ticket():
 
 
 @pytest.mark.parametrize("role,header", [("copy_rest", "ring.header[s]"), ("multiply", "ring.header[s]"),
+                                         ("multiply_scaled", "ring.header[m.at.s]"),
                                          ("finish", "sums.header[buf]")])
 def test_a_header_is_read_by_the_whole_warp_before_the_slot_moves_on(role, header):
     """A lane's arrival on a slot's barrier is what lets the slot be used again, its
