@@ -13,9 +13,9 @@ adapters of many requests beside the latent projections:
 With ``few_tokens`` a call of at most 32 tokens, with 1.5 tokens to an expert or fewer on
 average, runs dispatch, experts and combine as one operator, ``experts_few``.  It reads an
 expert's weights once for every two tokens; the other path, once for 16.  Whole layers,
-this way and the other, us: 8 of 384 experts of 7168 x 2048, 1 token 52 and 97, 24 tokens
+this way and the other, us: 8 of 384 experts of 7168 x 2048, 1 token 53 and 97, 24 tokens
 672 and 752; 8 of 128 experts of 4096 x 1536, 24 tokens 277 and 280, 32 tokens 351 and 307;
-2 of 8 experts of 4096 x 14336, 8 tokens 179 and 205, 16 tokens 297 and 206.
+2 of 8 experts of 4096 x 14336, 8 tokens 186 and 202, 16 tokens 302 and 209.
 
 The latent path is the one of the "Kimi K3 latent up-projection" page
 (KimiSparseMoeBlock.forward: router on the full width, down-projection, experts,

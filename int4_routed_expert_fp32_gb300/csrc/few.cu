@@ -6,7 +6,8 @@
 //
 //   few_front_kernel   the router's logits (one pass over its fp32 weight), x as
 //                      fp16 in the order of the packed nibbles, counters to zero
-//   few_kernel         two persistent CTAs per SM.  Every CTA selects the experts
+//   few_kernel         two persistent CTAs per SM (one, with bf16 weights and 15 to 19
+//                      tokens or more: few_stages).  Every CTA selects the experts
 //                      (the same arithmetic everywhere, cheaper than another
 //                      launch), then takes units of work in ticket order: 16
 //                      gate rows and the 16 up rows of the same columns, times the
@@ -35,7 +36,7 @@
 // 2 each), HBM 1570: near enough to one another that they do not overlap fully.
 //
 // Measured (graphs of calls; behind it the bytes at the measured copy rate): the layer of
-// one token, 8 of 384 experts, 7168 x 2048: 52 us, 31; of 32 tokens: 819 us, 689; 6
+// one token, 8 of 384 experts, 7168 x 2048: 53 us, 31; of 32 tokens: 812 us, 689; 6
 // tokens of 3584 x 1024, experts alone: 50 us, 20; 16 tokens of 256 x 128: 26 us, the
 // latency of its steps.
 #include "few.cuh"
@@ -59,7 +60,9 @@ constexpr int kFrontThreads = 256;
 constexpr int kFrontExperts = 2;             // router rows of a CTA
 constexpr int kFrontTokens = 4;              // tokens at a time
 static_assert(kFrontTokens * kFrontExperts == 8, "sums over the warp");
-constexpr int kFrontLoads = 7;               // float4 of a router row held by a thread
+// float4 of a router row held by a thread: 7168 columns a pass over the tokens.  Wider rows
+// take another (32 tokens, 384 small experts: H 7168 219 us, 7232 223).
+constexpr int kFrontLoads = 7;
 
 // Ring slot: weights (32 rows of C / 2 bytes: for each row block of 16, pieces of 128
 // bytes of its rows, swizzled), scales (32 rows, swizzled), rows of tokens: fp16
@@ -1134,7 +1137,8 @@ struct Turn {
 // their own, from the slot where multiply() stopped, which has been waited for; where that
 // goes on, or -1.  The products of a group's halves are made apart, and together too: with
 // one unit for both halves a token gets the bits that it gets from multiply4, so that they
-// do not depend on the other token.  Few calls come here, and the units come from L2.
+// do not depend on the other token.  Few calls come here, and the units come from L2 (one
+// token of 8 experts, 7168 x 2048, all of h below 2^-11: 63 us, of ordinary size 48).
 __device__ __noinline__ int multiply_scaled(int warp, int lane, int from) {
   Context& cx = context();
   const FewArgs& a = cx.a;
@@ -1698,7 +1702,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 // Shared memory of a CTA when two, or when one, share an SM, less the ring's alignment.
 constexpr int kRoomOfTwo = 113 * 1024 - 1024, kRoomOfOne = 227 * 1024 - 1024;
 
-// Two slots at least; where two CTAs leave no room for that, one takes the SM.
+// Two slots at least; where two CTAs leave no room for that, one takes the SM.  With latent
+// projections or a shared expert, whose units have the partial sums of 8 tokens, that is so
+// from 15 tokens on at k = 8, 16 at k = 6, 19 at k = 2: 8 of 384 experts, latent 3584 x 1024,
+// 14 tokens 204 us, 15 tokens 248; 6 of 128, 4096 x 1408 and shared 2816, 15 tokens 156, 16
+// tokens 201.
 int few_stages(const FewArgs& a) {
   const Layout lay(a);
   int n = (kRoomOfTwo - lay.rest()) / lay.slot;

@@ -30,7 +30,8 @@ def tokens(g, T, width):
 
 
 @pytest.mark.parametrize("T,D,E,k,I", [(9, 256, 6, 3, 128), (9, 320, 8, 3, 192), (18, 128, 4, 2, 2112),
-                                       (1, 64, 1, 1, 64), (30, 2304, 7, 4, 320)])
+                                       (1, 64, 1, 1, 64), (30, 2304, 7, 4, 320), (9, 256, 6, 3, 256),
+                                       (32, 64, 64, 32, 64)])
 def test_experts_of_small_tokens(moe, T, D, E, k, I):
     g = torch.Generator().manual_seed(T + D + I)
     w = experts(g, E, D, I)
@@ -98,7 +99,8 @@ def test_padded_rows_beside_small_ones(moe):
 
 LAYERS = [dict(T=9, H=256, E=6, k=2, I=128), dict(T=9, H=320, E=6, k=2, I=192, L=576, norm=True),
           dict(T=9, H=320, E=6, k=2, I=192, L=576), dict(T=18, H=128, E=5, k=3, I=64, L=2112, norm=True),
-          dict(T=9, H=192, E=4, k=2, I=64, S=128), dict(T=20, H=192, E=7, k=2, I=64, L=320, S=128)]
+          dict(T=9, H=256, E=6, k=2, I=256, L=512, norm=True), dict(T=9, H=192, E=4, k=2, I=64, S=128),
+          dict(T=20, H=192, E=7, k=2, I=64, L=320, S=128)]
 
 
 @pytest.mark.parametrize("c", LAYERS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
