@@ -6,8 +6,8 @@
 //
 //   few_front_kernel   the router's logits (one pass over its fp32 weight), x as
 //                      fp16 in the order of the packed nibbles, counters to zero
-//   few_kernel         two persistent CTAs per SM (one, with bf16 weights and 15 to 19
-//                      tokens or more: few_stages).  Every CTA selects the experts
+//   few_kernel         two persistent CTAs per SM (one, with bf16 weights and from some
+//                      15 tokens on: few_stages).  Every CTA selects the experts
 //                      (the same arithmetic everywhere, cheaper than another
 //                      launch), then takes units of work in ticket order: 16
 //                      gate rows and the 16 up rows of the same columns, times the
@@ -1704,7 +1704,7 @@ constexpr int kRoomOfTwo = 113 * 1024 - 1024, kRoomOfOne = 227 * 1024 - 1024;
 
 // Two slots at least; where two CTAs leave no room for that, one takes the SM.  With latent
 // projections or a shared expert, whose units have the partial sums of 8 tokens, that is so
-// from 15 tokens on at k = 8, 16 at k = 6, 19 at k = 2: 8 of 384 experts, latent 3584 x 1024,
+// from 12 tokens on at k = 16, 15 at k = 8, 16 at k = 6, 19 at k = 2: 8 of 384 experts, latent 3584 x 1024,
 // 14 tokens 204 us, 15 tokens 248; 6 of 128, 4096 x 1408 and shared 2816, 15 tokens 156, 16
 // tokens 201.
 int few_stages(const FewArgs& a) {
